@@ -1,4 +1,4 @@
-"""Python binding of libloom (the C ABI in include/loom.h and loom_tuning.h).
+"""Python binding of libloom (the C ABI in include/loom.h, loom_tuning.h and loom_token.h).
 
 The functions keep the C names and only marshal arguments: tensors become
 device pointers, the stream defaults to torch's current stream, and a status
@@ -32,6 +32,8 @@ LOOM_ERR_ARG = -7
 
 LOOM_DEVERR_COUNT_RANGE = 0x1
 LOOM_DEVERR_TIMEOUT = 0x2
+LOOM_DEVERR_NONFINITE = 0x4
+LOOM_DEVERR_NO_TOKEN = 0x8
 
 LOOM_OP_I8_UNPACK = 0
 LOOM_OP_FULL_TILE_SUM = 1
@@ -41,6 +43,11 @@ LOOM_OP_PACKED_DOT = 4
 LOOM_OP_LANE_SUMS = 5
 LOOM_OP_ROUTED_COMBINE = 6
 LOOM_OP_STAGE_ROWS = 7
+LOOM_OP_QUANTIZE_TOKENS = 8
+LOOM_OP_I8_MATMUL = 9
+LOOM_OP_LAYER_NORM = 10
+LOOM_OP_LAYER_NORM_BACKWARD = 11
+LOOM_OP_SAMPLE_TOKENS = 12
 
 LOOM_KERNEL_UNPACK = 1
 LOOM_KERNEL_ROWSUM_STAGED = 2
@@ -59,6 +66,15 @@ LOOM_KERNEL_ROUTED_DIRECT = 14
 LOOM_KERNEL_STAGE_ROWS = 15
 LOOM_KERNEL_DOT_TENSOR_ROWS = 16
 LOOM_KERNEL_ROWSUM_SEGMENTS = 17
+LOOM_KERNEL_I8_MATMUL_DP4A = 18
+LOOM_KERNEL_NORM_ROWS = 20
+LOOM_KERNEL_NORM_LONG = 21
+LOOM_KERNEL_NORM_BACKWARD = 22
+LOOM_KERNEL_SAMPLE = 24
+
+LOOM_F32 = 0
+LOOM_F16 = 1
+LOOM_BF16 = 2
 
 LOOM_MAX_DEPTH = 8
 LOOM_PATH_AUTO = 0
@@ -77,7 +93,9 @@ EXPORTS = (
     "loom_i8_dequant_dot_ex", "loom_i8_dequant_dot_workspace_bytes", "loom_i8_dequant_dot_noalloc",
     "loom_packed_dot", "loom_packed_dot_ex", "loom_sum_rows", "loom_sum_rows_ex", "loom_sum_guarded_rows",
     "loom_sum_guarded_rows_ex", "loom_routed_combine", "loom_routed_combine_ex", "loom_stage_rows",
-    "loom_stream_floor",
+    "loom_stream_floor", "loom_token_launch_config", "loom_quantize_tokens", "loom_i8_matmul", "loom_i8_matmul_ex",
+    "loom_layer_norm", "loom_layer_norm_i8", "loom_layer_norm_backward", "loom_layer_norm_backward_workspace_bytes",
+    "loom_sample_tokens",
 )
 
 
@@ -136,6 +154,15 @@ def _bind() -> ctypes.CDLL:
         "loom_stage_rows": [P, P, i64, i64, i32, i32, P, i32, P],
         "loom_i8_unpack": [P, i64, P, P],
         "loom_stream_floor": [P, i64, i32, i32, i32, P, P, P],
+        "loom_token_launch_config": [i32, P, i32, ctypes.POINTER(loom_launch)],
+        "loom_quantize_tokens": [P, i32, i64, i32, i64, P, P, P, P],
+        "loom_i8_matmul": [P, P, i32, i32, P, P, i32, P, P, i32, i64, P, P],
+        "loom_i8_matmul_ex": [P, P, i32, i32, P, P, i32, P, P, i32, i64, P, P, ctypes.POINTER(loom_tuning), P],
+        "loom_layer_norm": [P, i32, i64, i32, i64, P, P, f32, P, i64, P, P, P],
+        "loom_layer_norm_i8": [P, i32, i64, i32, i64, P, P, f32, P, P, P, P],
+        "loom_layer_norm_backward": [P, i64, P, i64, i32, i64, i32, P, P, P, P, i64, P, P, P, i64, P],
+        "loom_layer_norm_backward_workspace_bytes": [i64, i32, ctypes.POINTER(i64)],
+        "loom_sample_tokens": [P, i32, i64, i32, i64, P, f32, P, i32, P, f32, P, f32, P, P, P, P, P],
         "loom_status_string": [i32],
         "loom_abi_version": [],
     }
@@ -496,3 +523,200 @@ def loom_stream_floor(src, nbytes: int, schedule: int, depth: int, ctas_per_sm: 
     tensor or address); ``sink`` is a device int64 word."""
     _check(_lib.loom_stream_floor(_ptr(src), int(nbytes), int(schedule), int(depth), int(ctas_per_sm),
                                   _ptr(sink), _ptr(error), _stream(stream, sink)), "loom_stream_floor")
+
+
+# ---- token operators (loom_token.h) ----------------------------------------------------
+_dtypes: dict = {}
+
+
+def _dtype(dtype) -> int:
+    """LOOM_F32 / LOOM_F16 / LOOM_BF16 of a torch dtype (or one of those numbers)."""
+    if isinstance(dtype, int):
+        return dtype
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: LOOM_F32, torch.float16: LOOM_F16, torch.bfloat16: LOOM_BF16})
+    if dtype not in _dtypes:
+        raise LoomError(LOOM_ERR_ARG, f"element type {dtype}")
+    return _dtypes[dtype]
+
+
+def _matrix(t, where: str):
+    """(rows, width, stride) of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise LoomError(LOOM_ERR_SHAPE, f"{where}: a matrix with contiguous rows is wanted")
+    return t.shape[0], t.shape[1], t.stride(0)
+
+
+def _floats(where: str, n: int, *tensors):
+    """The optional tensors are contiguous f32 of n elements each."""
+    import torch
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()):
+            raise LoomError(LOOM_ERR_SHAPE, f"{where}: {n} contiguous float32 values are wanted")
+
+
+def loom_token_launch_config(op: int, workload) -> dict:
+    arr = (ctypes.c_int64 * max(1, len(workload)))(*[int(v) for v in workload])
+    out = loom_launch()
+    _check(_lib.loom_token_launch_config(int(op), arr, len(workload), ctypes.byref(out)), "loom_token_launch_config")
+    return out.as_dict()
+
+
+def loom_quantize_tokens(x, *, q=None, scale=None, error=None, stream=None):
+    """Tokens ``x[tokens][k]`` (float32, float16 or bfloat16) to signed bytes with one scale
+    each; returns ``(q_packed int32 [tokens][k/4], scale float32 [tokens])``."""
+    import torch
+    tokens, k, stride = _matrix(x, "loom_quantize_tokens")
+    if q is None:
+        q = _empty(x, (tokens, k // 4), torch.int32)
+    if scale is None:
+        scale = _empty(x, (tokens,), torch.float32)
+    with _on_device(x):
+        _check(_lib.loom_quantize_tokens(x.data_ptr(), _dtype(x.dtype), tokens, k, stride, _ptr(q), _ptr(scale),
+                                         _ptr(error), _stream(stream, x)), "loom_quantize_tokens")
+    return q, scale
+
+
+def loom_i8_matmul(w_packed, scale_w, n_rows: int, k: int, x_packed, scale_x, tokens: int, *, bias=None, y=None,
+                   y_dtype=None, acc=None, want_acc: bool = False, stream=None):
+    """``y[tokens][n_rows]`` of type ``y_dtype`` (float32 by default; the type of ``y`` where it
+    is given) and, when requested, ``acc`` int32; returns ``(y, acc)``.  ``w_packed`` and
+    ``x_packed`` hold the signed bytes row after row (int8 tensors, or their int32 words)."""
+    return _i8_matmul("loom_i8_matmul", w_packed, scale_w, n_rows, k, x_packed, scale_x, tokens, bias, y, y_dtype, acc,
+                      want_acc, stream)
+
+
+def loom_i8_matmul_ex(w_packed, scale_w, n_rows: int, k: int, x_packed, scale_x, tokens: int, *, bias=None, y=None,
+                      y_dtype=None, acc=None, want_acc: bool = False, error=None, tuning=None, stream=None):
+    tp = ctypes.byref(tuning) if tuning is not None else None
+    return _i8_matmul("loom_i8_matmul_ex", w_packed, scale_w, n_rows, k, x_packed, scale_x, tokens, bias, y, y_dtype, acc,
+                      want_acc, stream, _ptr(error), tp)
+
+
+def _i8_matmul(name, w_packed, scale_w, n_rows, k, x_packed, scale_x, tokens, bias, y, y_dtype, acc, want_acc, stream,
+               *more):
+    import torch
+    if y is None:
+        y = _empty(w_packed, (tokens, n_rows), torch.float32 if y_dtype is None else y_dtype)
+    if acc is None and want_acc:
+        acc = _empty(w_packed, (tokens, n_rows), torch.int32)
+    _, _, stride = _matrix(y, name)
+    with _on_device(w_packed):
+        _check(getattr(_lib, name)(_ptr(w_packed), _ptr(scale_w), int(n_rows), int(k), _ptr(x_packed), _ptr(scale_x),
+                                   int(tokens), _ptr(bias), y.data_ptr(), _dtype(y.dtype), stride, _ptr(acc), *more,
+                                   _stream(stream, w_packed)), name)
+    return y, acc
+
+
+def loom_layer_norm(x, gain=None, bias=None, eps: float = 1e-5, *, y=None, mean=None, rstd=None,
+                    want_stats: bool = True, stream=None):
+    """Layer norm of the rows of ``x`` (float32, float16 or bfloat16); ``gain`` and ``bias``
+    float32 or None.  Returns ``(y, mean, rstd)``, the last two float32 per row as the
+    backward pass takes them (None without ``want_stats``)."""
+    import torch
+    rows, width, stride = _matrix(x, "loom_layer_norm")
+    _floats("loom_layer_norm", width, gain, bias)
+    if y is None:
+        y = _empty(x, (rows, width), x.dtype)
+    if want_stats:
+        mean = _empty(x, (rows,), torch.float32) if mean is None else mean
+        rstd = _empty(x, (rows,), torch.float32) if rstd is None else rstd
+    if y.dtype != x.dtype:
+        raise LoomError(LOOM_ERR_ARG, "loom_layer_norm: y has another type than x")
+    _, _, y_stride = _matrix(y, "loom_layer_norm")
+    with _on_device(x):
+        _check(_lib.loom_layer_norm(x.data_ptr(), _dtype(x.dtype), rows, width, stride, _ptr(gain), _ptr(bias), eps,
+                                    y.data_ptr(), y_stride, _ptr(mean), _ptr(rstd), _stream(stream, x)),
+               "loom_layer_norm")
+    return y, mean, rstd
+
+
+def loom_layer_norm_i8(x, gain=None, bias=None, eps: float = 1e-5, *, q=None, scale=None, error=None, stream=None):
+    """``loom_quantize_tokens`` of layer norm's rows, which are never written; returns
+    ``(q_packed, scale)``."""
+    import torch
+    rows, width, stride = _matrix(x, "loom_layer_norm_i8")
+    _floats("loom_layer_norm_i8", width, gain, bias)
+    if q is None:
+        q = _empty(x, (rows, width // 4), torch.int32)
+    if scale is None:
+        scale = _empty(x, (rows,), torch.float32)
+    with _on_device(x):
+        _check(_lib.loom_layer_norm_i8(x.data_ptr(), _dtype(x.dtype), rows, width, stride, _ptr(gain), _ptr(bias), eps,
+                                       _ptr(q), _ptr(scale), _ptr(error), _stream(stream, x)), "loom_layer_norm_i8")
+    return q, scale
+
+
+def loom_layer_norm_backward_workspace_bytes(rows: int, width: int) -> int:
+    """Bytes of the workspace of ``loom_layer_norm_backward`` on the current device."""
+    out = ctypes.c_int64(0)
+    _check(_lib.loom_layer_norm_backward_workspace_bytes(int(rows), int(width), ctypes.byref(out)),
+           "loom_layer_norm_backward_workspace_bytes")
+    return int(out.value)
+
+
+def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=None, dbias=None, want_dx: bool = True,
+                             want_params: bool = True, workspace=AUTO, stream=None):
+    """Gradients of layer norm: ``(dx, dgain, dbias)`` from ``dy`` and ``x`` (same type), the
+    forward pass's ``mean`` and ``rstd``, and ``gain``.  ``want_dx`` / ``want_params`` leave
+    out what is not needed (None).  ``workspace``: a tensor, an ``(address, bytes)`` pair, or
+    "auto" (allocated for the call from torch's allocator)."""
+    import torch
+    rows, width, x_stride = _matrix(x, "loom_layer_norm_backward")
+    _, _, dy_stride = _matrix(dy, "loom_layer_norm_backward")
+    _floats("loom_layer_norm_backward", width, gain)
+    _floats("loom_layer_norm_backward", rows, mean, rstd)
+    if dy.dtype != x.dtype or dy.shape != x.shape:
+        raise LoomError(LOOM_ERR_SHAPE, "loom_layer_norm_backward: dy has another type or shape than x")
+    if dx is None and want_dx:
+        dx = _empty(x, (rows, width), x.dtype)
+    if want_params:
+        dgain = _empty(x, (width,), torch.float32) if dgain is None else dgain
+        dbias = _empty(x, (width,), torch.float32) if dbias is None else dbias
+    dx_stride = 0
+    if dx is not None:
+        if dx.dtype != x.dtype or dx.shape != x.shape:
+            raise LoomError(LOOM_ERR_SHAPE, "loom_layer_norm_backward: dx has another type or shape than x")
+        _, _, dx_stride = _matrix(dx, "loom_layer_norm_backward")
+    with _on_device(x):
+        st = _stream(stream, x)
+        if isinstance(workspace, str) and workspace == AUTO:
+            nbytes = loom_layer_norm_backward_workspace_bytes(rows, width)
+            workspace = _empty(x, (nbytes,), torch.uint8)
+            if stream is not None:   # the allocator may hand it out again only after this stream's work
+                workspace.record_stream(torch.cuda.ExternalStream(st, device=x.device))
+        wp, wb = (workspace if isinstance(workspace, tuple) else
+                  (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+        _check(_lib.loom_layer_norm_backward(dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, _dtype(x.dtype), rows, width,
+                                             _ptr(gain), _ptr(mean), _ptr(rstd), _ptr(dx), dx_stride, _ptr(dgain),
+                                             _ptr(dbias), wp, int(wb), st), "loom_layer_norm_backward")
+    return dx, dgain, dbias
+
+
+def loom_sample_tokens(logits, uniform, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, logprob=None,
+                       want_logprob: bool = True, error=None, stream=None):
+    """The next token of each row of ``logits[rows][vocab]`` from ``uniform`` float32 ``[rows]``
+    in [0, 1); each setting is a number for every row or a device tensor with one per row
+    (``top_k`` int32, the others float32).  Returns ``(token int32, logprob float32)``."""
+    import torch
+    rows, vocab, stride = _matrix(logits, "loom_sample_tokens")
+    _floats("loom_sample_tokens", rows, uniform)
+    args = []
+    for name, v, dtype, off in (("temperature", temperature, torch.float32, 1.0), ("top_k", top_k, torch.int32, 0),
+                                ("top_p", top_p, torch.float32, 1.0), ("min_p", min_p, torch.float32, 0.0)):
+        if isinstance(v, torch.Tensor):
+            if v.dtype != dtype or v.numel() != rows or not v.is_contiguous():
+                raise LoomError(LOOM_ERR_SHAPE, f"loom_sample_tokens: {name}: {rows} contiguous {dtype} values are wanted")
+            args += [v.data_ptr(), off]
+        else:
+            args += [None, v]
+    if token is None:
+        token = _empty(logits, (rows,), torch.int32)
+    if logprob is None and want_logprob:
+        logprob = _empty(logits, (rows,), torch.float32)
+    with _on_device(logits):
+        _check(_lib.loom_sample_tokens(logits.data_ptr(), _dtype(logits.dtype), rows, vocab, stride, *args, _ptr(uniform),
+                                       _ptr(token), _ptr(logprob), _ptr(error), _stream(stream, logits)),
+               "loom_sample_tokens")
+    return token, logprob

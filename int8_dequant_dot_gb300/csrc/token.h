@@ -1,0 +1,96 @@
+// token.h -- parameters and launchers shared between the host layer of the
+// token operators (token_api.cu) and their kernels.  Not part of the ABI.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/loom_token.h"
+#include "internal.h"
+
+namespace loom {
+
+inline int64_t dtype_bytes(int32_t dtype) { return dtype == LOOM_F32 ? 4 : 2; }
+
+// ---- 8-bit matrix product (i8_matmul.cu: dp4a) -----------------------------------
+constexpr int MM_DP4A_PASS = 8;       // tokens per pass of the dp4a kernel
+constexpr int MM_DP4A_CTAS_PER_SM = 2;
+
+struct MatmulParams {
+    const int8_t *w;          // [n][k]
+    const float *scale_w;
+    const int8_t *x;          // [tokens][k]
+    const float *scale_x;
+    const float *bias;        // [n] or NULL
+    void *y;                  // [tokens][n], rows y_stride elements apart
+    int32_t *acc;             // [tokens][n] or NULL
+    int32_t *error;
+    int64_t y_stride;
+    int32_t tokens, n, k, y_dtype;
+    int32_t rows_per_cta;     // dp4a kernel
+    uint64_t wait_ns;
+};
+cudaError_t launch_matmul_dp4a(const MatmulParams &p, bool vec16, const loom_launch &L, cudaStream_t stream);
+
+// ---- rows: quantisation and layer norm (token_rows.cu) ----------------------------
+enum class RowMode { Quantize = 0, Norm = 1, NormI8 = 2 };
+struct RowsParams {
+    const void *x;
+    int64_t rows, x_stride;
+    int32_t width;
+    float eps;
+    const float *gain, *bias;   // or NULL
+    void *y;                    // Norm: rows y_stride apart
+    int64_t y_stride;
+    float *mean, *rstd;         // Norm: or NULL
+    int8_t *q;                  // Quantize, NormI8: [rows][width]
+    float *scale;
+    int32_t *error;
+};
+// `vec` is the number of elements per load: the widest of 16 bytes, 8 bytes and one
+// element that every row's start and the width allow (row_vec).
+int row_vec(int32_t dtype, int32_t width, const void *const *pointers, const int64_t *strides, int n);
+bool rows_geometry(int64_t rows, int32_t width, loom_launch *out);
+cudaError_t launch_rows(const RowsParams &p, RowMode mode, int32_t dtype, int vec, const loom_launch &L,
+                        cudaStream_t stream);
+
+constexpr int NG_EPT = 8;                       // elements a thread of the register kernel holds
+constexpr int32_t NG_MAX_WIDTH = 1024 * NG_EPT; // wider rows take two passes
+
+struct NormGradParams {
+    const void *dy, *x;
+    int64_t dy_stride, x_stride, dx_stride, rows;
+    int32_t width;
+    const float *gain;          // or NULL
+    const float *mean, *rstd;
+    void *dx;                   // or NULL
+    float *dgain, *dbias;       // or NULL
+    float *partial;             // [parts][2][width] partial column sums (workspace), or NULL
+    float *row_sums;            // [rows][2]: rows wider than NG_MAX_WIDTH (workspace)
+};
+// Geometry of the launch that takes the column sums; *parts (may be NULL) receives the
+// number of partial sums per column.
+bool norm_grad_geometry(int64_t rows, int32_t width, int64_t sms, loom_launch *out, int64_t *parts);
+int64_t norm_grad_workspace_bytes(int64_t rows, int32_t width, int64_t sms);
+cudaError_t launch_norm_grad(const NormGradParams &p, int32_t dtype, int vec, const loom_launch &L, int64_t parts,
+                             cudaStream_t stream);
+
+// ---- sampling (token_sample.cu) -----------------------------------------------------
+struct SampleParams {
+    const void *logits;
+    int64_t rows, stride;
+    int32_t vocab;
+    const float *d_temperature;
+    const int32_t *d_top_k;
+    const float *d_top_p, *d_min_p;   // per row, or NULL for the values below
+    float temperature, top_p, min_p;
+    int32_t top_k;
+    const float *uniform;
+    int32_t *token;
+    float *logprob;
+    int32_t *error;
+};
+bool sample_geometry(int64_t rows, int32_t vocab, int32_t dtype, int64_t sms, loom_launch *out);
+cudaError_t launch_sample(const SampleParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream);
+
+}  // namespace loom
