@@ -44,6 +44,7 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
 
 /* Kernels they select (loom_launch.kernel). */
 #define LOOM_KERNEL_I8_MATMUL_DP4A 18   /* few tokens: dp4a, weights streamed once per pass of up to 8 tokens */
+#define LOOM_KERNEL_I8_MATMUL_TENSOR 19 /* tcgen05 MMA on exact f16 copies; units_per_cta = channels */
 #define LOOM_KERNEL_NORM_ROWS 20        /* one CTA (or warp) per row, the row held in registers */
 #define LOOM_KERNEL_NORM_LONG 21        /* rows longer than the registers of a CTA, read again from L2 */
 #define LOOM_KERNEL_NORM_BACKWARD 22    /* CTAs over shares of the rows, column sums in registers */

@@ -67,6 +67,7 @@ LOOM_KERNEL_STAGE_ROWS = 15
 LOOM_KERNEL_DOT_TENSOR_ROWS = 16
 LOOM_KERNEL_ROWSUM_SEGMENTS = 17
 LOOM_KERNEL_I8_MATMUL_DP4A = 18
+LOOM_KERNEL_I8_MATMUL_TENSOR = 19
 LOOM_KERNEL_NORM_ROWS = 20
 LOOM_KERNEL_NORM_LONG = 21
 LOOM_KERNEL_NORM_BACKWARD = 22

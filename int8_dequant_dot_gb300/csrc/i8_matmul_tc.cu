@@ -1,0 +1,729 @@
+// i8_matmul_tc.cu -- matrix product of 8-bit tokens and 8-bit weights on the
+// 5th-generation tensor cores (tcgen05, sm_103a), for nine tokens to many.
+//
+//   acc[t][r] = sum_k W[r][k] X[t][k],  y[t][r] = (float)acc * (sw[r] * sx[t]) + bias[r]
+//
+// sm_103a multiplies no 8-bit integers on its tensor cores at a useful rate, but every
+// int8 is an f16, every product of two is exact in f32, and at most 1024 of them stay
+// within 2^24, where f32 holds every whole number.  So the bytes stay bytes in memory
+// and L2 and become f16 inside the SM, and a finished f32 accumulator of 1024 k at most
+// is turned into int32 and added up in registers: acc is exact for any k.
+//
+// Design
+//  * D[channel][token]: 128 channels are the MMA's M (tensor-memory lanes) of each CTA,
+//    the tokens its N (32 to 256).  Up to 128 tokens a CTA works alone; above, CTA pairs
+//    share each MMA (cta_group::2, M = 256): each CTA converts its 128 channels and half
+//    of the tokens, so a byte converted once feeds twice the products.
+//  * Shared memory moves 128 bytes a cycle, for copies, converters and MMA operands
+//    together, and is what runs out first.  So the f16 weights go to tensor memory
+//    (tcgen05.st; the MMA's A operand) and only the f16 tokens go back to shared memory.
+//    A stage of 128 k of a 256 x 256 pair tile then moves 128 KB in 1024 MMA cycles.
+//  * Roles (20 warps): a loader copies 128 bytes of k of each row into a ring (one thread
+//    by TMA; where rows are not whole 16-byte pieces, three warps by asynchronous 4-byte
+//    copies), completing on an mbarrier; two groups of four converter warps take
+//    alternate stages; one thread issues the MMAs; eight epilogue warps drain finished
+//    accumulators (each thread one channel and half the tokens, 128 running int32 sums in
+//    registers) and store: the lanes of a warp are neighbouring channels of a token.
+//  * Tensor memory: three accumulators of up to 128 tokens, used in turn, and two f16 weight
+//    buffers.  A tile of more than 128 tokens is two halves that share each stage: the
+//    accumulator of one half drains while the other's MMAs run, and a third takes the
+//    next 1024 k.
+//  * Registers go where they are needed (setmaxnreg).
+//  * With fewer tiles than SMs, k is split over the CTAs (or pairs) of a cluster, and their
+//    int32 sums are added through distributed shared memory: whole numbers, so the bits do
+//    not depend on the split.
+//  * Every wait is bounded; one that runs out sets LOOM_DEVERR_TIMEOUT, every role stops at
+//    its next wait, copies and MMAs in flight finish, tensor memory is freed, affected y are
+//    NaN and acc INT32_MIN.
+#include "tc_ptx.cuh"
+#include "token_ops.cuh"
+
+namespace loom {
+namespace {
+
+constexpr int MT_KSTEP = 128;                 // k per stage: two 64-k swizzle atoms of the token operand
+constexpr int MT_CHUNK_STEPS = 1024 / MT_KSTEP;   // stages per f32 accumulator
+constexpr int MT_M = 128;                     // channels per CTA
+constexpr int MT_LOADERS = 3;                 // warps 1..3 (warp 0 issues the MMAs)
+constexpr int MT_CONV_WARP = 4, MT_EPI_WARP = 12, MT_EPI_WARPS = 8;
+constexpr int MT_THREADS = 32 * (MT_EPI_WARP + MT_EPI_WARPS);
+constexpr int MT_LAUNCH_REGS = 96;            // 640 x 96 = 128 x 48 + 256 x 64 + 256 x 152
+constexpr int MT_ACCS = 3, MT_ACC_COLS = 128; // accumulators in tensor memory ...
+constexpr int MT_A_BUFS = 2, MT_A_COLS = 64;  // ... and weight buffers behind them
+constexpr uint32_t MT_TMEM_COLS = 512, MT_A_COL = MT_ACCS * MT_ACC_COLS;
+constexpr int MT_DEPTH = 3;                   // stages of the token operand
+constexpr int MT_MAX_AHEAD = 8;               // stages of bytes in the copy ring
+constexpr uint32_t MT_AREA = 1024;            // barriers, tensor-memory slot, abort word
+constexpr int MT_GROUP_T = 16;                // token tiles walked together (they share weight rows in L2)
+constexpr uint32_t MT_MAX_SMEM = 227u * 1024u;
+constexpr uint32_t MT_ROOM = MT_MAX_SMEM - 2 * MT_AREA;    // barriers, and the base's own alignment
+
+__device__ __forceinline__ uint32_t bar_staged(uint32_t area, int s) { return area + 16 + 8 * s; }
+__device__ __forceinline__ uint32_t bar_freed(uint32_t area, int s) { return area + 16 + 8 * (MT_MAX_AHEAD + s); }
+__device__ __forceinline__ uint32_t bar_full(uint32_t area, int s) { return area + 16 + 8 * (2 * MT_MAX_AHEAD + s); }
+__device__ __forceinline__ uint32_t bar_empty(uint32_t area, int s) { return area + 16 + 8 * (2 * MT_MAX_AHEAD + MT_DEPTH + s); }
+__device__ __forceinline__ uint32_t bar_acc_full(uint32_t area, int b) { return area + 16 + 8 * (2 * MT_MAX_AHEAD + 2 * MT_DEPTH + b); }
+__device__ __forceinline__ uint32_t bar_acc_empty(uint32_t area, int b) { return area + 16 + 8 * (2 * MT_MAX_AHEAD + 2 * MT_DEPTH + MT_ACCS + b); }
+__device__ __forceinline__ uint32_t bar_drain(uint32_t area) { return area + 16 + 8 * (2 * MT_MAX_AHEAD + 2 * MT_DEPTH + 2 * MT_ACCS); }
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+
+// One arrival on the barrier at `bar` of CTA `rank` (CG 1: on this CTA's).  The release is
+// the default one, of CTA scope: what the other CTA must see went through the async proxy
+// (fence_async_smem) or tensor memory (fence_before) first.  A release of cluster scope
+// would wait for the thread's loads in flight (measured: 1100 to 2200 cycles a stage).
+template <int CG> __device__ __forceinline__ void arrive(uint32_t bar, uint32_t rank)
+{
+    if (CG == 1)
+        tc::mbar_arrive(bar);
+    else
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to(bar, rank)) : "memory");
+}
+
+// True in one lane of a converged warp.  Branching on this instruction's predicate (and not on
+// a lane number) tells the compiler that one thread runs what follows.
+__device__ __forceinline__ bool elected()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+// The upper word of tc::smem_desc_sw128, the same for every operand here; the lower word
+// is the start address in 16-byte units and a constant.
+constexpr uint32_t MT_DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29), MT_DESC_LOW = 1u << 16;
+
+// D += A (tensor memory) x B (shared memory, lower descriptor word `b`).
+template <int CG> __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+{
+    if (CG == 1)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+                     "r"(MT_DESC_HIGH)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc),
+                     "r"(MT_DESC_HIGH)
+                     : "memory");
+}
+
+// Arrives on `bar` (of both CTAs of the pair) when the MMAs issued so far are done.
+template <int CG> __device__ __forceinline__ void commit(uint32_t bar, uint32_t pair_mask)
+{
+    if (CG == 1)
+        tc::commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                     "h"((uint16_t)pair_mask)
+                     : "memory");
+}
+
+template <int CG> __device__ __forceinline__ void tmem_alloc(uint32_t slot)
+{
+    if (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(MT_TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(MT_TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CG> __device__ __forceinline__ void tmem_free(uint32_t tmem)
+{
+    if (CG == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(MT_TMEM_COLS) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(MT_TMEM_COLS) : "memory");
+}
+
+// Place of 16-byte piece j of row `row` in a stage of bytes: rows of 128 bytes in the TMA's
+// 128-byte swizzle.  Eight lanes meet eight different banks when they hold one piece of
+// eight rows (the weights' converters) or four pieces of rows r and r ^ 5 (the tokens').
+__device__ __forceinline__ uint32_t piece_at(int row, int j) { return (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4)); }
+
+// 16 bytes -> 16 f16.
+__device__ __forceinline__ void to_f16(const int4 &v, uint32_t *h)
+{
+    tc::i8x4_to_f16x4((uint32_t)v.x, h[0], h[1]);
+    tc::i8x4_to_f16x4((uint32_t)v.y, h[2], h[3]);
+    tc::i8x4_to_f16x4((uint32_t)v.z, h[4], h[5]);
+    tc::i8x4_to_f16x4((uint32_t)v.w, h[6], h[7]);
+}
+
+struct Tile {
+    int64_t m0, t0;     // first channel and token of the tile
+};
+
+__device__ __forceinline__ Tile tile_at(const MatmulTcPlan &q, int64_t i)
+{
+    const int64_t per_group = (int64_t)MT_GROUP_T * q.tiles_m, g = i / per_group, in = i % per_group;
+    const int64_t wide = min((int64_t)MT_GROUP_T, (int64_t)q.tiles_t - g * MT_GROUP_T);
+    return Tile{in / wide * MT_M * q.cg, (g * MT_GROUP_T + in % wide) * q.tile_t};
+}
+
+// This CTA's work: its tiles are first, first + stride, ..., each over k stages [step0, step1).
+struct Work {
+    int64_t first, stride, tiles;
+    int step0, step1;
+};
+
+// ---- loaders -----------------------------------------------------------------------
+// Rows that are whole 16-byte pieces: one thread, two TMA copies a stage.  Copies in flight
+// land before it returns.
+template <int CG>
+__device__ __forceinline__ void load_role(const MatmulParams &p, const MatmulTcPlan &q, const CUtensorMap *map_w, const CUtensorMap *map_x,
+                                          uint32_t area, uint32_t ring, uint32_t pair_rank, const Work &w)
+{
+    const int rows = q.tile_t / (CG * CG);                  // of a half (CG 1: of all)
+    const uint64_t once = dev::l2_evict_first_policy(), again = dev::l2_evict_last_policy();
+    const uint64_t policy_w = q.tiles_t > 1 ? again : once;
+    int s = 0;
+    uint32_t phase = 1;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t i = w.first; ok && i < w.tiles; i += w.stride) {
+        const Tile t = tile_at(q, i);
+        const int m0 = (int)(t.m0 + pair_rank * MT_M), t0 = (int)t.t0 + (int)pair_rank * rows;
+        for (int step = w.step0; step < w.step1; ++step, ++issued) {
+            ok = tc::role_wait(area + 8, p.error, p.wait_ns, bar_freed(area, s), phase);
+            if (!ok)
+                break;
+            const uint32_t to = ring + (uint32_t)s * q.ahead_bytes;
+            dev::mbar_arrive_expect_tx(bar_staged(area, s), q.ahead_bytes);
+            tc::tma_load_2d(to, map_w, step * MT_KSTEP, m0, bar_staged(area, s), policy_w);
+#pragma unroll
+            for (int h = 0; h < CG; ++h)
+                tc::tma_load_2d(to + (uint32_t)(MT_M + h * rows) * 128, map_x, step * MT_KSTEP, t0 + h * rows * CG, bar_staged(area, s), again);
+            if (++s == q.ahead) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    if (!ok)
+        for (int64_t i = issued > q.ahead ? issued - q.ahead : 0; i < issued; ++i)
+            dev::mbar_wait_bounded(bar_staged(area, (int)(i % q.ahead)), (uint32_t)(i / q.ahead) & 1u, 1000000000ull);
+}
+
+// Any other rows: warps copy four bytes a lane, a row of a stage at a time, eight rows (a
+// swizzle period) unrolled.
+__device__ __forceinline__ void copy_rows(uint32_t to, const int8_t *base, int64_t row0, int64_t total, int64_t pitch, int rows, int at, int left,
+                                          int loader, int lane)
+{
+    for (int r = 8 * loader; r < rows; r += 8 * MT_LOADERS) {
+        const int8_t *from = base + (row0 + r) * pitch + at;
+        const int64_t live = total - row0 - r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool have = j < live && left > 0;          // else zeros, and nothing is read
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + (uint32_t)(r + j) * 128 + ((((uint32_t)lane >> 2) ^ j) << 4)),
+                         "l"(have ? from + j * pitch : base), "r"(have ? 4 : 0)
+                         : "memory");
+        }
+    }
+}
+
+template <int CG>
+__device__ __forceinline__ void load_words_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t ring, int loader, int lane,
+                                                uint32_t pair_rank, const Work &w)
+{
+    const int rows = q.tile_t / (CG * CG);                  // of a half (CG 1: of all)
+    int s = 0;
+    uint32_t phase = 1;
+    for (int64_t i = w.first; i < w.tiles; i += w.stride) {
+        const Tile t = tile_at(q, i);
+        const int64_t m0 = t.m0 + pair_rank * MT_M;
+        for (int step = w.step0; step < w.step1; ++step) {
+            if (!__all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_freed(area, s), phase)))
+                return;
+            const uint32_t to = ring + (uint32_t)s * q.ahead_bytes + 4 * ((uint32_t)lane & 3);
+            const int at = step * MT_KSTEP + 4 * lane, left = p.k - at;
+            copy_rows(to, p.w, m0, p.n, p.k, MT_M, at, left, loader, lane);
+#pragma unroll
+            for (int h = 0; h < CG; ++h)
+                copy_rows(to + (uint32_t)(MT_M + h * rows) * 128, p.x, t.t0 + (h * CG + (int)pair_rank) * rows, p.tokens, p.k, rows, at, left, loader,
+                          lane);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_staged(area, s)) : "memory");
+            if (++s == q.ahead) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+}
+
+// ---- converters ----------------------------------------------------------------------
+// Group `group` of four warps takes stages group, group + 2, ... of the CTA's `stages`.
+template <int CG>
+__device__ __forceinline__ void convert_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t ring, uint32_t operands,
+                                             uint32_t tmem, int group, int sub, int lane, uint32_t leader, uint32_t stages)
+{
+    const int b_rows = q.tile_t / CG;
+    // the tokens' pieces of this thread: piece v of rows r0, r0 + 16, ...; eight lanes hold four
+    // pieces of rows r and r ^ 5, whose reads and (twice as wide) writes fall on different banks
+    const int pair = sub * 2 + (lane >> 4), v = (lane & 3) | ((lane >> 3) & 1) << 2;
+    const int r0 = (pair >> 2) * 8 + ((pair & 3) ^ ((lane & 4) ? 5 : 0));
+    const uint32_t b_from = MT_M * 128 + piece_at(r0, v);                  // r0 + 16: the same place 16 rows on
+    const uint32_t b_to = (uint32_t)((v >> 2) * b_rows * 128 + (r0 >> 3) * 1024 + (r0 & 7) * 128);
+    const uint32_t c0 = b_to + ((((v & 3) * 2) ^ (r0 & 7)) << 4), c1 = b_to + ((((v & 3) * 2 + 1) ^ (r0 & 7)) << 4);
+    const int row = 32 * sub + lane, key = row & 7;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * sub) << 16) + MT_A_COL + (uint32_t)group * MT_A_COLS;
+    int s = group;
+    uint32_t s_phase = 0;
+    uint32_t it = (uint32_t)group;
+    for (; it < stages; it += 2) {
+        while (s >= q.ahead) {
+            s -= q.ahead;
+            s_phase ^= 1u;
+        }
+        const uint32_t d = it % MT_DEPTH, turn = it / MT_DEPTH;
+        const bool staged = dev::mbar_try_wait(bar_staged(area, s), s_phase), empty = dev::mbar_try_wait(bar_empty(area, (int)d), (turn & 1u) ^ 1u);
+        bool ok = staged || tc::role_wait(area + 8, p.error, p.wait_ns, bar_staged(area, s), s_phase);
+        ok = ok && (empty || tc::role_wait(area + 8, p.error, p.wait_ns, bar_empty(area, (int)d), (turn & 1u) ^ 1u));
+        if (!__all_sync(dev::FULL_MASK, ok))
+            return;
+        const uint32_t from = ring + (uint32_t)s * q.ahead_bytes, a_from = from + (uint32_t)row * 128;
+        const uint32_t to = operands + d * q.stage_bytes;
+        for (int r = 0; r < b_rows; r += 64) {
+            int4 in[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r + 16 * j < b_rows)
+                    in[j] = tc::lds128(from + b_from + (uint32_t)(r + 16 * j) * 128);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r + 16 * j < b_rows) {
+                    uint32_t out[8];
+                    to_f16(in[j], out);
+                    tc::sts128(to + c0 + (uint32_t)(r + 16 * j) * 128, out[0], out[1], out[2], out[3]);
+                    tc::sts128(to + c1 + (uint32_t)(r + 16 * j) * 128, out[4], out[5], out[6], out[7]);
+                }
+        }
+        int4 next[2] = {tc::lds128(a_from + (uint32_t)((0 ^ key) << 4)), tc::lds128(a_from + (uint32_t)((1 ^ key) << 4))};
+        // the weight buffer: free when the MMAs of the stage before the last are done, which is
+        // later than what the token stage waits for
+        if (it >= MT_A_BUFS) {
+            const uint32_t old = it - MT_A_BUFS;
+            if (!__all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_empty(area, (int)(old % MT_DEPTH)), (old / MT_DEPTH) & 1u)))
+                return;
+        }
+        tc::fence_after();
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            uint32_t out[16];
+            to_f16(next[0], out);
+            to_f16(next[1], out + 8);
+            if (h < 3) {
+                next[0] = tc::lds128(a_from + (uint32_t)(((2 * h + 2) ^ key) << 4));
+                next[1] = tc::lds128(a_from + (uint32_t)(((2 * h + 3) ^ key) << 4));
+            }
+            tc::st16(lane_base + 16 * h, out);
+        }
+        tc::wait_st();
+        tc::fence_before();
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tc::mbar_arrive(bar_freed(area, s));
+            arrive<CG>(bar_full(area, (int)d), leader);
+        }
+        s += 2;
+    }
+    // the MMAs' arrivals on this CTA's barriers come before it may leave
+    for (; it < stages + MT_DEPTH; it += 2)
+        if (!__all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_empty(area, (int)(it % MT_DEPTH)), ((it / MT_DEPTH) & 1u) ^ 1u)))
+            return;
+}
+
+// ---- MMA issue -------------------------------------------------------------------------
+// By one thread, of the leading CTA of a pair; false when a wait ran out.
+template <int CG>
+__device__ __forceinline__ bool mma_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t operands, uint32_t tmem,
+                                         uint32_t pair_mask, int64_t work, int step0, int step1)
+{
+    const uint32_t rows = (uint32_t)q.tile_t / (CG * CG);    // token rows of a half in this CTA
+    const uint32_t idesc = tc::idesc_f16(128 * CG, q.tile_t / CG), atom = rows * CG * 8;   // 16-byte units
+    uint32_t acc = 0, acc_phase = 1, s = 0, phase = 0, buf = 0;
+    for (; work > 0; --work)
+        for (int step = step0; step < step1;) {
+            const uint32_t second = acc + 1 == MT_ACCS ? 0 : acc + 1, second_phase = second == 0 ? acc_phase ^ 1u : acc_phase;
+            const int first = step, last = min(step + MT_CHUNK_STEPS, step1);
+#pragma unroll 1
+            for (; step < last; ++step) {
+                if (!tc::role_wait(area + 8, p.error, p.wait_ns, bar_full(area, (int)s), phase))
+                    return false;
+                const uint32_t a = tmem + MT_A_COL + buf * MT_A_COLS, b = MT_DESC_LOW | ((operands + s * q.stage_bytes) >> 4);
+                const int slices = (p.k - step * MT_KSTEP + 15) / 16;    // of 16 k that hold anything
+#pragma unroll
+                for (int h = 0; h < CG; ++h) {
+                    const uint32_t u = h == 0 ? acc : second;
+                    if (step == first &&
+                        !tc::role_wait(area + 8, p.error, p.wait_ns, bar_acc_empty(area, (int)u), h == 0 ? acc_phase : second_phase))
+                        return false;
+                    tc::fence_after();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < slices)
+                            mma<CG>(tmem + u * MT_ACC_COLS, a + 8 * j, b + (j >> 2) * atom + h * rows * 8 + 2 * (j & 3), idesc,
+                                    step > first || j > 0);      // the first MMA overwrites the accumulator
+                    if (step == last - 1)
+                        commit<CG>(bar_acc_full(area, (int)u), pair_mask);
+                }
+                commit<CG>(bar_empty(area, (int)s), pair_mask);
+                buf ^= 1u;
+                if (++s == MT_DEPTH) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            acc += CG;
+            if (acc >= MT_ACCS) {
+                acc -= MT_ACCS;
+                acc_phase ^= 1u;
+            }
+        }
+    return true;
+}
+
+// ---- epilogue ------------------------------------------------------------------------
+// Up to N tokens from `t` on of one channel.  The compiler barrier keeps the next tokens'
+// scales behind this call's stores: the running sums leave few registers.
+template <int N>
+__device__ __forceinline__ void store_tokens(const MatmulParams &p, int64_t t, int64_t channel, const int32_t *a, float sw, float bias, bool ok)
+{
+    asm volatile("" ::: "memory");
+    const int have = (int)min((int64_t)N, p.tokens - t);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < have) {
+            float f = __fmul_rn((float)a[i], __fmul_rn(sw, p.scale_x[t + i]));
+            if (p.bias)
+                f = __fadd_rn(f, bias);
+            dev::store_as(p.y, p.y_dtype, (t + i) * p.y_stride + channel, ok ? f : __uint_as_float(0x7fc00000u));
+            if (p.acc)
+                p.acc[(t + i) * p.n + channel] = ok ? a[i] : INT32_MIN;
+        }
+}
+
+// Adds whole numbers |v| <= 2^24 held in f32 to int32 sums, two at a time and with additions
+// alone (conversions run at a quarter of their rate or less): v + 1.5 2^26 is v rounded to a
+// multiple of 8 with v / 8 in its low bits, the rest, at most 4, gets its low bits from 1.5 2^23.
+// The constants' own bits are taken off the sums at the end (MT_BIAS a drain, modulo 2^32).
+constexpr float MT_M8 = 100663296.0f, MT_M1 = 12582912.0f;        // 1.5 2^26, 1.5 2^23
+constexpr uint32_t MT_BIAS = 8u * 0x4cc00000u + 0x4b400000u;      // their bit patterns
+__device__ __forceinline__ void add_whole2(uint32_t r0, uint32_t r1, int32_t &s0, int32_t &s1)
+{
+    const uint64_t m8 = dev::pack2(MT_M8, MT_M8), m1 = dev::pack2(MT_M1, MT_M1);
+    const uint64_t v = dev::pack2(__uint_as_float(r0), __uint_as_float(r1));
+    const uint64_t h = dev::add2(v, m8);
+    const uint64_t l = dev::add2(dev::sub2(v, dev::sub2(h, m8)), m1);
+    float h0, h1, l0, l1;
+    dev::unpack2(h, h0, h1);
+    dev::unpack2(l, l0, l1);
+    s0 = (int32_t)((uint32_t)s0 + (__float_as_uint(h0) << 3) + __float_as_uint(l0));
+    s1 = (int32_t)((uint32_t)s1 + (__float_as_uint(h1) << 3) + __float_as_uint(l1));
+}
+
+// Adds a tile's accumulators (one for each half and 1024 k) to `sum`: of this thread's channel,
+// `cols` tokens of each half; false when a wait ran out.
+template <int CG>
+__device__ __forceinline__ bool drain_tile(const MatmulParams &p, uint32_t area, uint32_t from, int cols, int lane, uint32_t leader, uint32_t &acc,
+                                           uint32_t &phase, const Work &w, bool ok, int32_t (&sum)[64 * CG])
+{
+    const uint32_t chunks = (uint32_t)(w.step1 - w.step0 + MT_CHUNK_STEPS - 1) / MT_CHUNK_STEPS;
+#pragma unroll
+    for (int i = 0; i < 64 * CG; ++i)
+        sum[i] = (int32_t)(0u - chunks * MT_BIAS);
+    for (uint32_t c = 0; ok && c < chunks; ++c)
+#pragma unroll
+        for (int h = 0; h < CG; ++h) {
+            ok = ok && __all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_acc_full(area, (int)acc), phase));
+            if (!ok)
+                break;
+            tc::fence_after();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (16 * j < cols) {
+                    uint32_t r[16];
+                    tc::ld16(from + acc * MT_ACC_COLS + 16 * j, r);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        add_whole2(r[i], r[i + 1], sum[64 * h + 16 * j + i], sum[64 * h + 16 * j + i + 1]);
+                }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                arrive<CG>(bar_acc_empty(area, (int)acc), leader);
+            if (++acc == MT_ACCS) {
+                acc = 0;
+                phase ^= 1u;
+            }
+        }
+    return ok;
+}
+
+template <int CG, bool V16>
+__global__ void __launch_bounds__(MT_THREADS, 1)
+    i8_matmul_tc_kernel(const MatmulParams p, const MatmulTcPlan q, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x)
+{
+    extern __shared__ unsigned char raw[];
+    const uint32_t area = (dev::smem_u32(raw) + 1023u) & ~1023u, operands = area + MT_AREA;
+    const uint32_t ring = operands + MT_DEPTH * q.stage_bytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const uint32_t pair_rank = CG == 1 ? 0 : rank & 1u, leader = CG == 1 ? rank : rank & ~1u, pair_mask = 3u << (rank & ~1u);
+    const int part = (int)(rank / CG);                       // this CTA's share of k
+    Work w;
+    {
+        const int steps = (p.k + MT_KSTEP - 1) / MT_KSTEP;
+        w.step0 = (int)((int64_t)steps * part / q.split);
+        w.step1 = (int)((int64_t)steps * (part + 1) / q.split);
+        w.first = blockIdx.x / (CG * q.split);
+        w.stride = gridDim.x / (CG * q.split);
+        w.tiles = (int64_t)q.tiles_m * q.tiles_t;
+    }
+    const int64_t work = (w.tiles - w.first + w.stride - 1) / w.stride;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < q.ahead; ++s) {
+            dev::mbar_init(bar_staged(area, s), V16 ? 1 : 32 * MT_LOADERS);
+            dev::mbar_init(bar_freed(area, s), 4);
+        }
+        for (int s = 0; s < MT_DEPTH; ++s) {
+            dev::mbar_init(bar_full(area, s), 4 * CG);
+            dev::mbar_init(bar_empty(area, s), 1);
+        }
+        for (int b = 0; b < MT_ACCS; ++b) {
+            dev::mbar_init(bar_acc_full(area, b), 1);
+            dev::mbar_init(bar_acc_empty(area, b), MT_EPI_WARPS * CG);
+        }
+        dev::mbar_init(bar_drain(area), 1);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(area + 8), "r"(0u) : "memory");
+        dev::fence_barrier_init();
+    }
+    dev::follow_previous_kernel();
+    if (warp == 0)
+        tmem_alloc<CG>(area);
+    tc::fence_before();
+    cluster_sync();
+    tc::fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(area));
+
+    if (warp < MT_CONV_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp > 0) {
+            if (!V16) {
+                load_words_role<CG>(p, q, area, ring, warp - 1, lane, pair_rank, w);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            } else if (warp == 1 && elected()) {
+                load_role<CG>(p, q, &map_w, &map_x, area, ring, pair_rank, w);
+            }
+        } else if (CG == 1 || pair_rank == 0) {
+            if (elected() && !mma_role<CG>(p, q, area, operands, tmem, pair_mask, work, w.step0, w.step1)) {
+                // let the MMAs in flight finish before tensor memory is freed
+                commit<CG>(bar_drain(area), pair_mask & (0u - pair_mask));   // on this CTA alone
+                const uint64_t t0 = dev::global_ns();
+                while (!dev::mbar_try_wait(bar_drain(area), 0) && dev::global_ns() - t0 < 1000000000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp < MT_EPI_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        convert_role<CG>(p, q, area, ring, operands, tmem, (warp - MT_CONV_WARP) >> 2, warp & 3, lane, leader, (uint32_t)(work * (w.step1 - w.step0)));
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        const int sub = warp & 3, half = (warp - MT_EPI_WARP) >> 2, cols = q.tile_t / (2 * CG);   // tokens of a half for each warp
+        const uint32_t from = tmem + ((uint32_t)(32 * sub) << 16) + half * cols;
+        uint32_t acc = 0, phase = 0;
+        bool ok = true;
+        int32_t sum[64 * CG];
+        for (int64_t i = w.first; i < w.tiles; i += w.stride) {
+            ok = drain_tile<CG>(p, area, from, cols, lane, leader, acc, phase, w, ok, sum);
+            if (q.split > 1) {
+                // sums of this share of k, [token][128 channels], over the operand stages (all of
+                // them are used up: the accumulator is the last thing that read them)
+#pragma unroll
+                for (int h = 0; h < CG; ++h)
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (j < cols)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(operands + (uint32_t)((2 * h + half) * cols + j) * 512 +
+                                                                         (uint32_t)(32 * sub + lane) * 4),
+                                         "r"(sum[64 * h + j])
+                                         : "memory");
+                break;   // one tile per cluster
+            }
+            const Tile t = tile_at(q, i);
+            const int64_t channel = t.m0 + pair_rank * MT_M + 32 * sub + lane;
+            if (channel < p.n) {
+                const float sw = p.scale_w[channel], bias = p.bias ? p.bias[channel] : 0.0f;
+#pragma unroll
+                for (int h = 0; h < CG; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (16 * j < cols)
+                            store_tokens<16>(p, t.t0 + (2 * h + half) * cols + 16 * j, channel, sum + 64 * h + 16 * j, sw, bias, ok);
+            }
+        }
+        __syncwarp();
+    }
+    __syncwarp();
+    tc::fence_before();
+    cluster_sync();      // every CTA's MMAs are done, its sums are in shared memory
+    tc::fence_after();
+    if (q.split > 1 && warp >= MT_EPI_WARP) {
+        const int sub = warp & 3, half = (warp - MT_EPI_WARP) >> 2;
+        const Tile t = tile_at(q, w.first);
+        const int64_t channel = t.m0 + pair_rank * MT_M + 32 * sub + lane;
+        bool ok = true;
+        for (int s = 0; s < CG * q.split; ++s) {
+            uint32_t bad;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(bad) : "r"(map_to(area + 8, (uint32_t)s)) : "memory");
+            ok = ok && bad == 0;
+        }
+        if (channel < p.n) {
+            const float sw = p.scale_w[channel], bias = p.bias ? p.bias[channel] : 0.0f;
+            // groups of four tokens, shared out over the CTAs of the split and the two warps of each channel
+            for (int c = 4 * (part * 2 + half); c < q.tile_t; c += 8 * q.split) {
+                int32_t a[4] = {0, 0, 0, 0};
+                for (int s = 0; s < q.split; ++s) {
+                    const uint32_t at = map_to(operands, (uint32_t)(s * CG) + pair_rank) + (uint32_t)(c * 512 + (32 * sub + lane) * 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        int32_t v;
+                        asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(at + 512 * j) : "memory");
+                        a[j] += v;
+                    }
+                }
+                store_tokens<4>(p, t.t0 + c, channel, a, sw, bias, ok);
+            }
+        }
+        __syncwarp();
+    }
+    if (q.split > 1)
+        cluster_sync();  // no CTA leaves while another reads its sums
+    if (warp == 0)
+        tmem_free<CG>(tmem);
+}
+
+// Rows of k bytes in boxes of 128 bytes of `rows` rows, 128-byte swizzle.
+bool encode_rows(CUtensorMap *map, const int8_t *base, int64_t k, int64_t outer, int rows)
+{
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                               const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) == cudaSuccess && r == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<Encode>(f)
+                   : nullptr;
+    }();
+    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)outer}, strides[1] = {(cuuint64_t)k};
+    const cuuint32_t box[2] = {MT_KSTEP, (cuuint32_t)rows}, unit[2] = {1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(base), dims, strides, box, unit,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CG, bool V16> cudaError_t launch_cg(const MatmulParams &p, const MatmulTcPlan &q, cudaStream_t stream)
+{
+    const auto kernel = i8_matmul_tc_kernel<CG, V16>;
+    // setmaxnreg hands out the registers that the launch brought: were there fewer, the
+    // epilogue's request would wait for ever
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess)
+        return e;
+    if (fa.numRegs < MT_LAUNCH_REGS)
+        return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q.smem_bytes);
+    if (e != cudaSuccess)
+        return e;
+    CUtensorMap map_w = {}, map_x = {};
+    if (V16 && (!encode_rows(&map_w, p.w, p.k, p.n, MT_M) || !encode_rows(&map_x, p.x, p.k, p.tokens, q.tile_t / (CG * CG))))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)q.grid);
+    cfg.blockDim = dim3(MT_THREADS);
+    cfg.dynamicSmemBytes = q.smem_bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)(CG * q.split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, q, map_w, map_x);
+}
+
+}  // namespace
+
+int matmul_tc_threads() { return MT_THREADS; }
+
+// Tile, split of k and grid.  The time of a choice is its waves of tiles times the stages of
+// one tile, plus what a tile (or a split) costs once, in units of a stage.
+void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, int64_t sms, MatmulTcPlan *out)
+{
+    MatmulTcPlan best = {};
+    double best_cost = 0.0;
+    const int cg = tokens <= 128 ? 1 : 2;
+    const int64_t steps = (k + MT_KSTEP - 1) / MT_KSTEP, tiles_t = (tokens + 128 * cg - 1) / (128 * cg);
+    const int64_t tiles_m = (n + MT_M * cg - 1) / (MT_M * cg), tiles = tiles_m * tiles_t;
+    const int64_t quantum = 32 * cg;      // each half's columns, shared by two warps (and CTAs), are whole 16s
+    const int64_t tile_t = ((tokens + tiles_t - 1) / tiles_t + quantum - 1) / quantum * quantum;   // up to 128 cg
+    for (int split = 1; cg * split <= 8; split *= 2) {
+        // clusters of four and eight CTAs leave some SMs of a GPC idle
+        const int64_t size = cg * split, slots = size <= 2 ? sms / size : size == 4 ? sms / 4 - 2 : sms / 8 - 3;
+        if (slots < 1 || (split > 1 && (tiles > slots || split > steps)))
+            continue;
+        const int64_t waves = (tiles + slots - 1) / slots;
+        const double cost = (double)waves * ((double)((steps + split - 1) / split) + 2.0) + (split > 1 ? 3.0 + tile_t / 64.0 : 0.0);
+        if (best.split == 0 || cost < best_cost) {
+            best_cost = cost;
+            best.split = split;
+            best.grid = (tiles < slots ? tiles : slots) * size;
+        }
+    }
+    best.cg = cg;
+    best.tile_t = (int32_t)tile_t;
+    best.tiles_m = (int32_t)tiles_m;
+    best.tiles_t = (int32_t)tiles_t;
+    best.stage_bytes = (uint32_t)(tile_t / cg) * 2 * MT_KSTEP;
+    best.ahead_bytes = (uint32_t)(MT_M + tile_t / cg) * MT_KSTEP;
+    const int64_t room = (MT_ROOM - MT_DEPTH * best.stage_bytes) / best.ahead_bytes;
+    best.ahead = (int32_t)(room < MT_MAX_AHEAD ? room : MT_MAX_AHEAD);
+    uint32_t bytes = MT_DEPTH * best.stage_bytes + (uint32_t)best.ahead * best.ahead_bytes;
+    const uint32_t sums = best.split > 1 ? (uint32_t)tile_t * 512u : 0u;
+    bytes = bytes > sums ? bytes : sums;
+    bytes = bytes > 116u * 1024u ? bytes : 116u * 1024u;   // more than half an SM: one CTA, which owns tensor memory
+    best.smem_bytes = 2 * MT_AREA + bytes;
+    *out = best;
+}
+
+cudaError_t launch_matmul_tc(const MatmulParams &p, const MatmulTcPlan &q, bool vec16, cudaStream_t stream)
+{
+    if (q.cg == 1)
+        return vec16 ? launch_cg<1, true>(p, q, stream) : launch_cg<1, false>(p, q, stream);
+    return vec16 ? launch_cg<2, true>(p, q, stream) : launch_cg<2, false>(p, q, stream);
+}
+
+}  // namespace loom
