@@ -11,21 +11,22 @@
 //
 // Design
 //  * D[channel][token]: 128 channels are the MMA's M (tensor-memory lanes) of each CTA,
-//    the tokens its N (32 to 256).  Up to 128 tokens a CTA works alone; above, CTA pairs
-//    share each MMA (cta_group::2, M = 256): each CTA converts its 128 channels and half
-//    of the tokens, so a byte converted once feeds twice the products.
+//    the tokens its N.  Up to 32 tokens a CTA works alone; above, CTA pairs share each MMA
+//    (cta_group::2, M = 256): each CTA converts its 128 channels and half of the tokens, so
+//    a byte converted once feeds twice the products.  A tile holds up to 256 tokens, above
+//    128 as two halves with MMAs of their own.
 //  * Shared memory moves 128 bytes a cycle, for copies, converters and MMA operands
 //    together, and is what runs out first.  So the f16 weights go to tensor memory
 //    (tcgen05.st; the MMA's A operand) and only the f16 tokens go back to shared memory.
 //    A stage of 128 k of a 256 x 256 pair tile then moves 128 KB in 1024 MMA cycles.
-//  * Roles (20 warps): a loader copies 128 bytes of k of each row into a ring (one thread
+//  * Roles (20 warps, with one half 28): a loader copies 128 bytes of k of each row into a ring (one thread
 //    by TMA; where rows are not whole 16-byte pieces, three warps by asynchronous 4-byte
-//    copies), completing on an mbarrier; two groups of four converter warps take
-//    alternate stages; one thread issues the MMAs; eight epilogue warps drain finished
+//    copies), completing on an mbarrier; two groups of four converter warps (with one
+//    half: four groups) take stages in turn; one thread issues the MMAs; eight epilogue warps drain finished
 //    accumulators (each thread one channel and half the tokens, 128 running int32 sums in
 //    registers) and store: the lanes of a warp are neighbouring channels of a token.
-//  * Tensor memory: three accumulators of up to 128 tokens, used in turn, and two f16 weight
-//    buffers.  A tile of more than 128 tokens is two halves that share each stage: the
+//  * Tensor memory: accumulators of up to 128 tokens, used in turn (two alone, three in a
+//    pair), and a f16 weight buffer for each group of converters.  In a pair a tile of more than 128 tokens is two halves that share each stage: the
 //    accumulator of one half drains while the other's MMAs run, and a third takes the
 //    next 1024 k.
 //  * Registers go where they are needed (setmaxnreg).
@@ -45,13 +46,24 @@ constexpr int MT_KSTEP = 128;                 // k per stage: two 64-k swizzle a
 constexpr int MT_CHUNK_STEPS = 1024 / MT_KSTEP;   // stages per f32 accumulator
 constexpr int MT_M = 128;                     // channels per CTA
 constexpr int MT_LOADERS = 3;                 // warps 1..3 (warp 0 issues the MMAs)
-constexpr int MT_CONV_WARP = 4, MT_EPI_WARP = 12, MT_EPI_WARPS = 8;
-constexpr int MT_THREADS = 32 * (MT_EPI_WARP + MT_EPI_WARPS);
-constexpr int MT_LAUNCH_REGS = 96;            // 640 x 96 = 128 x 48 + 256 x 64 + 256 x 152
-constexpr int MT_ACCS = 3, MT_ACC_COLS = 128; // accumulators in tensor memory ...
-constexpr int MT_A_BUFS = 2, MT_A_COLS = 64;  // ... and weight buffers behind them
-constexpr uint32_t MT_TMEM_COLS = 512, MT_A_COL = MT_ACCS * MT_ACC_COLS;
-constexpr int MT_DEPTH = 3;                   // stages of the token operand
+constexpr int MT_CONV_WARP = 4, MT_EPI_WARPS = 8;
+constexpr int MT_ACC_COLS = 128, MT_A_COLS = 64;   // tensor memory: an accumulator, a weight buffer
+constexpr uint32_t MT_TMEM_COLS = 512;
+// What goes by the number H of halves of a tile (of at most 128 tokens each).  With one, the
+// weights' stream is the bound: four groups of converters keep up with memory, and the
+// epilogue's sums are half as many.
+template <int H> struct Shape {
+    static constexpr int GROUPS = H == 1 ? 4 : 2;     // converter groups of four warps = weight buffers
+    static constexpr int DEPTH = H == 1 ? 4 : 3;      // stages of the token operand
+    static constexpr int ACCS = H == 1 ? 2 : 3;       // accumulators
+    static constexpr int EPI_WARP = MT_CONV_WARP + 4 * GROUPS;
+    static constexpr int THREADS = 32 * (EPI_WARP + MT_EPI_WARPS);
+    // 896 x 72 >= 128 x 48 + 512 x 64 + 256 x 96;  640 x 96 = 128 x 48 + 256 x 56 + 256 x 160
+    static constexpr int LAUNCH_REGS = H == 1 ? 72 : 96;
+    static constexpr uint32_t A_COL = ACCS * MT_ACC_COLS;
+    static_assert(A_COL + GROUPS * MT_A_COLS <= MT_TMEM_COLS, "tensor memory");
+};
+constexpr int MT_DEPTH = 4, MT_ACCS = 3;      // the most of either, for the barriers' places
 constexpr int MT_MAX_AHEAD = 8;               // stages of bytes in the copy ring
 constexpr uint32_t MT_AREA = 1024;            // barriers, tensor-memory slot, abort word
 constexpr int MT_GROUP_T = 16;                // token tiles walked together (they share weight rows in L2)
@@ -182,11 +194,11 @@ struct Work {
 // ---- loaders -----------------------------------------------------------------------
 // Rows that are whole 16-byte pieces: one thread, two TMA copies a stage.  Copies in flight
 // land before it returns.
-template <int CG>
+template <int CG, int H>
 __device__ __forceinline__ void load_role(const MatmulParams &p, const MatmulTcPlan &q, const CUtensorMap *map_w, const CUtensorMap *map_x,
                                           uint32_t area, uint32_t ring, uint32_t pair_rank, const Work &w)
 {
-    const int rows = q.tile_t / (CG * CG);                  // of a half (CG 1: of all)
+    const int rows = q.tile_t / (CG * H);                   // of a half, in this CTA
     const uint64_t once = dev::l2_evict_first_policy(), again = dev::l2_evict_last_policy();
     const uint64_t policy_w = q.tiles_t > 1 ? again : once;
     int s = 0;
@@ -204,7 +216,7 @@ __device__ __forceinline__ void load_role(const MatmulParams &p, const MatmulTcP
             dev::mbar_arrive_expect_tx(bar_staged(area, s), q.ahead_bytes);
             tc::tma_load_2d(to, map_w, step * MT_KSTEP, m0, bar_staged(area, s), policy_w);
 #pragma unroll
-            for (int h = 0; h < CG; ++h)
+            for (int h = 0; h < H; ++h)
                 tc::tma_load_2d(to + (uint32_t)(MT_M + h * rows) * 128, map_x, step * MT_KSTEP, t0 + h * rows * CG, bar_staged(area, s), again);
             if (++s == q.ahead) {
                 s = 0;
@@ -218,28 +230,41 @@ __device__ __forceinline__ void load_role(const MatmulParams &p, const MatmulTcP
 }
 
 // Any other rows: warps copy four bytes a lane, a row of a stage at a time, eight rows (a
-// swizzle period) unrolled.
+// swizzle period) unrolled.  Rows and bytes past the end are zeros, and nothing is read there.
 __device__ __forceinline__ void copy_rows(uint32_t to, const int8_t *base, int64_t row0, int64_t total, int64_t pitch, int rows, int at, int left,
                                           int loader, int lane)
 {
-    for (int r = 8 * loader; r < rows; r += 8 * MT_LOADERS) {
-        const int8_t *from = base + (row0 + r) * pitch + at;
-        const int64_t live = total - row0 - r;
+    const int8_t *from = base + (row0 + 8 * loader) * pitch + at;
+    const int64_t live = total - row0;
+    uint32_t place[8];                                 // of this lane's word in row j of a period
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool have = j < live && left > 0;          // else zeros, and nothing is read
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + (uint32_t)(r + j) * 128 + ((((uint32_t)lane >> 2) ^ j) << 4)),
-                         "l"(have ? from + j * pitch : base), "r"(have ? 4 : 0)
-                         : "memory");
+    for (int j = 0; j < 8; ++j)
+        place[j] = to + (uint32_t)(8 * loader + j) * 128 + ((((uint32_t)lane >> 2) ^ j) << 4);
+    for (int r = 8 * loader; r < rows; r += 8 * MT_LOADERS, from += 8 * MT_LOADERS * pitch) {
+        if (r + 8 <= live && __all_sync(dev::FULL_MASK, left > 0)) {
+            const int8_t *row = from;
+#pragma unroll
+            for (int j = 0; j < 8; ++j, row += pitch)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(place[j]), "l"(row) : "memory");
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool have = r + j < live && left > 0;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(place[j]), "l"(have ? from + j * pitch : base), "r"(have ? 4 : 0)
+                             : "memory");
+            }
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            place[j] += 8 * MT_LOADERS * 128;
     }
 }
 
-template <int CG>
+template <int CG, int H>
 __device__ __forceinline__ void load_words_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t ring, int loader, int lane,
                                                 uint32_t pair_rank, const Work &w)
 {
-    const int rows = q.tile_t / (CG * CG);                  // of a half (CG 1: of all)
+    const int rows = q.tile_t / (CG * H);                   // of a half, in this CTA
     int s = 0;
     uint32_t phase = 1;
     for (int64_t i = w.first; i < w.tiles; i += w.stride) {
@@ -252,7 +277,7 @@ __device__ __forceinline__ void load_words_role(const MatmulParams &p, const Mat
             const int at = step * MT_KSTEP + 4 * lane, left = p.k - at;
             copy_rows(to, p.w, m0, p.n, p.k, MT_M, at, left, loader, lane);
 #pragma unroll
-            for (int h = 0; h < CG; ++h)
+            for (int h = 0; h < H; ++h)
                 copy_rows(to + (uint32_t)(MT_M + h * rows) * 128, p.x, t.t0 + (h * CG + (int)pair_rank) * rows, p.tokens, p.k, rows, at, left, loader,
                           lane);
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_staged(area, s)) : "memory");
@@ -264,12 +289,25 @@ __device__ __forceinline__ void load_words_role(const MatmulParams &p, const Mat
     }
 }
 
+// Whether a phase of `bar` is over, without waiting (try_wait may suspend the thread).
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // ---- converters ----------------------------------------------------------------------
-// Group `group` of four warps takes stages group, group + 2, ... of the CTA's `stages`.
-template <int CG>
+// Group `group` of four warps takes every GROUPS-th of the CTA's `stages`.
+template <int CG, int H>
 __device__ __forceinline__ void convert_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t ring, uint32_t operands,
                                              uint32_t tmem, int group, int sub, int lane, uint32_t leader, uint32_t stages)
 {
+    using S = Shape<H>;
     const int b_rows = q.tile_t / CG;
     // the tokens' pieces of this thread: piece v of rows r0, r0 + 16, ...; eight lanes hold four
     // pieces of rows r and r ^ 5, whose reads and (twice as wide) writes fall on different banks
@@ -279,21 +317,27 @@ __device__ __forceinline__ void convert_role(const MatmulParams &p, const Matmul
     const uint32_t b_to = (uint32_t)((v >> 2) * b_rows * 128 + (r0 >> 3) * 1024 + (r0 & 7) * 128);
     const uint32_t c0 = b_to + ((((v & 3) * 2) ^ (r0 & 7)) << 4), c1 = b_to + ((((v & 3) * 2 + 1) ^ (r0 & 7)) << 4);
     const int row = 32 * sub + lane, key = row & 7;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * sub) << 16) + MT_A_COL + (uint32_t)group * MT_A_COLS;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * sub) << 16) + S::A_COL + (uint32_t)group * MT_A_COLS;
     int s = group;
     uint32_t s_phase = 0;
+    while (s >= q.ahead) {
+        s -= q.ahead;
+        s_phase ^= 1u;
+    }
     uint32_t it = (uint32_t)group;
-    for (; it < stages; it += 2) {
-        while (s >= q.ahead) {
-            s -= q.ahead;
-            s_phase ^= 1u;
-        }
-        const uint32_t d = it % MT_DEPTH, turn = it / MT_DEPTH;
-        const bool staged = dev::mbar_try_wait(bar_staged(area, s), s_phase), empty = dev::mbar_try_wait(bar_empty(area, (int)d), (turn & 1u) ^ 1u);
-        bool ok = staged || tc::role_wait(area + 8, p.error, p.wait_ns, bar_staged(area, s), s_phase);
-        ok = ok && (empty || tc::role_wait(area + 8, p.error, p.wait_ns, bar_empty(area, (int)d), (turn & 1u) ^ 1u));
+    bool staged = false, empty = false;
+    for (; it < stages; it += S::GROUPS) {
+        const uint32_t d = it % S::DEPTH, turn = it / S::DEPTH;
+        // first the token stage, whose last MMAs were behind every earlier stage's conversion: then
+        // the ring (of at least DEPTH stages) is at most one phase behind what is asked of it
+        bool ok = empty || tc::role_wait(area + 8, p.error, p.wait_ns, bar_empty(area, (int)d), (turn & 1u) ^ 1u);
+        ok = ok && (staged || tc::role_wait(area + 8, p.error, p.wait_ns, bar_staged(area, s), s_phase));
         if (!__all_sync(dev::FULL_MASK, ok))
             return;
+        // the weight buffer is free when the MMAs of this group's last stage are done: with fewer
+        // buffers than token stages, later than what is waited for so far
+        const uint32_t old = it - S::GROUPS, old_bar = bar_empty(area, (int)(old % S::DEPTH)), old_phase = (old / S::DEPTH) & 1u;
+        bool a_free = S::DEPTH == S::GROUPS || it < S::GROUPS || test_wait(old_bar, old_phase);
         const uint32_t from = ring + (uint32_t)s * q.ahead_bytes, a_from = from + (uint32_t)row * 128;
         const uint32_t to = operands + d * q.stage_bytes;
         for (int r = 0; r < b_rows; r += 64) {
@@ -311,14 +355,11 @@ __device__ __forceinline__ void convert_role(const MatmulParams &p, const Matmul
                     tc::sts128(to + c1 + (uint32_t)(r + 16 * j) * 128, out[4], out[5], out[6], out[7]);
                 }
         }
+        // the weights: this thread's row, two pieces at a time
         int4 next[2] = {tc::lds128(a_from + (uint32_t)((0 ^ key) << 4)), tc::lds128(a_from + (uint32_t)((1 ^ key) << 4))};
-        // the weight buffer: free when the MMAs of the stage before the last are done, which is
-        // later than what the token stage waits for
-        if (it >= MT_A_BUFS) {
-            const uint32_t old = it - MT_A_BUFS;
-            if (!__all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_empty(area, (int)(old % MT_DEPTH)), (old / MT_DEPTH) & 1u)))
-                return;
-        }
+        a_free = a_free || tc::role_wait(area + 8, p.error, p.wait_ns, old_bar, old_phase);
+        if (!__all_sync(dev::FULL_MASK, a_free))
+            return;
         tc::fence_after();
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -331,6 +372,16 @@ __device__ __forceinline__ void convert_role(const MatmulParams &p, const Matmul
             }
             tc::st16(lane_base + 16 * h, out);
         }
+        // the next stage's barriers are asked while the stores land
+        int s_next = s + S::GROUPS;
+        uint32_t s_next_phase = s_phase;
+        while (s_next >= q.ahead) {
+            s_next -= q.ahead;
+            s_next_phase ^= 1u;
+        }
+        const uint32_t n = it + S::GROUPS;
+        empty = test_wait(bar_empty(area, (int)(n % S::DEPTH)), ((n / S::DEPTH) & 1u) ^ 1u);
+        staged = empty && test_wait(bar_staged(area, s_next), s_next_phase);
         tc::wait_st();
         tc::fence_before();
         tc::fence_async_smem();
@@ -339,35 +390,37 @@ __device__ __forceinline__ void convert_role(const MatmulParams &p, const Matmul
             tc::mbar_arrive(bar_freed(area, s));
             arrive<CG>(bar_full(area, (int)d), leader);
         }
-        s += 2;
+        s = s_next;
+        s_phase = s_next_phase;
     }
     // the MMAs' arrivals on this CTA's barriers come before it may leave
-    for (; it < stages + MT_DEPTH; it += 2)
-        if (!__all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_empty(area, (int)(it % MT_DEPTH)), ((it / MT_DEPTH) & 1u) ^ 1u)))
+    for (; it < stages + S::DEPTH; it += S::GROUPS)
+        if (!__all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_empty(area, (int)(it % S::DEPTH)), ((it / S::DEPTH) & 1u) ^ 1u)))
             return;
 }
 
 // ---- MMA issue -------------------------------------------------------------------------
 // By one thread, of the leading CTA of a pair; false when a wait ran out.
-template <int CG>
+template <int CG, int H>
 __device__ __forceinline__ bool mma_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t operands, uint32_t tmem,
                                          uint32_t pair_mask, int64_t work, int step0, int step1)
 {
-    const uint32_t rows = (uint32_t)q.tile_t / (CG * CG);    // token rows of a half in this CTA
-    const uint32_t idesc = tc::idesc_f16(128 * CG, q.tile_t / CG), atom = rows * CG * 8;   // 16-byte units
+    using S = Shape<H>;
+    const uint32_t rows = (uint32_t)q.tile_t / (CG * H);     // token rows of a half in this CTA
+    const uint32_t idesc = tc::idesc_f16(128 * CG, q.tile_t / H), atom = rows * H * 8;   // 16-byte units
     uint32_t acc = 0, acc_phase = 1, s = 0, phase = 0, buf = 0;
     for (; work > 0; --work)
         for (int step = step0; step < step1;) {
-            const uint32_t second = acc + 1 == MT_ACCS ? 0 : acc + 1, second_phase = second == 0 ? acc_phase ^ 1u : acc_phase;
+            const uint32_t second = acc + 1 == S::ACCS ? 0 : acc + 1, second_phase = second == 0 ? acc_phase ^ 1u : acc_phase;
             const int first = step, last = min(step + MT_CHUNK_STEPS, step1);
 #pragma unroll 1
             for (; step < last; ++step) {
                 if (!tc::role_wait(area + 8, p.error, p.wait_ns, bar_full(area, (int)s), phase))
                     return false;
-                const uint32_t a = tmem + MT_A_COL + buf * MT_A_COLS, b = MT_DESC_LOW | ((operands + s * q.stage_bytes) >> 4);
+                const uint32_t a = tmem + S::A_COL + buf * MT_A_COLS, b = MT_DESC_LOW | ((operands + s * q.stage_bytes) >> 4);
                 const int slices = (p.k - step * MT_KSTEP + 15) / 16;    // of 16 k that hold anything
 #pragma unroll
-                for (int h = 0; h < CG; ++h) {
+                for (int h = 0; h < H; ++h) {
                     const uint32_t u = h == 0 ? acc : second;
                     if (step == first &&
                         !tc::role_wait(area + 8, p.error, p.wait_ns, bar_acc_empty(area, (int)u), h == 0 ? acc_phase : second_phase))
@@ -382,15 +435,15 @@ __device__ __forceinline__ bool mma_role(const MatmulParams &p, const MatmulTcPl
                         commit<CG>(bar_acc_full(area, (int)u), pair_mask);
                 }
                 commit<CG>(bar_empty(area, (int)s), pair_mask);
-                buf ^= 1u;
-                if (++s == MT_DEPTH) {
+                buf = buf + 1 == S::GROUPS ? 0 : buf + 1;
+                if (++s == S::DEPTH) {
                     s = 0;
                     phase ^= 1u;
                 }
             }
-            acc += CG;
-            if (acc >= MT_ACCS) {
-                acc -= MT_ACCS;
+            acc += H;
+            if (acc >= S::ACCS) {
+                acc -= S::ACCS;
                 acc_phase ^= 1u;
             }
         }
@@ -417,56 +470,84 @@ __device__ __forceinline__ void store_tokens(const MatmulParams &p, int64_t t, i
         }
 }
 
-// Adds whole numbers |v| <= 2^24 held in f32 to int32 sums, two at a time and with additions
-// alone (conversions run at a quarter of their rate or less): v + 1.5 2^26 is v rounded to a
-// multiple of 8 with v / 8 in its low bits, the rest, at most 4, gets its low bits from 1.5 2^23.
-// The constants' own bits are taken off the sums at the end (MT_BIAS a drain, modulo 2^32).
-constexpr float MT_M8 = 100663296.0f, MT_M1 = 12582912.0f;        // 1.5 2^26, 1.5 2^23
-constexpr uint32_t MT_BIAS = 8u * 0x4cc00000u + 0x4b400000u;      // their bit patterns
-__device__ __forceinline__ void add_whole2(uint32_t r0, uint32_t r1, int32_t &s0, int32_t &s1)
+// Two runs of 16 columns, waited for together.
+__device__ __forceinline__ void ld16x2(uint32_t taddr, uint32_t (&r)[32])
 {
-    const uint64_t m8 = dev::pack2(MT_M8, MT_M8), m1 = dev::pack2(MT_M1, MT_M1);
-    const uint64_t v = dev::pack2(__uint_as_float(r0), __uint_as_float(r1));
-    const uint64_t h = dev::add2(v, m8);
-    const uint64_t l = dev::add2(dev::sub2(v, dev::sub2(h, m8)), m1);
-    float h0, h1, l0, l1;
-    dev::unpack2(h, h0, h1);
-    dev::unpack2(l, l0, l1);
-    s0 = (int32_t)((uint32_t)s0 + (__float_as_uint(h0) << 3) + __float_as_uint(l0));
-    s1 = (int32_t)((uint32_t)s1 + (__float_as_uint(h1) << 3) + __float_as_uint(l1));
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// N tokens' sums of one channel from column `c` on, of all `split` CTAs, and their outputs.  The
+// loads of two CTAs are in flight together: each takes a trip through the cluster's network.
+template <int N, int CG>
+__device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, int c, int split, uint32_t first, int64_t t, int64_t channel, bool ok)
+{
+    int32_t a[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        a[j] = 0;
+    for (int s = 0; s < split; s += 2) {          // split is even
+        const uint32_t from0 = map_to(at, (uint32_t)(s * CG) + first) + (uint32_t)c * 512;
+        const uint32_t from1 = map_to(at, (uint32_t)((s + 1) * CG) + first) + (uint32_t)c * 512;
+        int32_t v0[N], v1[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v0[j]) : "r"(from0 + 512 * j) : "memory");
+            asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v1[j]) : "r"(from1 + 512 * j) : "memory");
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            a[j] += v0[j] + v1[j];
+    }
+    store_tokens<N>(p, t, channel, a, p.scale_w[channel], p.bias ? p.bias[channel] : 0.0f, ok);
 }
 
 // Adds a tile's accumulators (one for each half and 1024 k) to `sum`: of this thread's channel,
 // `cols` tokens of each half; false when a wait ran out.
-template <int CG>
+template <int CG, int H>
 __device__ __forceinline__ bool drain_tile(const MatmulParams &p, uint32_t area, uint32_t from, int cols, int lane, uint32_t leader, uint32_t &acc,
-                                           uint32_t &phase, const Work &w, bool ok, int32_t (&sum)[64 * CG])
+                                           uint32_t &phase, const Work &w, bool ok, int32_t (&sum)[64 * H])
 {
     const uint32_t chunks = (uint32_t)(w.step1 - w.step0 + MT_CHUNK_STEPS - 1) / MT_CHUNK_STEPS;
 #pragma unroll
-    for (int i = 0; i < 64 * CG; ++i)
-        sum[i] = (int32_t)(0u - chunks * MT_BIAS);
+    for (int i = 0; i < 64 * H; ++i)
+        sum[i] = 0;
     for (uint32_t c = 0; ok && c < chunks; ++c)
 #pragma unroll
-        for (int h = 0; h < CG; ++h) {
+        for (int h = 0; h < H; ++h) {
             ok = ok && __all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_acc_full(area, (int)acc), phase));
             if (!ok)
                 break;
             tc::fence_after();
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (16 * j < cols) {
-                    uint32_t r[16];
-                    tc::ld16(from + acc * MT_ACC_COLS + 16 * j, r);
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t at = from + acc * MT_ACC_COLS + 32 * j;
+                if (32 * j + 16 < cols) {
+                    uint32_t r[32];
+                    ld16x2(at, r);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        add_whole2(r[i], r[i + 1], sum[64 * h + 16 * j + i], sum[64 * h + 16 * j + i + 1]);
+                    for (int i = 0; i < 32; ++i)
+                        sum[64 * h + 32 * j + i] += __float2int_rn(__uint_as_float(r[i]));
+                } else if (32 * j < cols) {
+                    uint32_t r[16];
+                    tc::ld16(at, r);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[64 * h + 32 * j + i] += __float2int_rn(__uint_as_float(r[i]));
                 }
+            }
             tc::fence_before();
             __syncwarp();
             if (lane == 0)
                 arrive<CG>(bar_acc_empty(area, (int)acc), leader);
-            if (++acc == MT_ACCS) {
+            if (++acc == Shape<H>::ACCS) {
                 acc = 0;
                 phase ^= 1u;
             }
@@ -474,13 +555,14 @@ __device__ __forceinline__ bool drain_tile(const MatmulParams &p, uint32_t area,
     return ok;
 }
 
-template <int CG, bool V16>
-__global__ void __launch_bounds__(MT_THREADS, 1)
+template <int CG, int H, bool V16>
+__global__ void __launch_bounds__(Shape<H>::THREADS, 1)
     i8_matmul_tc_kernel(const MatmulParams p, const MatmulTcPlan q, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x)
 {
+    using S = Shape<H>;
     extern __shared__ unsigned char raw[];
     const uint32_t area = (dev::smem_u32(raw) + 1023u) & ~1023u, operands = area + MT_AREA;
-    const uint32_t ring = operands + MT_DEPTH * q.stage_bytes;
+    const uint32_t ring = operands + S::DEPTH * q.stage_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -502,11 +584,11 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
             dev::mbar_init(bar_staged(area, s), V16 ? 1 : 32 * MT_LOADERS);
             dev::mbar_init(bar_freed(area, s), 4);
         }
-        for (int s = 0; s < MT_DEPTH; ++s) {
+        for (int s = 0; s < S::DEPTH; ++s) {
             dev::mbar_init(bar_full(area, s), 4 * CG);
             dev::mbar_init(bar_empty(area, s), 1);
         }
-        for (int b = 0; b < MT_ACCS; ++b) {
+        for (int b = 0; b < S::ACCS; ++b) {
             dev::mbar_init(bar_acc_full(area, b), 1);
             dev::mbar_init(bar_acc_empty(area, b), MT_EPI_WARPS * CG);
         }
@@ -514,12 +596,16 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(area + 8), "r"(0u) : "memory");
         dev::fence_barrier_init();
     }
-    dev::follow_previous_kernel();
+    if (V16 && warp == 1 && lane == 0) {
+        tc::prefetch_map(&map_w);
+        tc::prefetch_map(&map_x);
+    }
     if (warp == 0)
         tmem_alloc<CG>(area);
     tc::fence_before();
     cluster_sync();
     tc::fence_after();
+    dev::follow_previous_kernel();     // nothing above touches global memory
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(area));
 
@@ -527,13 +613,13 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp > 0) {
             if (!V16) {
-                load_words_role<CG>(p, q, area, ring, warp - 1, lane, pair_rank, w);
+                load_words_role<CG, H>(p, q, area, ring, warp - 1, lane, pair_rank, w);
                 asm volatile("cp.async.wait_all;" ::: "memory");
             } else if (warp == 1 && elected()) {
-                load_role<CG>(p, q, &map_w, &map_x, area, ring, pair_rank, w);
+                load_role<CG, H>(p, q, &map_w, &map_x, area, ring, pair_rank, w);
             }
         } else if (CG == 1 || pair_rank == 0) {
-            if (elected() && !mma_role<CG>(p, q, area, operands, tmem, pair_mask, work, w.step0, w.step1)) {
+            if (elected() && !mma_role<CG, H>(p, q, area, operands, tmem, pair_mask, work, w.step0, w.step1)) {
                 // let the MMAs in flight finish before tensor memory is freed
                 commit<CG>(bar_drain(area), pair_mask & (0u - pair_mask));   // on this CTA alone
                 const uint64_t t0 = dev::global_ns();
@@ -542,24 +628,30 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp < MT_EPI_WARP) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        convert_role<CG>(p, q, area, ring, operands, tmem, (warp - MT_CONV_WARP) >> 2, warp & 3, lane, leader, (uint32_t)(work * (w.step1 - w.step0)));
+    } else if (warp < S::EPI_WARP) {
+        if (H == 1)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        convert_role<CG, H>(p, q, area, ring, operands, tmem, (warp - MT_CONV_WARP) >> 2, warp & 3, lane, leader, (uint32_t)(work * (w.step1 - w.step0)));
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-        const int sub = warp & 3, half = (warp - MT_EPI_WARP) >> 2, cols = q.tile_t / (2 * CG);   // tokens of a half for each warp
+        if (H == 1)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        const int sub = warp & 3, half = (warp - S::EPI_WARP) >> 2, cols = q.tile_t / (2 * H);   // tokens of a half for each warp
         const uint32_t from = tmem + ((uint32_t)(32 * sub) << 16) + half * cols;
         uint32_t acc = 0, phase = 0;
         bool ok = true;
-        int32_t sum[64 * CG];
+        int32_t sum[64 * H];
         for (int64_t i = w.first; i < w.tiles; i += w.stride) {
-            ok = drain_tile<CG>(p, area, from, cols, lane, leader, acc, phase, w, ok, sum);
+            ok = drain_tile<CG, H>(p, area, from, cols, lane, leader, acc, phase, w, ok, sum);
             if (q.split > 1) {
                 // sums of this share of k, [token][128 channels], over the operand stages (all of
                 // them are used up: the accumulator is the last thing that read them)
 #pragma unroll
-                for (int h = 0; h < CG; ++h)
+                for (int h = 0; h < H; ++h)
 #pragma unroll
                     for (int j = 0; j < 64; ++j)
                         if (j < cols)
@@ -574,7 +666,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
             if (channel < p.n) {
                 const float sw = p.scale_w[channel], bias = p.bias ? p.bias[channel] : 0.0f;
 #pragma unroll
-                for (int h = 0; h < CG; ++h)
+                for (int h = 0; h < H; ++h)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (16 * j < cols)
@@ -587,8 +679,8 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     tc::fence_before();
     cluster_sync();      // every CTA's MMAs are done, its sums are in shared memory
     tc::fence_after();
-    if (q.split > 1 && warp >= MT_EPI_WARP) {
-        const int sub = warp & 3, half = (warp - MT_EPI_WARP) >> 2;
+    if (q.split > 1 && warp >= S::EPI_WARP) {
+        const int sub = warp & 3, half = (warp - S::EPI_WARP) >> 2;
         const Tile t = tile_at(q, w.first);
         const int64_t channel = t.m0 + pair_rank * MT_M + 32 * sub + lane;
         bool ok = true;
@@ -598,21 +690,14 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
             ok = ok && bad == 0;
         }
         if (channel < p.n) {
-            const float sw = p.scale_w[channel], bias = p.bias ? p.bias[channel] : 0.0f;
-            // groups of four tokens, shared out over the CTAs of the split and the two warps of each channel
-            for (int c = 4 * (part * 2 + half); c < q.tile_t; c += 8 * q.split) {
-                int32_t a[4] = {0, 0, 0, 0};
-                for (int s = 0; s < q.split; ++s) {
-                    const uint32_t at = map_to(operands, (uint32_t)(s * CG) + pair_rank) + (uint32_t)(c * 512 + (32 * sub + lane) * 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        int32_t v;
-                        asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(at + 512 * j) : "memory");
-                        a[j] += v;
-                    }
-                }
-                store_tokens<4>(p, t.t0 + c, channel, a, sw, bias, ok);
-            }
+            const uint32_t at = operands + (uint32_t)(32 * sub + lane) * 4, first = pair_rank, turn = (uint32_t)(part * 2 + half);
+            // groups of tokens, shared out over the CTAs of the split and the two warps of each channel
+            if (q.tile_t >= 32 * q.split)
+                for (int c = 16 * (int)turn; c < q.tile_t; c += 32 * q.split)
+                    store_sums<16, CG>(p, at, c, q.split, first, t.t0 + c, channel, ok);
+            else
+                for (int c = 4 * (int)turn; c < q.tile_t; c += 8 * q.split)
+                    store_sums<4, CG>(p, at, c, q.split, first, t.t0 + c, channel, ok);
         }
         __syncwarp();
     }
@@ -642,26 +727,26 @@ bool encode_rows(CUtensorMap *map, const int8_t *base, int64_t k, int64_t outer,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, bool V16> cudaError_t launch_cg(const MatmulParams &p, const MatmulTcPlan &q, cudaStream_t stream)
+template <int CG, int H, bool V16> cudaError_t launch_cg(const MatmulParams &p, const MatmulTcPlan &q, cudaStream_t stream)
 {
-    const auto kernel = i8_matmul_tc_kernel<CG, V16>;
+    const auto kernel = i8_matmul_tc_kernel<CG, H, V16>;
     // setmaxnreg hands out the registers that the launch brought: were there fewer, the
     // epilogue's request would wait for ever
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess)
         return e;
-    if (fa.numRegs < MT_LAUNCH_REGS)
+    if (fa.numRegs < Shape<H>::LAUNCH_REGS)
         return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q.smem_bytes);
     if (e != cudaSuccess)
         return e;
     CUtensorMap map_w = {}, map_x = {};
-    if (V16 && (!encode_rows(&map_w, p.w, p.k, p.n, MT_M) || !encode_rows(&map_x, p.x, p.k, p.tokens, q.tile_t / (CG * CG))))
+    if (V16 && (!encode_rows(&map_w, p.w, p.k, p.n, MT_M) || !encode_rows(&map_x, p.x, p.k, p.tokens, q.tile_t / (CG * H))))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)q.grid);
-    cfg.blockDim = dim3(MT_THREADS);
+    cfg.blockDim = dim3(Shape<H>::THREADS);
     cfg.dynamicSmemBytes = q.smem_bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -677,7 +762,7 @@ template <int CG, bool V16> cudaError_t launch_cg(const MatmulParams &p, const M
 
 }  // namespace
 
-int matmul_tc_threads() { return MT_THREADS; }
+int matmul_tc_threads(const MatmulTcPlan &q) { return q.halves == 1 ? Shape<1>::THREADS : Shape<2>::THREADS; }
 
 // Tile, split of k and grid.  The time of a choice is its waves of tiles times the stages of
 // one tile, plus what a tile (or a split) costs once, in units of a stage.
@@ -685,11 +770,11 @@ void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, int64_t sms, MatmulTcP
 {
     MatmulTcPlan best = {};
     double best_cost = 0.0;
-    const int cg = tokens <= 128 ? 1 : 2;
-    const int64_t steps = (k + MT_KSTEP - 1) / MT_KSTEP, tiles_t = (tokens + 128 * cg - 1) / (128 * cg);
+    const int cg = tokens <= 32 ? 1 : 2, halves = tokens <= 128 ? 1 : 2;
+    const int64_t steps = (k + MT_KSTEP - 1) / MT_KSTEP, tiles_t = (tokens + 255) / 256;
     const int64_t tiles_m = (n + MT_M * cg - 1) / (MT_M * cg), tiles = tiles_m * tiles_t;
-    const int64_t quantum = 32 * cg;      // each half's columns, shared by two warps (and CTAs), are whole 16s
-    const int64_t tile_t = ((tokens + tiles_t - 1) / tiles_t + quantum - 1) / quantum * quantum;   // up to 128 cg
+    const int64_t quantum = 32 * halves;  // each half's columns, shared by two warps (and CTAs), are whole 16s
+    const int64_t tile_t = ((tokens + tiles_t - 1) / tiles_t + quantum - 1) / quantum * quantum;   // up to 256
     for (int split = 1; cg * split <= 8; split *= 2) {
         // clusters of four and eight CTAs leave some SMs of a GPC idle
         const int64_t size = cg * split, slots = size <= 2 ? sms / size : size == 4 ? sms / 4 - 2 : sms / 8 - 3;
@@ -704,14 +789,16 @@ void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, int64_t sms, MatmulTcP
         }
     }
     best.cg = cg;
+    best.halves = halves;
     best.tile_t = (int32_t)tile_t;
     best.tiles_m = (int32_t)tiles_m;
     best.tiles_t = (int32_t)tiles_t;
     best.stage_bytes = (uint32_t)(tile_t / cg) * 2 * MT_KSTEP;
     best.ahead_bytes = (uint32_t)(MT_M + tile_t / cg) * MT_KSTEP;
-    const int64_t room = (MT_ROOM - MT_DEPTH * best.stage_bytes) / best.ahead_bytes;
+    const uint32_t operands = (uint32_t)(halves == 1 ? Shape<1>::DEPTH : Shape<2>::DEPTH) * best.stage_bytes;
+    const int64_t room = (MT_ROOM - operands) / best.ahead_bytes;
     best.ahead = (int32_t)(room < MT_MAX_AHEAD ? room : MT_MAX_AHEAD);
-    uint32_t bytes = MT_DEPTH * best.stage_bytes + (uint32_t)best.ahead * best.ahead_bytes;
+    uint32_t bytes = operands + (uint32_t)best.ahead * best.ahead_bytes;
     const uint32_t sums = best.split > 1 ? (uint32_t)tile_t * 512u : 0u;
     bytes = bytes > sums ? bytes : sums;
     bytes = bytes > 116u * 1024u ? bytes : 116u * 1024u;   // more than half an SM: one CTA, which owns tensor memory
@@ -722,8 +809,10 @@ void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, int64_t sms, MatmulTcP
 cudaError_t launch_matmul_tc(const MatmulParams &p, const MatmulTcPlan &q, bool vec16, cudaStream_t stream)
 {
     if (q.cg == 1)
-        return vec16 ? launch_cg<1, true>(p, q, stream) : launch_cg<1, false>(p, q, stream);
-    return vec16 ? launch_cg<2, true>(p, q, stream) : launch_cg<2, false>(p, q, stream);
+        return vec16 ? launch_cg<1, 1, true>(p, q, stream) : launch_cg<1, 1, false>(p, q, stream);
+    if (q.halves == 1)
+        return vec16 ? launch_cg<2, 1, true>(p, q, stream) : launch_cg<2, 1, false>(p, q, stream);
+    return vec16 ? launch_cg<2, 2, true>(p, q, stream) : launch_cg<2, 2, false>(p, q, stream);
 }
 
 }  // namespace loom

@@ -33,14 +33,15 @@ struct MatmulParams {
 // tensor cores (i8_matmul_tc.cu)
 struct MatmulTcPlan {
     int64_t grid;
-    int32_t cg;               // CTAs per MMA: 1 (up to 128 tokens) or 2
-    int32_t tile_t;           // tokens per tile, a multiple of 32 up to 128 cg
+    int32_t cg;               // CTAs per MMA: 1 (up to 32 tokens) or 2
+    int32_t halves;           // 1, or 2 for tiles of more than 128 tokens
+    int32_t tile_t;           // tokens per tile, up to 256: a multiple of 32 per half
     int32_t split;            // shares of k, one per CTA (pair) of a cluster
     int32_t tiles_m, tiles_t; // tiles of channels (128 cg each) and of tokens
     int32_t ahead;            // stages of bytes in the copy ring
     uint32_t stage_bytes, ahead_bytes, smem_bytes;
 };
-int matmul_tc_threads();
+int matmul_tc_threads(const MatmulTcPlan &q);
 void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, int64_t sms, MatmulTcPlan *out);
 cudaError_t launch_matmul_tc(const MatmulParams &p, const MatmulTcPlan &q, bool vec16, cudaStream_t stream);
 cudaError_t launch_matmul_dp4a(const MatmulParams &p, bool vec16, const loom_launch &L, cudaStream_t stream);

@@ -61,7 +61,7 @@ loom_status matmul_geometry(int64_t tokens, int64_t n, int64_t k, int64_t path, 
     const bool tensor = path == LOOM_PATH_TENSOR || (path == LOOM_PATH_AUTO && tokens > MM_DP4A_PASS);
     if (tensor && k > 0 && n > 0 && tokens > 0) {
         matmul_tc_plan(tokens, n, k, sms, plan);
-        *out = plain_launch(plan->grid, 1, (uint32_t)matmul_tc_threads(), LOOM_KERNEL_I8_MATMUL_TENSOR, 128u);
+        *out = plain_launch(plan->grid, 1, (uint32_t)matmul_tc_threads(*plan), LOOM_KERNEL_I8_MATMUL_TENSOR, 128u);
         out->cluster[0] = (uint32_t)(plan->cg * plan->split);
         out->smem_bytes = plan->smem_bytes;
         return LOOM_OK;
