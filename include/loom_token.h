@@ -34,10 +34,11 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
 #define LOOM_DEVERR_NO_TOKEN 0x8  /* a row of logits held nothing to choose: its token is -1 */
 
 /* Operators of loom_token_launch_config. */
-#define LOOM_OP_QUANTIZE_TOKENS 8      /* workload {tokens, k, dtype, aligned (0/1, default 1)} */
+#define LOOM_OP_QUANTIZE_TOKENS 8      /* workload {tokens, k, dtype, aligned (0/1, default 1),
+                                          sm_count (0 = the current device)} */
 #define LOOM_OP_I8_MATMUL 9            /* workload {tokens, n, k, aligned (0/1, default 1), path
                                           (LOOM_PATH_*, default auto), sm_count (0 = the current device)} */
-#define LOOM_OP_LAYER_NORM 10          /* workload {rows, width, dtype, aligned (0/1, default 1)} */
+#define LOOM_OP_LAYER_NORM 10          /* workload as LOOM_OP_QUANTIZE_TOKENS, {rows, width, ...} */
 #define LOOM_OP_LAYER_NORM_BACKWARD 11 /* workload {rows, width, dtype, aligned (0/1, default 1),
                                           sm_count (0 = the current device)}: the first launch */
 #define LOOM_OP_SAMPLE_TOKENS 12       /* workload {rows, vocab, dtype, sm_count (0 = the current device)} */
@@ -45,7 +46,7 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
 /* Kernels they select (loom_launch.kernel). */
 #define LOOM_KERNEL_I8_MATMUL_DP4A 18   /* few tokens: dp4a, weights streamed once per pass of up to 8 tokens */
 #define LOOM_KERNEL_I8_MATMUL_TENSOR 19 /* tcgen05 MMA on exact f16 copies; units_per_cta = channels */
-#define LOOM_KERNEL_NORM_ROWS 20        /* one CTA (or warp) per row, the row held in registers */
+#define LOOM_KERNEL_NORM_ROWS 20        /* a CTA (or warp) holds a row in registers; CTAs walk over the rows */
 #define LOOM_KERNEL_NORM_LONG 21        /* rows longer than the registers of a CTA, read again from L2 */
 #define LOOM_KERNEL_NORM_BACKWARD 22    /* CTAs over shares of the rows, column sums in registers */
 #define LOOM_KERNEL_SAMPLE 24           /* logits to token */

@@ -527,34 +527,70 @@ def loom_stream_floor(src, nbytes: int, schedule: int, depth: int, ctas_per_sm: 
 
 
 # ---- token operators (loom_token.h) ----------------------------------------------------
+# One new token takes a few microseconds on the device, so these calls keep their own work
+# short: no context manager unless the device differs, one lookup for the stream.
+_torch = None
 _dtypes: dict = {}
+_current_stream = None      # device index -> handle of torch's current stream
+
+
+def _lazy():
+    """torch, and what the calls below look up in it, on first use."""
+    global _torch, _current_stream
+    if _torch is None:
+        import torch
+        _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _dtypes.update({torch.float32: LOOM_F32, torch.float16: LOOM_F16, torch.bfloat16: LOOM_BF16})
+        _torch = torch
+    return _torch
 
 
 def _dtype(dtype) -> int:
-    """LOOM_F32 / LOOM_F16 / LOOM_BF16 of a torch dtype (or one of those numbers)."""
-    if isinstance(dtype, int):
-        return dtype
-    if not _dtypes:
-        import torch
-        _dtypes.update({torch.float32: LOOM_F32, torch.float16: LOOM_F16, torch.bfloat16: LOOM_BF16})
-    if dtype not in _dtypes:
+    """LOOM_F32 / LOOM_F16 / LOOM_BF16 of a torch dtype."""
+    code = _dtypes.get(dtype)
+    if code is None:
         raise LoomError(LOOM_ERR_ARG, f"element type {dtype}")
-    return _dtypes[dtype]
+    return code
 
 
 def _matrix(t, where: str):
     """(rows, width, stride) of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise LoomError(LOOM_ERR_SHAPE, f"{where}: a matrix with contiguous rows is wanted")
-    return t.shape[0], t.shape[1], t.stride(0)
+    shape = t.shape
+    if len(shape) == 2:
+        rows, width = shape
+        stride, inner = t.stride()
+        if inner == 1 or width <= 1:
+            return rows, width, stride
+    raise LoomError(LOOM_ERR_SHAPE, f"{where}: a matrix with contiguous rows is wanted")
 
 
 def _floats(where: str, n: int, *tensors):
     """The optional tensors are contiguous f32 of n elements each."""
-    import torch
+    f32 = _torch.float32
     for t in tensors:
-        if t is not None and not isinstance(t, int) and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()):
+        if t is not None and (t.dtype is not f32 or t.numel() != n or not t.is_contiguous()):
             raise LoomError(LOOM_ERR_SHAPE, f"{where}: {n} contiguous float32 values are wanted")
+
+
+def _launch(where: str, like, stream, *args):
+    """The library call `where` on the device of `like` and on `stream` (its current one)."""
+    fn = getattr(_lib, where)
+    device = like.get_device()
+    if device < 0:
+        raise LoomError(LOOM_ERR_ARG, f"{where}: tensors on a GPU are wanted")
+    cuda = _torch.cuda
+    if stream is None:
+        stream = _current_stream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if cuda.current_device() == device:
+        status = fn(*args, stream)
+    else:
+        with cuda.device(device):
+            status = fn(*args, stream)
+    if status != LOOM_OK:
+        raise LoomError(status, where)
 
 
 def loom_token_launch_config(op: int, workload) -> dict:
@@ -567,15 +603,14 @@ def loom_token_launch_config(op: int, workload) -> dict:
 def loom_quantize_tokens(x, *, q=None, scale=None, error=None, stream=None):
     """Tokens ``x[tokens][k]`` (float32, float16 or bfloat16) to signed bytes with one scale
     each; returns ``(q_packed int32 [tokens][k/4], scale float32 [tokens])``."""
-    import torch
+    torch = _torch or _lazy()
     tokens, k, stride = _matrix(x, "loom_quantize_tokens")
+    dtype = _dtype(x.dtype)
     if q is None:
-        q = _empty(x, (tokens, k // 4), torch.int32)
+        q = torch.empty((tokens, k // 4), dtype=torch.int32, device=x.device)
     if scale is None:
-        scale = _empty(x, (tokens,), torch.float32)
-    with _on_device(x):
-        _check(_lib.loom_quantize_tokens(x.data_ptr(), _dtype(x.dtype), tokens, k, stride, _ptr(q), _ptr(scale),
-                                         _ptr(error), _stream(stream, x)), "loom_quantize_tokens")
+        scale = torch.empty(tokens, dtype=torch.float32, device=x.device)
+    _launch("loom_quantize_tokens", x, stream, x.data_ptr(), dtype, tokens, k, stride, _ptr(q), _ptr(scale), _ptr(error))
     return q, scale
 
 
@@ -595,18 +630,15 @@ def loom_i8_matmul_ex(w_packed, scale_w, n_rows: int, k: int, x_packed, scale_x,
                       want_acc, stream, _ptr(error), tp)
 
 
-def _i8_matmul(name, w_packed, scale_w, n_rows, k, x_packed, scale_x, tokens, bias, y, y_dtype, acc, want_acc, stream,
-               *more):
-    import torch
+def _i8_matmul(where, w_packed, scale_w, n_rows, k, x_packed, scale_x, tokens, bias, y, y_dtype, acc, want_acc, stream, *more):
+    torch = _torch or _lazy()
     if y is None:
-        y = _empty(w_packed, (tokens, n_rows), torch.float32 if y_dtype is None else y_dtype)
+        y = torch.empty((tokens, n_rows), dtype=torch.float32 if y_dtype is None else y_dtype, device=w_packed.device)
     if acc is None and want_acc:
-        acc = _empty(w_packed, (tokens, n_rows), torch.int32)
-    _, _, stride = _matrix(y, name)
-    with _on_device(w_packed):
-        _check(getattr(_lib, name)(_ptr(w_packed), _ptr(scale_w), int(n_rows), int(k), _ptr(x_packed), _ptr(scale_x),
-                                   int(tokens), _ptr(bias), y.data_ptr(), _dtype(y.dtype), stride, _ptr(acc), *more,
-                                   _stream(stream, w_packed)), name)
+        acc = torch.empty((tokens, n_rows), dtype=torch.int32, device=w_packed.device)
+    stride = _matrix(y, where)[2]
+    _launch(where, w_packed, stream, w_packed.data_ptr(), scale_w.data_ptr(), n_rows, k, x_packed.data_ptr(), scale_x.data_ptr(),
+            tokens, _ptr(bias), y.data_ptr(), _dtype(y.dtype), stride, _ptr(acc), *more)
     return y, acc
 
 
@@ -615,84 +647,107 @@ def loom_layer_norm(x, gain=None, bias=None, eps: float = 1e-5, *, y=None, mean=
     """Layer norm of the rows of ``x`` (float32, float16 or bfloat16); ``gain`` and ``bias``
     float32 or None.  Returns ``(y, mean, rstd)``, the last two float32 per row as the
     backward pass takes them (None without ``want_stats``)."""
-    import torch
+    torch = _torch or _lazy()
     rows, width, stride = _matrix(x, "loom_layer_norm")
+    dtype = _dtype(x.dtype)
     _floats("loom_layer_norm", width, gain, bias)
     if y is None:
-        y = _empty(x, (rows, width), x.dtype)
+        y = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+        y_stride = width
+    else:
+        if y.dtype != x.dtype or y.shape != x.shape:
+            raise LoomError(LOOM_ERR_SHAPE, "loom_layer_norm: y has another type or shape than x")
+        y_stride = _matrix(y, "loom_layer_norm")[2]
     if want_stats:
-        mean = _empty(x, (rows,), torch.float32) if mean is None else mean
-        rstd = _empty(x, (rows,), torch.float32) if rstd is None else rstd
-    if y.dtype != x.dtype:
-        raise LoomError(LOOM_ERR_ARG, "loom_layer_norm: y has another type than x")
-    _, _, y_stride = _matrix(y, "loom_layer_norm")
-    with _on_device(x):
-        _check(_lib.loom_layer_norm(x.data_ptr(), _dtype(x.dtype), rows, width, stride, _ptr(gain), _ptr(bias), eps,
-                                    y.data_ptr(), y_stride, _ptr(mean), _ptr(rstd), _stream(stream, x)),
-               "loom_layer_norm")
+        if mean is None:
+            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _launch("loom_layer_norm", x, stream, x.data_ptr(), dtype, rows, width, stride, _ptr(gain), _ptr(bias), eps, y.data_ptr(),
+            y_stride, _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
 
 def loom_layer_norm_i8(x, gain=None, bias=None, eps: float = 1e-5, *, q=None, scale=None, error=None, stream=None):
     """``loom_quantize_tokens`` of layer norm's rows, which are never written; returns
     ``(q_packed, scale)``."""
-    import torch
+    torch = _torch or _lazy()
     rows, width, stride = _matrix(x, "loom_layer_norm_i8")
+    dtype = _dtype(x.dtype)
     _floats("loom_layer_norm_i8", width, gain, bias)
     if q is None:
-        q = _empty(x, (rows, width // 4), torch.int32)
+        q = torch.empty((rows, width // 4), dtype=torch.int32, device=x.device)
     if scale is None:
-        scale = _empty(x, (rows,), torch.float32)
-    with _on_device(x):
-        _check(_lib.loom_layer_norm_i8(x.data_ptr(), _dtype(x.dtype), rows, width, stride, _ptr(gain), _ptr(bias), eps,
-                                       _ptr(q), _ptr(scale), _ptr(error), _stream(stream, x)), "loom_layer_norm_i8")
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _launch("loom_layer_norm_i8", x, stream, x.data_ptr(), dtype, rows, width, stride, _ptr(gain), _ptr(bias), eps, _ptr(q),
+            _ptr(scale), _ptr(error))
     return q, scale
 
 
 def loom_layer_norm_backward_workspace_bytes(rows: int, width: int) -> int:
     """Bytes of the workspace of ``loom_layer_norm_backward`` on the current device."""
     out = ctypes.c_int64(0)
-    _check(_lib.loom_layer_norm_backward_workspace_bytes(int(rows), int(width), ctypes.byref(out)),
+    _check(_lib.loom_layer_norm_backward_workspace_bytes(rows, width, ctypes.byref(out)),
            "loom_layer_norm_backward_workspace_bytes")
-    return int(out.value)
+    return out.value
 
 
 def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=None, dbias=None, want_dx: bool = True,
                              want_params: bool = True, workspace=AUTO, stream=None):
     """Gradients of layer norm: ``(dx, dgain, dbias)`` from ``dy`` and ``x`` (same type), the
     forward pass's ``mean`` and ``rstd``, and ``gain``.  ``want_dx`` / ``want_params`` leave
-    out what is not needed (None).  ``workspace``: a tensor, an ``(address, bytes)`` pair, or
-    "auto" (allocated for the call from torch's allocator)."""
-    import torch
-    rows, width, x_stride = _matrix(x, "loom_layer_norm_backward")
-    _, _, dy_stride = _matrix(dy, "loom_layer_norm_backward")
-    _floats("loom_layer_norm_backward", width, gain)
-    _floats("loom_layer_norm_backward", rows, mean, rstd)
+    out what is not needed (None).  ``workspace``: a tensor, an ``(address, bytes)`` pair, None,
+    or "auto" (taken for the call from torch's allocator)."""
+    torch = _torch or _lazy()
+    where = "loom_layer_norm_backward"
+    rows, width, x_stride = _matrix(x, where)
+    dtype = _dtype(x.dtype)
+    dy_stride = _matrix(dy, where)[2]
+    _floats(where, width, gain, dgain, dbias)
+    _floats(where, rows, mean, rstd)
+    device = x.device
     if dy.dtype != x.dtype or dy.shape != x.shape:
-        raise LoomError(LOOM_ERR_SHAPE, "loom_layer_norm_backward: dy has another type or shape than x")
-    if dx is None and want_dx:
-        dx = _empty(x, (rows, width), x.dtype)
-    if want_params:
-        dgain = _empty(x, (width,), torch.float32) if dgain is None else dgain
-        dbias = _empty(x, (width,), torch.float32) if dbias is None else dbias
-    dx_stride = 0
+        raise LoomError(LOOM_ERR_SHAPE, f"{where}: dy has another type or shape than x")
+    dx_stride = width
     if dx is not None:
         if dx.dtype != x.dtype or dx.shape != x.shape:
-            raise LoomError(LOOM_ERR_SHAPE, "loom_layer_norm_backward: dx has another type or shape than x")
-        _, _, dx_stride = _matrix(dx, "loom_layer_norm_backward")
-    with _on_device(x):
-        st = _stream(stream, x)
-        if isinstance(workspace, str) and workspace == AUTO:
-            nbytes = loom_layer_norm_backward_workspace_bytes(rows, width)
-            workspace = _empty(x, (nbytes,), torch.uint8)
-            if stream is not None:   # the allocator may hand it out again only after this stream's work
-                workspace.record_stream(torch.cuda.ExternalStream(st, device=x.device))
-        wp, wb = (workspace if isinstance(workspace, tuple) else
-                  (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
-        _check(_lib.loom_layer_norm_backward(dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, _dtype(x.dtype), rows, width,
-                                             _ptr(gain), _ptr(mean), _ptr(rstd), _ptr(dx), dx_stride, _ptr(dgain),
-                                             _ptr(dbias), wp, int(wb), st), "loom_layer_norm_backward")
+            raise LoomError(LOOM_ERR_SHAPE, f"{where}: dx has another type or shape than x")
+        dx_stride = _matrix(dx, where)[2]
+    elif want_dx:
+        dx = torch.empty((rows, width), dtype=x.dtype, device=device)
+    if want_params:
+        if dgain is None:
+            dgain = torch.empty(width, dtype=torch.float32, device=device)
+        if dbias is None:
+            dbias = torch.empty(width, dtype=torch.float32, device=device)
+    if workspace is None:
+        wp, wb = None, 0
+    elif isinstance(workspace, tuple):
+        wp, wb = workspace
+    else:
+        if workspace is AUTO or (isinstance(workspace, str) and workspace == AUTO):
+            if device.index == torch.cuda.current_device():
+                nbytes = loom_layer_norm_backward_workspace_bytes(rows, width)
+            else:
+                with torch.cuda.device(device):
+                    nbytes = loom_layer_norm_backward_workspace_bytes(rows, width)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            if stream is not None:   # the allocator may hand it out again only after that stream's work
+                handle = stream if isinstance(stream, int) else stream.cuda_stream
+                workspace.record_stream(torch.cuda.ExternalStream(handle, device=device))
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch(where, x, stream, dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, dtype, rows, width, _ptr(gain), mean.data_ptr(),
+            rstd.data_ptr(), _ptr(dx), dx_stride, _ptr(dgain), _ptr(dbias), wp, wb)
     return dx, dgain, dbias
+
+
+def _setting(name: str, v, dtype, rows: int):
+    """(device address or None, host value) of a sampling setting."""
+    if isinstance(v, _torch.Tensor):
+        if v.dtype != dtype or v.numel() != rows or not v.is_contiguous():
+            raise LoomError(LOOM_ERR_SHAPE, f"loom_sample_tokens: {name}: {rows} contiguous {dtype} values are wanted")
+        return v.data_ptr(), 0
+    return None, v
 
 
 def loom_sample_tokens(logits, uniform, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, logprob=None,
@@ -700,24 +755,18 @@ def loom_sample_tokens(logits, uniform, *, temperature=1.0, top_k=0, top_p=1.0, 
     """The next token of each row of ``logits[rows][vocab]`` from ``uniform`` float32 ``[rows]``
     in [0, 1); each setting is a number for every row or a device tensor with one per row
     (``top_k`` int32, the others float32).  Returns ``(token int32, logprob float32)``."""
-    import torch
+    torch = _torch or _lazy()
     rows, vocab, stride = _matrix(logits, "loom_sample_tokens")
+    dtype = _dtype(logits.dtype)
     _floats("loom_sample_tokens", rows, uniform)
-    args = []
-    for name, v, dtype, off in (("temperature", temperature, torch.float32, 1.0), ("top_k", top_k, torch.int32, 0),
-                                ("top_p", top_p, torch.float32, 1.0), ("min_p", min_p, torch.float32, 0.0)):
-        if isinstance(v, torch.Tensor):
-            if v.dtype != dtype or v.numel() != rows or not v.is_contiguous():
-                raise LoomError(LOOM_ERR_SHAPE, f"loom_sample_tokens: {name}: {rows} contiguous {dtype} values are wanted")
-            args += [v.data_ptr(), off]
-        else:
-            args += [None, v]
+    dt, t = _setting("temperature", temperature, torch.float32, rows)
+    dk, k = _setting("top_k", top_k, torch.int32, rows)
+    dp, p = _setting("top_p", top_p, torch.float32, rows)
+    dm, m = _setting("min_p", min_p, torch.float32, rows)
     if token is None:
-        token = _empty(logits, (rows,), torch.int32)
+        token = torch.empty(rows, dtype=torch.int32, device=logits.device)
     if logprob is None and want_logprob:
-        logprob = _empty(logits, (rows,), torch.float32)
-    with _on_device(logits):
-        _check(_lib.loom_sample_tokens(logits.data_ptr(), _dtype(logits.dtype), rows, vocab, stride, *args, _ptr(uniform),
-                                       _ptr(token), _ptr(logprob), _ptr(error), _stream(stream, logits)),
-               "loom_sample_tokens")
+        logprob = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _launch("loom_sample_tokens", logits, stream, logits.data_ptr(), dtype, rows, vocab, stride, dt, t, dk, k, dp, p, dm, m,
+            uniform.data_ptr(), _ptr(token), _ptr(logprob), _ptr(error))
     return token, logprob

@@ -732,13 +732,8 @@ template <int CG, int H, bool V16> cudaError_t launch_cg(const MatmulParams &p, 
     const auto kernel = i8_matmul_tc_kernel<CG, H, V16>;
     // setmaxnreg hands out the registers that the launch brought: were there fewer, the
     // epilogue's request would wait for ever
-    cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess)
-        return e;
-    if (fa.numRegs < Shape<H>::LAUNCH_REGS)
-        return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q.smem_bytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), Shape<H>::LAUNCH_REGS, done);
     if (e != cudaSuccess)
         return e;
     CUtensorMap map_w = {}, map_x = {};

@@ -64,12 +64,12 @@ struct RowsParams {
 // `vec` is the number of elements per load: the widest of 16 bytes, 8 bytes and one
 // element that every row's start and the width allow (row_vec).
 int row_vec(int32_t dtype, int32_t width, const void *const *pointers, const int64_t *strides, int n);
-bool rows_geometry(int64_t rows, int32_t width, loom_launch *out);
+bool rows_geometry(int64_t rows, int32_t width, int64_t sms, loom_launch *out);
 cudaError_t launch_rows(const RowsParams &p, RowMode mode, int32_t dtype, int vec, const loom_launch &L,
                         cudaStream_t stream);
 
-constexpr int NG_EPT = 8;                       // elements a thread of the register kernel holds
-constexpr int32_t NG_MAX_WIDTH = 1024 * NG_EPT; // wider rows take two passes
+constexpr int NG_EPT = 8;                 // columns per thread of the backward kernel; twice that ...
+constexpr int32_t NG_MAX_WIDTH = 8192;    // ... for rows that need over 256 threads; wider rows take two passes
 
 struct NormGradParams {
     const void *dy, *x;

@@ -86,6 +86,9 @@ loom_status bytes_shape(int64_t rows, int64_t k)
 
 bool short_stride(int64_t rows, int64_t stride, int64_t width) { return rows > 1 && stride < width; }
 
+// f32 parameters are read 16 bytes at a time beside wide row accesses.
+int param_vec(int vec, const void *a, const void *b) { return misaligned(a, 16) || misaligned(b, 16) ? 1 : vec; }
+
 // Offsets of a single row do not depend on its stride.
 int64_t used_stride(int64_t rows, int64_t stride) { return rows > 1 ? stride : 0; }
 
@@ -104,8 +107,12 @@ loom_status to_bytes(const void *d_x, int32_t dtype, int64_t rows, int32_t width
     if (misaligned(d_x, dtype_bytes(dtype)) || misaligned(q, 4) || misaligned(scale, 4) || misaligned(gain, 4) ||
         misaligned(bias, 4) || misaligned(error, 4))
         return LOOM_ERR_ALIGN;
+    int64_t sms = 0;
+    const loom_status counted = sm_count(&sms);
+    if (counted != LOOM_OK)
+        return counted;
     loom_launch L;
-    if (!rows_geometry(rows, width, &L))
+    if (!rows_geometry(rows, width, sms, &L))
         return LOOM_ERR_SHAPE;
     RowsParams p = {};
     p.x = d_x;
@@ -124,6 +131,7 @@ loom_status to_bytes(const void *d_x, int32_t dtype, int64_t rows, int32_t width
     int vec = row_vec(dtype, width, ptrs, strides, 1);
     if (vec == 8 && misaligned(q, 8))
         vec = 4;
+    vec = param_vec(vec, gain, bias);
     return of_cuda(launch_rows(p, mode, dtype, vec, L, static_cast<cudaStream_t>(stream)));
 }
 
@@ -145,7 +153,13 @@ extern "C" loom_status loom_token_launch_config(int32_t op, const int64_t *w, in
         const loom_status st = op == LOOM_OP_LAYER_NORM ? rows_shape(w[0], w[1]) : bytes_shape(w[0], w[1]);
         if (st != LOOM_OK)
             return st;
-        return rows_geometry(w[0], (int32_t)w[1], out) ? LOOM_OK : LOOM_ERR_SHAPE;
+        int64_t sms = opt(4, 0);
+        if (sms < 0)
+            return LOOM_ERR_ARG;
+        const loom_status known_sms = sms ? LOOM_OK : sm_count(&sms);
+        if (known_sms != LOOM_OK)
+            return known_sms;
+        return rows_geometry(w[0], (int32_t)w[1], sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
     }
     case LOOM_OP_I8_MATMUL:
         if (n < 3)
@@ -261,8 +275,12 @@ extern "C" loom_status loom_layer_norm(const void *d_x, int32_t dtype, int64_t r
     if (misaligned(d_x, dtype_bytes(dtype)) || misaligned(d_y, dtype_bytes(dtype)) || misaligned(d_gain, 4) ||
         misaligned(d_bias, 4) || misaligned(d_mean, 4) || misaligned(d_rstd, 4))
         return LOOM_ERR_ALIGN;
+    int64_t sms = 0;
+    const loom_status counted = sm_count(&sms);
+    if (counted != LOOM_OK)
+        return counted;
     loom_launch L;
-    if (!rows_geometry(rows, width, &L))
+    if (!rows_geometry(rows, width, sms, &L))
         return LOOM_ERR_SHAPE;
     RowsParams p = {};
     p.x = d_x;
@@ -278,7 +296,7 @@ extern "C" loom_status loom_layer_norm(const void *d_x, int32_t dtype, int64_t r
     p.rstd = d_rstd;
     const void *ptrs[] = {d_x, d_y};
     const int64_t strides[] = {p.x_stride, p.y_stride};
-    return of_cuda(launch_rows(p, RowMode::Norm, dtype, row_vec(dtype, width, ptrs, strides, 2), L,
+    return of_cuda(launch_rows(p, RowMode::Norm, dtype, param_vec(row_vec(dtype, width, ptrs, strides, 2), d_gain, d_bias), L,
                                static_cast<cudaStream_t>(stream)));
 }
 
@@ -346,7 +364,7 @@ extern "C" loom_status loom_layer_norm_backward(const void *d_dy, int64_t dy_str
     }
     const void *ptrs[] = {d_dy, d_x, d_dx ? d_dx : d_x};
     const int64_t strides[] = {p.dy_stride, p.x_stride, d_dx ? p.dx_stride : p.x_stride};
-    return of_cuda(launch_norm_grad(p, dtype, row_vec(dtype, width, ptrs, strides, 3), L, parts,
+    return of_cuda(launch_norm_grad(p, dtype, param_vec(row_vec(dtype, width, ptrs, strides, 3), d_gain, nullptr), L, parts,
                                     static_cast<cudaStream_t>(stream)));
 }
 

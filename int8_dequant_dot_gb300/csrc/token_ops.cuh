@@ -1,7 +1,9 @@
 // token_ops.cuh -- device helpers shared by the token operators' kernels.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
+#include <cstring>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -44,4 +46,48 @@ __device__ __forceinline__ float dequantized(int32_t acc, float sw, float sx, co
 }
 
 }  // namespace dev
+
+// Raises a kernel's dynamic shared-memory limit to all that a CTA may have, and checks that the
+// kernel brings at least `regs` registers a thread: once per device and kernel (`done` holds
+// a bit per device).
+inline cudaError_t prepare_kernel(const void *kernel, int regs, std::atomic<uint64_t> &done)
+{
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (done.load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e == cudaSuccess && fa.numRegs < regs)
+        e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - (int)fa.sharedSizeBytes);
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
+// As launch_with, for a kernel that prepare_kernel has seen.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_prepared(void (*kernel)(KArgs...), const loom_launch &L, cudaStream_t stream, Args &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(L.grid[0], L.grid[1], L.grid[2]);
+    cfg.blockDim = dim3(L.block[0], L.block[1], L.block[2]);
+    cfg.dynamicSmemBytes = L.smem_bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = L.cluster[0];
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = L.cluster[0] > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 }  // namespace loom

@@ -13,6 +13,8 @@
 //    the partial sums in a fixed order: no atomics, the same bits on every call.
 //    Rows wider than 8192 take two passes: the two sums of each row, then blocks
 //    of columns.
+//  * CTAs walk over the rows and copy them ahead into a ring of shared memory (bulk copies),
+//    two rows a turn.
 //  * Loads are as wide as every row's start allows: 16 or 8 bytes, else one element.
 #include "token_ops.cuh"
 
@@ -20,13 +22,34 @@ namespace loom {
 namespace {
 
 constexpr int ROW_WARP_ROWS = 4;      // rows per CTA where a warp takes a whole row
+
+// CTAs of `threads` threads that share an SM: 128 registers a thread.
+int64_t rows_per_sm(int64_t threads) { return threads >= 512 ? 1 : 512 / threads; }
+
 constexpr float TINY_AMAX = 7.888609052210118e-31f;   // 2^-100
 
 template <typename E, int V> struct alignas(sizeof(E) * V) Pack {
     E e[V];
 };
 
-template <typename E, int V> __device__ __forceinline__ void load_f32(const E *p, float (&v)[V])
+// A pack as it lies in memory, in whole registers until it is used.
+template <int BYTES> struct Raw;
+template <> struct Raw<16> { typedef uint4 T; };
+template <> struct Raw<8> { typedef uint2 T; };
+template <> struct Raw<4> { typedef uint32_t T; };
+template <> struct Raw<2> { typedef uint16_t T; };
+
+template <typename E, int V> __device__ __forceinline__ void unpack_f32(const typename Raw<sizeof(E) * V>::T &raw, float *v)
+{
+    Pack<E, V> q;
+    static_assert(sizeof(q) == sizeof(raw), "same bytes");
+    memcpy(&q, &raw, sizeof(q));
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        v[i] = dev::to_f32(q.e[i]);
+}
+
+template <typename E, int V> __device__ __forceinline__ void load_f32(const E *p, float *v)
 {
     const Pack<E, V> q = *reinterpret_cast<const Pack<E, V> *>(p);
 #pragma unroll
@@ -34,7 +57,7 @@ template <typename E, int V> __device__ __forceinline__ void load_f32(const E *p
         v[i] = dev::to_f32(q.e[i]);
 }
 
-template <typename E, int V> __device__ __forceinline__ void store_f32(E *p, const float (&v)[V])
+template <typename E, int V> __device__ __forceinline__ void store_f32(E *p, const float *v)
 {
     Pack<E, V> q;
 #pragma unroll
@@ -51,30 +74,42 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Sum over the CTA (or the warp where WARP); `red` holds one float per warp and is
-// not written again before every thread has read it (each reduction has its own).
-template <bool WARP> __device__ __forceinline__ float group_sum(float v, float *red)
+// Sums over the CTA (or the warp where WARP) of N values at once, behind one barrier; `red` holds
+// a float per value and warp and is not written again before every thread has read it.
+template <int N, bool WARP> __device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[32])
 {
-    v = warp_sum(v);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = warp_sum(v[i]);
     if (WARP)
-        return v;
+        return;
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     if (lane == 0)
-        red[threadIdx.x >> 5] = v;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            red[i][threadIdx.x >> 5] = v[i];
     __syncthreads();
-    return warp_sum(lane < warps ? red[lane] : 0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = warp_sum(lane < warps ? red[i][lane] : 0.0f);
 }
 
-template <bool WARP> __device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t *red)
+template <int N, bool WARP> __device__ __forceinline__ void group_maxima(uint32_t (&v)[N], float (*red)[32])
 {
-    v = __reduce_max_sync(dev::FULL_MASK, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = __reduce_max_sync(dev::FULL_MASK, v[i]);
     if (WARP)
-        return v;
+        return;
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     if (lane == 0)
-        red[threadIdx.x >> 5] = v;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            red[i][threadIdx.x >> 5] = __uint_as_float(v[i]);
     __syncthreads();
-    return __reduce_max_sync(dev::FULL_MASK, lane < warps ? red[lane] : 0u);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = __reduce_max_sync(dev::FULL_MASK, lane < warps ? __float_as_uint(red[i][lane]) : 0u);
 }
 
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -98,107 +133,343 @@ __device__ __forceinline__ int8_t to_byte(float v, float inv, bool bad)
     return bad ? (int8_t)0 : (int8_t)__float2int_rn(__fmul_rn(v, inv));
 }
 
-__device__ __forceinline__ float reciprocal_deviation(float squares, int32_t width, float eps)
+// Packed f32 pairs: two columns in one instruction, each rounded as on its own.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 {
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(squares, (float)width), eps)));
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
-// One row's outputs of V columns starting at c.
-template <RowMode M, int V>
-__device__ __forceinline__ void normalise(const RowsParams &p, int32_t c, float mean, float rstd, float (&v)[V])
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 {
-    float g[V], b[V];
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t both(float v) { return dev::pack2(v, v); }
+
+__device__ __forceinline__ float halves_sum(uint64_t v)
+{
+    float a, b;
+    dev::unpack2(v, a, b);
+    return a + b;
+}
+
+// Column of element i of a thread's N: packs of V columns, `group` packs apart.
+template <int V> __device__ __forceinline__ int column(int t, int group, int i) { return (t + i / V * group) * V + i % V; }
+
+// V parameters of columns from c on (`dflt` where there are none).  Wide accesses give them 16
+// bytes at a time, which the host has checked: every lane's own 32 bytes one float at a time
+// would cost the L1 eight times the accesses.
+template <int V> __device__ __forceinline__ void load_params(const float *p, int64_t c, float dflt, float *v)
+{
+    if (!p) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        g[i] = p.gain ? __ldg(p.gain + c + i) : 1.0f;
-        b[i] = p.bias ? __ldg(p.bias + c + i) : 0.0f;
+        for (int i = 0; i < V; ++i)
+            v[i] = dflt;
+    } else if (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 q = __ldg(reinterpret_cast<const float4 *>(p + c + i));
+            v[i] = q.x;
+            v[i + 1] = q.y;
+            v[i + 2] = q.z;
+            v[i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = __ldg(p + c + i);
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        v[i] = (v[i] - mean) * rstd * g[i] + b[i];
 }
 
-template <typename E, RowMode M, int V, int EPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * ROW_WARP_ROWS : 1024) rows_kernel(const RowsParams p)
+// ---- the read-ahead ring of a CTA that walks over rows ---------------------------------
+// Rows are copied whole into a ring of shared memory, several ahead, by bulk copies; a row that
+// does not start or end on 16 bytes is copied with the bytes around it that share its 16-byte
+// blocks.  Blocks that reach past the first or the last row are not the caller's: such a row
+// (and every row where there is no ring) is read with plain loads.
+struct Ring {
+    uint32_t slots, bars;       // shared-memory addresses
+    uint32_t slot_bytes;
+    int stages;                 // 0: no ring
+    bool late;                  // a copy did not land in time: the rows from then on are NaN
+};
+
+template <typename E> struct RowSpan {
+    const char *from;           // 16-byte block of the row's start
+    uint32_t bytes, offset;     // of the blocks; of the row in them
+    bool inside;
+};
+
+template <typename E> __device__ __forceinline__ RowSpan<E> span_of(const void *base, int64_t stride, int64_t rows, int32_t width, int64_t row)
 {
-    constexpr int NV = EPT / V;
-    __shared__ float red[3][32];
+    const uintptr_t first = reinterpret_cast<uintptr_t>(base), start = first + (uintptr_t)(row * stride) * sizeof(E);
+    const uintptr_t end = start + (uintptr_t)width * sizeof(E);
+    const uintptr_t last = first + (uintptr_t)((rows - 1) * stride + width) * sizeof(E);
+    const uintptr_t lo = start & ~(uintptr_t)15, hi = (end + 15) & ~(uintptr_t)15;
+    RowSpan<E> s;
+    s.from = reinterpret_cast<const char *>(lo);
+    s.bytes = (uint32_t)(hi - lo);
+    s.offset = (uint32_t)(start - lo);
+    s.inside = lo >= first && hi <= last;
+    return s;
+}
+
+__device__ __forceinline__ Ring make_ring(const void *raw, int stages, uint32_t slot_bytes)
+{
+    Ring r;
+    r.slots = dev::smem_u32(raw);
+    r.slot_bytes = slot_bytes;
+    r.bars = r.slots + (uint32_t)stages * slot_bytes;
+    r.stages = stages;
+    r.late = false;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i)
+            dev::mbar_init(r.bars + 8 * i, 1);
+        dev::fence_barrier_init();
+    }
+    __syncthreads();
+    return r;
+}
+
+// By one thread: the copies into the slot at `to`, completing on `bar`, of a turn's R rows from `row` on, of one or two matrices (b: NULL for
+// one).  A slot is R rows of places of `place` bytes, one for each matrix.  Not inlined: its
+// 64-bit arithmetic, for one thread, would cost all of them registers.
+template <typename E, int R>
+__device__ __noinline__ void ring_fill(uint32_t bar, uint32_t to, uint32_t place, const void *a, int64_t a_stride, const void *b, int64_t b_stride,
+                                          int64_t rows, int32_t width, int64_t row, uint64_t policy)
+{
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (row + i < rows) {
+            const RowSpan<E> sa = span_of<E>(a, a_stride, rows, width, row + i);
+            bytes += sa.inside ? sa.bytes : 0;
+            if (b) {
+                const RowSpan<E> sb = span_of<E>(b, b_stride, rows, width, row + i);
+                bytes += sb.inside ? sb.bytes : 0;
+            }
+        }
+    dev::mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (row + i < rows) {
+            const RowSpan<E> sa = span_of<E>(a, a_stride, rows, width, row + i);
+            if (sa.inside)
+                dev::bulk_g2s(to, sa.from, sa.bytes, bar, policy);
+            to += place;
+            if (b) {
+                const RowSpan<E> sb = span_of<E>(b, b_stride, rows, width, row + i);
+                if (sb.inside)
+                    dev::bulk_g2s(to, sb.from, sb.bytes, bar, policy);
+                to += place;
+            }
+        }
+}
+
+// V elements of a row from column c on, from the ring's slot or from memory.
+template <typename E, int V> __device__ __forceinline__ void read_row(const Ring &r, uint32_t slot_at, const RowSpan<E> &s, const E *row, int64_t c, float *v)
+{
+    typedef typename Raw<sizeof(E) * V>::T Bits;
+    Bits raw;
+    if (r.stages && s.inside) {
+        const uint32_t at = slot_at + s.offset + (uint32_t)c * (uint32_t)sizeof(E);
+        if constexpr (sizeof(Bits) == 16) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(__cvta_shared_to_generic(at));
+            memcpy(&raw, &q, sizeof(raw));
+        } else {
+            raw = *reinterpret_cast<const Bits *>(__cvta_shared_to_generic(at));
+        }
+    } else {
+        raw = *reinterpret_cast<const Bits *>(row + c);
+    }
+    unpack_f32<E, V>(raw, v);
+}
+
+// R rows at a time in the registers of a CTA, which walks over the rows, or one row in a warp's
+// (WARP: several rows a CTA, no ring).  What bounds it beside the rows' bytes is instruction
+// issue: many columns a thread and two rows a turn spread a turn's reductions over more
+// elements, and pairs of columns share their arithmetic.  KEEP: the parameters stay in
+// registers; read again for each row they are, for 16-bit rows, four times the row's own bytes.
+template <typename E, RowMode M, int V, int EPT, int R, bool WARP, int THREADS, bool KEEP>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rows_kernel(const RowsParams p, int stages, uint32_t place)
+{
+    constexpr int NV = EPT / V, NP = KEEP && M != RowMode::Quantize ? EPT : V;
+    constexpr bool WHOLE = V * sizeof(E) == 16;             // rows of whole 16-byte blocks
+    extern __shared__ __align__(16) unsigned char raw_ring[];
+    __shared__ float red[2][3][R][32];
     const int group = WARP ? 32 : blockDim.x, t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    const int per_cta = WARP ? blockDim.x >> 5 : R;
+    const int64_t step = (int64_t)gridDim.x * per_cta;
+    int64_t row0 = (int64_t)blockIdx.x * per_cta + (WARP ? threadIdx.x >> 5 : 0);
+    Ring ring = {};
+    if (!WARP && stages)
+        ring = make_ring(raw_ring, stages, R * place);
     dev::follow_previous_kernel();
-    if (WARP && row >= p.rows)
-        return;
-    const E *x = static_cast<const E *>(p.x) + row * p.x_stride;
-    float v[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (t + j * group) * V;
-        if (c < p.width)
-            load_f32<E, V>(x + c, v[j]);
-        else
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[j][i] = 0.0f;
-    }
-    if (M != RowMode::Quantize) {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                s += v[j][i];
-        const float mean = __fdiv_rn(group_sum<WARP>(s, red[0]), (float)p.width);
-        s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if ((t + j * group) * V < p.width)
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    s = fmaf(v[j][i] - mean, v[j][i] - mean, s);
-        const float rstd = reciprocal_deviation(group_sum<WARP>(s, red[1]), p.width, p.eps);
-        if (M == RowMode::Norm && t == 0) {
-            if (p.mean)
-                p.mean[row] = mean;
-            if (p.rstd)
-                p.rstd[row] = rstd;
-        }
+    const uint64_t policy = dev::l2_evict_first_policy();
+    if (!WARP && threadIdx.x == 0)
+        for (int i = 0; i < stages && row0 + i * step < p.rows; ++i)
+            ring_fill<E, R>(ring.bars + 8 * i, ring.slots + (uint32_t)i * ring.slot_bytes, place, p.x, p.x_stride, nullptr, 0, p.rows, p.width,
+                            row0 + i * step, policy);
+    float gain[NP], bias[NP];
+    if (KEEP && M != RowMode::Quantize)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (t + j * group) * V;
             if (c < p.width) {
-                normalise<M, V>(p, c, mean, rstd, v[j]);
-                if (M == RowMode::Norm)
-                    store_f32<E, V>(static_cast<E *>(p.y) + row * p.y_stride + c, v[j]);
+                load_params<V>(p.gain, c, 1.0f, gain + (KEEP ? j * V : 0));
+                load_params<V>(p.bias, c, 0.0f, bias + (KEEP ? j * V : 0));
             }
         }
-    }
-    if (M != RowMode::Norm) {
-        uint32_t a = 0;
+    const float per_width = __fdiv_rn(1.0f, (float)p.width);
+    int slot = 0, turn = 0;
+    uint32_t parity = 0;
+    for (; row0 < p.rows; row0 += step, turn ^= 1) {
+        if (!WARP && stages && !ring.late)
+            ring.late = !dev::mbar_wait_bounded(ring.bars + 8 * slot, parity, 1000000000ull);
+        float v[R][EPT];
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if ((t + j * group) * V < p.width)
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = row0 + r;
+            const E *x = static_cast<const E *>(p.x) + row * p.x_stride;
+            RowSpan<E> span = {nullptr, 0, 0, true};
+            if (!WARP && stages && !WHOLE)
+                span = span_of<E>(p.x, p.x_stride, p.rows, p.width, row);
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    a = max(a, magnitude_bits(v[j][i]));
-        float scale;
-        bool bad;
-        const float inv = byte_factor(group_max<WARP>(a, reinterpret_cast<uint32_t *>(red[2])), scale, bad);
-        if (t == 0) {
-            p.scale[row] = scale;
-            if (bad)
-                dev::flag_error(p.error, LOOM_DEVERR_NONFINITE);
-        }
-        int8_t *q = p.q + row * p.width;
+            for (int j = 0; j < NV; ++j) {
+                const int c = (t + j * group) * V;
+                if (c < p.width && row < p.rows)
+                    read_row<E, V>(ring, ring.slots + (uint32_t)slot * ring.slot_bytes + r * place, span, x, c, v[r] + j * V);
+                else
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (t + j * group) * V;
-            if (c < p.width) {
-                Pack<int8_t, V> o;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    o.e[i] = to_byte(v[j][i], inv, bad);
-                *reinterpret_cast<Pack<int8_t, V> *>(q + c) = o;
+                    for (int i = 0; i < V; ++i)
+                        v[r][j * V + i] = 0.0f;
             }
+            if (!WARP && ring.late)
+#pragma unroll
+                for (int i = 0; i < EPT; ++i)
+                    v[r][i] = __uint_as_float(0x7fc00000u);
+        }
+        // the slot is free behind the first reduction's barrier: every thread has read it
+        auto refill = [&]() {
+            if (!WARP && stages) {
+                if (threadIdx.x == 0 && row0 + stages * step < p.rows && !ring.late)
+                    ring_fill<E, R>(ring.bars + 8 * slot, ring.slots + (uint32_t)slot * ring.slot_bytes, place, p.x, p.x_stride, nullptr, 0, p.rows,
+                                    p.width, row0 + stages * step, policy);
+                if (++slot == stages) {
+                    slot = 0;
+                    parity ^= 1u;
+                }
+            }
+        };
+        if (M != RowMode::Quantize) {
+            float mean[R], rstd[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                uint64_t s = 0;
+#pragma unroll
+                for (int i = 0; i < EPT; i += 2)
+                    s = dev::add2(s, dev::pack2(v[r][i], v[r][i + 1]));
+                mean[r] = halves_sum(s);
+            }
+            group_sums<R, WARP>(mean, red[turn][0]);
+            refill();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                mean[r] *= per_width;
+                const uint64_t m = both(mean[r]);
+                uint64_t s = 0;
+#pragma unroll
+                for (int i = 0; i < EPT; i += 2) {
+                    const uint64_t d = dev::sub2(dev::pack2(v[r][i], v[r][i + 1]), m);
+                    dev::unpack2(d, v[r][i], v[r][i + 1]);       // from here on: about the mean
+                    const bool in0 = column<V>(t, group, i) < p.width, in1 = column<V>(t, group, i + 1) < p.width;
+                    if (V > 1) {
+                        if (in0)                                 // packs are in or out as a whole
+                            s = fma2(d, d, s);
+                    } else {
+                        const uint64_t q = dev::pack2(in0 ? v[r][i] : 0.0f, in1 ? v[r][i + 1] : 0.0f);
+                        s = fma2(q, q, s);
+                    }
+                }
+                rstd[r] = halves_sum(s);
+            }
+            group_sums<R, WARP>(rstd, red[turn][1]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                rstd[r] = rsqrtf(fmaf(rstd[r], per_width, p.eps));
+                if (M == RowMode::Norm && t == 0 && row0 + r < p.rows) {
+                    if (p.mean)
+                        p.mean[row0 + r] = mean[r];
+                    if (p.rstd)
+                        p.rstd[row0 + r] = rstd[r];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (t + j * group) * V;
+                if (c < p.width) {
+                    if (!KEEP) {
+                        load_params<V>(p.gain, c, 1.0f, gain);
+                        load_params<V>(p.bias, c, 0.0f, bias);
+                    }
+                    const float *g = gain + (KEEP ? j * V : 0), *b = bias + (KEEP ? j * V : 0);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        float *o = v[r] + j * V;
+                        if constexpr (V == 1) {
+                            o[0] = fmaf(o[0] * rstd[r], g[0], b[0]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < V; i += 2)
+                                dev::unpack2(fma2(mul2(dev::pack2(o[i], o[i + 1]), both(rstd[r])), dev::pack2(g[i], g[i + 1]), dev::pack2(b[i], b[i + 1])),
+                                             o[i], o[i + 1]);
+                        }
+                        if (M == RowMode::Norm && row0 + r < p.rows)
+                            store_f32<E, V>(static_cast<E *>(p.y) + (row0 + r) * p.y_stride + c, o);
+                    }
+                }
+            }
+        }
+        if (M != RowMode::Norm) {
+            uint32_t a[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                a[r] = 0;
+#pragma unroll
+                for (int i = 0; i < EPT; ++i)
+                    if (column<V>(t, group, i) < p.width)
+                        a[r] = max(a[r], magnitude_bits(v[r][i]));
+            }
+            group_maxima<R, WARP>(a, red[turn][2]);
+            if (M == RowMode::Quantize)
+                refill();
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (row0 + r < p.rows) {
+                    float scale;
+                    bool bad;
+                    const float inv = byte_factor(a[r], scale, bad);
+                    if (t == 0) {
+                        p.scale[row0 + r] = scale;
+                        if (bad)
+                            dev::flag_error(p.error, LOOM_DEVERR_NONFINITE);
+                    }
+                    int8_t *q = p.q + (row0 + r) * p.width;
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        const int c = (t + j * group) * V;
+                        if (c < p.width) {
+                            Pack<int8_t, V> o;
+#pragma unroll
+                            for (int i = 0; i < V; ++i)
+                                o.e[i] = to_byte(v[r][j * V + i], inv, bad);
+                            *reinterpret_cast<Pack<int8_t, V> *>(q + c) = o;
+                        }
+                    }
+                }
         }
     }
 }
@@ -206,65 +477,72 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARP_ROWS : 1024) rows_kernel(
 // The same for rows of any length: each pass reads the row again.
 template <typename E, RowMode M, int V> __global__ void __launch_bounds__(1024) long_rows_kernel(const RowsParams p)
 {
-    __shared__ float red[3][32];
+    __shared__ float red[3][1][32];
     const int64_t row = blockIdx.x;
     dev::follow_previous_kernel();
     const E *x = static_cast<const E *>(p.x) + row * p.x_stride;
     const int32_t c0 = threadIdx.x * V, step = blockDim.x * V;
-    float mean = 0.0f, rstd = 1.0f, v[V];
+    const float per_width = __fdiv_rn(1.0f, (float)p.width);
+    float mean[1] = {0.0f}, rstd[1] = {0.0f}, v[V], gain[V], bias[V];
     if (M != RowMode::Quantize) {
-        float s = 0.0f;
         for (int64_t c = c0; c < p.width; c += step) {
             load_f32<E, V>(x + c, v);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                s += v[i];
+                mean[0] += v[i];
         }
-        mean = __fdiv_rn(group_sum<false>(s, red[0]), (float)p.width);
-        s = 0.0f;
+        group_sums<1, false>(mean, red[0]);
+        mean[0] *= per_width;
         for (int64_t c = c0; c < p.width; c += step) {
             load_f32<E, V>(x + c, v);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                s = fmaf(v[i] - mean, v[i] - mean, s);
+                rstd[0] = fmaf(v[i] - mean[0], v[i] - mean[0], rstd[0]);
         }
-        rstd = reciprocal_deviation(group_sum<false>(s, red[1]), p.width, p.eps);
+        group_sums<1, false>(rstd, red[1]);
+        rstd[0] = rsqrtf(fmaf(rstd[0], per_width, p.eps));
     }
+    auto output = [&](int64_t c) {      // the row's values, normalised where it asks for that
+        load_f32<E, V>(x + c, v);
+        if (M != RowMode::Quantize) {
+            load_params<V>(p.gain, c, 1.0f, gain);
+            load_params<V>(p.bias, c, 0.0f, bias);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                v[i] = fmaf((v[i] - mean[0]) * rstd[0], gain[i], bias[i]);
+        }
+    };
     if (M == RowMode::Norm) {
         if (threadIdx.x == 0) {
             if (p.mean)
-                p.mean[row] = mean;
+                p.mean[row] = mean[0];
             if (p.rstd)
-                p.rstd[row] = rstd;
+                p.rstd[row] = rstd[0];
         }
         for (int64_t c = c0; c < p.width; c += step) {
-            load_f32<E, V>(x + c, v);
-            normalise<M, V>(p, (int32_t)c, mean, rstd, v);
+            output(c);
             store_f32<E, V>(static_cast<E *>(p.y) + row * p.y_stride + c, v);
         }
         return;
     }
-    uint32_t a = 0;
+    uint32_t a[1] = {0};
     for (int64_t c = c0; c < p.width; c += step) {
-        load_f32<E, V>(x + c, v);
-        if (M == RowMode::NormI8)
-            normalise<M, V>(p, (int32_t)c, mean, rstd, v);
+        output(c);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            a = max(a, magnitude_bits(v[i]));
+            a[0] = max(a[0], magnitude_bits(v[i]));
     }
     float scale;
     bool bad;
-    const float inv = byte_factor(group_max<false>(a, reinterpret_cast<uint32_t *>(red[2])), scale, bad);
+    group_maxima<1, false>(a, red[2]);
+    const float inv = byte_factor(a[0], scale, bad);
     if (threadIdx.x == 0) {
         p.scale[row] = scale;
         if (bad)
             dev::flag_error(p.error, LOOM_DEVERR_NONFINITE);
     }
     for (int64_t c = c0; c < p.width; c += step) {
-        load_f32<E, V>(x + c, v);
-        if (M == RowMode::NormI8)
-            normalise<M, V>(p, (int32_t)c, mean, rstd, v);
+        output(c);
         Pack<int8_t, V> o;
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -273,18 +551,64 @@ template <typename E, RowMode M, int V> __global__ void __launch_bounds__(1024) 
     }
 }
 
-constexpr int EPT_SMALL = 16, EPT_LARGE = 32;
+// Elements per thread and row: 16, two rows a turn, while 256 threads hold a row (so that two CTAs
+// share an SM and one computes while the other waits); then 32, one row a turn, with up to 512
+// threads of 128 registers, and at last 1024.
+constexpr int ROW_EPT = 16, ROW_EPT_WIDE = 32;
+inline int rows_ept(int32_t width) { return width <= 256 * ROW_EPT ? ROW_EPT : ROW_EPT_WIDE; }
+
+// The ring of a CTA of which `per_sm` share an SM, with places of row_bytes (and the blocks around
+// an unaligned row) for `rows_a_turn` rows of `matrices`: enough stages to keep 112 KiB of an SM in
+// flight.  None where no CTA has a second turn.
+constexpr int64_t RING_BYTES_SM = 112 * 1024, RING_MAX_STAGES = 8;
+struct RingPlan {
+    int stages;
+    uint32_t place, smem_bytes;
+};
+RingPlan plan_ring(int64_t rows, int64_t grid, int64_t per_sm, int64_t row_bytes, int matrices, int rows_a_turn)
+{
+    RingPlan r = {0, 0, 0};
+    const int64_t place = (row_bytes + 30) / 16 * 16, slot = place * matrices * rows_a_turn;
+    int64_t stages = RING_BYTES_SM / (per_sm * slot);
+    const int64_t turns = (rows + grid * rows_a_turn - 1) / (grid > 0 ? grid * rows_a_turn : 1);
+    stages = stages < 2 ? 2 : stages > RING_MAX_STAGES ? RING_MAX_STAGES : stages;
+    stages = stages < turns ? stages : turns;
+    if (stages < 2 || per_sm * (stages * (slot + 8) + 3072) > 226 * 1024)
+        return r;
+    r.stages = (int)stages;
+    r.place = (uint32_t)place;
+    r.smem_bytes = (uint32_t)(stages * (slot + 8));
+    return r;
+}
+
+template <typename... K, typename P> cudaError_t launch_ring(void (*kernel)(K...), const loom_launch &L, const P &p, const RingPlan &r, std::atomic<uint64_t> &done,
+                                                             cudaStream_t stream)
+{
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), 0, done);
+    return e != cudaSuccess ? e : launch_prepared(kernel, L, stream, p, r.stages, r.place);
+}
+
+template <typename E, RowMode M, int V, int EPT, int R, bool WARP, int THREADS, bool KEEP>
+cudaError_t launch_rows_k(const RowsParams &p, loom_launch L, const RingPlan &r, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    L.smem_bytes = r.smem_bytes;
+    return launch_ring(rows_kernel<E, M, V, EPT, R, WARP, THREADS, KEEP>, L, p, r, done, stream);
+}
 
 template <typename E, RowMode M, int V>
 cudaError_t launch_rows_v(const RowsParams &p, const loom_launch &L, cudaStream_t stream)
 {
     if (L.kernel == LOOM_KERNEL_NORM_LONG)
         return launch_with(long_rows_kernel<E, M, V>, L, stream, p);
-    if (p.width <= 32 * EPT_SMALL)
-        return launch_with(rows_kernel<E, M, V, EPT_SMALL, true>, L, stream, p);
-    if (p.width <= 1024 * EPT_SMALL)
-        return launch_with(rows_kernel<E, M, V, EPT_SMALL, false>, L, stream, p);
-    return launch_with(rows_kernel<E, M, V, EPT_LARGE, false>, L, stream, p);
+    if (p.width <= 32 * ROW_EPT)
+        return launch_rows_k<E, M, V, ROW_EPT, 1, true, 32 * ROW_WARP_ROWS, false>(p, L, RingPlan{0, 0, 0}, stream);
+    const int ept = rows_ept(p.width);
+    const RingPlan r = plan_ring(p.rows, L.grid[0], rows_per_sm(L.block[0]), (int64_t)p.width * (int64_t)sizeof(E), 1, ept == ROW_EPT ? 2 : 1);
+    if (ept == ROW_EPT)
+        return launch_rows_k<E, M, V, ROW_EPT, 2, false, 256, true>(p, L, r, stream);
+    return p.width <= 512 * ROW_EPT_WIDE ? launch_rows_k<E, M, V, ROW_EPT_WIDE, 1, false, 512, true>(p, L, r, stream)
+                                         : launch_rows_k<E, M, V, ROW_EPT_WIDE, 1, false, 1024, false>(p, L, r, stream);
 }
 
 template <typename E, int V>
@@ -298,108 +622,162 @@ cudaError_t launch_rows_m(const RowsParams &p, RowMode mode, const loom_launch &
 }
 
 // ---- backward ------------------------------------------------------------------
-// Sums of two values over the CTA (or warp).
-template <bool WARP> __device__ __forceinline__ void group_sum2(float &a, float &b, float2 *red)
+// Rows of up to NG_MAX_WIDTH, R at a time: every thread keeps EPT columns of all the rows its CTA
+// takes.
+template <typename E, int V, int EPT, int R, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 512, 1) norm_grad_kernel(const NormGradParams p, int stages, uint32_t place)
 {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (WARP)
-        return;
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0)
-        red[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    const float2 r = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
-    a = warp_sum(r.x);
-    b = warp_sum(r.y);
-}
-
-template <typename E, int V, bool WARP> __global__ void __launch_bounds__(1024) norm_grad_kernel(const NormGradParams p)
-{
-    constexpr int NV = NG_EPT / V;
-    extern __shared__ float shared_sums[];          // WARP: [warps][2][width] at the end
-    __shared__ float2 red[2][32];
+    constexpr int NV = EPT / V;
+    constexpr bool WHOLE = V * sizeof(E) == 16;
+    extern __shared__ __align__(16) unsigned char raw_ring[];   // WARP: [warps][2][width] f32 at the end
+    __shared__ float red[2][2 * R][32];
     const int group = WARP ? 32 : blockDim.x, t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-    const int per_cta = WARP ? blockDim.x >> 5 : 1, mine = WARP ? threadIdx.x >> 5 : 0;
-    float dg[NV][V], db[NV][V], gain[NV][V];
+    const int warps = blockDim.x >> 5, mine = WARP ? threadIdx.x >> 5 : 0;
+    Ring ring = {};
+    if (!WARP && stages)
+        ring = make_ring(raw_ring, stages, 2 * R * place);
+    uint64_t dg[EPT / 2], db[EPT / 2], gain[EPT / 2];         // pairs of columns
     dev::follow_previous_kernel();
+    const int64_t step = (int64_t)gridDim.x * (WARP ? warps : R);
+    int64_t row0 = (int64_t)blockIdx.x * (WARP ? warps : R) + mine;
+    const uint64_t policy = dev::l2_evict_first_policy();
+    if (!WARP && threadIdx.x == 0)
+        for (int i = 0; i < stages && row0 + i * step < p.rows; ++i)
+            ring_fill<E, R>(ring.bars + 8 * i, ring.slots + (uint32_t)i * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride, p.rows, p.width, row0 + i * step, policy);
+    {
+        float g[EPT];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (t + j * group) * V + i;
-            dg[j][i] = db[j][i] = 0.0f;
-            gain[j][i] = c < p.width && p.gain ? __ldg(p.gain + c) : 1.0f;
-        }
-    int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * per_cta + mine; row < p.rows; row += (int64_t)gridDim.x * per_cta) {
-        const E *x = static_cast<const E *>(p.x) + row * p.x_stride;
-        const E *dy = static_cast<const E *>(p.dy) + row * p.dy_stride;
-        const float mean = p.mean[row], rstd = p.rstd[row];
-        float xh[NV][V], d[NV][V];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (t + j * group) * V;
-            if (c < p.width) {
-                load_f32<E, V>(x + c, xh[j]);
-                load_f32<E, V>(dy + c, d[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    xh[j][i] = mean;
-                    d[j][i] = 0.0f;
-                }
-            }
-        }
-        float s1 = 0.0f, s2 = 0.0f;
+        for (int i = 0; i < EPT; ++i)
+            g[i] = 1.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
+            if ((t + j * group) * V < p.width)
+                load_params<V>(p.gain, (t + j * group) * V, 1.0f, g + j * V);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                xh[j][i] = (xh[j][i] - mean) * rstd;
-                const float g = d[j][i] * gain[j][i];
-                s1 += g;
-                s2 = fmaf(g, xh[j][i], s2);
-                dg[j][i] = fmaf(d[j][i], xh[j][i], dg[j][i]);
-                db[j][i] += d[j][i];
+        for (int i = 0; i < EPT / 2; ++i) {
+            dg[i] = db[i] = 0;
+            gain[i] = dev::pack2(g[2 * i], g[2 * i + 1]);
+        }
+    }
+    // the rows' statistics, a turn ahead: a load of their own would stand at each turn's start
+    float next_mean[R], next_rstd[R];
+    auto stats = [&](int64_t first) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = first + r < p.rows;
+            next_mean[r] = in ? p.mean[first + r] : 0.0f;
+            next_rstd[r] = in ? p.rstd[first + r] : 0.0f;
+        }
+    };
+    stats(row0);
+    const float per_width = __fdiv_rn(1.0f, (float)p.width);
+    int slot = 0, turn = 0;
+    uint32_t parity = 0;
+    for (; row0 < p.rows; row0 += step, turn ^= 1) {
+        float rstd[R], sums[2 * R];
+        uint64_t xh[R][EPT / 2], g[R][EPT / 2];               // xhat and dy * gain
+        float mean[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = next_mean[r];
+            rstd[r] = next_rstd[r];
+        }
+        stats(row0 + step);
+        if (!WARP && stages && !ring.late)
+            ring.late = !dev::mbar_wait_bounded(ring.bars + 8 * slot, parity, 1000000000ull);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = row0 + r;
+            const E *x = static_cast<const E *>(p.x) + row * p.x_stride;
+            const E *dy = static_cast<const E *>(p.dy) + row * p.dy_stride;
+            RowSpan<E> span_x = {nullptr, 0, 0, true}, span_dy = span_x;
+            if (!WARP && stages && !WHOLE) {
+                span_x = span_of<E>(p.x, p.x_stride, p.rows, p.width, row);
+                span_dy = span_of<E>(p.dy, p.dy_stride, p.rows, p.width, row);
             }
-        if (p.dx) {
-            group_sum2<WARP>(s1, s2, red[turn]);
-            turn ^= 1;
-            s1 = __fdiv_rn(s1, (float)p.width);
-            s2 = __fdiv_rn(s2, (float)p.width);
-            E *dx = static_cast<E *>(p.dx) + row * p.dx_stride;
+            const uint32_t at = ring.slots + (uint32_t)slot * ring.slot_bytes + 2 * r * place;
+            float xv[EPT], d[EPT];
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = (t + j * group) * V;
-                if (c < p.width) {
+                if (c < p.width && row < p.rows) {
+                    read_row<E, V>(ring, at, span_x, x, c, xv + j * V);
+                    read_row<E, V>(ring, at + place, span_dy, dy, c, d + j * V);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        d[j][i] = rstd * (d[j][i] * gain[j][i] - s1 - xh[j][i] * s2);
-                    store_f32<E, V>(dx + c, d[j]);
+                    for (int i = 0; i < V; ++i) {
+                        xv[j * V + i] = mean[r];
+                        d[j * V + i] = 0.0f;
+                    }
                 }
             }
+            if (!WARP && ring.late)
+#pragma unroll
+                for (int i = 0; i < EPT; ++i)
+                    d[i] = __uint_as_float(0x7fc00000u);
+            const uint64_t m = both(mean[r]), rs = both(rstd[r]);
+            uint64_t s1 = 0, s2 = 0;
+#pragma unroll
+            for (int i = 0; i < EPT / 2; ++i) {
+                const uint64_t dy2 = dev::pack2(d[2 * i], d[2 * i + 1]);
+                xh[r][i] = mul2(dev::sub2(dev::pack2(xv[2 * i], xv[2 * i + 1]), m), rs);
+                g[r][i] = mul2(dy2, gain[i]);
+                s1 = dev::add2(s1, g[r][i]);
+                s2 = fma2(g[r][i], xh[r][i], s2);
+                dg[i] = fma2(dy2, xh[r][i], dg[i]);
+                db[i] = dev::add2(db[i], dy2);
+            }
+            sums[2 * r] = halves_sum(s1);
+            sums[2 * r + 1] = halves_sum(s2);
         }
+        if (p.dx || (!WARP && stages))
+            group_sums<2 * R, WARP>(sums, red[turn]);      // behind its barrier the slot is free: every thread has read it
+        if (!WARP && stages) {
+            if (threadIdx.x == 0 && row0 + stages * step < p.rows && !ring.late)
+                ring_fill<E, R>(ring.bars + 8 * slot, ring.slots + (uint32_t)slot * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride, p.rows, p.width, row0 + stages * step, policy);
+            if (++slot == stages) {
+                slot = 0;
+                parity ^= 1u;
+            }
+        }
+        if (p.dx)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (row0 + r < p.rows) {
+                    // dx = rstd (g - mean(g) - xhat mean(g xhat))
+                    const uint64_t a = both(-(sums[2 * r] * per_width)), b = both(-(sums[2 * r + 1] * per_width)), rs = both(rstd[r]);
+                    E *dx = static_cast<E *>(p.dx) + (row0 + r) * p.dx_stride;
+                    float o[EPT];
+#pragma unroll
+                    for (int i = 0; i < EPT / 2; ++i)
+                        dev::unpack2(mul2(fma2(xh[r][i], b, dev::add2(g[r][i], a)), rs), o[2 * i], o[2 * i + 1]);
+#pragma unroll
+                    for (int j = 0; j < NV; ++j)
+                        if ((t + j * group) * V < p.width)
+                            store_f32<E, V>(dx + (t + j * group) * V, o + j * V);
+                }
     }
     if (!p.partial)
         return;
     float *out = p.partial + (int64_t)blockIdx.x * 2 * p.width;
+    float *shared_sums = reinterpret_cast<float *>(raw_ring);
     float *mine_out = WARP ? shared_sums + (int64_t)mine * 2 * p.width : out;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (t + j * group) * V + i;
-            if (c < p.width) {
-                mine_out[c] = dg[j][i];
-                mine_out[p.width + c] = db[j][i];
-            }
+    for (int i = 0; i < EPT; ++i) {
+        const int c = column<V>(t, group, i);
+        float g[2], b[2];
+        dev::unpack2(dg[i / 2], g[0], g[1]);
+        dev::unpack2(db[i / 2], b[0], b[1]);
+        if (c < p.width) {
+            mine_out[c] = g[i % 2];
+            mine_out[p.width + c] = b[i % 2];
         }
+    }
     if (WARP) {
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * p.width; i += blockDim.x) {
             float s = 0.0f;
-            for (int w = 0; w < per_cta; ++w)
+            for (int w = 0; w < warps; ++w)
                 s += shared_sums[w * 2 * p.width + i];
             out[i] = s;
         }
@@ -409,27 +787,29 @@ template <typename E, int V, bool WARP> __global__ void __launch_bounds__(1024) 
 // Rows wider than the registers of a CTA: the two sums of each row ...
 template <typename E, int V> __global__ void __launch_bounds__(1024) long_norm_sums_kernel(const NormGradParams p)
 {
-    __shared__ float2 red[32];
+    __shared__ float red[2][32];
     const int64_t row = blockIdx.x;
     dev::follow_previous_kernel();
     const E *x = static_cast<const E *>(p.x) + row * p.x_stride;
     const E *dy = static_cast<const E *>(p.dy) + row * p.dy_stride;
     const float mean = p.mean[row], rstd = p.rstd[row];
-    float s1 = 0.0f, s2 = 0.0f, xv[V], d[V];
+    float sums[2] = {0.0f, 0.0f}, xv[V], d[V];
     for (int64_t c = threadIdx.x * V; c < p.width; c += blockDim.x * V) {
+        float gain[V];
+        load_params<V>(p.gain, c, 1.0f, gain);
         load_f32<E, V>(x + c, xv);
         load_f32<E, V>(dy + c, d);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float g = d[i] * (p.gain ? __ldg(p.gain + c + i) : 1.0f);
-            s1 += g;
-            s2 = fmaf(g, (xv[i] - mean) * rstd, s2);
+            const float g = d[i] * gain[i];
+            sums[0] += g;
+            sums[1] = fmaf(g, (xv[i] - mean) * rstd, sums[1]);
         }
     }
-    group_sum2<false>(s1, s2, red);
+    group_sums<2, false>(sums, red);
     if (threadIdx.x == 0) {
-        p.row_sums[2 * row] = __fdiv_rn(s1, (float)p.width);
-        p.row_sums[2 * row + 1] = __fdiv_rn(s2, (float)p.width);
+        p.row_sums[2 * row] = __fdiv_rn(sums[0], (float)p.width);
+        p.row_sums[2 * row + 1] = __fdiv_rn(sums[1], (float)p.width);
     }
 }
 
@@ -443,11 +823,10 @@ __global__ void __launch_bounds__(NG_LONG_THREADS) long_norm_grad_kernel(const N
     if (c >= p.width)
         return;
     float dg[V], db[V], gain[V];
+    load_params<V>(p.gain, c, 1.0f, gain);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V; ++i)
         dg[i] = db[i] = 0.0f;
-        gain[i] = p.gain ? __ldg(p.gain + c + i) : 1.0f;
-    }
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const float mean = p.mean[row], rstd = p.rstd[row];
         float xv[V], d[V];
@@ -501,13 +880,25 @@ __global__ void __launch_bounds__(NG_SUM_COLS *NG_SUM_GROUPS)
     }
 }
 
+template <typename E, int V, int EPT, int R, bool WARP>
+cudaError_t launch_norm_grad_k(const NormGradParams &p, loom_launch L, const RingPlan &r, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    L.smem_bytes = r.smem_bytes;
+    return launch_ring(norm_grad_kernel<E, V, EPT, R, WARP>, L, p, r, done, stream);
+}
+
 template <typename E, int V>
 cudaError_t launch_norm_grad_v(const NormGradParams &p, const loom_launch &L, cudaStream_t stream)
 {
     if (p.width <= 32 * NG_EPT)
-        return launch_with(norm_grad_kernel<E, V, true>, L, stream, p);
-    if (p.width <= NG_MAX_WIDTH)
-        return launch_with(norm_grad_kernel<E, V, false>, L, stream, p);
+        return launch_norm_grad_k<E, V, NG_EPT, 1, true>(p, L, RingPlan{0, 0, L.smem_bytes}, stream);
+    if (p.width <= NG_MAX_WIDTH) {
+        const bool two = p.width <= 256 * NG_EPT;
+        const RingPlan r = plan_ring(p.rows, L.grid[0], rows_per_sm(L.block[0]), (int64_t)p.width * (int64_t)sizeof(E), 2, two ? 2 : 1);
+        return two ? launch_norm_grad_k<E, V, NG_EPT, 2, false>(p, L, r, stream)
+                   : launch_norm_grad_k<E, V, 2 * NG_EPT, 1, false>(p, L, r, stream);
+    }
     if (p.dx) {
         loom_launch S = L;
         S.grid[0] = (uint32_t)p.rows;
@@ -540,7 +931,7 @@ int row_vec(int32_t dtype, int32_t width, const void *const *pointers, const int
     return 1;
 }
 
-bool rows_geometry(int64_t rows, int32_t width, loom_launch *out)
+bool rows_geometry(int64_t rows, int32_t width, int64_t sms, loom_launch *out)
 {
     *out = loom_launch{};
     out->grid[1] = out->grid[2] = out->block[1] = out->block[2] = 1;
@@ -549,13 +940,17 @@ bool rows_geometry(int64_t rows, int32_t width, loom_launch *out)
     out->kernel = LOOM_KERNEL_NORM_ROWS;
     out->units_per_cta = 1;
     int64_t threads, grid = rows;
-    if (width <= 32 * EPT_SMALL) {
+    if (width <= 32 * ROW_EPT) {
         threads = 32 * ROW_WARP_ROWS;
         out->units_per_cta = ROW_WARP_ROWS;
         grid = (rows + ROW_WARP_ROWS - 1) / ROW_WARP_ROWS;
-    } else if (width <= 1024 * EPT_LARGE) {
-        const int ept = width <= 1024 * EPT_SMALL ? EPT_SMALL : EPT_LARGE;
+    } else if (width <= 1024 * 32) {
+        const int ept = rows_ept(width);
         threads = ((int64_t)width + 32 * ept - 1) / (32 * ept) * 32;
+        out->units_per_cta = ept == ROW_EPT ? 2 : 1;         // at a time
+        const int64_t most = sms * rows_per_sm(threads);
+        grid = (rows + out->units_per_cta - 1) / out->units_per_cta;
+        grid = grid < most ? grid : most;
     } else {
         threads = 1024;
         out->kernel = LOOM_KERNEL_NORM_LONG;
@@ -594,17 +989,18 @@ bool norm_grad_geometry(int64_t rows, int32_t width, int64_t sms, loom_launch *o
         threads = 256;
         per_sm = 4;
         out->units_per_cta = 8;
-        grid = (rows + 7) / 8;
         out->smem_bytes = (uint32_t)(8 * 2 * width * 4);
     } else if (width <= NG_MAX_WIDTH) {
-        threads = ((int64_t)width + 32 * NG_EPT - 1) / (32 * NG_EPT) * 32;
-        per_sm = threads >= 512 ? 1024 / threads : threads >= 256 ? 4 : 8;
-        per_sm = per_sm < 1 ? 1 : per_sm;
+        const int64_t ept = width <= 256 * NG_EPT ? NG_EPT : 2 * NG_EPT;
+        threads = ((int64_t)width + 32 * ept - 1) / (32 * ept) * 32;
+        per_sm = rows_per_sm(threads);
+        out->units_per_cta = ept == NG_EPT ? 2 : 1;          // rows at a time
     } else {
         threads = NG_LONG_THREADS;
         per_sm = 1;
     }
     const int64_t most = per_sm * sms;
+    grid = (rows + out->units_per_cta - 1) / out->units_per_cta;
     grid = grid < most ? grid : most;
     out->grid[0] = (uint32_t)grid;
     out->block[0] = (uint32_t)threads;

@@ -545,7 +545,8 @@ template <typename E> cudaError_t launch_e(const SampleParams &p, const loom_lau
     const int ranks = (int)L.cluster[0];
     const int slice = ((p.vocab + ranks - 1) / ranks + 15) / 16 * 16;
     const int seg = ((slice + SM_SEGMENTS - 1) / SM_SEGMENTS + 31) / 32 * 32;
-    cudaError_t e = cudaFuncSetAttribute(sample_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.smem_bytes);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(sample_kernel<E>), 0, done);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

@@ -108,13 +108,16 @@ def test_binding_refusals(loom):
 def test_launch_geometry(loom):
     cfg = loom.loom_token_launch_config
     for rows, width in ((1, 1), (5, 512), (5, 513), (7, 16384), (7, 16385), (2, 32768), (2, 32769)):
-        L = cfg(loom.LOOM_OP_LAYER_NORM, [rows, width, loom.LOOM_BF16])
+        L = cfg(loom.LOOM_OP_LAYER_NORM, [rows, width, loom.LOOM_BF16, 1, SMS])
         assert L["grid"][0] == -(-rows // L["units_per_cta"]) and 32 <= L["block"][0] <= 1024
         assert L["kernel"] == (loom.LOOM_KERNEL_NORM_LONG if width > 32768 else loom.LOOM_KERNEL_NORM_ROWS)
-        # the threads of a row hold all of it
-        if L["kernel"] == loom.LOOM_KERNEL_NORM_ROWS:
-            threads = L["block"][0] // L["units_per_cta"]
-            assert threads * (16 if width <= 16384 else 32) >= width
+        # the threads of a row hold all of it: 16 columns each, from 4097 columns on 32
+        if width <= 512:
+            assert L["block"][0] == 32 * L["units_per_cta"]
+        elif width <= 32768:
+            assert L["block"][0] * (16 if width <= 4096 else 32) >= width
+    L = cfg(loom.LOOM_OP_LAYER_NORM, [10 ** 6, 8192, loom.LOOM_BF16, 1, SMS])
+    assert L["grid"][0] == 2 * SMS and L["block"][0] == 256          # CTAs that walk over the rows
     for rows, width in ((1, 1), (100000, 64), (3, 8192), (3, 8193), (100000, 20000)):
         L = cfg(loom.LOOM_OP_LAYER_NORM_BACKWARD, [rows, width, loom.LOOM_F32, 1, SMS])
         assert 1 <= L["grid"][0] <= rows and L["block"][0] <= 1024
