@@ -104,7 +104,7 @@ struct SampleParams {
     float *logprob;
     int32_t *error;
 };
-bool sample_geometry(int64_t rows, int32_t vocab, int32_t dtype, int64_t sms, loom_launch *out);
+bool sample_geometry(int64_t rows, int32_t vocab, int64_t sms, loom_launch *out);
 cudaError_t launch_sample(const SampleParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream);
 
 }  // namespace loom

@@ -184,7 +184,13 @@ extern "C" loom_status loom_token_launch_config(int32_t op, const int64_t *w, in
             return LOOM_ERR_ARG;
         if (w[0] < 0 || w[0] > MAX_INT || w[1] < 1 || w[1] > MAX_INT)
             return LOOM_ERR_SHAPE;
-        return sample_geometry(w[0], (int32_t)w[1], (int32_t)w[2], opt(3, 0), out) ? LOOM_OK : LOOM_ERR_SHAPE;
+        if (!sample_geometry(w[0], (int32_t)w[1], 1, out))
+            return LOOM_ERR_SHAPE;
+        int64_t sms = opt(3, 0);
+        const loom_status counted = sms ? LOOM_OK : sm_count(&sms);
+        if (counted != LOOM_OK)
+            return counted;
+        return sample_geometry(w[0], (int32_t)w[1], sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
     }
     default: return LOOM_ERR_ARG;
     }
@@ -376,7 +382,7 @@ extern "C" loom_status loom_sample_tokens(const void *d_logits, int32_t dtype, i
 {
     loom_launch L;
     if (rows < 0 || rows > MAX_INT || vocab < 1 || short_stride(rows, stride, vocab) ||
-        !sample_geometry(rows, vocab, dtype, 0, &L))
+        !sample_geometry(rows, vocab, 1, &L))
         return LOOM_ERR_SHAPE;
     if (!known(dtype) || (!d_temperature && !(temperature >= 0.0f)) || (!d_top_p && !(top_p >= 0.0f)) ||
         (!d_min_p && !(min_p >= 0.0f)))
@@ -389,6 +395,11 @@ extern "C" loom_status loom_sample_tokens(const void *d_logits, int32_t dtype, i
         misaligned(d_top_p, 4) || misaligned(d_min_p, 4) || misaligned(d_uniform, 4) || misaligned(d_token, 4) ||
         misaligned(d_logprob, 4) || misaligned(d_error, 4))
         return LOOM_ERR_ALIGN;
+    int64_t sms = 0;
+    const loom_status counted = sm_count(&sms);
+    if (counted != LOOM_OK)
+        return counted;
+    sample_geometry(rows, vocab, sms, &L);
     SampleParams p = {};
     p.logits = d_logits;
     p.rows = rows;

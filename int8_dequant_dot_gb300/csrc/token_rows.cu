@@ -853,9 +853,10 @@ __global__ void __launch_bounds__(NG_LONG_THREADS) long_norm_grad_kernel(const N
     }
 }
 
-// Partial column sums [parts][2 width] -> dgain, dbias: 32 columns per CTA, eight
-// threads per column over interleaved parts, added in a fixed order.
-constexpr int NG_SUM_COLS = 32, NG_SUM_GROUPS = 8;
+// Partial column sums [parts][2 width] -> dgain, dbias: 32 columns per CTA, 32 threads per
+// column over interleaved parts (the latency of a thread's chain of loads is what this takes),
+// added in a fixed order.
+constexpr int NG_SUM_COLS = 32, NG_SUM_GROUPS = 32;
 __global__ void __launch_bounds__(NG_SUM_COLS *NG_SUM_GROUPS)
     norm_grad_columns_kernel(const float *partial, int64_t parts, int32_t width, float *dgain, float *dbias)
 {
@@ -871,7 +872,7 @@ __global__ void __launch_bounds__(NG_SUM_COLS *NG_SUM_GROUPS)
     part[group][col] = s;
     __syncthreads();
     if (group == 0 && c < 2 * (int64_t)width) {
-#pragma unroll
+#pragma unroll 8
         for (int g = 1; g < NG_SUM_GROUPS; ++g)
             s += part[g][col];
         float *out = c < width ? dgain : dbias;

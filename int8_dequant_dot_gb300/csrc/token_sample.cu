@@ -8,18 +8,19 @@
 //
 // Design
 //  * A row is read once: a cluster of 1 to 8 CTAs holds it in shared memory as
-//    f32 (slices of up to 49152 logits), and every later pass runs on chip.
-//  * No sort.  The k-th logit, and the one where the running weight reaches
-//    top_p of the total, are found by histogram: first over 2048 equal bins of
-//    (m - l) / T, which spread the bulk of a row over many bins (counts and
-//    weights, so one histogram serves both searches), then over the bit patterns
-//    of the logits in the bin that holds the boundary, 2048 at a time, until one
-//    pattern is left.  Logits whose weight is 0 cannot be chosen and take no part.
-//  * Equal logits at the boundary: the number of them that stays follows from the
-//    sums alone; the first ones in index order are kept, by a running count over
-//    segments of the row.
-//  * The draw: kept weight per segment (a warp each), a scan over segments and
-//    CTAs, and one warp walks the segment that holds floor(u total).
+//    f32 (slices of up to 49152 logits), and every later pass runs on chip.  What
+//    bounds a row is the chain of passes and cluster barriers, so both are few.
+//  * No sort.  A histogram over 2048 equal bins of (m - l) / T, which spread the
+//    bulk of a row over many bins, finds the bin in which top-k's count or top-p's
+//    weight is reached.  Logits whose weight is 0 cannot be chosen and take no part.
+//  * Where top-k leaves few logits (with those of its last bin at most 512), they are
+//    gathered in one CTA, which ranks them against each other and does the rest.
+//  * Otherwise the boundary's logit is found by histograms over the bit patterns in
+//    the boundary's bin, 2048 at a time, until one pattern is left.  Equal logits there:
+//    the number that stays follows from the sums alone, and the first ones in index
+//    order stay, by a running count over segments of the row.  The draw then sums the
+//    kept weight per segment (a warp each), scans over segments and CTAs, and one warp
+//    walks the segment that holds floor(u total).
 //  * A weight is added to a bin as two 32-bit halves (its upper and lower 16 bits:
 //    no slice can overflow them), which shared memory adds natively.
 #include "token_ops.cuh"
@@ -32,9 +33,13 @@ constexpr int SM_BINS = 2048;
 constexpr int SM_MAX_CLUSTER = 8;
 constexpr int SM_MAX_SLICE = 49152;        // logits of a CTA: 192 KiB
 constexpr int SM_SLICE = 16384;            // slices up to this leave room for a second CTA on the SM
+constexpr int SM_SHORT_SLICE = 2048;       // not worth another CTA
 constexpr int SM_SEGMENTS = 128;           // segments of a slice
+constexpr int SM_LIST = SM_THREADS;        // logits that one CTA ranks, one a thread
 constexpr uint32_t SM_FULL = 1u << 31;     // the weight of the largest logit
-constexpr float SM_BIN_SCALE = 95.0f;      // bins per unit of (m - l) / T: 2^-31 lies in bin 2041
+constexpr float SM_BIN_SCALE = 95.0f;      // bins per unit of (m - l) / T: weights are above 0 in
+                                           // bins below SM_EDGE_BIN and 0 above it
+constexpr uint32_t SM_EDGE_BIN = 2041;     // 21.4842 .. 21.4948; 2^-31 is at 21.4876
 constexpr uint32_t SM_KEY_NONE = 0x007fffffu;   // key of -infinity
 
 // Bit pattern of a logit whose whole-number order is the logits' order.
@@ -96,19 +101,20 @@ struct Found {            // where a search ended: what lies above bin `bin`
     uint32_t count_above, bin;
 };
 
+// What the CTAs of a cluster tell each other has two places, used in turn: one barrier then
+// parts the writing of a place from its next writing.
 struct Shared {
     uint32_t count[SM_BINS], low[SM_BINS], high[SM_BINS];
-    uint64_t share_mass[SM_MAX_CLUSTER];     // per CTA of the cluster
-    uint32_t share_count[SM_MAX_CLUSTER];
-    uint32_t key_max[SM_MAX_CLUSTER], key_min[SM_MAX_CLUSTER];
-    uint32_t first[SM_MAX_CLUSTER];
-    uint32_t ties[SM_MAX_CLUSTER];
-    uint64_t mass[SM_MAX_CLUSTER];
-    Found found;
+    uint64_t share_mass[2][SM_MAX_CLUSTER];     // per CTA of the cluster
+    uint32_t share_count[2][SM_MAX_CLUSTER];
+    uint32_t key_max[2][SM_MAX_CLUSTER], key_min[2][SM_MAX_CLUSTER];
+    Found found[2];
     uint64_t warp_mass[SM_WARPS];
     uint32_t warp_count[SM_WARPS], warp_a[SM_WARPS], warp_b[SM_WARPS];
     uint64_t seg_mass[SM_SEGMENTS];
     uint32_t seg_ties[SM_SEGMENTS];
+    uint32_t list_n;                            // gathered logits of this CTA
+    uint32_t list_key[SM_LIST], list_at[SM_LIST], list_w[SM_LIST];
 };
 
 struct Row {              // what the threads of a cluster agree on
@@ -117,6 +123,7 @@ struct Row {              // what the threads of a cluster agree on
     int n, slice, seg;    // logits of this CTA, of a full slice, of a segment
     uint32_t rank, ranks;
     float m, inv;
+    uint32_t turn;        // which places are used next
 };
 
 __device__ __forceinline__ void agree(const Row &r)
@@ -128,9 +135,11 @@ __device__ __forceinline__ void agree(const Row &r)
 }
 
 // Largest a and smallest b over the cluster.
-__device__ __forceinline__ void cluster_max_min(const Row &r, uint32_t &a, uint32_t &b)
+__device__ __forceinline__ void cluster_max_min(Row &r, uint32_t &a, uint32_t &b)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t turn = r.turn;
+    r.turn ^= 1u;
     a = __reduce_max_sync(dev::FULL_MASK, a);
     b = __reduce_min_sync(dev::FULL_MASK, b);
     if (lane == 0) {
@@ -141,17 +150,16 @@ __device__ __forceinline__ void cluster_max_min(const Row &r, uint32_t &a, uint3
     a = __reduce_max_sync(dev::FULL_MASK, lane < SM_WARPS ? r.s->warp_a[lane] : 0u);
     b = __reduce_min_sync(dev::FULL_MASK, lane < SM_WARPS ? r.s->warp_b[lane] : 0xffffffffu);
     if (threadIdx.x < r.ranks) {
-        store_remote(&r.s->key_max[r.rank], threadIdx.x, a);
-        store_remote(&r.s->key_min[r.rank], threadIdx.x, b);
+        store_remote(&r.s->key_max[turn][r.rank], threadIdx.x, a);
+        store_remote(&r.s->key_min[turn][r.rank], threadIdx.x, b);
     }
     agree(r);
     a = 0;
     b = 0xffffffffu;
     for (uint32_t q = 0; q < r.ranks; ++q) {
-        a = max(a, r.s->key_max[q]);
-        b = min(b, r.s->key_min[q]);
+        a = max(a, r.s->key_max[turn][q]);
+        b = min(b, r.s->key_min[turn][q]);
     }
-    agree(r);   // before the slots are written again
 }
 
 __device__ __forceinline__ void clear_bins(const Row &r)
@@ -193,27 +201,56 @@ __device__ __forceinline__ void scan(const Row &r, uint64_t &mass, uint32_t &cou
     __syncthreads();
 }
 
+// This CTA's mass and count to every CTA, and all of theirs: those of lower ranks, and in all.
+struct Shares {
+    uint64_t mass_below, mass;
+    uint32_t count_below, count;
+};
+__device__ __forceinline__ Shares share(Row &r, uint64_t mass, uint32_t count)   // values of the last thread
+{
+    const uint32_t turn = r.turn;
+    r.turn ^= 1u;
+    if (threadIdx.x == SM_THREADS - 1)
+        for (uint32_t q = 0; q < r.ranks; ++q) {
+            store_remote(&r.s->share_mass[turn][r.rank], q, mass);
+            store_remote(&r.s->share_count[turn][r.rank], q, count);
+        }
+    agree(r);
+    Shares t = {0, 0, 0, 0};
+    for (uint32_t q = 0; q < r.ranks; ++q) {
+        if (q < r.rank) {
+            t.mass_below += r.s->share_mass[turn][q];
+            t.count_below += r.s->share_count[turn][q];
+        }
+        t.mass += r.s->share_mass[turn][q];
+        t.count += r.s->share_count[turn][q];
+    }
+    return t;
+}
+
 // The bin in which the running count (or mass) from bin 0 up reaches `target`,
 // given that `start` lies above bin 0; bins of all CTAs together.  Each CTA adds up
-// its share of the bins.  Ends agreed: every CTA may clear its bins.
-__device__ Found search(const Row &r, bool by_mass, uint64_t target, Found start)
+// its share of the bins.  `all`: what the bins hold.  Where the target is not reached the
+// bin is SM_BINS.  Afterwards every CTA may clear its bins.
+template <bool BY_MASS> __device__ Found search(Row &r, uint64_t target, Found start, Shares *all = nullptr)
 {
     Shared *s = r.s;
     agree(r);   // every histogram is complete
     constexpr int MOST = SM_BINS / SM_THREADS;      // bins per thread with one CTA
-    const int share = SM_BINS / (int)r.ranks;
-    const int per = share >= SM_THREADS ? share / SM_THREADS : 1;
-    const int bin0 = (int)r.rank * share + (int)threadIdx.x * per;
+    const int bins = SM_BINS / (int)r.ranks;
+    const int per = bins >= SM_THREADS ? bins / SM_THREADS : 1;
+    const int bin0 = (int)r.rank * bins + (int)threadIdx.x * per;
     uint64_t m[MOST], mass = 0;
     uint32_t c[MOST], count = 0;
 #pragma unroll
     for (int j = 0; j < MOST; ++j) {
         m[j] = 0;
         c[j] = 0;
-        if (j < per && (int)threadIdx.x * per + j < share)
+        if (j < per && (int)threadIdx.x * per + j < bins)
             for (uint32_t q = 0; q < r.ranks; ++q) {
                 c[j] += load_remote(&s->count[bin0 + j], q);
-                m[j] += load_remote(&s->low[bin0 + j], q) + ((uint64_t)load_remote(&s->high[bin0 + j], q) << 16);
+                if (BY_MASS)
+                    m[j] += load_remote(&s->low[bin0 + j], q) + ((uint64_t)load_remote(&s->high[bin0 + j], q) << 16);
             }
         mass += m[j];
         count += c[j];
@@ -221,53 +258,56 @@ __device__ Found search(const Row &r, bool by_mass, uint64_t target, Found start
     const uint64_t own_mass = mass;
     const uint32_t own_count = count;
     scan(r, mass, count);
-    if (threadIdx.x == SM_THREADS - 1)
-        for (uint32_t q = 0; q < r.ranks; ++q) {
-            store_remote(&s->share_mass[r.rank], q, mass);
-            store_remote(&s->share_count[r.rank], q, count);
-        }
-    agree(r);
-    uint64_t above_mass = start.mass_above + mass - own_mass;
-    uint32_t above_count = start.count_above + count - own_count;
-    for (uint32_t q = 0; q < r.rank; ++q) {
-        above_mass += s->share_mass[q];
-        above_count += s->share_count[q];
-    }
+    const uint32_t turn = r.turn;
+    if (threadIdx.x == 0)
+        s->found[turn].bin = SM_BINS;               // (the owner writes after the next barrier)
+    const Shares t = share(r, mass, count);
+    if (all)
+        *all = t;
+    uint64_t above_mass = start.mass_above + t.mass_below + mass - own_mass;
+    uint32_t above_count = start.count_above + t.count_below + count - own_count;
 #pragma unroll
     for (int j = 0; j < MOST; ++j) {
-        const uint64_t before = by_mass ? above_mass : above_count, has = by_mass ? m[j] : c[j];
+        const uint64_t before = BY_MASS ? above_mass : above_count, has = BY_MASS ? m[j] : c[j];
         if (before < target && target <= before + has)
             for (uint32_t q = 0; q < r.ranks; ++q) {
-                store_remote(&s->found.mass_above, q, above_mass);
-                store_remote(&s->found.count_above, q, above_count);
-                store_remote(&s->found.bin, q, (uint32_t)(bin0 + j));
+                store_remote(&s->found[turn].mass_above, q, above_mass);
+                store_remote(&s->found[turn].count_above, q, above_count);
+                store_remote(&s->found[turn].bin, q, (uint32_t)(bin0 + j));
             }
         above_mass += m[j];
         above_count += c[j];
     }
     agree(r);
-    const Found f = s->found;
-    agree(r);   // before `found` is written again
-    return f;
+    return s->found[turn];
 }
 
 __device__ __forceinline__ uint32_t bin_of(float l, float m, float inv)
 {
-    return (uint32_t)min(SM_BINS - 1, (int)(-exponent_of(l, m, inv) * SM_BIN_SCALE));
+    // (fminf takes what is no number, a logit without weight, to the last bin)
+    return l == m ? 0u : (uint32_t)(int)fminf(-exponent_of(l, m, inv) * SM_BIN_SCALE, (float)(SM_BINS - 1));
+}
+
+// Whether a logit takes part (its weight is above 0), from its bin: the exponential is needed at
+// the edge alone.
+__device__ __forceinline__ bool takes_part(float l, uint32_t bin, const Row &r)
+{
+    return bin < SM_EDGE_BIN || (bin == SM_EDGE_BIN && weight_of(l, r.m, r.inv) > 0);
 }
 
 struct Boundary {        // the last logit that stays, and how many of its equals
     uint32_t key, keep;
-    uint64_t mass;       // kept in all
+    uint64_t mass;       // kept in all (searches by mass)
 };
 
 // The boundary in bin `f.bin` of the first histogram: `target` is reached there.
-__device__ Boundary refine(const Row &r, bool by_mass, uint64_t target, Found f)
+template <bool BY_MASS> __device__ Boundary refine(Row &r, uint64_t target, Found f)
 {
     uint32_t hi = 0, lo = 0xffffffffu;
     for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
         const float l = r.l[i];
-        if (weight_of(l, r.m, r.inv) > 0 && bin_of(l, r.m, r.inv) == f.bin) {
+        const uint32_t bin = bin_of(l, r.m, r.inv);
+        if (bin == f.bin && takes_part(l, bin, r)) {
             hi = max(hi, key_of(l));
             lo = min(lo, key_of(l));
         }
@@ -279,23 +319,86 @@ __device__ Boundary refine(const Row &r, bool by_mass, uint64_t target, Found f)
         for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
             const float l = r.l[i];
             const uint32_t key = key_of(l);
-            if (key >= lo && key <= hi) {
-                const uint32_t w = weight_of(l, r.m, r.inv);
-                if (w > 0)
-                    add_to_bin(r.s, (hi - key) >> shift, w);
+            if (key >= lo && key <= hi && takes_part(l, f.bin, r)) {
+                if (BY_MASS)
+                    add_to_bin(r.s, (hi - key) >> shift, weight_of(l, r.m, r.inv));
+                else
+                    atomicAdd(&r.s->count[(hi - key) >> shift], 1u);
             }
         }
-        f = search(r, by_mass, target, f);
+        const uint32_t first_bin = f.bin;
+        f = search<BY_MASS>(r, target, f);
         hi -= f.bin << shift;
         lo = max(lo, hi - min(hi, (1u << shift) - 1));
+        f.bin = first_bin;
     }
-    const float l = __uint_as_float(hi ^ ((hi >> 31) ? 0x80000000u : 0xffffffffu));
-    const uint64_t w = weight_of(l, r.m, r.inv);
-    Boundary b;
-    b.key = hi;
-    b.keep = by_mass ? (uint32_t)((target - f.mass_above + w - 1) / w) : (uint32_t)target - f.count_above;
-    b.mass = f.mass_above + b.keep * w;
+    Boundary b = {hi, 0, 0};
+    if (BY_MASS) {
+        const uint64_t w = weight_of(__uint_as_float(hi ^ ((hi >> 31) ? 0x80000000u : 0xffffffffu)), r.m, r.inv);
+        b.keep = (uint32_t)((target - f.mass_above + w - 1) / w);
+        b.mass = f.mass_above + b.keep * w;
+    } else {
+        b.keep = (uint32_t)target - f.count_above;
+    }
     return b;
+}
+
+// Sums over the CTA of a mass, for every thread.
+__device__ __forceinline__ uint64_t cta_sum(const Row &r, uint64_t mass)
+{
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1)
+        mass += __shfl_xor_sync(dev::FULL_MASK, mass, d);
+    if ((threadIdx.x & 31) == 0)
+        r.s->warp_mass[threadIdx.x >> 5] = mass;
+    __syncthreads();
+    mass = 0;
+    for (int w = 0; w < SM_WARPS; ++w)
+        mass += r.s->warp_mass[w];
+    __syncthreads();
+    return mass;
+}
+
+__device__ __forceinline__ uint64_t draw_at(float u, uint64_t total)
+{
+    const double drawn = floor((double)u * (double)total);
+    return drawn >= (double)total ? total - 1 : drawn > 0.0 ? (uint64_t)drawn : 0u;
+}
+
+// The whole choice among the `n` logits of the list, one a thread: their order by counting, then
+// the filters and the draw by sums over the list.
+__device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int64_t row, int32_t top_k, bool by_p, float top_p, double min_w)
+{
+    Shared *s = r.s;
+    const int e = threadIdx.x;
+    const uint32_t key = e < n ? s->list_key[e] : 0u, at = e < n ? s->list_at[e] : 0xffffffffu, w = e < n ? s->list_w[e] : 0u;
+    uint32_t rank = 0;
+    uint64_t before = 0;
+    for (int j = 0; j < n; ++j)
+        if (s->list_key[j] > key || (s->list_key[j] == key && s->list_at[j] < at)) {
+            ++rank;
+            before += s->list_w[j];
+        }
+    bool keep = e < n && rank < (uint32_t)top_k;
+    if (by_p) {
+        const double want = ceil((double)top_p * (double)cta_sum(r, keep ? w : 0u));
+        keep = keep && before < (want >= 1.0 ? (uint64_t)want : 1u);
+    }
+    keep = keep && (double)w >= min_w;
+    const uint64_t total = cta_sum(r, keep ? w : 0u);
+    if (e < n)
+        s->list_key[e] = keep ? w : 0u;          // from here on: the kept weight
+    __syncthreads();
+    const uint64_t drawn = draw_at(p.uniform[row], total);
+    uint64_t run = 0;
+    for (int j = 0; j < n; ++j)
+        if (s->list_at[j] < at)
+            run += s->list_key[j];
+    if (keep && run <= drawn && drawn < run + w) {
+        p.token[row] = (int32_t)at;
+        if (p.logprob)
+            p.logprob[row] = (float)log((double)w / (double)total);
+    }
 }
 
 template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kernel(const SampleParams p, int slice, int seg)
@@ -308,6 +411,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r.ranks));
     r.rank = cluster_rank();
+    r.turn = 0;
     r.slice = slice;
     r.seg = seg;
     const int64_t row = blockIdx.x / r.ranks;
@@ -381,60 +485,83 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     const double min_w = (double)min_p * 2147483648.0;
     const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.0f;
     Boundary last = {SM_KEY_NONE, 0xffffffffu, 0};   // everything stays
-    if (by_k || by_p) {
+    const Found nothing = {0, 0, 0};
+    bool cut_k = false;
+    if (by_k) {           // counts alone: no exponentials
         clear_bins(r);
-        uint64_t mass = 0;
-        uint32_t count = 0;
         for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
-            const uint32_t w = weight_of(r.l[i], r.m, r.inv);
-            if (w > 0) {
-                add_to_bin(s, bin_of(r.l[i], r.m, r.inv), w);
-                mass += w;
-                ++count;
-            }
+            const uint32_t bin = bin_of(r.l[i], r.m, r.inv);
+            if (takes_part(r.l[i], bin, r))
+                atomicAdd(&s->count[bin], 1u);
         }
-        scan(r, mass, count);
-        if (threadIdx.x == SM_THREADS - 1)
-            for (uint32_t q = 0; q < r.ranks; ++q) {
-                store_remote(&s->mass[r.rank], q, mass);
-                store_remote(&s->ties[r.rank], q, count);
-            }
-        agree(r);
-        uint64_t all = 0;
-        uint32_t choices = 0;
-        for (uint32_t q = 0; q < r.ranks; ++q) {
-            all += s->mass[q];
-            choices += s->ties[q];
-        }
-        const Found nothing = {0, 0, 0};
-        Found at_k = nothing, at_p = nothing;
-        const bool cut_k = by_k && choices > (uint32_t)top_k;
-        if (cut_k)
-            at_k = search(r, false, (uint64_t)top_k, nothing);
-        // top-p's target needs the mass that top-k leaves, and the first histogram: keep
-        // that histogram by searching for the boundary bin once the mass is known; the
-        // refinement of top-k overwrites it, so it is built again only when both cut.
+        if (threadIdx.x == 0)
+            s->list_n = 0;
+        Shares all;
+        const Found f = search<false>(r, (uint64_t)top_k, nothing, &all);
+        cut_k = all.count > (uint32_t)top_k;
         if (cut_k) {
-            last = refine(r, false, (uint64_t)top_k, at_k);
-            all = last.mass;
-            if (by_p) {
-                clear_bins(r);
-                for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
-                    const float l = r.l[i];
-                    if (key_of(l) >= last.key) {
-                        const uint32_t w = weight_of(l, r.m, r.inv);
-                        if (w > 0)
-                            add_to_bin(s, bin_of(l, r.m, r.inv), w);
+            // the logits of the bins down to the boundary's, if they are few
+            for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
+                const float l = r.l[i];
+                const uint32_t bin = bin_of(l, r.m, r.inv);
+                if (bin <= f.bin && takes_part(l, bin, r)) {
+                    const uint32_t e = atomicAdd(&s->list_n, 1u);
+                    if (e < SM_LIST) {
+                        s->list_key[e] = key_of(l);
+                        s->list_at[e] = (uint32_t)(start + i);
+                        s->list_w[e] = weight_of(l, r.m, r.inv);
                     }
                 }
             }
+            __syncthreads();
+            const uint32_t mine = s->list_n;
+            const Shares lists = share(r, 0, mine);
+            if (lists.count <= SM_LIST) {
+                if (r.rank == 0) {
+                    uint32_t to = mine;
+                    for (uint32_t q = 1; q < r.ranks; ++q) {
+                        const uint32_t n = load_remote(&s->list_n, q);
+                        for (uint32_t e = threadIdx.x; e < n; e += SM_THREADS) {
+                            s->list_key[to + e] = load_remote(&s->list_key[e], q);
+                            s->list_at[to + e] = load_remote(&s->list_at[e], q);
+                            s->list_w[to + e] = load_remote(&s->list_w[e], q);
+                        }
+                        to += n;
+                    }
+                    __syncthreads();
+                }
+                agree(r);      // the other CTAs' lists are read
+                if (r.rank == 0)
+                    choose_from_list(p, r, (int)lists.count, row, top_k, by_p, top_p, min_w);
+                return;
+            }
+            last = refine<false>(r, (uint64_t)top_k, f);
         }
-        if (by_p) {
-            const double want = ceil((double)top_p * (double)all);
-            const uint64_t target = want >= 1.0 ? (uint64_t)want : 1u;   // a NaN top_p: the first alone
-            at_p = search(r, true, target, nothing);
-            last = refine(r, true, target, at_p);
+    }
+    if (by_p) {
+        clear_bins(r);
+        const uint32_t from = cut_k ? last.key : 0u;   // of the boundary's equals all: the target lies among those that stay
+        uint64_t mass = 0;
+        uint32_t unused_count = 0;
+        for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
+            const float l = r.l[i];
+            const uint32_t key = key_of(l);
+            if (key < from)
+                continue;
+            const uint32_t w = weight_of(l, r.m, r.inv);
+            if (w > 0) {
+                add_to_bin(s, bin_of(l, r.m, r.inv), w);
+                if (!cut_k || key > from)
+                    mass += w;
+            }
         }
+        scan(r, mass, unused_count);
+        uint64_t all = share(r, mass, 0).mass;
+        if (cut_k)
+            all += (uint64_t)last.keep * weight_of(__uint_as_float(last.key ^ ((last.key >> 31) ? 0x80000000u : 0xffffffffu)), r.m, r.inv);
+        const double want = ceil((double)top_p * (double)all);
+        const uint64_t target = want >= 1.0 ? (uint64_t)want : 1u;   // a NaN top_p: the first alone
+        last = refine<true>(r, target, search<true>(r, target, nothing));
     }
 
     // kept weight of each segment, its equals of the boundary counted apart
@@ -469,40 +596,22 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     uint32_t ties = threadIdx.x < SM_SEGMENTS ? s->seg_ties[threadIdx.x] : 0u;
     const uint32_t own_ties = ties;
     scan(r, mass, ties);
-    if (threadIdx.x == SM_THREADS - 1)
-        for (uint32_t q = 0; q < r.ranks; ++q)
-            store_remote(&s->ties[r.rank], q, ties);
-    agree(r);
-    uint32_t ties_before = ties - own_ties;    // of this thread's segment
-    for (uint32_t q = 0; q < r.rank; ++q)
-        ties_before += s->ties[q];
+    const uint32_t ties_before = ties - own_ties + share(r, 0, ties).count_below;    // of this thread's segment
     const uint32_t kept_ties = ties_before < last.keep ? min(own_ties, last.keep - ties_before) : 0u;
     uint32_t none = 0;
     const uint64_t own_mass = threadIdx.x < SM_SEGMENTS ? s->seg_mass[threadIdx.x] + kept_ties * edge_w : 0u;
     mass = own_mass;
     scan(r, mass, none);
-    if (threadIdx.x == SM_THREADS - 1)
-        for (uint32_t q = 0; q < r.ranks; ++q)
-            store_remote(&s->mass[r.rank], q, mass);
-    agree(r);
-    uint64_t total = 0, before = mass - own_mass;
-    for (uint32_t q = 0; q < r.ranks; ++q) {
-        if (q < r.rank)
-            before += s->mass[q];
-        total += s->mass[q];
-    }
-    const double drawn = floor((double)p.uniform[row] * (double)total);
-    const uint64_t at = drawn >= (double)total ? total - 1 : drawn > 0.0 ? (uint64_t)drawn : 0u;
+    const uint64_t cta_mass = mass;       // of the last thread: this CTA's
+    const Shares kept = share(r, mass, 0);
+    const uint64_t total = kept.mass, before = kept.mass_below + mass - own_mass;
+    const uint64_t at = draw_at(p.uniform[row], total);
     if (threadIdx.x < SM_SEGMENTS && before <= at && at < before + own_mass) {
         s->warp_mass[0] = at - before;      // what to walk into this segment, and with how many equals
         s->warp_count[0] = last.keep > ties_before ? last.keep - ties_before : 0u;
         s->warp_a[0] = threadIdx.x;
     }
-    uint64_t base = 0;
-    for (uint32_t q = 0; q < r.rank; ++q)
-        base += s->mass[q];
-    const bool here = base <= at && at < base + s->mass[r.rank];
-    __syncthreads();
+    const bool here = __syncthreads_or(threadIdx.x == SM_THREADS - 1 && kept.mass_below <= at && at < kept.mass_below + cta_mass);
     if (here && warp == 0) {
         uint64_t left = s->warp_mass[0];
         uint32_t keep = s->warp_count[0];
@@ -567,10 +676,12 @@ template <typename E> cudaError_t launch_e(const SampleParams &p, const loom_lau
 
 }  // namespace
 
-bool sample_geometry(int64_t rows, int32_t vocab, int32_t, int64_t, loom_launch *out)
+bool sample_geometry(int64_t rows, int32_t vocab, int64_t sms, loom_launch *out)
 {
+    // Slices of up to SM_SLICE (two CTAs an SM); shorter ones while that leaves SMs without work:
+    // a pass over a slice takes as long as it is.
     int ranks = 1;
-    while (ranks < SM_MAX_CLUSTER && vocab > ranks * SM_SLICE)
+    while (ranks < SM_MAX_CLUSTER && (vocab > ranks * SM_SLICE || (rows * ranks * 2 <= sms && vocab > ranks * SM_SHORT_SLICE)))
         ranks *= 2;
     if (vocab > ranks * SM_MAX_SLICE || rows * ranks > 0x7fffffff)
         return false;
