@@ -13,8 +13,8 @@
 //  * No sort.  A histogram over 2048 equal bins of (m - l) / T, which spread the
 //    bulk of a row over many bins, finds the bin in which top-k's count or top-p's
 //    weight is reached.  Logits whose weight is 0 cannot be chosen and take no part.
-//  * Where top-k leaves few logits (with those of its last bin at most 512), they are
-//    gathered in one CTA, which ranks them against each other and does the rest.
+//  * Where top-k leaves few logits (with those of its last bin at most 2048), they are
+//    gathered in one CTA, which sorts them (bitonic, in shared memory) and does the rest.
 //  * Otherwise the boundary's logit is found by histograms over the bit patterns in
 //    the boundary's bin, 2048 at a time, until one pattern is left.  Equal logits there:
 //    the number that stays follows from the sums alone, and the first ones in index
@@ -35,7 +35,7 @@ constexpr int SM_MAX_SLICE = 49152;        // logits of a CTA: 192 KiB
 constexpr int SM_SLICE = 16384;            // slices up to this leave room for a second CTA on the SM
 constexpr int SM_SHORT_SLICE = 2048;       // not worth another CTA
 constexpr int SM_SEGMENTS = 128;           // segments of a slice
-constexpr int SM_LIST = SM_THREADS;        // logits that one CTA ranks, one a thread
+constexpr int SM_LIST = SM_BINS;           // logits that one CTA sorts: their list takes the bins' place
 constexpr uint32_t SM_FULL = 1u << 31;     // the weight of the largest logit
 constexpr float SM_BIN_SCALE = 95.0f;      // bins per unit of (m - l) / T: weights are above 0 in
                                            // bins below SM_EDGE_BIN and 0 above it
@@ -51,13 +51,11 @@ __device__ __forceinline__ uint32_t key_of(float l)
 
 __device__ __forceinline__ float exponent_of(float l, float m, float inv) { return (l - m) * inv; }
 
+// (What is no number, or -infinity, converts to 0.)
 __device__ __forceinline__ uint32_t weight_of(float l, float m, float inv)
 {
-    if (l == m)
-        return SM_FULL;
-    if (l == -INFINITY)
-        return 0;
-    return __float2uint_rz(expf(exponent_of(l, m, inv)) * 2147483648.0f);
+    const uint32_t w = __float2uint_rz(expf(exponent_of(l, m, inv)) * 2147483648.0f);
+    return l == m ? SM_FULL : w;
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -77,6 +75,13 @@ __device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank)
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(dev::smem_u32(p)), "r"(rank));
     return a;
+}
+
+__device__ __forceinline__ uint64_t load_remote(const uint64_t *p, uint32_t rank)
+{
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(p, rank)) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ uint32_t load_remote(const uint32_t *p, uint32_t rank)
@@ -103,8 +108,16 @@ struct Found {            // where a search ended: what lies above bin `bin`
 
 // What the CTAs of a cluster tell each other has two places, used in turn: one barrier then
 // parts the writing of a place from its next writing.
-struct Shared {
-    uint32_t count[SM_BINS], low[SM_BINS], high[SM_BINS];
+struct alignas(16) Shared {       // (the slice behind it is read 16 bytes at a time)
+    union {
+        struct {
+            uint32_t count[SM_BINS], low[SM_BINS], high[SM_BINS];
+        };
+        struct {                                // gathered logits: (~key, index) in one word, so that
+            uint64_t list_order[SM_LIST];       // their order is that of the words; and their weights
+            uint32_t list_w[SM_LIST];
+        };
+    };
     uint64_t share_mass[2][SM_MAX_CLUSTER];     // per CTA of the cluster
     uint32_t share_count[2][SM_MAX_CLUSTER];
     uint32_t key_max[2][SM_MAX_CLUSTER], key_min[2][SM_MAX_CLUSTER];
@@ -114,8 +127,9 @@ struct Shared {
     uint64_t seg_mass[SM_SEGMENTS];
     uint32_t seg_ties[SM_SEGMENTS];
     uint32_t list_n;                            // gathered logits of this CTA
-    uint32_t list_key[SM_LIST], list_at[SM_LIST], list_w[SM_LIST];
 };
+
+static_assert(sizeof(Shared) % 16 == 0, "the slice is 16-byte aligned");
 
 struct Row {              // what the threads of a cluster agree on
     Shared *s;
@@ -125,6 +139,19 @@ struct Row {              // what the threads of a cluster agree on
     float m, inv;
     uint32_t turn;        // which places are used next
 };
+
+// f(logit, place) for every logit of the slice, four neighbours a thread at a time (their
+// arithmetic overlaps).  The slice is filled up to a multiple of four with -infinity.
+template <typename F> __device__ __forceinline__ void for_each(const Row &r, F f)
+{
+    for (int i = 4 * threadIdx.x; i < r.n; i += 4 * SM_THREADS) {
+        const float4 q = *reinterpret_cast<const float4 *>(r.l + i);
+        f(q.x, i);
+        f(q.y, i + 1);
+        f(q.z, i + 2);
+        f(q.w, i + 3);
+    }
+}
 
 __device__ __forceinline__ void agree(const Row &r)
 {
@@ -171,7 +198,6 @@ __device__ __forceinline__ void clear_bins(const Row &r)
 
 __device__ __forceinline__ void add_to_bin(Shared *s, uint32_t bin, uint32_t w)
 {
-    atomicAdd(&s->count[bin], 1u);
     atomicAdd(&s->low[bin], w & 0xffffu);
     atomicAdd(&s->high[bin], w >> 16);
 }
@@ -248,8 +274,9 @@ template <bool BY_MASS> __device__ Found search(Row &r, uint64_t target, Found s
         c[j] = 0;
         if (j < per && (int)threadIdx.x * per + j < bins)
             for (uint32_t q = 0; q < r.ranks; ++q) {
-                c[j] += load_remote(&s->count[bin0 + j], q);
-                if (BY_MASS)
+                if (!BY_MASS)
+                    c[j] += load_remote(&s->count[bin0 + j], q);
+                else
                     m[j] += load_remote(&s->low[bin0 + j], q) + ((uint64_t)load_remote(&s->high[bin0 + j], q) << 16);
             }
         mass += m[j];
@@ -304,20 +331,18 @@ struct Boundary {        // the last logit that stays, and how many of its equal
 template <bool BY_MASS> __device__ Boundary refine(Row &r, uint64_t target, Found f)
 {
     uint32_t hi = 0, lo = 0xffffffffu;
-    for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
-        const float l = r.l[i];
+    for_each(r, [&](float l, int) {
         const uint32_t bin = bin_of(l, r.m, r.inv);
         if (bin == f.bin && takes_part(l, bin, r)) {
             hi = max(hi, key_of(l));
             lo = min(lo, key_of(l));
         }
-    }
+    });
     cluster_max_min(r, hi, lo);
     for (int level = 0; level < 3 && hi > lo; ++level) {   // bins of equal size, the largest keys first
         const int shift = max(0, 32 - __clz(hi - lo) - 11);
         clear_bins(r);
-        for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
-            const float l = r.l[i];
+        for_each(r, [&](float l, int) {
             const uint32_t key = key_of(l);
             if (key >= lo && key <= hi && takes_part(l, f.bin, r)) {
                 if (BY_MASS)
@@ -325,7 +350,7 @@ template <bool BY_MASS> __device__ Boundary refine(Row &r, uint64_t target, Foun
                 else
                     atomicAdd(&r.s->count[(hi - key) >> shift], 1u);
             }
-        }
+        });
         const uint32_t first_bin = f.bin;
         f = search<BY_MASS>(r, target, f);
         hi -= f.bin << shift;
@@ -343,61 +368,120 @@ template <bool BY_MASS> __device__ Boundary refine(Row &r, uint64_t target, Foun
     return b;
 }
 
-// Sums over the CTA of a mass, for every thread.
-__device__ __forceinline__ uint64_t cta_sum(const Row &r, uint64_t mass)
-{
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1)
-        mass += __shfl_xor_sync(dev::FULL_MASK, mass, d);
-    if ((threadIdx.x & 31) == 0)
-        r.s->warp_mass[threadIdx.x >> 5] = mass;
-    __syncthreads();
-    mass = 0;
-    for (int w = 0; w < SM_WARPS; ++w)
-        mass += r.s->warp_mass[w];
-    __syncthreads();
-    return mass;
-}
-
 __device__ __forceinline__ uint64_t draw_at(float u, uint64_t total)
 {
     const double drawn = floor((double)u * (double)total);
     return drawn >= (double)total ? total - 1 : drawn > 0.0 ? (uint64_t)drawn : 0u;
 }
 
-// The whole choice among the `n` logits of the list, one a thread: their order by counting, then
-// the filters and the draw by sums over the list.
-__device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int64_t row, int32_t top_k, bool by_p, float top_p, double min_w)
+// The first `n` words (a power of two) and, where PAIRS, their weights in rising order of the words.
+template <bool PAIRS> __device__ void sort_list(Shared *s, int n)
+{
+    for (int k = 2; k <= n; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            for (int i = threadIdx.x; i < n / 2; i += SM_THREADS) {
+                const int a = 2 * i - (i & (j - 1)), b = a + j;
+                const uint64_t x = s->list_order[a], y = s->list_order[b];
+                if ((x > y) == ((a & k) == 0)) {
+                    s->list_order[a] = y;
+                    s->list_order[b] = x;
+                    if (PAIRS) {
+                        const uint32_t w = s->list_w[a];
+                        s->list_w[a] = s->list_w[b];
+                        s->list_w[b] = w;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+}
+
+__device__ __forceinline__ int power_of_two(int n)
+{
+    int p = 2;
+    while (p < n)
+        p <<= 1;
+    return p;
+}
+
+// The whole choice among the `n` logits of the list: top-k and top-p along their order, the draw
+// along their indices.  Each thread holds four neighbours of the sorted list.
+__device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int64_t row, int32_t top_k, bool by_p, float top_p, uint32_t least)
 {
     Shared *s = r.s;
-    const int e = threadIdx.x;
-    const uint32_t key = e < n ? s->list_key[e] : 0u, at = e < n ? s->list_at[e] : 0xffffffffu, w = e < n ? s->list_w[e] : 0u;
-    uint32_t rank = 0;
-    uint64_t before = 0;
-    for (int j = 0; j < n; ++j)
-        if (s->list_key[j] > key || (s->list_key[j] == key && s->list_at[j] < at)) {
-            ++rank;
-            before += s->list_w[j];
-        }
-    bool keep = e < n && rank < (uint32_t)top_k;
-    if (by_p) {
-        const double want = ceil((double)top_p * (double)cta_sum(r, keep ? w : 0u));
-        keep = keep && before < (want >= 1.0 ? (uint64_t)want : 1u);
+    const int e0 = 4 * (int)threadIdx.x;
+    int size = power_of_two(n);
+    for (int e = n + threadIdx.x; e < size; e += SM_THREADS) {
+        s->list_order[e] = ~0ull;
+        s->list_w[e] = 0;
     }
-    keep = keep && (double)w >= min_w;
-    const uint64_t total = cta_sum(r, keep ? w : 0u);
-    if (e < n)
-        s->list_key[e] = keep ? w : 0u;          // from here on: the kept weight
     __syncthreads();
-    const uint64_t drawn = draw_at(p.uniform[row], total);
-    uint64_t run = 0;
-    for (int j = 0; j < n; ++j)
-        if (s->list_at[j] < at)
-            run += s->list_key[j];
-    if (keep && run <= drawn && drawn < run + w) {
-        p.token[row] = (int32_t)at;
-        if (p.logprob)
-            p.logprob[row] = (float)log((double)w / (double)total);
+    sort_list<true>(s, size);
+    uint64_t order[4], mass = 0;
+    uint32_t w[4], none = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const bool in = e0 + j < n && e0 + j < top_k;
+        order[j] = in ? s->list_order[e0 + j] : ~0ull;
+        w[j] = in ? s->list_w[e0 + j] : 0u;
+        mass += w[j];
+    }
+    uint64_t run = mass;
+    scan(r, run, none);
+    run -= mass;                               // above this thread's first
+    uint64_t target = ~0ull;
+    if (by_p) {
+        if (threadIdx.x == SM_THREADS - 1)
+            s->seg_mass[0] = run + mass;
+        __syncthreads();
+        const double want = ceil((double)top_p * (double)s->seg_mass[0]);
+        target = want >= 1.0 ? (uint64_t)want : 1u;
+    }
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {              // kept: index and weight in one word
+        const bool keep = w[j] > 0 && run < target && w[j] >= least;
+        run += w[j];
+        order[j] = keep ? (order[j] << 32) | w[j] : ~0ull;
+        mine += keep;
+    }
+    // what stays stands at the front: its weights fall along the order
+    const int last = __reduce_max_sync(dev::FULL_MASK, mine ? e0 + 4 : 0);
+    if ((threadIdx.x & 31) == 0)
+        s->warp_a[threadIdx.x >> 5] = (uint32_t)last;
+    __syncthreads();
+    size = 0;
+    for (int q = 0; q < SM_WARPS; ++q)
+        size = max(size, (int)s->warp_a[q]);
+    size = power_of_two(size);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (e0 + j < size)
+            s->list_order[e0 + j] = order[j];
+    __syncthreads();
+    sort_list<false>(s, size);
+    mass = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        order[j] = e0 + j < size ? s->list_order[e0 + j] : ~0ull;
+        w[j] = order[j] == ~0ull ? 0u : (uint32_t)order[j];
+        mass += w[j];
+    }
+    run = mass;
+    scan(r, run, none);
+    if (threadIdx.x == SM_THREADS - 1)
+        s->seg_mass[1] = run;
+    __syncthreads();
+    const uint64_t total = s->seg_mass[1], at = draw_at(p.uniform[row], total);
+    run -= mass;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (run <= at && at < run + w[j]) {
+            p.token[row] = (int32_t)(order[j] >> 32);
+            if (p.logprob)
+                p.logprob[row] = (float)log((double)w[j] / (double)total);
+        }
+        run += w[j];
     }
 }
 
@@ -425,6 +509,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     constexpr int V = dev::Vec16<E>::N;
     if (reinterpret_cast<uintptr_t>(src) % 16 == 0) {
         const int whole = r.n / V;
+#pragma unroll 4
         for (int i = threadIdx.x; i < whole; i += SM_THREADS) {
             const dev::Vec16<E> v = reinterpret_cast<const dev::Vec16<E> *>(src)[i];
 #pragma unroll
@@ -449,6 +534,8 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
             top = max(top, key_of(l));
         }
     }
+    if (threadIdx.x < 3 && r.n + (int)threadIdx.x < (r.n + 3) / 4 * 4)
+        r.l[r.n + threadIdx.x] = -INFINITY;
     agree(r);   // every CTA of the cluster runs: its shared memory may be written
     cluster_max_min(r, top, unused);
     if (top == SM_KEY_NONE) {
@@ -465,9 +552,10 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     const float t = p.d_temperature ? p.d_temperature[row] : p.temperature;
     if (!(t > 0.0f)) {   // greedy: the first of the largest
         uint32_t none = 0, first = 0xffffffffu;
-        for (int i = threadIdx.x; i < r.n; i += SM_THREADS)
-            if (r.l[i] == r.m)
+        for_each(r, [&](float l, int i) {
+            if (l == r.m)
                 first = min(first, (uint32_t)(start + i));
+        });
         cluster_max_min(r, none, first);
         if (r.rank == 0 && threadIdx.x == 0) {
             p.token[row] = (int32_t)first;
@@ -482,18 +570,18 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     const int32_t top_k = p.d_top_k ? p.d_top_k[row] : p.top_k;
     const float top_p = p.d_top_p ? p.d_top_p[row] : p.top_p;
     const float min_p = fminf(fmaxf(p.d_min_p ? p.d_min_p[row] : p.min_p, 0.0f), 1.0f);   // NaN: 0
-    const double min_w = (double)min_p * 2147483648.0;
+    const uint32_t least = (uint32_t)ceil((double)min_p * 2147483648.0);     // w >= min_p * 2^31
     const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.0f;
     Boundary last = {SM_KEY_NONE, 0xffffffffu, 0};   // everything stays
     const Found nothing = {0, 0, 0};
     bool cut_k = false;
     if (by_k) {           // counts alone: no exponentials
         clear_bins(r);
-        for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
-            const uint32_t bin = bin_of(r.l[i], r.m, r.inv);
-            if (takes_part(r.l[i], bin, r))
+        for_each(r, [&](float l, int) {
+            const uint32_t bin = bin_of(l, r.m, r.inv);
+            if (takes_part(l, bin, r))
                 atomicAdd(&s->count[bin], 1u);
-        }
+        });
         if (threadIdx.x == 0)
             s->list_n = 0;
         Shares all;
@@ -501,18 +589,16 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         cut_k = all.count > (uint32_t)top_k;
         if (cut_k) {
             // the logits of the bins down to the boundary's, if they are few
-            for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
-                const float l = r.l[i];
+            for_each(r, [&](float l, int i) {
                 const uint32_t bin = bin_of(l, r.m, r.inv);
                 if (bin <= f.bin && takes_part(l, bin, r)) {
                     const uint32_t e = atomicAdd(&s->list_n, 1u);
                     if (e < SM_LIST) {
-                        s->list_key[e] = key_of(l);
-                        s->list_at[e] = (uint32_t)(start + i);
+                        s->list_order[e] = ((uint64_t)~key_of(l) << 32) | (uint32_t)(start + i);
                         s->list_w[e] = weight_of(l, r.m, r.inv);
                     }
                 }
-            }
+            });
             __syncthreads();
             const uint32_t mine = s->list_n;
             const Shares lists = share(r, 0, mine);
@@ -522,8 +608,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
                     for (uint32_t q = 1; q < r.ranks; ++q) {
                         const uint32_t n = load_remote(&s->list_n, q);
                         for (uint32_t e = threadIdx.x; e < n; e += SM_THREADS) {
-                            s->list_key[to + e] = load_remote(&s->list_key[e], q);
-                            s->list_at[to + e] = load_remote(&s->list_at[e], q);
+                            s->list_order[to + e] = load_remote(&s->list_order[e], q);
                             s->list_w[to + e] = load_remote(&s->list_w[e], q);
                         }
                         to += n;
@@ -532,7 +617,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
                 }
                 agree(r);      // the other CTAs' lists are read
                 if (r.rank == 0)
-                    choose_from_list(p, r, (int)lists.count, row, top_k, by_p, top_p, min_w);
+                    choose_from_list(p, r, (int)lists.count, row, top_k, by_p, top_p, least);
                 return;
             }
             last = refine<false>(r, (uint64_t)top_k, f);
@@ -543,18 +628,15 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         const uint32_t from = cut_k ? last.key : 0u;   // of the boundary's equals all: the target lies among those that stay
         uint64_t mass = 0;
         uint32_t unused_count = 0;
-        for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
-            const float l = r.l[i];
+        for_each(r, [&](float l, int) {
             const uint32_t key = key_of(l);
-            if (key < from)
-                continue;
-            const uint32_t w = weight_of(l, r.m, r.inv);
+            const uint32_t w = key < from ? 0u : weight_of(l, r.m, r.inv);
             if (w > 0) {
                 add_to_bin(s, bin_of(l, r.m, r.inv), w);
                 if (!cut_k || key > from)
                     mass += w;
             }
-        }
+        });
         scan(r, mass, unused_count);
         uint64_t all = share(r, mass, 0).mass;
         if (cut_k)
@@ -567,27 +649,28 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     // kept weight of each segment, its equals of the boundary counted apart
     const float edge = __uint_as_float(last.key ^ ((last.key >> 31) ? 0x80000000u : 0xffffffffu));
     uint64_t edge_w = weight_of(edge, r.m, r.inv);
-    if ((double)edge_w < min_w)
+    if (edge_w < least)
         edge_w = 0;
     for (int g = warp; g < SM_SEGMENTS; g += SM_WARPS) {
         uint64_t mass = 0;
         uint32_t ties = 0;
         const int end = min(r.n, (g + 1) * seg);
-        for (int i = g * seg + lane; i < end; i += 32) {
-            const float l = r.l[i];
-            if (l > edge) {
-                const uint32_t w = weight_of(l, r.m, r.inv);
-                mass += (double)w >= min_w ? w : 0u;
-            } else if (l == edge) {
-                ++ties;
+        for (int i = g * seg + 4 * lane; i < end; i += 128) {
+            const float4 q = *reinterpret_cast<const float4 *>(r.l + i);
+            const float l[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = weight_of(l[j], r.m, r.inv);
+                mass += l[j] > edge && w >= least ? w : 0u;
+                ties += l[j] == edge;
             }
         }
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-            mass += __shfl_xor_sync(dev::FULL_MASK, mass, d);
+        // (a lane's share is below 2^43)
+        const uint32_t low = __reduce_add_sync(dev::FULL_MASK, (uint32_t)mass & 0xffffffu);
+        const uint32_t high = __reduce_add_sync(dev::FULL_MASK, (uint32_t)(mass >> 24));
         ties = __reduce_add_sync(dev::FULL_MASK, ties);
         if (lane == 0) {
-            s->seg_mass[g] = mass;
+            s->seg_mass[g] = low + ((uint64_t)high << 24);
             s->seg_ties[g] = ties;
         }
     }
@@ -624,7 +707,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
             uint64_t w = 0;
             if (i < end && (l > edge || (l == edge && mine < keep))) {
                 w = weight_of(l, r.m, r.inv);
-                w = (double)w >= min_w ? w : 0u;
+                w = w >= least ? w : 0u;
             }
             uint64_t run = w;
 #pragma unroll
@@ -653,7 +736,7 @@ template <typename E> cudaError_t launch_e(const SampleParams &p, const loom_lau
 {
     const int ranks = (int)L.cluster[0];
     const int slice = ((p.vocab + ranks - 1) / ranks + 15) / 16 * 16;
-    const int seg = ((slice + SM_SEGMENTS - 1) / SM_SEGMENTS + 31) / 32 * 32;
+    const int seg = ((slice + SM_SEGMENTS - 1) / SM_SEGMENTS + 127) / 128 * 128;   // whole rounds of a warp's float4
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(sample_kernel<E>), 0, done);
     if (e != cudaSuccess)
