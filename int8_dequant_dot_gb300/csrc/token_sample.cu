@@ -15,8 +15,9 @@
 //    weight is reached.  Logits whose weight is 0 cannot be chosen and take no part.
 //  * Where top-k leaves few logits (with those of its last bin at most 2048), they are
 //    gathered in one CTA, which sorts them (bitonic, in shared memory) and does the rest.
-//  * Otherwise the boundary's logit is found by histograms over the bit patterns in
-//    the boundary's bin, 2048 at a time, until one pattern is left.  Equal logits there:
+//  * Otherwise the boundary's bin alone is gathered and sorted; one with more logits than
+//    that (equal ones, mostly) is searched by histograms over their bit patterns, 2048 at a
+//    time, until one pattern is left.  Equal logits there:
 //    the number that stays follows from the sums alone, and the first ones in index
 //    order stay, by a running count over segments of the row.  The draw then sums the
 //    kept weight per segment (a warp each), scans over segments and CTAs, and one warp
@@ -324,55 +325,7 @@ __device__ __forceinline__ bool takes_part(float l, uint32_t bin, const Row &r)
 
 struct Boundary {        // the last logit that stays, and how many of its equals
     uint32_t key, keep;
-    uint64_t mass;       // kept in all (searches by mass)
 };
-
-// The boundary in bin `f.bin` of the first histogram: `target` is reached there.
-template <bool BY_MASS> __device__ Boundary refine(Row &r, uint64_t target, Found f)
-{
-    uint32_t hi = 0, lo = 0xffffffffu;
-    for_each(r, [&](float l, int) {
-        const uint32_t bin = bin_of(l, r.m, r.inv);
-        if (bin == f.bin && takes_part(l, bin, r)) {
-            hi = max(hi, key_of(l));
-            lo = min(lo, key_of(l));
-        }
-    });
-    cluster_max_min(r, hi, lo);
-    for (int level = 0; level < 3 && hi > lo; ++level) {   // bins of equal size, the largest keys first
-        const int shift = max(0, 32 - __clz(hi - lo) - 11);
-        clear_bins(r);
-        for_each(r, [&](float l, int) {
-            const uint32_t key = key_of(l);
-            if (key >= lo && key <= hi && takes_part(l, f.bin, r)) {
-                if (BY_MASS)
-                    add_to_bin(r.s, (hi - key) >> shift, weight_of(l, r.m, r.inv));
-                else
-                    atomicAdd(&r.s->count[(hi - key) >> shift], 1u);
-            }
-        });
-        const uint32_t first_bin = f.bin;
-        f = search<BY_MASS>(r, target, f);
-        hi -= f.bin << shift;
-        lo = max(lo, hi - min(hi, (1u << shift) - 1));
-        f.bin = first_bin;
-    }
-    Boundary b = {hi, 0, 0};
-    if (BY_MASS) {
-        const uint64_t w = weight_of(__uint_as_float(hi ^ ((hi >> 31) ? 0x80000000u : 0xffffffffu)), r.m, r.inv);
-        b.keep = (uint32_t)((target - f.mass_above + w - 1) / w);
-        b.mass = f.mass_above + b.keep * w;
-    } else {
-        b.keep = (uint32_t)target - f.count_above;
-    }
-    return b;
-}
-
-__device__ __forceinline__ uint64_t draw_at(float u, uint64_t total)
-{
-    const double drawn = floor((double)u * (double)total);
-    return drawn >= (double)total ? total - 1 : drawn > 0.0 ? (uint64_t)drawn : 0u;
-}
 
 // The first `n` words (a power of two) and, where PAIRS, their weights in rising order of the words.
 template <bool PAIRS> __device__ void sort_list(Shared *s, int n)
@@ -404,19 +357,147 @@ __device__ __forceinline__ int power_of_two(int n)
     return p;
 }
 
-// The whole choice among the `n` logits of the list: top-k and top-p along their order, the draw
-// along their indices.  Each thread holds four neighbours of the sorted list.
-__device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int64_t row, int32_t top_k, bool by_p, float top_p, uint32_t least)
+// The logits for which member(logit, bin) holds, listed in the cluster's first CTA if they are
+// at most SM_LIST; how many there are.  The list takes the place of the histograms.
+template <typename P> __device__ uint32_t gather(Row &r, int start, P member)
 {
     Shared *s = r.s;
-    const int e0 = 4 * (int)threadIdx.x;
-    int size = power_of_two(n);
+    if (threadIdx.x == 0)
+        s->list_n = 0;
+    __syncthreads();
+    for_each(r, [&](float l, int i) {
+        const uint32_t bin = bin_of(l, r.m, r.inv);
+        if (member(bin) && takes_part(l, bin, r)) {
+            const uint32_t e = atomicAdd(&s->list_n, 1u);
+            if (e < SM_LIST) {
+                s->list_order[e] = ((uint64_t)~key_of(l) << 32) | (uint32_t)(start + i);
+                s->list_w[e] = weight_of(l, r.m, r.inv);
+            }
+        }
+    });
+    __syncthreads();
+    const uint32_t mine = s->list_n;
+    const uint32_t all = share(r, 0, mine).count;
+    if (all > SM_LIST || r.ranks == 1)
+        return all;
+    if (r.rank == 0) {
+        uint32_t to = mine;
+        for (uint32_t q = 1; q < r.ranks; ++q) {
+            const uint32_t n = load_remote(&s->list_n, q);
+            for (uint32_t e = threadIdx.x; e < n; e += SM_THREADS) {
+                s->list_order[to + e] = load_remote(&s->list_order[e], q);
+                s->list_w[to + e] = load_remote(&s->list_w[e], q);
+            }
+            to += n;
+        }
+    }
+    agree(r);      // the other CTAs' lists are read
+    return all;
+}
+
+// Fills a list of n up to a power of two, which it returns, and sorts it.
+__device__ int sorted_list(Shared *s, int n)
+{
+    const int size = power_of_two(n);
     for (int e = n + threadIdx.x; e < size; e += SM_THREADS) {
         s->list_order[e] = ~0ull;
         s->list_w[e] = 0;
     }
     __syncthreads();
     sort_list<true>(s, size);
+    return size;
+}
+
+// The boundary in bin `f.bin` of the first histogram: `target` is reached there.
+template <bool BY_MASS> __device__ Boundary refine(Row &r, int start, uint64_t target, Found f)
+{
+    const uint32_t members = gather(r, start, [&](uint32_t bin) { return bin == f.bin; });
+    if (members <= SM_LIST) {      // sorted, the boundary is where the running sum gets there
+        const uint32_t turn = r.turn;
+        r.turn ^= 1u;
+        if (r.rank == 0) {
+            Shared *s = r.s;
+            sorted_list(s, (int)members);
+            const int e0 = 4 * (int)threadIdx.x;
+            uint64_t mass = 0;
+            uint32_t none = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                mass += e0 + j < (int)members ? (BY_MASS ? s->list_w[e0 + j] : 1u) : 0u;
+            uint64_t run = mass;
+            scan(r, run, none);
+            run += (BY_MASS ? f.mass_above : f.count_above) - mass;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (e0 + j < (int)members) {
+                    const uint64_t next = run + (BY_MASS ? s->list_w[e0 + j] : 1u);
+                    if (run < target && target <= next) {
+                        const uint32_t order = (uint32_t)(s->list_order[e0 + j] >> 32);
+                        int first = 0, past = e0 + j;      // the first of its equals
+                        while (first < past) {
+                            const int mid = (first + past) / 2;
+                            if ((uint32_t)(s->list_order[mid] >> 32) < order)
+                                first = mid + 1;
+                            else
+                                past = mid;
+                        }
+                        for (uint32_t q = 0; q < r.ranks; ++q) {
+                            store_remote(&s->found[turn].bin, q, ~order);
+                            store_remote(&s->found[turn].count_above, q, (uint32_t)(e0 + j - first + 1));
+                        }
+                    }
+                    run = next;
+                }
+        }
+        agree(r);
+        return Boundary{r.s->found[turn].bin, r.s->found[turn].count_above};
+    }
+    uint32_t hi = 0, lo = 0xffffffffu;
+    for_each(r, [&](float l, int) {
+        const uint32_t bin = bin_of(l, r.m, r.inv);
+        if (bin == f.bin && takes_part(l, bin, r)) {
+            hi = max(hi, key_of(l));
+            lo = min(lo, key_of(l));
+        }
+    });
+    cluster_max_min(r, hi, lo);
+    for (int level = 0; level < 3 && hi > lo; ++level) {   // bins of equal size, the largest keys first
+        const int shift = max(0, 32 - __clz(hi - lo) - 11);
+        clear_bins(r);
+        for_each(r, [&](float l, int) {
+            const uint32_t key = key_of(l);
+            if (key >= lo && key <= hi && takes_part(l, f.bin, r)) {
+                if (BY_MASS)
+                    add_to_bin(r.s, (hi - key) >> shift, weight_of(l, r.m, r.inv));
+                else
+                    atomicAdd(&r.s->count[(hi - key) >> shift], 1u);
+            }
+        });
+        const uint32_t first_bin = f.bin;
+        f = search<BY_MASS>(r, target, f);
+        hi -= f.bin << shift;
+        lo = max(lo, hi - min(hi, (1u << shift) - 1));
+        f.bin = first_bin;
+    }
+    if (!BY_MASS)
+        return Boundary{hi, (uint32_t)target - f.count_above};
+    const uint64_t w = weight_of(__uint_as_float(hi ^ ((hi >> 31) ? 0x80000000u : 0xffffffffu)), r.m, r.inv);
+    return Boundary{hi, (uint32_t)((target - f.mass_above + w - 1) / w)};
+}
+
+__device__ __forceinline__ uint64_t draw_at(float u, uint64_t total)
+{
+    const double drawn = floor((double)u * (double)total);
+    return drawn >= (double)total ? total - 1 : drawn > 0.0 ? (uint64_t)drawn : 0u;
+}
+
+// The whole choice among the `n` logits of the list: top-k and top-p along their order, the draw
+// along their indices.  Each thread holds four neighbours of the sorted list.
+__device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int64_t row, int32_t top_k, bool by_p, float top_p, uint32_t least)
+{
+    Shared *s = r.s;
+    const int e0 = 4 * (int)threadIdx.x;
+    int size = sorted_list(s, n);
     uint64_t order[4], mass = 0;
     uint32_t w[4], none = 0;
 #pragma unroll
@@ -572,7 +653,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     const float min_p = fminf(fmaxf(p.d_min_p ? p.d_min_p[row] : p.min_p, 0.0f), 1.0f);   // NaN: 0
     const uint32_t least = (uint32_t)ceil((double)min_p * 2147483648.0);     // w >= min_p * 2^31
     const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.0f;
-    Boundary last = {SM_KEY_NONE, 0xffffffffu, 0};   // everything stays
+    Boundary last = {SM_KEY_NONE, 0xffffffffu};   // everything stays
     const Found nothing = {0, 0, 0};
     bool cut_k = false;
     if (by_k) {           // counts alone: no exponentials
@@ -582,45 +663,20 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
             if (takes_part(l, bin, r))
                 atomicAdd(&s->count[bin], 1u);
         });
-        if (threadIdx.x == 0)
-            s->list_n = 0;
         Shares all;
         const Found f = search<false>(r, (uint64_t)top_k, nothing, &all);
         cut_k = all.count > (uint32_t)top_k;
         if (cut_k) {
             // the logits of the bins down to the boundary's, if they are few
-            for_each(r, [&](float l, int i) {
-                const uint32_t bin = bin_of(l, r.m, r.inv);
-                if (bin <= f.bin && takes_part(l, bin, r)) {
-                    const uint32_t e = atomicAdd(&s->list_n, 1u);
-                    if (e < SM_LIST) {
-                        s->list_order[e] = ((uint64_t)~key_of(l) << 32) | (uint32_t)(start + i);
-                        s->list_w[e] = weight_of(l, r.m, r.inv);
-                    }
+            if (top_k <= SM_LIST) {
+                const uint32_t n = gather(r, start, [&](uint32_t bin) { return bin <= f.bin; });
+                if (n <= SM_LIST) {
+                    if (r.rank == 0)
+                        choose_from_list(p, r, (int)n, row, top_k, by_p, top_p, least);
+                    return;
                 }
-            });
-            __syncthreads();
-            const uint32_t mine = s->list_n;
-            const Shares lists = share(r, 0, mine);
-            if (lists.count <= SM_LIST) {
-                if (r.rank == 0) {
-                    uint32_t to = mine;
-                    for (uint32_t q = 1; q < r.ranks; ++q) {
-                        const uint32_t n = load_remote(&s->list_n, q);
-                        for (uint32_t e = threadIdx.x; e < n; e += SM_THREADS) {
-                            s->list_order[to + e] = load_remote(&s->list_order[e], q);
-                            s->list_w[to + e] = load_remote(&s->list_w[e], q);
-                        }
-                        to += n;
-                    }
-                    __syncthreads();
-                }
-                agree(r);      // the other CTAs' lists are read
-                if (r.rank == 0)
-                    choose_from_list(p, r, (int)lists.count, row, top_k, by_p, top_p, least);
-                return;
             }
-            last = refine<false>(r, (uint64_t)top_k, f);
+            last = refine<false>(r, start, (uint64_t)top_k, f);
         }
     }
     if (by_p) {
@@ -643,7 +699,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
             all += (uint64_t)last.keep * weight_of(__uint_as_float(last.key ^ ((last.key >> 31) ? 0x80000000u : 0xffffffffu)), r.m, r.inv);
         const double want = ceil((double)top_p * (double)all);
         const uint64_t target = want >= 1.0 ? (uint64_t)want : 1u;   // a NaN top_p: the first alone
-        last = refine<true>(r, target, search<true>(r, target, nothing));
+        last = refine<true>(r, start, target, search<true>(r, target, nothing));
     }
 
     // kept weight of each segment, its equals of the boundary counted apart
