@@ -9,7 +9,8 @@
 // Design
 //  * A row is read once: a cluster of 1 to 8 CTAs holds it in shared memory as
 //    f32 (slices of up to 49152 logits), and every later pass runs on chip.  What
-//    bounds a row is the chain of passes and cluster barriers, so both are few.
+//    bounds a row is the chain of passes, scans and cluster barriers (about 500 cycles
+//    each), so all are few, and 64-bit floating point is left to one thread.
 //  * No sort.  A histogram over 2048 equal bins of (m - l) / T, which spread the
 //    bulk of a row over many bins, finds the bin in which top-k's count or top-p's
 //    weight is reached.  Logits whose weight is 0 cannot be chosen and take no part.
@@ -126,6 +127,7 @@ struct alignas(16) Shared {       // (the slice behind it is read 16 bytes at a 
     uint64_t warp_mass[SM_WARPS];
     uint32_t warp_count[SM_WARPS], warp_a[SM_WARPS], warp_b[SM_WARPS];
     uint64_t seg_mass[SM_SEGMENTS];
+    uint64_t word;                              // one thread's to all
     uint32_t seg_ties[SM_SEGMENTS];
     uint32_t list_n;                            // gathered logits of this CTA
 };
@@ -203,29 +205,24 @@ __device__ __forceinline__ void add_to_bin(Shared *s, uint32_t bin, uint32_t w)
     atomicAdd(&s->high[bin], w >> 16);
 }
 
-// Inclusive scans over the CTA's threads.
-__device__ __forceinline__ void scan(const Row &r, uint64_t &mass, uint32_t &count)
+// Inclusive scan over the CTA's threads (T uint64_t or uint32_t).
+template <typename T> __device__ __forceinline__ T scan(const Row &r, T v)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T *sums = reinterpret_cast<T *>(r.s->warp_mass);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const uint64_t m = __shfl_up_sync(dev::FULL_MASK, mass, d);
-        const uint32_t c = __shfl_up_sync(dev::FULL_MASK, count, d);
-        if (lane >= d) {
-            mass += m;
-            count += c;
-        }
+        const T up = __shfl_up_sync(dev::FULL_MASK, v, d);
+        v += lane >= d ? up : (T)0;
     }
-    if (lane == 31) {
-        r.s->warp_mass[warp] = mass;
-        r.s->warp_count[warp] = count;
-    }
+    if (lane == 31)
+        sums[warp] = v;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        mass += r.s->warp_mass[w];
-        count += r.s->warp_count[w];
-    }
+#pragma unroll
+    for (int w = 0; w < SM_WARPS - 1; ++w)
+        v += w < warp ? sums[w] : (T)0;
     __syncthreads();
+    return v;
 }
 
 // This CTA's mass and count to every CTA, and all of theirs: those of lower ranks, and in all.
@@ -285,7 +282,10 @@ template <bool BY_MASS> __device__ Found search(Row &r, uint64_t target, Found s
     }
     const uint64_t own_mass = mass;
     const uint32_t own_count = count;
-    scan(r, mass, count);
+    if (BY_MASS)
+        mass = scan(r, mass);
+    else
+        count = scan(r, count);
     const uint32_t turn = r.turn;
     if (threadIdx.x == 0)
         s->found[turn].bin = SM_BINS;               // (the owner writes after the next barrier)
@@ -377,35 +377,52 @@ template <typename P> __device__ uint32_t gather(Row &r, int start, P member)
     });
     __syncthreads();
     const uint32_t mine = s->list_n;
-    const uint32_t all = share(r, 0, mine).count;
-    if (all > SM_LIST || r.ranks == 1)
-        return all;
-    if (r.rank == 0) {
-        uint32_t to = mine;
-        for (uint32_t q = 1; q < r.ranks; ++q) {
-            const uint32_t n = load_remote(&s->list_n, q);
-            for (uint32_t e = threadIdx.x; e < n; e += SM_THREADS) {
-                s->list_order[to + e] = load_remote(&s->list_order[e], q);
-                s->list_w[to + e] = load_remote(&s->list_w[e], q);
-            }
-            to += n;
+    const Shares lists = share(r, 0, mine);
+    if (lists.count > SM_LIST || r.ranks == 1)
+        return lists.count;
+    if (r.rank > 0)                // behind the lists of the CTAs before
+        for (uint32_t e = threadIdx.x; e < mine; e += SM_THREADS) {
+            store_remote(&s->list_order[lists.count_below + e], 0, s->list_order[e]);
+            store_remote(&s->list_w[lists.count_below + e], 0, s->list_w[e]);
         }
-    }
-    agree(r);      // the other CTAs' lists are read
-    return all;
+    agree(r);
+    return lists.count;
 }
 
-// Fills a list of n up to a power of two, which it returns, and sorts it.
-__device__ int sorted_list(Shared *s, int n)
+// Sorts the first n words and, where PAIRS, their weights.  A short list is ranked by counting, each
+// of its words (all different) against the others by as many threads as there are for it: one
+// pass, where the sorting network has a barrier a step.
+template <bool PAIRS> __device__ void sorted_list(Shared *s, int n)
 {
+    if (n <= SM_THREADS) {
+        int each = 1;                              // threads of a word: neighbours in a warp
+        while (each < 16 && 2 * each * n <= SM_THREADS)
+            each *= 2;
+        const int e = (int)threadIdx.x / each, part = (int)threadIdx.x % each;
+        const uint64_t mine = e < n ? s->list_order[e] : ~0ull;
+        const uint32_t w = PAIRS && e < n ? s->list_w[e] : 0u;
+        int rank = 0;
+#pragma unroll 4
+        for (int j = part; j < n; j += each)
+            rank += s->list_order[j] < mine;
+        for (int d = each >> 1; d > 0; d >>= 1)
+            rank += __shfl_xor_sync(dev::FULL_MASK, rank, d);
+        __syncthreads();
+        if (e < n && part == 0) {
+            s->list_order[rank] = mine;
+            if (PAIRS)
+                s->list_w[rank] = w;
+        }
+        __syncthreads();
+        return;
+    }
     const int size = power_of_two(n);
     for (int e = n + threadIdx.x; e < size; e += SM_THREADS) {
         s->list_order[e] = ~0ull;
         s->list_w[e] = 0;
     }
     __syncthreads();
-    sort_list<true>(s, size);
-    return size;
+    sort_list<PAIRS>(s, size);
 }
 
 // The boundary in bin `f.bin` of the first histogram: `target` is reached there.
@@ -417,15 +434,13 @@ template <bool BY_MASS> __device__ Boundary refine(Row &r, int start, uint64_t t
         r.turn ^= 1u;
         if (r.rank == 0) {
             Shared *s = r.s;
-            sorted_list(s, (int)members);
+            sorted_list<true>(s, (int)members);
             const int e0 = 4 * (int)threadIdx.x;
             uint64_t mass = 0;
-            uint32_t none = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 mass += e0 + j < (int)members ? (BY_MASS ? s->list_w[e0 + j] : 1u) : 0u;
-            uint64_t run = mass;
-            scan(r, run, none);
+            uint64_t run = scan(r, mass);
             run += (BY_MASS ? f.mass_above : f.count_above) - mass;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -485,10 +500,28 @@ template <bool BY_MASS> __device__ Boundary refine(Row &r, int start, uint64_t t
     return Boundary{hi, (uint32_t)((target - f.mass_above + w - 1) / w)};
 }
 
-__device__ __forceinline__ uint64_t draw_at(float u, uint64_t total)
+// floor(u total), and ceil(part total) but at least 1, by one thread (the SM has few 64-bit units)
+// for all of the CTA.
+__device__ uint64_t draw_at(Shared *s, float u, uint64_t total)
 {
-    const double drawn = floor((double)u * (double)total);
-    return drawn >= (double)total ? total - 1 : drawn > 0.0 ? (uint64_t)drawn : 0u;
+    if (threadIdx.x == 0) {
+        const double drawn = floor((double)u * (double)total);
+        s->word = drawn >= (double)total ? total - 1 : drawn > 0.0 ? (uint64_t)drawn : 0u;
+    }
+    __syncthreads();
+    return s->word;
+}
+
+__device__ uint64_t part_of(Shared *s, float part, uint64_t total)
+{
+    if (threadIdx.x == 0) {
+        const double want = ceil((double)part * (double)total);
+        s->word = want >= 1.0 ? (uint64_t)want : 1u;      // no number: the first alone
+    }
+    __syncthreads();
+    const uint64_t word = s->word;
+    __syncthreads();
+    return word;
 }
 
 // The whole choice among the `n` logits of the list: top-k and top-p along their order, the draw
@@ -497,9 +530,9 @@ __device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int
 {
     Shared *s = r.s;
     const int e0 = 4 * (int)threadIdx.x;
-    int size = sorted_list(s, n);
+    sorted_list<true>(s, n);
     uint64_t order[4], mass = 0;
-    uint32_t w[4], none = 0;
+    uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const bool in = e0 + j < n && e0 + j < top_k;
@@ -507,16 +540,13 @@ __device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int
         w[j] = in ? s->list_w[e0 + j] : 0u;
         mass += w[j];
     }
-    uint64_t run = mass;
-    scan(r, run, none);
-    run -= mass;                               // above this thread's first
+    uint64_t run = scan(r, mass) - mass;       // above this thread's first
     uint64_t target = ~0ull;
     if (by_p) {
         if (threadIdx.x == SM_THREADS - 1)
             s->seg_mass[0] = run + mass;
         __syncthreads();
-        const double want = ceil((double)top_p * (double)s->seg_mass[0]);
-        target = want >= 1.0 ? (uint64_t)want : 1u;
+        target = part_of(s, top_p, s->seg_mass[0]);
     }
     int mine = 0;
 #pragma unroll
@@ -524,37 +554,35 @@ __device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int
         const bool keep = w[j] > 0 && run < target && w[j] >= least;
         run += w[j];
         order[j] = keep ? (order[j] << 32) | w[j] : ~0ull;
-        mine += keep;
+        mine = keep ? e0 + j + 1 : mine;
     }
-    // what stays stands at the front: its weights fall along the order
-    const int last = __reduce_max_sync(dev::FULL_MASK, mine ? e0 + 4 : 0);
+    // what stays stands at the front, for weights fall along the order
+    mine = __reduce_max_sync(dev::FULL_MASK, mine);
     if ((threadIdx.x & 31) == 0)
-        s->warp_a[threadIdx.x >> 5] = (uint32_t)last;
+        s->warp_a[threadIdx.x >> 5] = (uint32_t)mine;
     __syncthreads();
-    size = 0;
+    int kept = 0;
+#pragma unroll
     for (int q = 0; q < SM_WARPS; ++q)
-        size = max(size, (int)s->warp_a[q]);
-    size = power_of_two(size);
+        kept = max(kept, (int)s->warp_a[q]);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (e0 + j < size)
+        if (e0 + j < kept)
             s->list_order[e0 + j] = order[j];
     __syncthreads();
-    sort_list<false>(s, size);
+    sorted_list<false>(s, kept);
     mass = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        order[j] = e0 + j < size ? s->list_order[e0 + j] : ~0ull;
+        order[j] = e0 + j < kept ? s->list_order[e0 + j] : ~0ull;
         w[j] = order[j] == ~0ull ? 0u : (uint32_t)order[j];
         mass += w[j];
     }
-    run = mass;
-    scan(r, run, none);
+    run = scan(r, mass) - mass;
     if (threadIdx.x == SM_THREADS - 1)
-        s->seg_mass[1] = run;
+        s->seg_mass[1] = run + mass;
     __syncthreads();
-    const uint64_t total = s->seg_mass[1], at = draw_at(p.uniform[row], total);
-    run -= mass;
+    const uint64_t total = s->seg_mass[1], at = draw_at(s, p.uniform[row], total);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (run <= at && at < run + w[j]) {
@@ -651,7 +679,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     const int32_t top_k = p.d_top_k ? p.d_top_k[row] : p.top_k;
     const float top_p = p.d_top_p ? p.d_top_p[row] : p.top_p;
     const float min_p = fminf(fmaxf(p.d_min_p ? p.d_min_p[row] : p.min_p, 0.0f), 1.0f);   // NaN: 0
-    const uint32_t least = (uint32_t)ceil((double)min_p * 2147483648.0);     // w >= min_p * 2^31
+    const uint32_t least = __float2uint_ru(min_p * 2147483648.0f);     // w >= min_p * 2^31 (exact)
     const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.0f;
     Boundary last = {SM_KEY_NONE, 0xffffffffu};   // everything stays
     const Found nothing = {0, 0, 0};
@@ -683,7 +711,6 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         clear_bins(r);
         const uint32_t from = cut_k ? last.key : 0u;   // of the boundary's equals all: the target lies among those that stay
         uint64_t mass = 0;
-        uint32_t unused_count = 0;
         for_each(r, [&](float l, int) {
             const uint32_t key = key_of(l);
             const uint32_t w = key < from ? 0u : weight_of(l, r.m, r.inv);
@@ -693,12 +720,10 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
                     mass += w;
             }
         });
-        scan(r, mass, unused_count);
-        uint64_t all = share(r, mass, 0).mass;
+        uint64_t all = share(r, scan(r, mass), 0).mass;
         if (cut_k)
             all += (uint64_t)last.keep * weight_of(__uint_as_float(last.key ^ ((last.key >> 31) ? 0x80000000u : 0xffffffffu)), r.m, r.inv);
-        const double want = ceil((double)top_p * (double)all);
-        const uint64_t target = want >= 1.0 ? (uint64_t)want : 1u;   // a NaN top_p: the first alone
+        const uint64_t target = part_of(s, top_p, all);
         last = refine<true>(r, start, target, search<true>(r, target, nothing));
     }
 
@@ -731,58 +756,75 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         }
     }
     __syncthreads();
-    uint64_t mass = 0;
-    uint32_t ties = threadIdx.x < SM_SEGMENTS ? s->seg_ties[threadIdx.x] : 0u;
-    const uint32_t own_ties = ties;
-    scan(r, mass, ties);
-    const uint32_t ties_before = ties - own_ties + share(r, 0, ties).count_below;    // of this thread's segment
-    const uint32_t kept_ties = ties_before < last.keep ? min(own_ties, last.keep - ties_before) : 0u;
-    uint32_t none = 0;
+    uint32_t ties_before = 0, kept_ties = 0;       // the boundary's equals before this thread's segment, and kept in it
+    if (edge_w > 0) {
+        const uint32_t own_ties = threadIdx.x < SM_SEGMENTS ? s->seg_ties[threadIdx.x] : 0u, ties = scan(r, own_ties);
+        ties_before = ties - own_ties + share(r, 0, ties).count_below;
+        kept_ties = ties_before < last.keep ? min(own_ties, last.keep - ties_before) : 0u;
+    }
     const uint64_t own_mass = threadIdx.x < SM_SEGMENTS ? s->seg_mass[threadIdx.x] + kept_ties * edge_w : 0u;
-    mass = own_mass;
-    scan(r, mass, none);
-    const uint64_t cta_mass = mass;       // of the last thread: this CTA's
+    const uint64_t mass = scan(r, own_mass);       // of the last thread: this CTA's
     const Shares kept = share(r, mass, 0);
     const uint64_t total = kept.mass, before = kept.mass_below + mass - own_mass;
-    const uint64_t at = draw_at(p.uniform[row], total);
+    const uint64_t at = draw_at(s, p.uniform[row], total);
     if (threadIdx.x < SM_SEGMENTS && before <= at && at < before + own_mass) {
         s->warp_mass[0] = at - before;      // what to walk into this segment, and with how many equals
         s->warp_count[0] = last.keep > ties_before ? last.keep - ties_before : 0u;
         s->warp_a[0] = threadIdx.x;
     }
-    const bool here = __syncthreads_or(threadIdx.x == SM_THREADS - 1 && kept.mass_below <= at && at < kept.mass_below + cta_mass);
+    const bool here = __syncthreads_or(threadIdx.x == SM_THREADS - 1 && kept.mass_below <= at && at < kept.mass_below + mass);
     if (here && warp == 0) {
         uint64_t left = s->warp_mass[0];
         uint32_t keep = s->warp_count[0];
         const int g = (int)s->warp_a[0], end = min(r.n, (g + 1) * seg);
-        for (int i0 = g * seg; i0 < end; i0 += 32) {
-            const int i = i0 + lane;
-            const float l = i < end ? r.l[i] : -INFINITY;
-            const uint32_t tie_lanes = __ballot_sync(dev::FULL_MASK, i < end && l == edge);
-            const uint32_t mine = __popc(tie_lanes & ((1u << lane) - 1u));
-            uint64_t w = 0;
-            if (i < end && (l > edge || (l == edge && mine < keep))) {
-                w = weight_of(l, r.m, r.inv);
-                w = w >= least ? w : 0u;
+        for (int i0 = g * seg; i0 < end; i0 += 128) {      // four neighbours a lane
+            const int i = i0 + 4 * lane;
+            float l[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (i < end)
+                memcpy(l, r.l + i, sizeof(l));             // (filled up with -infinity)
+            uint32_t ties = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                ties += l[j] == edge;
+            uint32_t tie_run = ties;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t q = __shfl_up_sync(dev::FULL_MASK, tie_run, d);
+                tie_run += lane >= d ? q : 0u;
             }
-            uint64_t run = w;
+            const uint32_t round_ties = __shfl_sync(dev::FULL_MASK, tie_run, 31);
+            tie_run -= ties;
+            uint32_t w[4];
+            uint64_t sum = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool tie = l[j] == edge, stays = l[j] > edge || (tie && tie_run < keep);
+                w[j] = stays ? weight_of(l[j], r.m, r.inv) : 0u;
+                w[j] = w[j] >= least ? w[j] : 0u;
+                tie_run += tie;
+                sum += w[j];
+            }
+            uint64_t run = sum;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const uint64_t q = __shfl_up_sync(dev::FULL_MASK, run, d);
-                if (lane >= d)
-                    run += q;
+                run += lane >= d ? q : 0u;
             }
             const uint32_t past = __ballot_sync(dev::FULL_MASK, run > left);
             if (past) {
                 if (lane == __ffs(past) - 1) {
-                    p.token[row] = start + i;
+                    run -= sum;
+                    int j = 0;
+                    while (j < 3 && run + w[j] <= left)
+                        run += w[j++];
+                    p.token[row] = start + i + j;
                     if (p.logprob)
-                        p.logprob[row] = (float)log((double)w / (double)total);
+                        p.logprob[row] = (float)log((double)w[j] / (double)total);
                 }
                 break;
             }
             left -= __shfl_sync(dev::FULL_MASK, run, 31);
-            keep -= min(keep, (uint32_t)__popc(tie_lanes));
+            keep -= min(keep, round_ties);
         }
     }
     agree(r);   // no CTA ends while another may read its shared memory
