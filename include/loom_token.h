@@ -93,7 +93,9 @@ loom_status loom_i8_matmul(const int32_t *d_w_packed, const float *d_scale_w, in
 
 /* loom_i8_matmul with a device error word and tuning (either may be NULL).  Of
  * the tuning, `path` picks the engine (LOOM_PATH_DIRECT: dp4a; LOOM_PATH_TENSOR:
- * tensor cores; LOOM_PATH_STAGED -> LOOM_ERR_ARG) and wait_ns limits each device
+ * tensor cores, which want both matrices to start on 16 bytes, else LOOM_ERR_ALIGN;
+ * LOOM_PATH_STAGED -> LOOM_ERR_ARG; by default tensor cores where that holds and there are
+ * more than 8 tokens) and wait_ns limits each device
  * wait of the tensor-core kernel: one that runs out sets LOOM_DEVERR_TIMEOUT, the
  * affected y are NaN (acc INT32_MIN), and the device stays usable.  The engine
  * does not change a result. */

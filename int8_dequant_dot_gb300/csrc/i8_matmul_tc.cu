@@ -19,12 +19,18 @@
 //    together, and is what runs out first.  So the f16 weights go to tensor memory
 //    (tcgen05.st; the MMA's A operand) and only the f16 tokens go back to shared memory.
 //    A stage of 128 k of a 256 x 256 pair tile then moves 128 KB in 1024 MMA cycles.
-//  * Roles (20 warps, with one half 28): a loader copies 128 bytes of k of each row into a ring (one thread
-//    by TMA; where rows are not whole 16-byte pieces, three warps by asynchronous 4-byte
-//    copies), completing on an mbarrier; two groups of four converter warps (with one
+//  * Roles (20 warps, with one half 28): a loader copies 128 bytes of k of each row into a
+//    ring by TMA, completing on an mbarrier (rows that are not whole 16-byte pieces: see
+//    below); two groups of four converter warps (with one
 //    half: four groups) take stages in turn; one thread issues the MMAs; eight epilogue warps drain finished
 //    accumulators (each thread one channel and half the tokens, 128 running int32 sums in
 //    registers) and store: the lanes of a warp are neighbouring channels of a token.
+//  * Rows whose k is a multiple of 4 alone: TMA needs a row pitch of whole 16s, which four rows
+//    have together.  The matrix is seen as n / 4 rows of 4 k bytes; the rows of one of four
+//    classes (row mod 4) lie at a column of it, and a box of 144 bytes from the 16-byte
+//    boundary before brings their 128 bytes, which the converters shift into place.  The last
+//    n mod 4 rows are copied word by word.  (A bulk copy a row, and four-byte copies for all
+//    rows, took three and two times as long as the boxes.)
 //  * Tensor memory: accumulators of up to 128 tokens, used in turn (two alone, three in a
 //    pair), and a f16 weight buffer for each group of converters.  In a pair a tile of more than 128 tokens is two halves that share each stage: the
 //    accumulator of one half drains while the other's MMAs run, and a third takes the
@@ -45,7 +51,6 @@ namespace {
 constexpr int MT_KSTEP = 128;                 // k per stage: two 64-k swizzle atoms of the token operand
 constexpr int MT_CHUNK_STEPS = 1024 / MT_KSTEP;   // stages per f32 accumulator
 constexpr int MT_M = 128;                     // channels per CTA
-constexpr int MT_LOADERS = 3;                 // warps 1..3 (warp 0 issues the MMAs)
 constexpr int MT_CONV_WARP = 4, MT_EPI_WARPS = 8;
 constexpr int MT_ACC_COLS = 128, MT_A_COLS = 64;   // tensor memory: an accumulator, a weight buffer
 constexpr uint32_t MT_TMEM_COLS = 512;
@@ -174,6 +179,10 @@ __device__ __forceinline__ void to_f16(const int4 &v, uint32_t *h)
     tc::i8x4_to_f16x4((uint32_t)v.w, h[6], h[7]);
 }
 
+// The channel of a tensor-memory lane among its warp's 32.  Without whole 16-byte pieces the lanes
+// take rows of one class by eights: neighbours of a box, on different banks.
+template <bool V16> __device__ __forceinline__ int channel_of(int lane) { return V16 ? lane : (lane & 7) * 4 + (lane >> 3); }
+
 struct Tile {
     int64_t m0, t0;     // first channel and token of the tile
 };
@@ -229,64 +238,99 @@ __device__ __forceinline__ void load_role(const MatmulParams &p, const MatmulTcP
             dev::mbar_wait_bounded(bar_staged(area, (int)(i % q.ahead)), (uint32_t)(i / q.ahead) & 1u, 1000000000ull);
 }
 
-// Any other rows: warps copy four bytes a lane, a row of a stage at a time, eight rows (a
-// swizzle period) unrolled.  Rows and bytes past the end are zeros, and nothing is read there.
-__device__ __forceinline__ void copy_rows(uint32_t to, const int8_t *base, int64_t row0, int64_t total, int64_t pitch, int rows, int at, int left,
-                                          int loader, int lane)
-{
-    const int8_t *from = base + (row0 + 8 * loader) * pitch + at;
-    const int64_t live = total - row0;
-    uint32_t place[8];                                 // of this lane's word in row j of a period
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        place[j] = to + (uint32_t)(8 * loader + j) * 128 + ((((uint32_t)lane >> 2) ^ j) << 4);
-    for (int r = 8 * loader; r < rows; r += 8 * MT_LOADERS, from += 8 * MT_LOADERS * pitch) {
-        if (r + 8 <= live && __all_sync(dev::FULL_MASK, left > 0)) {
-            const int8_t *row = from;
-#pragma unroll
-            for (int j = 0; j < 8; ++j, row += pitch)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(place[j]), "l"(row) : "memory");
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool have = r + j < live && left > 0;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(place[j]), "l"(have ? from + j * pitch : base), "r"(have ? 4 : 0)
-                             : "memory");
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            place[j] += 8 * MT_LOADERS * 128;
-    }
-}
+// Rows of any k that is a multiple of 4.  A stage is, for each class of rows (row mod 4), the boxes
+// of the weights (32 rows of 144 bytes) and of each half's tokens, and places for the up to three
+// last rows of either matrix.
+constexpr int MT_PLACE = MT_KSTEP + 16;
+constexpr uint32_t MT_CLASS_W = MT_M / 4 * MT_PLACE;
+__host__ __device__ constexpr uint32_t class_x(int rows) { return ((uint32_t)rows / 4 * MT_PLACE + 127u) & ~127u; }   // TMA boxes start on 128 bytes
+__host__ __device__ constexpr uint32_t last_rows_at(int rows, int halves) { return 4 * (MT_CLASS_W + (uint32_t)halves * class_x(rows)); }
+__host__ __device__ constexpr uint32_t quads_stage(int rows, int halves) { return (last_rows_at(rows, halves) + 6 * MT_PLACE + 1023u) & ~1023u; }
 
+// By one thread: the boxes.
 template <int CG, int H>
-__device__ __forceinline__ void load_words_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t ring, int loader, int lane,
-                                                uint32_t pair_rank, const Work &w)
+__device__ __forceinline__ void load_quads_role(const MatmulParams &p, const MatmulTcPlan &q, const CUtensorMap *map_w, const CUtensorMap *map_x,
+                                                uint32_t area, uint32_t ring, uint32_t pair_rank, const Work &w)
 {
-    const int rows = q.tile_t / (CG * H);                   // of a half, in this CTA
+    const int rows = q.tile_t / (CG * H);                  // of a half, in this CTA
+    const uint32_t x_class = class_x(rows), bytes = (p.n >= 4 ? 4 * MT_CLASS_W : 0) + (p.tokens >= 4 ? (uint32_t)(H * rows * MT_PLACE) : 0);
+    const uint64_t policy = dev::l2_evict_last_policy();
     int s = 0;
     uint32_t phase = 1;
-    for (int64_t i = w.first; i < w.tiles; i += w.stride) {
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t i = w.first; ok && i < w.tiles; i += w.stride) {
         const Tile t = tile_at(q, i);
-        const int64_t m0 = t.m0 + pair_rank * MT_M;
-        for (int step = w.step0; step < w.step1; ++step) {
-            if (!__all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_freed(area, s), phase)))
-                return;
-            const uint32_t to = ring + (uint32_t)s * q.ahead_bytes + 4 * ((uint32_t)lane & 3);
-            const int at = step * MT_KSTEP + 4 * lane, left = p.k - at;
-            copy_rows(to, p.w, m0, p.n, p.k, MT_M, at, left, loader, lane);
+        const int m4 = (int)((t.m0 + pair_rank * MT_M) / 4), t4 = (int)(t.t0 / 4) + (int)pair_rank * (rows / 4);
+        for (int step = w.step0; step < w.step1; ++step, ++issued) {
+            ok = tc::role_wait(area + 8, p.error, p.wait_ns, bar_freed(area, s), phase);
+            if (!ok)
+                break;
+            const uint32_t to = ring + (uint32_t)s * q.ahead_bytes, bar = bar_staged(area, s);
+            dev::mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
-            for (int h = 0; h < H; ++h)
-                copy_rows(to + (uint32_t)(MT_M + h * rows) * 128, p.x, t.t0 + (h * CG + (int)pair_rank) * rows, p.tokens, p.k, rows, at, left, loader,
-                          lane);
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_staged(area, s)) : "memory");
+            for (int c = 0; c < 4; ++c) {
+                const int x = (c * p.k + step * MT_KSTEP) & ~15;
+                if (p.n >= 4)
+                    tc::tma_load_2d(to + c * MT_CLASS_W, map_w, x, m4, bar, policy);
+                if (p.tokens >= 4)
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        tc::tma_load_2d(to + 4 * MT_CLASS_W + (uint32_t)(h * 4 + c) * x_class, map_x, x, t4 + h * CG * (rows / 4), bar, policy);
+            }
             if (++s == q.ahead) {
                 s = 0;
                 phase ^= 1u;
             }
         }
     }
+    if (!ok)
+        for (int64_t i = issued > q.ahead ? issued - q.ahead : 0; i < issued; ++i)
+            dev::mbar_wait_bounded(bar_staged(area, (int)(i % q.ahead)), (uint32_t)(i / q.ahead) & 1u, 1000000000ull);
+}
+
+// By one warp: the last rows of both matrices, a word a lane.
+template <int CG, int H>
+__device__ __forceinline__ void load_last_rows_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t ring, int lane, const Work &w)
+{
+    int s = 0;
+    uint32_t phase = 1;
+    for (int64_t i = w.first; i < w.tiles; i += w.stride)
+        for (int step = w.step0; step < w.step1; ++step) {
+            if (!__all_sync(dev::FULL_MASK, tc::role_wait(area + 8, p.error, p.wait_ns, bar_freed(area, s), phase)))
+                return;
+            const uint32_t to = ring + (uint32_t)s * q.ahead_bytes + last_rows_at(q.tile_t / (CG * H), H);
+            const int at = step * MT_KSTEP + 4 * lane;
+            if (at < p.k)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int8_t *base = m ? p.x : p.w;
+                    const int total = m ? p.tokens : p.n;
+                    for (int j = 0; j < (total & 3); ++j) {
+                        const int8_t *row = base + (int64_t)((total & ~3) + j) * p.k;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + (uint32_t)(m * 3 + j) * MT_PLACE + 4 * lane +
+                                                                                     ((uint32_t)(j * p.k) & 15u)),
+                                     "l"(row + at)
+                                     : "memory");
+                    }
+                }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_staged(area, s)) : "memory");
+            if (++s == q.ahead) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
+}
+
+// N words from the `shift`-th of N + 3 on.
+template <int N> __device__ __forceinline__ void shift_words(uint32_t (&w)[N + 3], int shift)
+{
+#pragma unroll
+    for (int i = 0; i < N + 2; ++i)
+        w[i] = (shift & 1) ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        w[i] = (shift & 2) ? w[i + 2] : w[i];
 }
 
 // Whether a phase of `bar` is over, without waiting (try_wait may suspend the thread).
@@ -303,9 +347,9 @@ __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity)
 
 // ---- converters ----------------------------------------------------------------------
 // Group `group` of four warps takes every GROUPS-th of the CTA's `stages`.
-template <int CG, int H>
+template <int CG, int H, bool V16>
 __device__ __forceinline__ void convert_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t ring, uint32_t operands,
-                                             uint32_t tmem, int group, int sub, int lane, uint32_t leader, uint32_t stages)
+                                             uint32_t tmem, int group, int sub, int lane, uint32_t pair_rank, uint32_t leader, uint32_t stages, const Work &work)
 {
     using S = Shape<H>;
     const int b_rows = q.tile_t / CG;
@@ -316,7 +360,17 @@ __device__ __forceinline__ void convert_role(const MatmulParams &p, const Matmul
     const uint32_t b_from = MT_M * 128 + piece_at(r0, v);                  // r0 + 16: the same place 16 rows on
     const uint32_t b_to = (uint32_t)((v >> 2) * b_rows * 128 + (r0 >> 3) * 1024 + (r0 & 7) * 128);
     const uint32_t c0 = b_to + ((((v & 3) * 2) ^ (r0 & 7)) << 4), c1 = b_to + ((((v & 3) * 2 + 1) ^ (r0 & 7)) << 4);
-    const int row = 32 * sub + lane, key = row & 7;
+    const int row = 32 * sub + channel_of<V16>(lane), key = row & 7;
+    // Without whole 16-byte pieces: the word of a place that a row's bytes start at (tiles start
+    // at rows of whole 16s, so it stays), and this thread's places in the boxes.
+    const int a_shift = (int)((uint32_t)(row * p.k) & 15u) / 4, b_shift = (int)((uint32_t)(r0 * p.k) & 15u) / 4;
+    const int half_rows = b_rows / H;
+    const uint32_t a_place = (uint32_t)(row & 3) * MT_CLASS_W + (uint32_t)(row >> 2) * MT_PLACE;
+    const uint32_t b_place = 4 * MT_CLASS_W + (uint32_t)(r0 & 3) * class_x(half_rows) + (uint32_t)(r0 >> 2) * MT_PLACE + 16 * (uint32_t)v;
+    int64_t tile = work.first;
+    const int steps = work.step1 - work.step0;
+    int step = group % steps;                      // of the stage, from step0
+    tile += group / steps * work.stride;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * sub) << 16) + S::A_COL + (uint32_t)group * MT_A_COLS;
     int s = group;
     uint32_t s_phase = 0;
@@ -338,25 +392,55 @@ __device__ __forceinline__ void convert_role(const MatmulParams &p, const Matmul
         // buffers than token stages, later than what is waited for so far
         const uint32_t old = it - S::GROUPS, old_bar = bar_empty(area, (int)(old % S::DEPTH)), old_phase = (old / S::DEPTH) & 1u;
         bool a_free = S::DEPTH == S::GROUPS || it < S::GROUPS || test_wait(old_bar, old_phase);
-        const uint32_t from = ring + (uint32_t)s * q.ahead_bytes, a_from = from + (uint32_t)row * 128;
+        const uint32_t from = ring + (uint32_t)s * q.ahead_bytes;
+        uint32_t a_from = from + (V16 ? (uint32_t)row * 128 : 0u);
         const uint32_t to = operands + d * q.stage_bytes;
-        for (int r = 0; r < b_rows; r += 64) {
-            int4 in[4];
+        if constexpr (V16) {
+            for (int r = 0; r < b_rows; r += 64) {
+                int4 in[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (r + 16 * j < b_rows)
-                    in[j] = tc::lds128(from + b_from + (uint32_t)(r + 16 * j) * 128);
+                for (int j = 0; j < 4; ++j)
+                    if (r + 16 * j < b_rows)
+                        in[j] = tc::lds128(from + b_from + (uint32_t)(r + 16 * j) * 128);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (r + 16 * j < b_rows) {
-                    uint32_t out[8];
-                    to_f16(in[j], out);
-                    tc::sts128(to + c0 + (uint32_t)(r + 16 * j) * 128, out[0], out[1], out[2], out[3]);
-                    tc::sts128(to + c1 + (uint32_t)(r + 16 * j) * 128, out[4], out[5], out[6], out[7]);
-                }
+                for (int j = 0; j < 4; ++j)
+                    if (r + 16 * j < b_rows) {
+                        uint32_t out[8];
+                        to_f16(in[j], out);
+                        tc::sts128(to + c0 + (uint32_t)(r + 16 * j) * 128, out[0], out[1], out[2], out[3]);
+                        tc::sts128(to + c1 + (uint32_t)(r + 16 * j) * 128, out[4], out[5], out[6], out[7]);
+                    }
+            }
+        } else {
+            // what lies past k is some other row's: zero for the tokens, so that it counts for nothing
+            const Tile t = tile_at(q, tile);
+            const int left = (p.k - (work.step0 + step) * MT_KSTEP - 16 * v) / 4;
+            const uint32_t last_rows = from + last_rows_at(half_rows, H);
+            const uint32_t a_row = (uint32_t)(t.m0 + pair_rank * MT_M + row - (p.n & ~3));       // of the last rows, from 0
+            a_from = a_row < 3 ? last_rows + a_row * MT_PLACE : from + a_place;
+#pragma unroll 2
+            for (int r = 0; r < b_rows; r += 16) {
+                const int h = H == 2 && r >= half_rows ? 1 : 0, in_half = r - h * half_rows;
+                const uint32_t b_row = (uint32_t)(t.t0 + (h * CG + (int)pair_rank) * half_rows + in_half + r0 - (p.tokens & ~3));
+                const uint32_t at = b_row < 3 ? last_rows + (3 + b_row) * MT_PLACE + 16 * (uint32_t)v
+                                                            : from + b_place + (uint32_t)h * 4 * class_x(half_rows) + (uint32_t)in_half / 4 * MT_PLACE;
+                const int4 lo = tc::lds128(at), hi = tc::lds128(at + 16);
+                uint32_t in[7] = {(uint32_t)lo.x, (uint32_t)lo.y, (uint32_t)lo.z, (uint32_t)lo.w, (uint32_t)hi.x, (uint32_t)hi.y, (uint32_t)hi.z};
+                shift_words<4>(in, b_shift);
+                uint32_t out[8];
+                to_f16(make_int4(left > 0 ? (int)in[0] : 0, left > 1 ? (int)in[1] : 0, left > 2 ? (int)in[2] : 0, left > 3 ? (int)in[3] : 0), out);
+                tc::sts128(to + c0 + (uint32_t)r * 128, out[0], out[1], out[2], out[3]);
+                tc::sts128(to + c1 + (uint32_t)r * 128, out[4], out[5], out[6], out[7]);
+            }
         }
         // the weights: this thread's row, two pieces at a time
-        int4 next[2] = {tc::lds128(a_from + (uint32_t)((0 ^ key) << 4)), tc::lds128(a_from + (uint32_t)((1 ^ key) << 4))};
+        int4 next[2];
+        if constexpr (V16) {
+            next[0] = tc::lds128(a_from + (uint32_t)((0 ^ key) << 4));
+            next[1] = tc::lds128(a_from + (uint32_t)((1 ^ key) << 4));
+        } else {
+            next[1] = tc::lds128(a_from);
+        }
         a_free = a_free || tc::role_wait(area + 8, p.error, p.wait_ns, old_bar, old_phase);
         if (!__all_sync(dev::FULL_MASK, a_free))
             return;
@@ -364,11 +448,21 @@ __device__ __forceinline__ void convert_role(const MatmulParams &p, const Matmul
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             uint32_t out[16];
-            to_f16(next[0], out);
-            to_f16(next[1], out + 8);
-            if (h < 3) {
-                next[0] = tc::lds128(a_from + (uint32_t)(((2 * h + 2) ^ key) << 4));
-                next[1] = tc::lds128(a_from + (uint32_t)(((2 * h + 3) ^ key) << 4));
+            if constexpr (V16) {
+                to_f16(next[0], out);
+                to_f16(next[1], out + 8);
+                if (h < 3) {
+                    next[0] = tc::lds128(a_from + (uint32_t)(((2 * h + 2) ^ key) << 4));
+                    next[1] = tc::lds128(a_from + (uint32_t)(((2 * h + 3) ^ key) << 4));
+                }
+            } else {
+                const int4 a = next[1], b = tc::lds128(a_from + 32 * h + 16);
+                next[1] = tc::lds128(a_from + 32 * h + 32);
+                uint32_t in[11] = {(uint32_t)a.x, (uint32_t)a.y, (uint32_t)a.z, (uint32_t)a.w, (uint32_t)b.x, (uint32_t)b.y, (uint32_t)b.z,
+                                   (uint32_t)b.w, (uint32_t)next[1].x, (uint32_t)next[1].y, (uint32_t)next[1].z};
+                shift_words<8>(in, a_shift);
+                to_f16(make_int4((int)in[0], (int)in[1], (int)in[2], (int)in[3]), out);
+                to_f16(make_int4((int)in[4], (int)in[5], (int)in[6], (int)in[7]), out + 8);
             }
             tc::st16(lane_base + 16 * h, out);
         }
@@ -392,6 +486,8 @@ __device__ __forceinline__ void convert_role(const MatmulParams &p, const Matmul
         }
         s = s_next;
         s_phase = s_next_phase;
+        for (step += S::GROUPS; step >= steps; tile += work.stride)
+            step -= steps;
     }
     // the MMAs' arrivals on this CTA's barriers come before it may leave
     for (; it < stages + S::DEPTH; it += S::GROUPS)
@@ -581,7 +677,7 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < q.ahead; ++s) {
-            dev::mbar_init(bar_staged(area, s), V16 ? 1 : 32 * MT_LOADERS);
+            dev::mbar_init(bar_staged(area, s), V16 ? 1 : 1 + 32);
             dev::mbar_init(bar_freed(area, s), 4);
         }
         for (int s = 0; s < S::DEPTH; ++s) {
@@ -596,7 +692,7 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(area + 8), "r"(0u) : "memory");
         dev::fence_barrier_init();
     }
-    if (V16 && warp == 1 && lane == 0) {
+    if (warp == 1 && lane == 0) {
         tc::prefetch_map(&map_w);
         tc::prefetch_map(&map_x);
     }
@@ -612,10 +708,13 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
     if (warp < MT_CONV_WARP) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp > 0) {
-            if (!V16) {
-                load_words_role<CG, H>(p, q, area, ring, warp - 1, lane, pair_rank, w);
+            if (!V16 && warp == 1) {
+                if (elected())
+                    load_quads_role<CG, H>(p, q, &map_w, &map_x, area, ring, pair_rank, w);
+            } else if (!V16 && warp == 2) {
+                load_last_rows_role<CG, H>(p, q, area, ring, lane, w);
                 asm volatile("cp.async.wait_all;" ::: "memory");
-            } else if (warp == 1 && elected()) {
+            } else if (V16 && warp == 1 && elected()) {
                 load_role<CG, H>(p, q, &map_w, &map_x, area, ring, pair_rank, w);
             }
         } else if (CG == 1 || pair_rank == 0) {
@@ -633,7 +732,7 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        convert_role<CG, H>(p, q, area, ring, operands, tmem, (warp - MT_CONV_WARP) >> 2, warp & 3, lane, leader, (uint32_t)(work * (w.step1 - w.step0)));
+        convert_role<CG, H, V16>(p, q, area, ring, operands, tmem, (warp - MT_CONV_WARP) >> 2, warp & 3, lane, pair_rank, leader, (uint32_t)(work * (w.step1 - w.step0)), w);
         __syncwarp();
     } else {
         if (H == 1)
@@ -662,7 +761,7 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
                 break;   // one tile per cluster
             }
             const Tile t = tile_at(q, i);
-            const int64_t channel = t.m0 + pair_rank * MT_M + 32 * sub + lane;
+            const int64_t channel = t.m0 + pair_rank * MT_M + 32 * sub + channel_of<V16>(lane);
             if (channel < p.n) {
                 const float sw = p.scale_w[channel], bias = p.bias ? p.bias[channel] : 0.0f;
 #pragma unroll
@@ -682,7 +781,7 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
     if (q.split > 1 && warp >= S::EPI_WARP) {
         const int sub = warp & 3, half = (warp - S::EPI_WARP) >> 2;
         const Tile t = tile_at(q, w.first);
-        const int64_t channel = t.m0 + pair_rank * MT_M + 32 * sub + lane;
+        const int64_t channel = t.m0 + pair_rank * MT_M + 32 * sub + channel_of<V16>(lane);
         bool ok = true;
         for (int s = 0; s < CG * q.split; ++s) {
             uint32_t bad;
@@ -707,8 +806,8 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
         tmem_free<CG>(tmem);
 }
 
-// Rows of k bytes in boxes of 128 bytes of `rows` rows, 128-byte swizzle.
-bool encode_rows(CUtensorMap *map, const int8_t *base, int64_t k, int64_t outer, int rows)
+// Rows of `pitch` bytes in boxes of `width` bytes of `rows` rows; boxes of 128 bytes swizzled.
+bool encode_rows(CUtensorMap *map, const int8_t *base, int64_t pitch, int64_t outer, int width, int rows)
 {
     typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -720,10 +819,10 @@ bool encode_rows(CUtensorMap *map, const int8_t *base, int64_t k, int64_t outer,
                    ? reinterpret_cast<Encode>(f)
                    : nullptr;
     }();
-    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)outer}, strides[1] = {(cuuint64_t)k};
-    const cuuint32_t box[2] = {MT_KSTEP, (cuuint32_t)rows}, unit[2] = {1, 1};
+    const cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)(outer > 0 ? outer : 1)}, strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)rows}, unit[2] = {1, 1};
     return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(base), dims, strides, box, unit,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, width == MT_KSTEP ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -737,7 +836,10 @@ template <int CG, int H, bool V16> cudaError_t launch_cg(const MatmulParams &p, 
     if (e != cudaSuccess)
         return e;
     CUtensorMap map_w = {}, map_x = {};
-    if (V16 && (!encode_rows(&map_w, p.w, p.k, p.n, MT_M) || !encode_rows(&map_x, p.x, p.k, p.tokens, q.tile_t / (CG * H))))
+    const int rows = q.tile_t / (CG * H);
+    if (V16 ? !encode_rows(&map_w, p.w, p.k, p.n, MT_KSTEP, MT_M) || !encode_rows(&map_x, p.x, p.k, p.tokens, MT_KSTEP, rows)
+            : !encode_rows(&map_w, p.w, 4 * (int64_t)p.k, p.n / 4, MT_PLACE, MT_M / 4) ||
+                  !encode_rows(&map_x, p.x, 4 * (int64_t)p.k, p.tokens / 4, MT_PLACE, rows / 4))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)q.grid);
@@ -761,7 +863,7 @@ int matmul_tc_threads(const MatmulTcPlan &q) { return q.halves == 1 ? Shape<1>::
 
 // Tile, split of k and grid.  The time of a choice is its waves of tiles times the stages of
 // one tile, plus what a tile (or a split) costs once, in units of a stage.
-void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, int64_t sms, MatmulTcPlan *out)
+void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, bool vec16, int64_t sms, MatmulTcPlan *out)
 {
     MatmulTcPlan best = {};
     double best_cost = 0.0;
@@ -789,7 +891,7 @@ void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, int64_t sms, MatmulTcP
     best.tiles_m = (int32_t)tiles_m;
     best.tiles_t = (int32_t)tiles_t;
     best.stage_bytes = (uint32_t)(tile_t / cg) * 2 * MT_KSTEP;
-    best.ahead_bytes = (uint32_t)(MT_M + tile_t / cg) * MT_KSTEP;
+    best.ahead_bytes = vec16 ? (uint32_t)(MT_M + tile_t / cg) * MT_KSTEP : quads_stage((int)tile_t / (cg * halves), halves);
     const uint32_t operands = (uint32_t)(halves == 1 ? Shape<1>::DEPTH : Shape<2>::DEPTH) * best.stage_bytes;
     const int64_t room = (MT_ROOM - operands) / best.ahead_bytes;
     best.ahead = (int32_t)(room < MT_MAX_AHEAD ? room : MT_MAX_AHEAD);

@@ -46,7 +46,8 @@ loom_launch plain_launch(int64_t gx, int64_t gy, uint32_t block, uint32_t kernel
 }
 
 // `sms` 0: the current device's.
-loom_status matmul_geometry(int64_t tokens, int64_t n, int64_t k, int64_t path, int64_t sms, loom_launch *out,
+// `aligned`: both matrices start on 16 bytes (the tensor cores' copies need that).
+loom_status matmul_geometry(int64_t tokens, int64_t n, int64_t k, bool aligned, int64_t path, int64_t sms, loom_launch *out,
                             MatmulTcPlan *plan)
 {
     if (tokens < 0 || tokens > MAX_INT || n < 0 || n > MAX_INT || k < 0 || k > MAX_K || k % 4)
@@ -58,9 +59,11 @@ loom_status matmul_geometry(int64_t tokens, int64_t n, int64_t k, int64_t path, 
         if (st != LOOM_OK)
             return st;
     }
-    const bool tensor = path == LOOM_PATH_TENSOR || (path == LOOM_PATH_AUTO && tokens > MM_DP4A_PASS);
+    if (path == LOOM_PATH_TENSOR && !aligned)
+        return LOOM_ERR_ALIGN;
+    const bool tensor = path == LOOM_PATH_TENSOR || (path == LOOM_PATH_AUTO && aligned && tokens > MM_DP4A_PASS);
     if (tensor && k > 0 && n > 0 && tokens > 0) {
-        matmul_tc_plan(tokens, n, k, sms, plan);
+        matmul_tc_plan(tokens, n, k, k % 16 == 0, sms, plan);
         *out = plain_launch(plan->grid, 1, (uint32_t)matmul_tc_threads(*plan), LOOM_KERNEL_I8_MATMUL_TENSOR, 128u);
         out->cluster[0] = (uint32_t)(plan->cg * plan->split);
         out->smem_bytes = plan->smem_bytes;
@@ -166,7 +169,7 @@ extern "C" loom_status loom_token_launch_config(int32_t op, const int64_t *w, in
             return LOOM_ERR_ARG;
     {
         MatmulTcPlan plan;
-        return matmul_geometry(w[0], w[1], w[2], opt(4, LOOM_PATH_AUTO), opt(5, 0), out, &plan);
+        return matmul_geometry(w[0], w[1], w[2], opt(3, 1) != 0, opt(4, LOOM_PATH_AUTO), opt(5, 0), out, &plan);
     }
     case LOOM_OP_LAYER_NORM_BACKWARD: {
         if (n < 3 || !known((int32_t)w[2]) || opt(4, 0) < 0)
@@ -229,9 +232,10 @@ extern "C" loom_status loom_i8_matmul_ex(const int32_t *d_w_packed, const float 
     if (misaligned(d_w_packed, 4) || misaligned(d_x_packed, 4) || misaligned(d_scale_w, 4) || misaligned(d_scale_x, 4) ||
         misaligned(d_bias, 4) || misaligned(d_acc, 4) || misaligned(d_error, 4) || misaligned(d_y, dtype_bytes(y_dtype)))
         return LOOM_ERR_ALIGN;
+    const bool aligned = !misaligned(d_w_packed, 16) && !misaligned(d_x_packed, 16);
     loom_launch L;
     MatmulTcPlan plan;
-    const loom_status st = matmul_geometry(tokens, n_rows, k, tuning ? tuning->path : LOOM_PATH_AUTO, 0, &L, &plan);
+    const loom_status st = matmul_geometry(tokens, n_rows, k, aligned, tuning ? tuning->path : LOOM_PATH_AUTO, 0, &L, &plan);
     if (st != LOOM_OK)
         return st;
     MatmulParams p = {};
@@ -250,10 +254,9 @@ extern "C" loom_status loom_i8_matmul_ex(const int32_t *d_w_packed, const float 
     p.y_dtype = y_dtype;
     p.rows_per_cta = (int32_t)L.units_per_cta;
     p.wait_ns = tuning && tuning->wait_ns ? (uint64_t)tuning->wait_ns : DEFAULT_WAIT_NS;
-    const bool vec16 = k % 16 == 0 && !misaligned(d_w_packed, 16) && !misaligned(d_x_packed, 16);
     if (L.kernel == LOOM_KERNEL_I8_MATMUL_TENSOR)
-        return of_cuda(launch_matmul_tc(p, plan, vec16, static_cast<cudaStream_t>(stream)));
-    return of_cuda(launch_matmul_dp4a(p, vec16, L, static_cast<cudaStream_t>(stream)));
+        return of_cuda(launch_matmul_tc(p, plan, k % 16 == 0, static_cast<cudaStream_t>(stream)));
+    return of_cuda(launch_matmul_dp4a(p, aligned && k % 16 == 0, L, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" loom_status loom_i8_matmul(const int32_t *d_w_packed, const float *d_scale_w, int32_t n_rows, int32_t k,
