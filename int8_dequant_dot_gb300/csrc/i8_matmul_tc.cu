@@ -589,9 +589,10 @@ __device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, i
 #pragma unroll
     for (int j = 0; j < N; ++j)
         a[j] = 0;
-    for (int s = 0; s < split; s += 2) {          // split is even
+    for (int s = 0; s < split; s += 2) {
+        const bool two = s + 1 < split;
         const uint32_t from0 = map_to(at, (uint32_t)(s * CG) + first) + (uint32_t)c * 512;
-        const uint32_t from1 = map_to(at, (uint32_t)((s + 1) * CG) + first) + (uint32_t)c * 512;
+        const uint32_t from1 = map_to(at, (uint32_t)((two ? s + 1 : s) * CG) + first) + (uint32_t)c * 512;
         int32_t v0[N], v1[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -600,7 +601,7 @@ __device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, i
         }
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            a[j] += v0[j] + v1[j];
+            a[j] += v0[j] + (two ? v1[j] : 0);
     }
     store_tokens<N>(p, t, channel, a, p.scale_w[channel], p.bias ? p.bias[channel] : 0.0f, ok);
 }
@@ -872,9 +873,11 @@ void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, bool vec16, int64_t sm
     const int64_t tiles_m = (n + MT_M * cg - 1) / (MT_M * cg), tiles = tiles_m * tiles_t;
     const int64_t quantum = 32 * halves;  // each half's columns, shared by two warps (and CTAs), are whole 16s
     const int64_t tile_t = ((tokens + tiles_t - 1) / tiles_t + quantum - 1) / quantum * quantum;   // up to 256
-    for (int split = 1; cg * split <= 8; split *= 2) {
-        // clusters of four and eight CTAs leave some SMs of a GPC idle
-        const int64_t size = cg * split, slots = size <= 2 ? sms / size : size == 4 ? sms / 4 - 2 : sms / 8 - 3;
+    // clusters of 1 to 8 of these CTAs (one an SM) that fit GB300's 152 SMs at a time, by
+    // cudaOccupancyMaxActiveClusters: a cluster lies within one of the GPU's uneven groups of SMs
+    static const int fits[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+    for (int split = 1; cg * split <= 8; ++split) {
+        const int64_t size = cg * split, slots = fits[size] * sms / 152;
         if (slots < 1 || (split > 1 && (tiles > slots || split > steps)))
             continue;
         const int64_t waves = (tiles + slots - 1) / slots;
