@@ -139,7 +139,7 @@ struct Row {              // what the threads of a cluster agree on
     float *l;             // this CTA's slice
     int n, slice, seg;    // logits of this CTA, of a full slice, of a segment
     uint32_t rank, ranks;
-    float m, inv;
+    float m, inv, bins_per_unit;      // largest logit, 1 / T, SM_BIN_SCALE / T
     uint32_t turn;        // which places are used next
 };
 
@@ -192,10 +192,15 @@ __device__ __forceinline__ void cluster_max_min(Row &r, uint32_t &a, uint32_t &b
     }
 }
 
-__device__ __forceinline__ void clear_bins(const Row &r)
+template <bool BY_MASS> __device__ __forceinline__ void clear_bins(const Row &r)
 {
-    for (int i = threadIdx.x; i < SM_BINS; i += SM_THREADS)
-        r.s->count[i] = r.s->low[i] = r.s->high[i] = 0;
+#pragma unroll
+    for (int i = threadIdx.x; i < SM_BINS; i += SM_THREADS) {
+        if (BY_MASS)
+            r.s->low[i] = r.s->high[i] = 0;
+        else
+            r.s->count[i] = 0;
+    }
     __syncthreads();
 }
 
@@ -310,10 +315,10 @@ template <bool BY_MASS> __device__ Found search(Row &r, uint64_t target, Found s
     return s->found[turn];
 }
 
-__device__ __forceinline__ uint32_t bin_of(float l, float m, float inv)
+// (fminf takes what is no number, a logit without weight, to the last bin.)
+__device__ __forceinline__ uint32_t bin_of(float l, const Row &r)
 {
-    // (fminf takes what is no number, a logit without weight, to the last bin)
-    return l == m ? 0u : (uint32_t)(int)fminf(-exponent_of(l, m, inv) * SM_BIN_SCALE, (float)(SM_BINS - 1));
+    return l == r.m ? 0u : (uint32_t)(int)fminf((r.m - l) * r.bins_per_unit, (float)(SM_BINS - 1));
 }
 
 // Whether a logit takes part (its weight is above 0), from its bin: the exponential is needed at
@@ -366,7 +371,7 @@ template <typename P> __device__ uint32_t gather(Row &r, int start, P member)
         s->list_n = 0;
     __syncthreads();
     for_each(r, [&](float l, int i) {
-        const uint32_t bin = bin_of(l, r.m, r.inv);
+        const uint32_t bin = bin_of(l, r);
         if (member(bin) && takes_part(l, bin, r)) {
             const uint32_t e = atomicAdd(&s->list_n, 1u);
             if (e < SM_LIST) {
@@ -469,7 +474,7 @@ template <bool BY_MASS> __device__ Boundary refine(Row &r, int start, uint64_t t
     }
     uint32_t hi = 0, lo = 0xffffffffu;
     for_each(r, [&](float l, int) {
-        const uint32_t bin = bin_of(l, r.m, r.inv);
+        const uint32_t bin = bin_of(l, r);
         if (bin == f.bin && takes_part(l, bin, r)) {
             hi = max(hi, key_of(l));
             lo = min(lo, key_of(l));
@@ -478,7 +483,7 @@ template <bool BY_MASS> __device__ Boundary refine(Row &r, int start, uint64_t t
     cluster_max_min(r, hi, lo);
     for (int level = 0; level < 3 && hi > lo; ++level) {   // bins of equal size, the largest keys first
         const int shift = max(0, 32 - __clz(hi - lo) - 11);
-        clear_bins(r);
+        clear_bins<BY_MASS>(r);
         for_each(r, [&](float l, int) {
             const uint32_t key = key_of(l);
             if (key >= lo && key <= hi && takes_part(l, f.bin, r)) {
@@ -612,37 +617,37 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     r.n = max(0, min(slice, p.vocab - start));
     dev::follow_previous_kernel();
 
-    // the slice, with NaN as -infinity and one zero
+    // the slice, with NaN as -infinity (fmaxf) and one zero (-0 + 0 = 0)
     const E *src = static_cast<const E *>(p.logits) + row * p.stride + start;
-    uint32_t top = SM_KEY_NONE, unused = 0xffffffffu;
+    float largest = -INFINITY;
+    auto put = [&](int i, E v) {
+        const float l = fmaxf(__fadd_rn(dev::to_f32(v), 0.0f), -INFINITY);
+        r.l[i] = l;
+        largest = fmaxf(largest, l);
+    };
     constexpr int V = dev::Vec16<E>::N;
+    int done = 0;
     if (reinterpret_cast<uintptr_t>(src) % 16 == 0) {
-        const int whole = r.n / V;
+        done = r.n / V * V;
 #pragma unroll 4
-        for (int i = threadIdx.x; i < whole; i += SM_THREADS) {
-            const dev::Vec16<E> v = reinterpret_cast<const dev::Vec16<E> *>(src)[i];
+        for (int i = V * threadIdx.x; i < done; i += V * SM_THREADS) {
+            const dev::Vec16<E> v = *reinterpret_cast<const dev::Vec16<E> *>(src + i);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float l = __fadd_rn(dev::to_f32(v.e[j]), 0.0f);
-                l = l == l ? l : -INFINITY;
-                r.l[i * V + j] = l;
-                top = max(top, key_of(l));
+            for (int j = 0; j < V; j += 4) {
+                float4 q;
+                q.x = fmaxf(__fadd_rn(dev::to_f32(v.e[j]), 0.0f), -INFINITY);
+                q.y = fmaxf(__fadd_rn(dev::to_f32(v.e[j + 1]), 0.0f), -INFINITY);
+                q.z = fmaxf(__fadd_rn(dev::to_f32(v.e[j + 2]), 0.0f), -INFINITY);
+                q.w = fmaxf(__fadd_rn(dev::to_f32(v.e[j + 3]), 0.0f), -INFINITY);
+                *reinterpret_cast<float4 *>(r.l + i + j) = q;
+                largest = fmaxf(largest, fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)));
             }
         }
-        for (int i = whole * V + threadIdx.x; i < r.n; i += SM_THREADS) {
-            float l = __fadd_rn(dev::to_f32(src[i]), 0.0f);
-            l = l == l ? l : -INFINITY;
-            r.l[i] = l;
-            top = max(top, key_of(l));
-        }
-    } else {
-        for (int i = threadIdx.x; i < r.n; i += SM_THREADS) {
-            float l = __fadd_rn(dev::to_f32(src[i]), 0.0f);
-            l = l == l ? l : -INFINITY;
-            r.l[i] = l;
-            top = max(top, key_of(l));
-        }
     }
+#pragma unroll 8
+    for (int i = done + threadIdx.x; i < r.n; i += SM_THREADS)
+        put(i, src[i]);
+    uint32_t top = key_of(largest), unused = 0xffffffffu;
     if (threadIdx.x < 3 && r.n + (int)threadIdx.x < (r.n + 3) / 4 * 4)
         r.l[r.n + threadIdx.x] = -INFINITY;
     agree(r);   // every CTA of the cluster runs: its shared memory may be written
@@ -675,6 +680,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         return;
     }
     r.inv = __fdiv_rn(1.0f, t);
+    r.bins_per_unit = r.inv * SM_BIN_SCALE;
 
     const int32_t top_k = p.d_top_k ? p.d_top_k[row] : p.top_k;
     const float top_p = p.d_top_p ? p.d_top_p[row] : p.top_p;
@@ -685,9 +691,9 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     const Found nothing = {0, 0, 0};
     bool cut_k = false;
     if (by_k) {           // counts alone: no exponentials
-        clear_bins(r);
+        clear_bins<false>(r);
         for_each(r, [&](float l, int) {
-            const uint32_t bin = bin_of(l, r.m, r.inv);
+            const uint32_t bin = bin_of(l, r);
             if (takes_part(l, bin, r))
                 atomicAdd(&s->count[bin], 1u);
         });
@@ -708,14 +714,14 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         }
     }
     if (by_p) {
-        clear_bins(r);
+        clear_bins<true>(r);
         const uint32_t from = cut_k ? last.key : 0u;   // of the boundary's equals all: the target lies among those that stay
         uint64_t mass = 0;
         for_each(r, [&](float l, int) {
             const uint32_t key = key_of(l);
             const uint32_t w = key < from ? 0u : weight_of(l, r.m, r.inv);
             if (w > 0) {
-                add_to_bin(s, bin_of(l, r.m, r.inv), w);
+                add_to_bin(s, bin_of(l, r), w);
                 if (!cut_k || key > from)
                     mass += w;
             }
