@@ -51,13 +51,16 @@ __device__ __forceinline__ uint32_t key_of(float l)
     return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__device__ __forceinline__ float exponent_of(float l, float m, float inv) { return (l - m) * inv; }
+__device__ __forceinline__ float logit_of(uint32_t key) { return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu)); }
 
-// (What is no number, or -infinity, converts to 0.)
-__device__ __forceinline__ uint32_t weight_of(float l, float m, float inv)
+// 2^31 for the largest logit, which is finite here.  (What is no number, or -infinity, converts to 0.)
+__device__ __forceinline__ uint32_t weight_of(float l, float m, float inv) { return __float2uint_rz(expf((l - m) * inv) * 2147483648.0f); }
+
+// Sum over a warp of what adds up to less than 2^56.
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v)
 {
-    const uint32_t w = __float2uint_rz(expf(exponent_of(l, m, inv)) * 2147483648.0f);
-    return l == m ? SM_FULL : w;
+    const uint32_t low = __reduce_add_sync(dev::FULL_MASK, (uint32_t)v & 0xffffffu);
+    return low + ((uint64_t)__reduce_add_sync(dev::FULL_MASK, (uint32_t)(v >> 24)) << 24);
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -184,12 +187,8 @@ __device__ __forceinline__ void cluster_max_min(Row &r, uint32_t &a, uint32_t &b
         store_remote(&r.s->key_min[turn][r.rank], threadIdx.x, b);
     }
     agree(r);
-    a = 0;
-    b = 0xffffffffu;
-    for (uint32_t q = 0; q < r.ranks; ++q) {
-        a = max(a, r.s->key_max[turn][q]);
-        b = min(b, r.s->key_min[turn][q]);
-    }
+    a = __reduce_max_sync(dev::FULL_MASK, lane < (int)r.ranks ? r.s->key_max[turn][lane] : 0u);
+    b = __reduce_min_sync(dev::FULL_MASK, lane < (int)r.ranks ? r.s->key_min[turn][lane] : 0xffffffffu);
 }
 
 template <bool BY_MASS> __device__ __forceinline__ void clear_bins(const Row &r)
@@ -210,6 +209,8 @@ __device__ __forceinline__ void add_to_bin(Shared *s, uint32_t bin, uint32_t w)
     atomicAdd(&s->high[bin], w >> 16);
 }
 
+__device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(dev::FULL_MASK, v); }
+
 // Inclusive scan over the CTA's threads (T uint64_t or uint32_t).
 template <typename T> __device__ __forceinline__ T scan(const Row &r, T v)
 {
@@ -223,9 +224,7 @@ template <typename T> __device__ __forceinline__ T scan(const Row &r, T v)
     if (lane == 31)
         sums[warp] = v;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < SM_WARPS - 1; ++w)
-        v += w < warp ? sums[w] : (T)0;
+    v += warp_sum(lane < warp ? sums[lane] : (T)0);
     __syncthreads();
     return v;
 }
@@ -237,24 +236,20 @@ struct Shares {
 };
 __device__ __forceinline__ Shares share(Row &r, uint64_t mass, uint32_t count)   // values of the last thread
 {
-    const uint32_t turn = r.turn;
+    const uint32_t turn = r.turn, lane = threadIdx.x & 31;
     r.turn ^= 1u;
-    if (threadIdx.x == SM_THREADS - 1)
-        for (uint32_t q = 0; q < r.ranks; ++q) {
-            store_remote(&r.s->share_mass[turn][r.rank], q, mass);
-            store_remote(&r.s->share_count[turn][r.rank], q, count);
+    if (threadIdx.x >= SM_THREADS - 32) {
+        mass = __shfl_sync(dev::FULL_MASK, mass, 31);
+        count = __shfl_sync(dev::FULL_MASK, count, 31);
+        if (lane < r.ranks) {
+            store_remote(&r.s->share_mass[turn][r.rank], lane, mass);
+            store_remote(&r.s->share_count[turn][r.rank], lane, count);
         }
-    agree(r);
-    Shares t = {0, 0, 0, 0};
-    for (uint32_t q = 0; q < r.ranks; ++q) {
-        if (q < r.rank) {
-            t.mass_below += r.s->share_mass[turn][q];
-            t.count_below += r.s->share_count[turn][q];
-        }
-        t.mass += r.s->share_mass[turn][q];
-        t.count += r.s->share_count[turn][q];
     }
-    return t;
+    agree(r);
+    mass = lane < r.ranks ? r.s->share_mass[turn][lane] : 0u;
+    count = lane < r.ranks ? r.s->share_count[turn][lane] : 0u;
+    return Shares{warp_sum(lane < r.rank ? mass : (uint64_t)0), warp_sum(mass), warp_sum(lane < r.rank ? count : 0u), warp_sum(count)};
 }
 
 // The bin in which the running count (or mass) from bin 0 up reaches `target`,
@@ -318,7 +313,7 @@ template <bool BY_MASS> __device__ Found search(Row &r, uint64_t target, Found s
 // (fminf takes what is no number, a logit without weight, to the last bin.)
 __device__ __forceinline__ uint32_t bin_of(float l, const Row &r)
 {
-    return l == r.m ? 0u : (uint32_t)(int)fminf((r.m - l) * r.bins_per_unit, (float)(SM_BINS - 1));
+    return (uint32_t)(int)fminf((r.m - l) * r.bins_per_unit, (float)(SM_BINS - 1));
 }
 
 // Whether a logit takes part (its weight is above 0), from its bin: the exponential is needed at
@@ -362,21 +357,22 @@ __device__ __forceinline__ int power_of_two(int n)
     return p;
 }
 
-// The logits for which member(logit, bin) holds, listed in the cluster's first CTA if they are
+// The logits of the bins `from` to `to` that take part, listed in the cluster's first CTA if they are
 // at most SM_LIST; how many there are.  The list takes the place of the histograms.
-template <typename P> __device__ uint32_t gather(Row &r, int start, P member)
+__device__ uint32_t gather(Row &r, int start, uint32_t from, uint32_t to)
 {
     Shared *s = r.s;
+    const float low = (float)from, high = (float)(to + 1);
     if (threadIdx.x == 0)
         s->list_n = 0;
     __syncthreads();
     for_each(r, [&](float l, int i) {
-        const uint32_t bin = bin_of(l, r);
-        if (member(bin) && takes_part(l, bin, r)) {
-            const uint32_t e = atomicAdd(&s->list_n, 1u);
+        const float at = (r.m - l) * r.bins_per_unit;      // its whole part is the bin
+        if (at >= low && at < high) {
+            const uint32_t w = weight_of(l, r.m, r.inv), e = w > 0 ? atomicAdd(&s->list_n, 1u) : (uint32_t)SM_LIST;
             if (e < SM_LIST) {
                 s->list_order[e] = ((uint64_t)~key_of(l) << 32) | (uint32_t)(start + i);
-                s->list_w[e] = weight_of(l, r.m, r.inv);
+                s->list_w[e] = w;
             }
         }
     });
@@ -433,7 +429,7 @@ template <bool PAIRS> __device__ void sorted_list(Shared *s, int n)
 // The boundary in bin `f.bin` of the first histogram: `target` is reached there.
 template <bool BY_MASS> __device__ Boundary refine(Row &r, int start, uint64_t target, Found f)
 {
-    const uint32_t members = gather(r, start, [&](uint32_t bin) { return bin == f.bin; });
+    const uint32_t members = gather(r, start, f.bin, f.bin);
     if (members <= SM_LIST) {      // sorted, the boundary is where the running sum gets there
         const uint32_t turn = r.turn;
         r.turn ^= 1u;
@@ -501,7 +497,7 @@ template <bool BY_MASS> __device__ Boundary refine(Row &r, int start, uint64_t t
     }
     if (!BY_MASS)
         return Boundary{hi, (uint32_t)target - f.count_above};
-    const uint64_t w = weight_of(__uint_as_float(hi ^ ((hi >> 31) ? 0x80000000u : 0xffffffffu)), r.m, r.inv);
+    const uint64_t w = weight_of(logit_of(hi), r.m, r.inv);
     return Boundary{hi, (uint32_t)((target - f.mass_above + w - 1) / w)};
 }
 
@@ -529,7 +525,145 @@ __device__ uint64_t part_of(Shared *s, float part, uint64_t total)
     return word;
 }
 
-// The whole choice among the `n` logits of the list: top-k and top-p along their order, the draw
+// Mass of all threads.
+__device__ uint64_t total_of(Shared *s, uint64_t mass)
+{
+    const int lane = threadIdx.x & 31;
+    mass = warp_sum(mass);
+    if (lane == 0)
+        s->warp_mass[threadIdx.x >> 5] = mass;
+    __syncthreads();
+    mass = warp_sum(lane < SM_WARPS ? s->warp_mass[lane] : (uint64_t)0);
+    __syncthreads();
+    return mass;
+}
+
+// The entry of some, each thread having four of them (weights `w`, 0 for none), at which their running
+// weight in rising order of `order` reaches `target` (at least 1, and not more than there is), and its
+// weight.  `place(j)`, below SM_BINS, rises with the order: the entries of the place in question alone
+// are sorted.
+struct Entry {
+    uint64_t order;
+    uint32_t w;
+};
+template <typename P> __device__ Entry reach(const Row &r, const uint64_t (&order)[4], const uint32_t (&w)[4], uint64_t target, P place)
+{
+    Shared *s = r.s;
+    const int e0 = 4 * (int)threadIdx.x;
+    clear_bins<true>(r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (w[j] > 0)
+            add_to_bin(s, place(j), w[j]);
+    if (threadIdx.x == 0)
+        s->list_n = 0;
+    __syncthreads();
+    uint64_t m[4], mass = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        m[j] = s->low[e0 + j] + ((uint64_t)s->high[e0 + j] << 16);
+        mass += m[j];
+    }
+    uint64_t run = scan(r, mass) - mass;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (run < target && target <= run + m[j]) {
+            s->found[0].bin = (uint32_t)(e0 + j);
+            s->found[0].mass_above = run;
+        }
+        run += m[j];
+    }
+    __syncthreads();                     // (and the bins have been read: the list takes their place)
+    const uint32_t bin = s->found[0].bin;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (w[j] > 0 && place(j) == bin) {
+            const uint32_t e = atomicAdd(&s->list_n, 1u);
+            s->list_order[e] = order[j];
+            s->list_w[e] = w[j];
+        }
+    __syncthreads();
+    const int n = (int)s->list_n;
+    sorted_list<true>(s, n);
+    uint32_t own[4];
+    mass = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        own[j] = e0 + j < n ? s->list_w[e0 + j] : 0u;
+        mass += own[j];
+    }
+    run = s->found[0].mass_above + scan(r, mass) - mass;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (run < target && target <= run + own[j]) {
+            s->word = s->list_order[e0 + j];
+            s->warp_a[0] = own[j];
+        }
+        run += own[j];
+    }
+    __syncthreads();
+    const Entry found = {s->word, s->warp_a[0]};
+    __syncthreads();
+    return found;
+}
+
+// The whole choice among the `n` logits of a long list, the first `keep` of those of bin `bin` (and
+// all of the bins above) being top-k's.  No sort of all: each cut is found by places, a histogram of
+// the weights over the bins (top-p) or over ranges of the index (the draw), and one place's entries.
+// (Sorted twice, 1000 logits take 20 us longer.)
+__device__ void choose_from_long_list(const SampleParams &p, const Row &r, int n, int64_t row, uint32_t bin, int keep, bool by_p, float top_p,
+                                      uint32_t least)
+{
+    Shared *s = r.s;
+    uint64_t order[4];
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int e = (int)threadIdx.x + j * SM_THREADS;
+        order[j] = e < n ? s->list_order[e] : ~0ull;
+        w[j] = e < n ? s->list_w[e] : 0u;
+    }
+    auto bin_at = [&](int j) { return bin_of(logit_of(~(uint32_t)(order[j] >> 32)), r); };
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s->list_n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (w[j] > 0 && bin_at(j) == bin)
+            s->list_order[atomicAdd(&s->list_n, 1u)] = order[j];
+    __syncthreads();
+    if (keep < (int)s->list_n) {
+        sorted_list<false>(s, (int)s->list_n);
+        const uint64_t last = s->list_order[keep - 1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = order[j] <= last ? w[j] : 0u;
+    }
+    __syncthreads();
+    if (by_p) {
+        const uint64_t target = part_of(s, top_p, total_of(s, (uint64_t)w[0] + w[1] + w[2] + w[3]));
+        const uint64_t last = reach(r, order, w, target, bin_at).order;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = order[j] <= last ? w[j] : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        w[j] = w[j] >= least ? w[j] : 0u;
+        order[j] = (uint32_t)order[j];         // the index
+    }
+    const uint64_t total = total_of(s, (uint64_t)w[0] + w[1] + w[2] + w[3]), at = draw_at(s, p.uniform[row], total);
+    const int shift = max(0, 32 - __clz(p.vocab - 1) - 11);
+    const Entry drawn = reach(r, order, w, at + 1, [&](int j) { return (uint32_t)order[j] >> shift; });
+    if (threadIdx.x == 0) {
+        p.token[row] = (int32_t)drawn.order;
+        if (p.logprob)
+            p.logprob[row] = (float)log((double)drawn.w / (double)total);
+    }
+}
+
+// The whole choice among the `n` logits of a short list: top-k and top-p along their order, the draw
 // along their indices.  Each thread holds four neighbours of the sorted list.
 __device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int64_t row, int32_t top_k, bool by_p, float top_p, uint32_t least)
 {
@@ -662,7 +796,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         agree(r);
         return;
     }
-    r.m = __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xffffffffu));
+    r.m = logit_of(top);
     const float t = p.d_temperature ? p.d_temperature[row] : p.temperature;
     if (!(t > 0.0f)) {   // greedy: the first of the largest
         uint32_t none = 0, first = 0xffffffffu;
@@ -681,6 +815,17 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     }
     r.inv = __fdiv_rn(1.0f, t);
     r.bins_per_unit = r.inv * SM_BIN_SCALE;
+    if (isinf(r.m) || isinf(r.bins_per_unit)) {
+        // The largest logits alone have weight, or (at temperatures near 2^-120) those that differ from
+        // them by as little: these are scaled, exactly.
+        const bool scaled = !isinf(r.inv) && fabsf(r.m) < 0x1p60f;
+        for (int i = threadIdx.x; i < r.n; i += SM_THREADS)
+            r.l[i] = scaled ? r.l[i] * 0x1p60f : r.l[i] == r.m ? 0.0f : -INFINITY;
+        r.m = scaled ? r.m * 0x1p60f : 0.0f;
+        r.inv = scaled ? r.inv * 0x1p-60f : 1.0f;
+        r.bins_per_unit = r.inv * SM_BIN_SCALE;
+        __syncthreads();
+    }
 
     const int32_t top_k = p.d_top_k ? p.d_top_k[row] : p.top_k;
     const float top_p = p.d_top_p ? p.d_top_p[row] : p.top_p;
@@ -703,10 +848,12 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         if (cut_k) {
             // the logits of the bins down to the boundary's, if they are few
             if (top_k <= SM_LIST) {
-                const uint32_t n = gather(r, start, [&](uint32_t bin) { return bin <= f.bin; });
+                const uint32_t n = gather(r, start, 0, f.bin);
                 if (n <= SM_LIST) {
-                    if (r.rank == 0)
+                    if (r.rank == 0 && n <= SM_THREADS)
                         choose_from_list(p, r, (int)n, row, top_k, by_p, top_p, least);
+                    else if (r.rank == 0)
+                        choose_from_long_list(p, r, (int)n, row, f.bin, top_k - (int)f.count_above, by_p, top_p, least);
                     return;
                 }
             }
@@ -715,26 +862,23 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     }
     if (by_p) {
         clear_bins<true>(r);
-        const uint32_t from = cut_k ? last.key : 0u;   // of the boundary's equals all: the target lies among those that stay
+        const float from = logit_of(last.key);         // of the boundary's equals all: the target lies among those that stay
         uint64_t mass = 0;
         for_each(r, [&](float l, int) {
-            const uint32_t key = key_of(l);
-            const uint32_t w = key < from ? 0u : weight_of(l, r.m, r.inv);
-            if (w > 0) {
+            const uint32_t w = l >= from ? weight_of(l, r.m, r.inv) : 0u;
+            if (w > 0)
                 add_to_bin(s, bin_of(l, r), w);
-                if (!cut_k || key > from)
-                    mass += w;
-            }
+            mass += l > from ? w : 0u;
         });
         uint64_t all = share(r, scan(r, mass), 0).mass;
         if (cut_k)
-            all += (uint64_t)last.keep * weight_of(__uint_as_float(last.key ^ ((last.key >> 31) ? 0x80000000u : 0xffffffffu)), r.m, r.inv);
+            all += (uint64_t)last.keep * weight_of(logit_of(last.key), r.m, r.inv);
         const uint64_t target = part_of(s, top_p, all);
         last = refine<true>(r, start, target, search<true>(r, target, nothing));
     }
 
     // kept weight of each segment, its equals of the boundary counted apart
-    const float edge = __uint_as_float(last.key ^ ((last.key >> 31) ? 0x80000000u : 0xffffffffu));
+    const float edge = logit_of(last.key);
     uint64_t edge_w = weight_of(edge, r.m, r.inv);
     if (edge_w < least)
         edge_w = 0;
@@ -745,19 +889,25 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         for (int i = g * seg + 4 * lane; i < end; i += 128) {
             const float4 q = *reinterpret_cast<const float4 *>(r.l + i);
             const float l[4] = {q.x, q.y, q.z, q.w};
+            if (edge_w == 0) {                         // (nothing was cut, or min-p cuts further)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t w = weight_of(l[j], r.m, r.inv);
-                mass += l[j] > edge && w >= least ? w : 0u;
-                ties += l[j] == edge;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = weight_of(l[j], r.m, r.inv);
+                    mass += w >= least ? w : 0u;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = weight_of(l[j], r.m, r.inv);
+                    mass += l[j] > edge && w >= least ? w : 0u;
+                    ties += l[j] == edge;
+                }
             }
         }
-        // (a lane's share is below 2^43)
-        const uint32_t low = __reduce_add_sync(dev::FULL_MASK, (uint32_t)mass & 0xffffffu);
-        const uint32_t high = __reduce_add_sync(dev::FULL_MASK, (uint32_t)(mass >> 24));
-        ties = __reduce_add_sync(dev::FULL_MASK, ties);
+        mass = warp_sum(mass);
+        ties = warp_sum(ties);
         if (lane == 0) {
-            s->seg_mass[g] = low + ((uint64_t)high << 24);
+            s->seg_mass[g] = mass;
             s->seg_ties[g] = ties;
         }
     }

@@ -131,6 +131,36 @@ def test_masked_rows(env, setting):
     _check(env, x, torch.rand(9, generator=g, device="cuda"), *setting, err_want=loom.LOOM_DEVERR_NO_TOKEN)
 
 
+@pytest.mark.parametrize("top_k", [513, 700, 1500, 2040])
+@pytest.mark.parametrize("setting", [(1.0, 1.0, 0.0), (0.7, 0.9, 0.0), (1.4, 0.97, 0.05)])
+def test_many_of_top_k(env, top_k, setting):
+    # long lists: spread logits, levels of many equals, one crowded level among others, neighbours in index
+    torch, _ = env
+    g = torch.Generator(device="cuda").manual_seed(top_k)
+    v = 30000
+    x = torch.randn(5, v, generator=g, device="cuda")
+    x[1] = torch.floor(x[1] * 40) / 40
+    x[2] = torch.where(torch.rand(v, generator=g, device="cuda") < 0.06, 2.0, x[2])
+    x[3] -= torch.arange(v, device="cuda") * 0.002
+    x[4], x[4, 29000:] = -float("inf"), torch.randn(1000, generator=g, device="cuda")
+    t, p, mp = setting
+    _check(env, x, torch.rand(5, generator=g, device="cuda"), t, top_k, p, mp)
+
+
+@pytest.mark.parametrize("temperature", [1e-30, 3e-37, 1e-37, 3e-39, 1e-40])
+@pytest.mark.parametrize("setting", [(0, 1.0, 0.0), (7, 1.0, 0.0), (0, 0.8, 0.0), (900, 0.8, 0.01)])
+def test_temperatures_near_zero(env, temperature, setting):
+    torch, _ = env
+    g = torch.Generator(device="cuda").manual_seed(3)
+    v = 3000
+    x = torch.randn(5, v, generator=g, device="cuda")
+    x[1] *= temperature                             # differences of the temperature's size
+    x[2] = torch.randint(0, 9, (v,), generator=g, device="cuda") * (0.5 * temperature)
+    x[3] = torch.randint(0, 3, (v,), generator=g, device="cuda").float()
+    x[4], x[4, 7] = x[4] * temperature, -float("inf")
+    _check(env, x, torch.rand(5, generator=g, device="cuda"), temperature, *setting)
+
+
 def test_random_numbers_at_and_past_the_ends(env):
     torch, loom = env
     g = torch.Generator(device="cuda").manual_seed(12)
