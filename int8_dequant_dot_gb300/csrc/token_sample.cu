@@ -82,13 +82,6 @@ __device__ __forceinline__ uint32_t remote(const void *p, uint32_t rank)
     return a;
 }
 
-__device__ __forceinline__ uint64_t load_remote(const uint64_t *p, uint32_t rank)
-{
-    uint64_t v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(p, rank)) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ uint32_t load_remote(const uint32_t *p, uint32_t rank)
 {
     uint32_t v;
@@ -159,6 +152,16 @@ template <typename F> __device__ __forceinline__ void for_each(const Row &r, F f
     }
 }
 
+// The same with the four together, f(logits, place): for what branches only after its arithmetic.
+template <typename F> __device__ __forceinline__ void for_fours(const Row &r, F f)
+{
+    for (int i = 4 * threadIdx.x; i < r.n; i += 4 * SM_THREADS) {
+        const float4 q = *reinterpret_cast<const float4 *>(r.l + i);
+        const float l[4] = {q.x, q.y, q.z, q.w};
+        f(l, i);
+    }
+}
+
 __device__ __forceinline__ void agree(const Row &r)
 {
     if (r.ranks > 1)
@@ -206,7 +209,8 @@ template <bool BY_MASS> __device__ __forceinline__ void clear_bins(const Row &r)
 __device__ __forceinline__ void add_to_bin(Shared *s, uint32_t bin, uint32_t w)
 {
     atomicAdd(&s->low[bin], w & 0xffffu);
-    atomicAdd(&s->high[bin], w >> 16);
+    if (w >> 16)
+        atomicAdd(&s->high[bin], w >> 16);
 }
 
 __device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(dev::FULL_MASK, v); }
@@ -270,13 +274,24 @@ template <bool BY_MASS> __device__ Found search(Row &r, uint64_t target, Found s
     for (int j = 0; j < MOST; ++j) {
         m[j] = 0;
         c[j] = 0;
-        if (j < per && (int)threadIdx.x * per + j < bins)
-            for (uint32_t q = 0; q < r.ranks; ++q) {
-                if (!BY_MASS)
-                    c[j] += load_remote(&s->count[bin0 + j], q);
-                else
-                    m[j] += load_remote(&s->low[bin0 + j], q) + ((uint64_t)load_remote(&s->high[bin0 + j], q) << 16);
+        if (j < per && (int)threadIdx.x * per + j < bins) {      // all loads of a bin in flight together
+            uint32_t low[SM_MAX_CLUSTER], high[SM_MAX_CLUSTER];
+#pragma unroll
+            for (uint32_t q = 0; q < SM_MAX_CLUSTER; ++q) {
+                low[q] = high[q] = 0;
+                if (q < r.ranks) {
+                    low[q] = load_remote(BY_MASS ? &s->low[bin0 + j] : &s->count[bin0 + j], q);
+                    if (BY_MASS)
+                        high[q] = load_remote(&s->high[bin0 + j], q);
+                }
             }
+#pragma unroll
+            for (uint32_t q = 0; q < SM_MAX_CLUSTER; ++q)
+                if (BY_MASS)
+                    m[j] += low[q] + ((uint64_t)high[q] << 16);
+                else
+                    c[j] += low[q];
+        }
         mass += m[j];
         count += c[j];
     }
@@ -366,15 +381,24 @@ __device__ uint32_t gather(Row &r, int start, uint32_t from, uint32_t to)
     if (threadIdx.x == 0)
         s->list_n = 0;
     __syncthreads();
-    for_each(r, [&](float l, int i) {
-        const float at = (r.m - l) * r.bins_per_unit;      // its whole part is the bin
-        if (at >= low && at < high) {
-            const uint32_t w = weight_of(l, r.m, r.inv), e = w > 0 ? atomicAdd(&s->list_n, 1u) : (uint32_t)SM_LIST;
-            if (e < SM_LIST) {
-                s->list_order[e] = ((uint64_t)~key_of(l) << 32) | (uint32_t)(start + i);
-                s->list_w[e] = w;
-            }
+    for_fours(r, [&](const float (&l)[4], int i) {
+        bool in[4], any = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float at = (r.m - l[j]) * r.bins_per_unit;      // its whole part is the bin
+            in[j] = at >= low && at < high;
+            any = any || in[j];
         }
+        if (any)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in[j]) {
+                    const uint32_t w = weight_of(l[j], r.m, r.inv), e = w > 0 ? atomicAdd(&s->list_n, 1u) : (uint32_t)SM_LIST;
+                    if (e < SM_LIST) {
+                        s->list_order[e] = ((uint64_t)~key_of(l[j]) << 32) | (uint32_t)(start + i + j);
+                        s->list_w[e] = w;
+                    }
+                }
     });
     __syncthreads();
     const uint32_t mine = s->list_n;
@@ -501,29 +525,75 @@ template <bool BY_MASS> __device__ Boundary refine(Row &r, int start, uint64_t t
     return Boundary{hi, (uint32_t)((target - f.mass_above + w - 1) / w)};
 }
 
-// floor(u total), and ceil(part total) but at least 1, by one thread (the SM has few 64-bit units)
-// for all of the CTA.
-__device__ uint64_t draw_at(Shared *s, float u, uint64_t total)
+// ---- numbers of 64 bits ------------------------------------------------------------
+// The SM's 64-bit floating-point units are few (a logarithm takes 4000 cycles, a product and its
+// floor 800), so these are put together from whole numbers and f32.
+
+// The 64-bit floating-point product f total of a positive f below 1 and a total below 2^52, rounded
+// down or up to a whole number.
+__device__ __forceinline__ uint64_t product(float f, uint64_t total, bool up)
 {
-    if (threadIdx.x == 0) {
-        const double drawn = floor((double)u * (double)total);
-        s->word = drawn >= (double)total ? total - 1 : drawn > 0.0 ? (uint64_t)drawn : 0u;
+    const uint32_t b = __float_as_uint(f), e = b >> 23;
+    const uint32_t m = e ? (b & 0x7fffffu) | 0x800000u : b, s = e ? 150 - e : 149;      // f = m 2^-s
+    uint64_t low = m * total, high = __umul64hi(m, total);
+    const int drop = 22 - __clzll(high << 53 | low >> 11);       // bits past 53: to nearest, ties to even
+    if (drop > 0) {
+        const uint64_t add = (1ull << (drop - 1)) - 1 + ((low >> drop) & 1);
+        low += add;
+        high += low < add;
+        low &= ~0ull << drop;
     }
-    __syncthreads();
-    return s->word;
+    if (s >= 76)
+        return up;
+    const uint64_t rest = s < 64 ? low & ((1ull << s) - 1) : low | (high & ((1ull << (s - 64)) - 1));
+    return (s < 64 ? low >> s | high << (64 - s) : high >> (s - 64)) + (up && rest);
 }
 
-__device__ uint64_t part_of(Shared *s, float part, uint64_t total)
+// log(w / total), 0 < w <= total < 2^51, to f32's last place but for about 3 cases in 10^5.  With
+// w / total = 2^-k a / b and a / b within [2^-1/2, 2^1/2], s = (a - b) / (a + b) is
+//   log(a / b) = 2 s (1 + z / 3 + z^2 / 5 + ...),  z = s^2 <= 0.0295,
+// in pairs of f32 (value and rest), the higher terms, which count for less, in one.
+__device__ float log_of_part(uint32_t w, uint64_t total)
 {
-    if (threadIdx.x == 0) {
-        const double want = ceil((double)part * (double)total);
-        s->word = want >= 1.0 ? (uint64_t)want : 1u;      // no number: the first alone
+    int k = __clzll((long long)w) - __clzll((long long)total);
+    uint64_t a = (uint64_t)w << k, b = total;
+    if ((float)a > 1.4142135f * (float)b) {
+        b *= 2;
+        --k;
+    } else if (1.4142135f * (float)a < (float)b) {
+        a *= 2;
+        ++k;
     }
-    __syncthreads();
-    const uint64_t word = s->word;
-    __syncthreads();
-    return word;
+    const int64_t num = (int64_t)(a - b), den = (int64_t)(a + b);
+    const float num_hi = (float)num, num_lo = (float)(num - (int64_t)num_hi), den_hi = (float)den, den_lo = (float)(den - (int64_t)den_hi);
+    const float s_hi = __fdiv_rn(num_hi, den_hi);
+    const float s_lo = __fdiv_rn(__fadd_rn(__fmaf_rn(-s_hi, den_hi, num_hi), __fmaf_rn(-s_hi, den_lo, num_lo)), den_hi);
+    const float z_hi = __fmul_rn(s_hi, s_hi), z_lo = __fmaf_rn(s_hi, s_hi, -z_hi) + 2.0f * s_hi * s_lo;
+    const float tail = 1.0f / 7 + z_hi * (1.0f / 9 + z_hi * (1.0f / 11 + z_hi * (1.0f / 13 + z_hi * (1.0f / 15))));
+    const float fifth = 0.2f, fifth_lo = (float)(0.2 - (double)0.2f), third = 1.0f / 3, third_lo = (float)(1.0 / 3 - (double)(1.0f / 3));
+    float p = __fmul_rn(z_hi, tail);                          // 1/5 + z tail
+    const float q_hi = __fadd_rn(fifth, p), q_lo = __fadd_rn(__fsub_rn(p, __fsub_rn(q_hi, fifth)), fifth_lo);
+    p = __fmul_rn(z_hi, q_hi);                                // 1/3 + z q
+    float p_lo = __fmaf_rn(z_hi, q_hi, -p) + (z_hi * q_lo + z_lo * q_hi);
+    const float t_hi = __fadd_rn(third, p), t_lo = __fadd_rn(__fsub_rn(p, __fsub_rn(t_hi, third)), __fadd_rn(third_lo, p_lo));
+    const float y = __fmul_rn(z_hi, t_hi), y_lo = __fmaf_rn(z_hi, t_hi, -y) + (z_hi * t_lo + z_lo * t_hi);
+    p = __fmul_rn(s_hi, y);                                   // s + s z t
+    p_lo = __fmaf_rn(s_hi, y, -p) + (s_hi * y_lo + s_lo * y);
+    const float l_hi = __fadd_rn(s_hi, p), l_lo = __fadd_rn(__fsub_rn(p, __fsub_rn(l_hi, s_hi)), __fadd_rn(s_lo, p_lo));
+    if (k == 0)
+        return 2.0f * __fadd_rn(l_hi, l_lo);
+    const float ln2 = 45426.0f / 65536, ln2_lo = (float)(0.69314718055994530942 - 45426.0 / 65536);   // k ln2 is exact
+    const float whole = -(float)k * ln2, sum = __fadd_rn(whole, 2.0f * l_hi);
+    return __fadd_rn(sum, __fadd_rn(__fsub_rn(2.0f * l_hi, __fsub_rn(sum, whole)), __fmaf_rn(-(float)k, ln2_lo, 2.0f * l_lo)));
 }
+
+// floor(u total) cut to [0, total), and ceil(part total) but at least 1.
+__device__ __forceinline__ uint64_t draw_at(float u, uint64_t total)
+{
+    return u >= 1.0f ? total - 1 : u > 0.0f ? min(product(u, total, false), total - 1) : 0u;
+}
+
+__device__ __forceinline__ uint64_t part_of(float part, uint64_t total) { return part > 0.0f ? max((uint64_t)1, product(part, total, true)) : 1u; }
 
 // Mass of all threads.
 __device__ uint64_t total_of(Shared *s, uint64_t mass)
@@ -642,7 +712,7 @@ __device__ void choose_from_long_list(const SampleParams &p, const Row &r, int n
     }
     __syncthreads();
     if (by_p) {
-        const uint64_t target = part_of(s, top_p, total_of(s, (uint64_t)w[0] + w[1] + w[2] + w[3]));
+        const uint64_t target = part_of(top_p, total_of(s, (uint64_t)w[0] + w[1] + w[2] + w[3]));
         const uint64_t last = reach(r, order, w, target, bin_at).order;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -653,13 +723,13 @@ __device__ void choose_from_long_list(const SampleParams &p, const Row &r, int n
         w[j] = w[j] >= least ? w[j] : 0u;
         order[j] = (uint32_t)order[j];         // the index
     }
-    const uint64_t total = total_of(s, (uint64_t)w[0] + w[1] + w[2] + w[3]), at = draw_at(s, p.uniform[row], total);
+    const uint64_t total = total_of(s, (uint64_t)w[0] + w[1] + w[2] + w[3]), at = draw_at(p.uniform[row], total);
     const int shift = max(0, 32 - __clz(p.vocab - 1) - 11);
     const Entry drawn = reach(r, order, w, at + 1, [&](int j) { return (uint32_t)order[j] >> shift; });
     if (threadIdx.x == 0) {
         p.token[row] = (int32_t)drawn.order;
         if (p.logprob)
-            p.logprob[row] = (float)log((double)drawn.w / (double)total);
+            p.logprob[row] = log_of_part(drawn.w, total);
     }
 }
 
@@ -685,7 +755,7 @@ __device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int
         if (threadIdx.x == SM_THREADS - 1)
             s->seg_mass[0] = run + mass;
         __syncthreads();
-        target = part_of(s, top_p, s->seg_mass[0]);
+        target = part_of(top_p, s->seg_mass[0]);
     }
     int mine = 0;
 #pragma unroll
@@ -721,13 +791,13 @@ __device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int
     if (threadIdx.x == SM_THREADS - 1)
         s->seg_mass[1] = run + mass;
     __syncthreads();
-    const uint64_t total = s->seg_mass[1], at = draw_at(s, p.uniform[row], total);
+    const uint64_t total = s->seg_mass[1], at = draw_at(p.uniform[row], total);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (run <= at && at < run + w[j]) {
             p.token[row] = (int32_t)(order[j] >> 32);
             if (p.logprob)
-                p.logprob[row] = (float)log((double)w[j] / (double)total);
+                p.logprob[row] = log_of_part(w[j], total);
         }
         run += w[j];
     }
@@ -749,10 +819,23 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     const int64_t row = blockIdx.x / r.ranks;
     const int start = (int)r.rank * slice;
     r.n = max(0, min(slice, p.vocab - start));
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");      // waited for behind the loads
     dev::follow_previous_kernel();
 
-    // the slice, with NaN as -infinity (fmaxf) and one zero (-0 + 0 = 0)
     const E *src = static_cast<const E *>(p.logits) + row * p.stride + start;
+    if (threadIdx.x == 0) {
+        // The slice of the cluster that will follow on these SMs is on its way to L2 meanwhile: the
+        // passes leave memory idle.
+        uint32_t sms;
+        asm("mov.u32 %0, %%nsmid;" : "=r"(sms));
+        const int64_t ahead = max(1u, (slice <= SM_SLICE ? 2u : 1u) * sms / r.ranks);
+        const uintptr_t next = (reinterpret_cast<uintptr_t>(src + ahead * p.stride) + 15) & ~(uintptr_t)15;
+        const uint32_t bytes = (uint32_t)max(0, r.n * (int)sizeof(E) - 16) & ~15u;
+        if (row + ahead < gridDim.x / r.ranks && bytes > 0)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next), "r"(bytes) : "memory");
+    }
+
+    // the slice, with NaN as -infinity (fmaxf) and one zero (-0 + 0 = 0)
     float largest = -INFINITY;
     auto put = [&](int i, E v) {
         const float l = fmaxf(__fadd_rn(dev::to_f32(v), 0.0f), -INFINITY);
@@ -784,7 +867,9 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     uint32_t top = key_of(largest), unused = 0xffffffffu;
     if (threadIdx.x < 3 && r.n + (int)threadIdx.x < (r.n + 3) / 4 * 4)
         r.l[r.n + threadIdx.x] = -INFINITY;
-    agree(r);   // every CTA of the cluster runs: its shared memory may be written
+    // every CTA of the cluster runs: its shared memory may be written.  (It may end when it is done:
+    // the last that any other does with it comes before a barrier of all.)
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     cluster_max_min(r, top, unused);
     if (top == SM_KEY_NONE) {
         if (r.rank == 0 && threadIdx.x == 0) {
@@ -793,7 +878,6 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
                 p.logprob[row] = __uint_as_float(0x7fc00000u);
             dev::flag_error(p.error, LOOM_DEVERR_NO_TOKEN);
         }
-        agree(r);
         return;
     }
     r.m = logit_of(top);
@@ -810,7 +894,6 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
             if (p.logprob)
                 p.logprob[row] = 0.0f;
         }
-        agree(r);
         return;
     }
     r.inv = __fdiv_rn(1.0f, t);
@@ -837,10 +920,15 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     bool cut_k = false;
     if (by_k) {           // counts alone: no exponentials
         clear_bins<false>(r);
-        for_each(r, [&](float l, int) {
-            const uint32_t bin = bin_of(l, r);
-            if (takes_part(l, bin, r))
-                atomicAdd(&s->count[bin], 1u);
+        for_fours(r, [&](const float (&l)[4], int) {
+            uint32_t bin[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                bin[j] = bin_of(l[j], r);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (takes_part(l[j], bin[j], r))
+                    atomicAdd(&s->count[bin[j]], 1u);
         });
         Shares all;
         const Found f = search<false>(r, (uint64_t)top_k, nothing, &all);
@@ -864,16 +952,23 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         clear_bins<true>(r);
         const float from = logit_of(last.key);         // of the boundary's equals all: the target lies among those that stay
         uint64_t mass = 0;
-        for_each(r, [&](float l, int) {
-            const uint32_t w = l >= from ? weight_of(l, r.m, r.inv) : 0u;
-            if (w > 0)
-                add_to_bin(s, bin_of(l, r), w);
-            mass += l > from ? w : 0u;
+        for_fours(r, [&](const float (&l)[4], int) {
+            uint32_t w[4], bin[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                w[j] = l[j] >= from ? weight_of(l[j], r.m, r.inv) : 0u;
+                bin[j] = bin_of(l[j], r);
+                mass += l[j] > from ? w[j] : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (w[j] > 0)
+                    add_to_bin(s, bin[j], w[j]);
         });
         uint64_t all = share(r, scan(r, mass), 0).mass;
         if (cut_k)
             all += (uint64_t)last.keep * weight_of(logit_of(last.key), r.m, r.inv);
-        const uint64_t target = part_of(s, top_p, all);
+        const uint64_t target = part_of(top_p, all);
         last = refine<true>(r, start, target, search<true>(r, target, nothing));
     }
 
@@ -922,7 +1017,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     const uint64_t mass = scan(r, own_mass);       // of the last thread: this CTA's
     const Shares kept = share(r, mass, 0);
     const uint64_t total = kept.mass, before = kept.mass_below + mass - own_mass;
-    const uint64_t at = draw_at(s, p.uniform[row], total);
+    const uint64_t at = draw_at(p.uniform[row], total);
     if (threadIdx.x < SM_SEGMENTS && before <= at && at < before + own_mass) {
         s->warp_mass[0] = at - before;      // what to walk into this segment, and with how many equals
         s->warp_count[0] = last.keep > ties_before ? last.keep - ties_before : 0u;
@@ -975,7 +1070,7 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
                         run += w[j++];
                     p.token[row] = start + i + j;
                     if (p.logprob)
-                        p.logprob[row] = (float)log((double)w[j] / (double)total);
+                        p.logprob[row] = log_of_part(w[j], total);
                 }
                 break;
             }
@@ -983,7 +1078,6 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
             keep -= min(keep, round_ties);
         }
     }
-    agree(r);   // no CTA ends while another may read its shared memory
 }
 
 template <typename E> cudaError_t launch_e(const SampleParams &p, const loom_launch &L, cudaStream_t stream)
