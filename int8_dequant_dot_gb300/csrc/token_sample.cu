@@ -38,7 +38,6 @@ constexpr int SM_SLICE = 16384;            // slices up to this leave room for a
 constexpr int SM_SHORT_SLICE = 2048;       // not worth another CTA
 constexpr int SM_SEGMENTS = 128;           // segments of a slice
 constexpr int SM_LIST = SM_BINS;           // logits that one CTA sorts: their list takes the bins' place
-constexpr uint32_t SM_FULL = 1u << 31;     // the weight of the largest logit
 constexpr float SM_BIN_SCALE = 95.0f;      // bins per unit of (m - l) / T: weights are above 0 in
                                            // bins below SM_EDGE_BIN and 0 above it
 constexpr uint32_t SM_EDGE_BIN = 2041;     // 21.4842 .. 21.4948; 2^-31 is at 21.4876
@@ -99,9 +98,16 @@ __device__ __forceinline__ void store_remote(uint64_t *p, uint32_t rank, uint64_
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(p, rank)), "l"(v) : "memory");
 }
 
+__device__ __forceinline__ uint32_t add_remote(uint32_t *p, uint32_t rank, uint32_t v)
+{
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote(p, rank)), "r"(v) : "memory");
+    return old;
+}
+
 struct Found {            // where a search ended: what lies above bin `bin`
     uint64_t mass_above;
-    uint32_t count_above, bin;
+    uint32_t count_above, bin, count;      // count: in the bin (where counts were searched)
 };
 
 // What the CTAs of a cluster tell each other has two places, used in turn: one barrier then
@@ -302,8 +308,10 @@ template <bool BY_MASS> __device__ Found search(Row &r, uint64_t target, Found s
     else
         count = scan(r, count);
     const uint32_t turn = r.turn;
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
         s->found[turn].bin = SM_BINS;               // (the owner writes after the next barrier)
+        s->list_n = 0;
+    }
     const Shares t = share(r, mass, count);
     if (all)
         *all = t;
@@ -317,6 +325,7 @@ template <bool BY_MASS> __device__ Found search(Row &r, uint64_t target, Found s
                 store_remote(&s->found[turn].mass_above, q, above_mass);
                 store_remote(&s->found[turn].count_above, q, above_count);
                 store_remote(&s->found[turn].bin, q, (uint32_t)(bin0 + j));
+                store_remote(&s->found[turn].count, q, c[j]);
             }
         above_mass += m[j];
         above_count += c[j];
@@ -372,15 +381,13 @@ __device__ __forceinline__ int power_of_two(int n)
     return p;
 }
 
-// The logits of the bins `from` to `to` that take part, listed in the cluster's first CTA if they are
-// at most SM_LIST; how many there are.  The list takes the place of the histograms.
-__device__ uint32_t gather(Row &r, int start, uint32_t from, uint32_t to)
+// The logits of the bins `from` to `to` that take part, listed in the cluster's first CTA (each thread
+// asks it for a place) as far as they are at most SM_LIST.  The list takes the place of the
+// histograms.  Behind a search, that made its count 0.
+__device__ void gather(Row &r, int start, uint32_t from, uint32_t to)
 {
     Shared *s = r.s;
     const float low = (float)from, high = (float)(to + 1);
-    if (threadIdx.x == 0)
-        s->list_n = 0;
-    __syncthreads();
     for_fours(r, [&](const float (&l)[4], int i) {
         bool in[4], any = false;
 #pragma unroll
@@ -393,25 +400,14 @@ __device__ uint32_t gather(Row &r, int start, uint32_t from, uint32_t to)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (in[j]) {
-                    const uint32_t w = weight_of(l[j], r.m, r.inv), e = w > 0 ? atomicAdd(&s->list_n, 1u) : (uint32_t)SM_LIST;
+                    const uint32_t w = weight_of(l[j], r.m, r.inv), e = w > 0 ? add_remote(&s->list_n, 0, 1u) : (uint32_t)SM_LIST;
                     if (e < SM_LIST) {
-                        s->list_order[e] = ((uint64_t)~key_of(l[j]) << 32) | (uint32_t)(start + i + j);
-                        s->list_w[e] = w;
+                        store_remote(&s->list_order[e], 0, ((uint64_t)~key_of(l[j]) << 32) | (uint32_t)(start + i + j));
+                        store_remote(&s->list_w[e], 0, w);
                     }
                 }
     });
-    __syncthreads();
-    const uint32_t mine = s->list_n;
-    const Shares lists = share(r, 0, mine);
-    if (lists.count > SM_LIST || r.ranks == 1)
-        return lists.count;
-    if (r.rank > 0)                // behind the lists of the CTAs before
-        for (uint32_t e = threadIdx.x; e < mine; e += SM_THREADS) {
-            store_remote(&s->list_order[lists.count_below + e], 0, s->list_order[e]);
-            store_remote(&s->list_w[lists.count_below + e], 0, s->list_w[e]);
-        }
     agree(r);
-    return lists.count;
 }
 
 // Sorts the first n words and, where PAIRS, their weights.  A short list is ranked by counting, each
@@ -453,7 +449,11 @@ template <bool PAIRS> __device__ void sorted_list(Shared *s, int n)
 // The boundary in bin `f.bin` of the first histogram: `target` is reached there.
 template <bool BY_MASS> __device__ Boundary refine(Row &r, int start, uint64_t target, Found f)
 {
-    const uint32_t members = gather(r, start, f.bin, f.bin);
+    uint32_t members = f.count;
+    if (BY_MASS || members <= SM_LIST)
+        gather(r, start, f.bin, f.bin);
+    if (BY_MASS)
+        members = load_remote(&r.s->list_n, 0);          // (a barrier follows, before its CTA may change it or end)
     if (members <= SM_LIST) {      // sorted, the boundary is where the running sum gets there
         const uint32_t turn = r.turn;
         r.turn ^= 1u;
@@ -682,7 +682,7 @@ template <typename P> __device__ Entry reach(const Row &r, const uint64_t (&orde
 // the weights over the bins (top-p) or over ranges of the index (the draw), and one place's entries.
 // (Sorted twice, 1000 logits take 20 us longer.)
 __device__ void choose_from_long_list(const SampleParams &p, const Row &r, int n, int64_t row, uint32_t bin, int keep, bool by_p, float top_p,
-                                      uint32_t least)
+                                      uint32_t least, float u)
 {
     Shared *s = r.s;
     uint64_t order[4];
@@ -723,7 +723,7 @@ __device__ void choose_from_long_list(const SampleParams &p, const Row &r, int n
         w[j] = w[j] >= least ? w[j] : 0u;
         order[j] = (uint32_t)order[j];         // the index
     }
-    const uint64_t total = total_of(s, (uint64_t)w[0] + w[1] + w[2] + w[3]), at = draw_at(p.uniform[row], total);
+    const uint64_t total = total_of(s, (uint64_t)w[0] + w[1] + w[2] + w[3]), at = draw_at(u, total);
     const int shift = max(0, 32 - __clz(p.vocab - 1) - 11);
     const Entry drawn = reach(r, order, w, at + 1, [&](int j) { return (uint32_t)order[j] >> shift; });
     if (threadIdx.x == 0) {
@@ -735,7 +735,7 @@ __device__ void choose_from_long_list(const SampleParams &p, const Row &r, int n
 
 // The whole choice among the `n` logits of a short list: top-k and top-p along their order, the draw
 // along their indices.  Each thread holds four neighbours of the sorted list.
-__device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int64_t row, int32_t top_k, bool by_p, float top_p, uint32_t least)
+__device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int64_t row, int32_t top_k, bool by_p, float top_p, uint32_t least, float u)
 {
     Shared *s = r.s;
     const int e0 = 4 * (int)threadIdx.x;
@@ -791,7 +791,7 @@ __device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int
     if (threadIdx.x == SM_THREADS - 1)
         s->seg_mass[1] = run + mass;
     __syncthreads();
-    const uint64_t total = s->seg_mass[1], at = draw_at(p.uniform[row], total);
+    const uint64_t total = s->seg_mass[1], at = draw_at(u, total);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (run <= at && at < run + w[j]) {
@@ -803,7 +803,7 @@ __device__ void choose_from_list(const SampleParams &p, const Row &r, int n, int
     }
 }
 
-template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kernel(const SampleParams p, int slice, int seg)
+template <typename E> __global__ void __launch_bounds__(SM_THREADS, 2) sample_kernel(const SampleParams p, int slice, int seg)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     Row r;
@@ -823,17 +823,10 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     dev::follow_previous_kernel();
 
     const E *src = static_cast<const E *>(p.logits) + row * p.stride + start;
-    if (threadIdx.x == 0) {
-        // The slice of the cluster that will follow on these SMs is on its way to L2 meanwhile: the
-        // passes leave memory idle.
-        uint32_t sms;
-        asm("mov.u32 %0, %%nsmid;" : "=r"(sms));
-        const int64_t ahead = max(1u, (slice <= SM_SLICE ? 2u : 1u) * sms / r.ranks);
-        const uintptr_t next = (reinterpret_cast<uintptr_t>(src + ahead * p.stride) + 15) & ~(uintptr_t)15;
-        const uint32_t bytes = (uint32_t)max(0, r.n * (int)sizeof(E) - 16) & ~15u;
-        if (row + ahead < gridDim.x / r.ranks && bytes > 0)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next), "r"(bytes) : "memory");
-    }
+    // the row's settings, on their way with its logits
+    const float t = p.d_temperature ? p.d_temperature[row] : p.temperature, u = p.uniform[row];
+    const int32_t top_k = p.d_top_k ? p.d_top_k[row] : p.top_k;
+    const float top_p = p.d_top_p ? p.d_top_p[row] : p.top_p, least_p = p.d_min_p ? p.d_min_p[row] : p.min_p;
 
     // the slice, with NaN as -infinity (fmaxf) and one zero (-0 + 0 = 0)
     float largest = -INFINITY;
@@ -881,7 +874,6 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         return;
     }
     r.m = logit_of(top);
-    const float t = p.d_temperature ? p.d_temperature[row] : p.temperature;
     if (!(t > 0.0f)) {   // greedy: the first of the largest
         uint32_t none = 0, first = 0xffffffffu;
         for_each(r, [&](float l, int i) {
@@ -910,13 +902,11 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         __syncthreads();
     }
 
-    const int32_t top_k = p.d_top_k ? p.d_top_k[row] : p.top_k;
-    const float top_p = p.d_top_p ? p.d_top_p[row] : p.top_p;
-    const float min_p = fminf(fmaxf(p.d_min_p ? p.d_min_p[row] : p.min_p, 0.0f), 1.0f);   // NaN: 0
+    const float min_p = fminf(fmaxf(least_p, 0.0f), 1.0f);   // NaN: 0
     const uint32_t least = __float2uint_ru(min_p * 2147483648.0f);     // w >= min_p * 2^31 (exact)
     const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.0f;
     Boundary last = {SM_KEY_NONE, 0xffffffffu};   // everything stays
-    const Found nothing = {0, 0, 0};
+    const Found nothing = {};
     bool cut_k = false;
     if (by_k) {           // counts alone: no exponentials
         clear_bins<false>(r);
@@ -935,15 +925,14 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
         cut_k = all.count > (uint32_t)top_k;
         if (cut_k) {
             // the logits of the bins down to the boundary's, if they are few
-            if (top_k <= SM_LIST) {
-                const uint32_t n = gather(r, start, 0, f.bin);
-                if (n <= SM_LIST) {
-                    if (r.rank == 0 && n <= SM_THREADS)
-                        choose_from_list(p, r, (int)n, row, top_k, by_p, top_p, least);
-                    else if (r.rank == 0)
-                        choose_from_long_list(p, r, (int)n, row, f.bin, top_k - (int)f.count_above, by_p, top_p, least);
-                    return;
-                }
+            const uint32_t n = f.count_above + f.count;
+            if (n <= SM_LIST) {
+                gather(r, start, 0, f.bin);
+                if (r.rank == 0 && n <= SM_THREADS)
+                    choose_from_list(p, r, (int)n, row, top_k, by_p, top_p, least, u);
+                else if (r.rank == 0)
+                    choose_from_long_list(p, r, (int)n, row, f.bin, top_k - (int)f.count_above, by_p, top_p, least, u);
+                return;
             }
             last = refine<false>(r, start, (uint64_t)top_k, f);
         }
@@ -977,7 +966,8 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     uint64_t edge_w = weight_of(edge, r.m, r.inv);
     if (edge_w < least)
         edge_w = 0;
-    for (int g = warp; g < SM_SEGMENTS; g += SM_WARPS) {
+    const int segments = (r.n + seg - 1) / seg;         // (at most SM_SEGMENTS)
+    for (int g = warp; g < segments; g += SM_WARPS) {
         uint64_t mass = 0;
         uint32_t ties = 0;
         const int end = min(r.n, (g + 1) * seg);
@@ -1000,7 +990,8 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
             }
         }
         mass = warp_sum(mass);
-        ties = warp_sum(ties);
+        if (edge_w > 0)
+            ties = warp_sum(ties);
         if (lane == 0) {
             s->seg_mass[g] = mass;
             s->seg_ties[g] = ties;
@@ -1009,16 +1000,16 @@ template <typename E> __global__ void __launch_bounds__(SM_THREADS) sample_kerne
     __syncthreads();
     uint32_t ties_before = 0, kept_ties = 0;       // the boundary's equals before this thread's segment, and kept in it
     if (edge_w > 0) {
-        const uint32_t own_ties = threadIdx.x < SM_SEGMENTS ? s->seg_ties[threadIdx.x] : 0u, ties = scan(r, own_ties);
+        const uint32_t own_ties = (int)threadIdx.x < segments ? s->seg_ties[threadIdx.x] : 0u, ties = scan(r, own_ties);
         ties_before = ties - own_ties + share(r, 0, ties).count_below;
         kept_ties = ties_before < last.keep ? min(own_ties, last.keep - ties_before) : 0u;
     }
-    const uint64_t own_mass = threadIdx.x < SM_SEGMENTS ? s->seg_mass[threadIdx.x] + kept_ties * edge_w : 0u;
+    const uint64_t own_mass = (int)threadIdx.x < segments ? s->seg_mass[threadIdx.x] + kept_ties * edge_w : 0u;
     const uint64_t mass = scan(r, own_mass);       // of the last thread: this CTA's
     const Shares kept = share(r, mass, 0);
     const uint64_t total = kept.mass, before = kept.mass_below + mass - own_mass;
-    const uint64_t at = draw_at(p.uniform[row], total);
-    if (threadIdx.x < SM_SEGMENTS && before <= at && at < before + own_mass) {
+    const uint64_t at = draw_at(u, total);
+    if ((int)threadIdx.x < segments && before <= at && at < before + own_mass) {
         s->warp_mass[0] = at - before;      // what to walk into this segment, and with how many equals
         s->warp_count[0] = last.keep > ties_before ? last.keep - ties_before : 0u;
         s->warp_a[0] = threadIdx.x;
