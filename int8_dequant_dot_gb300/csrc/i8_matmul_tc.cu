@@ -605,28 +605,33 @@ __device__ __forceinline__ void ld16x2(uint32_t taddr, uint32_t (&r)[32])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// N tokens' sums of one channel from column `c` on, of all `split` CTAs, and their outputs.  The
-// loads of two CTAs are in flight together: each takes a trip through the cluster's network.
-template <int N, int CG>
-__device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, int c, int split, uint32_t first, int64_t t, int64_t channel, bool ok)
+// N sums of one channel, at an address of the cluster's shared memory.
+template <int N> __device__ __forceinline__ void read_sums(uint32_t at, int32_t (&v)[N])
 {
-    int32_t a[N];
 #pragma unroll
     for (int j = 0; j < N; ++j)
-        a[j] = 0;
-    for (int s = 0; s < split; s += 2) {
-        const bool two = s + 1 < split;
-        const uint32_t from0 = map_to(at, (uint32_t)(s * CG) + first) + (uint32_t)c * 512;
-        const uint32_t from1 = map_to(at, (uint32_t)((two ? s + 1 : s) * CG) + first) + (uint32_t)c * 512;
-        int32_t v0[N], v1[N];
+        asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v[j]) : "r"(at + 512 * j) : "memory");
+}
+
+// N tokens' sums of one channel at `at` (own shared memory, and the same place in the others), of all
+// `split` CTAs, and their outputs.  The cluster's network carries about 10 bytes a cycle for each CTA,
+// so the own sums are read locally, nothing twice, and each CTA begins with another neighbour.
+template <int N, int CG>
+__device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, int split, int part, uint32_t pair_rank, int64_t t, int64_t channel, bool ok)
+{
+    int32_t a[N], v[N], u[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v0[j]) : "r"(from0 + 512 * j) : "memory");
-            asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v1[j]) : "r"(from1 + 512 * j) : "memory");
-        }
+    for (int j = 0; j < N; ++j)
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a[j]) : "r"(at + 512 * j) : "memory");
+    for (int s = 1; s < split; s += 2) {          // two neighbours' in flight together
+        const int first = part + s < split ? part + s : part + s - split, second = first + 1 < split ? first + 1 : 0;
+        const bool two = s + 1 < split;
+        read_sums(map_to(at, (uint32_t)(first * CG) + pair_rank), v);
+        if (two)
+            read_sums(map_to(at, (uint32_t)(second * CG) + pair_rank), u);
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            a[j] += v0[j] + (two ? v1[j] : 0);
+            a[j] += v[j] + (two ? u[j] : 0);
     }
     store_tokens<N>(p, t, channel, a, p.scale_w[channel], p.bias ? p.bias[channel] : 0.0f, ok);
 }
@@ -815,14 +820,14 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
             ok = ok && bad == 0;
         }
         if (channel < p.n) {
-            const uint32_t at = operands + (uint32_t)(32 * sub + lane) * 4, first = pair_rank, turn = (uint32_t)(part * 2 + half);
+            const uint32_t at = operands + (uint32_t)(32 * sub + lane) * 4, turn = (uint32_t)(part * 2 + half);
             // groups of tokens, shared out over the CTAs of the split and the two warps of each channel
             if (q.tile_t >= 32 * q.split)
                 for (int c = 16 * (int)turn; c < q.tile_t; c += 32 * q.split)
-                    store_sums<16, CG>(p, at, c, q.split, first, t.t0 + c, channel, ok);
+                    store_sums<16, CG>(p, at + (uint32_t)c * 512, q.split, part, pair_rank, t.t0 + c, channel, ok);
             else
                 for (int c = 4 * (int)turn; c < q.tile_t; c += 8 * q.split)
-                    store_sums<4, CG>(p, at, c, q.split, first, t.t0 + c, channel, ok);
+                    store_sums<4, CG>(p, at + (uint32_t)c * 512, q.split, part, pair_rank, t.t0 + c, channel, ok);
         }
         __syncwarp();
     }
