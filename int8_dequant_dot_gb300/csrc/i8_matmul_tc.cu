@@ -551,40 +551,46 @@ __device__ __forceinline__ bool mma_role(const MatmulParams &p, const MatmulTcPl
 // decided once, not per element: a branch for each made a tile's stores take 30000 cycles, a
 // quarter of the tile.  The compiler barrier keeps the next tokens' scales behind this call's
 // stores: the running sums leave few registers.
-template <int N, typename E>
-__device__ __forceinline__ void put_tokens(const MatmulParams &p, int64_t t, int64_t channel, const int32_t *a, float sw, float bias, bool ok)
+template <int N, typename E, typename F>
+__device__ __forceinline__ void put_tokens(const MatmulParams &p, int64_t t, int64_t channel, const int32_t *a, F scale, float sw, float bias, bool ok)
 {
-    const float *sx = p.scale_x + t;
-    const int64_t stride = p.y_stride;
-    const bool add = p.bias != nullptr;
+    const int64_t stride = p.y_stride, left = p.tokens - t;
+    const bool add = p.bias != nullptr, live = channel < p.n;
     auto value = [&](int i) {
-        const float f = __fmul_rn((float)a[i], __fmul_rn(sw, sx[i]));
+        const float f = __fmul_rn((float)a[i], __fmul_rn(sw, scale(i)));
         return dev::from_f32<E>(ok ? (add ? __fadd_rn(f, bias) : f) : __uint_as_float(0x7fc00000u));
     };
     E *y = static_cast<E *>(p.y) + t * stride + channel;
-    if (t + N <= p.tokens) {
+    if (left >= N) {
 #pragma unroll
-        for (int i = 0; i < N; ++i, y += stride)
-            *y = value(i);
+        for (int i = 0; i < N; ++i, y += stride) {
+            const E v = value(i);
+            if (live)
+                *y = v;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i, y += stride)
-            if (t + i < p.tokens)
-                *y = value(i);
+            if (i < left) {
+                const E v = value(i);
+                if (live)
+                    *y = v;
+            }
     }
 }
 
-template <int N>
-__device__ __forceinline__ void store_tokens(const MatmulParams &p, int64_t t, int64_t channel, const int32_t *a, float sw, float bias, bool ok)
+// scale(i): token t + i's, asked for by whole warps and where there is such a token alone.
+template <int N, typename F>
+__device__ __forceinline__ void store_tokens(const MatmulParams &p, int64_t t, int64_t channel, const int32_t *a, F scale, float sw, float bias, bool ok)
 {
     asm volatile("" ::: "memory");
     if (p.y_dtype == LOOM_F32)
-        put_tokens<N, float>(p, t, channel, a, sw, bias, ok);
+        put_tokens<N, float>(p, t, channel, a, scale, sw, bias, ok);
     else if (p.y_dtype == LOOM_F16)
-        put_tokens<N, __half>(p, t, channel, a, sw, bias, ok);
+        put_tokens<N, __half>(p, t, channel, a, scale, sw, bias, ok);
     else
-        put_tokens<N, __nv_bfloat16>(p, t, channel, a, sw, bias, ok);
-    if (p.acc)
+        put_tokens<N, __nv_bfloat16>(p, t, channel, a, scale, sw, bias, ok);
+    if (p.acc && channel < p.n)
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (t + i < p.tokens)
@@ -617,8 +623,10 @@ template <int N> __device__ __forceinline__ void read_sums(uint32_t at, int32_t 
 // `split` CTAs, and their outputs.  The cluster's network carries about 10 bytes a cycle for each CTA,
 // so the own sums are read locally, nothing twice, and each CTA begins with another neighbour.
 template <int N, int CG>
-__device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, int split, int part, uint32_t pair_rank, int64_t t, int64_t channel, bool ok)
+__device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, int split, int part, uint32_t pair_rank, int64_t t, int64_t channel, int lane, float sw,
+                                           float bias, bool ok)
 {
+    const float sx = lane < N && t + lane < p.tokens ? p.scale_x[t + lane] : 0.0f;      // a lane's token, on its way with the sums
     int32_t a[N], v[N], u[N];
 #pragma unroll
     for (int j = 0; j < N; ++j)
@@ -633,7 +641,7 @@ __device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, i
         for (int j = 0; j < N; ++j)
             a[j] += v[j] + (two ? u[j] : 0);
     }
-    store_tokens<N>(p, t, channel, a, p.scale_w[channel], p.bias ? p.bias[channel] : 0.0f, ok);
+    store_tokens<N>(p, t, channel, a, [&](int i) { return __shfl_sync(dev::FULL_MASK, sx, i); }, sw, bias, ok);
 }
 
 // Adds a tile's accumulators (one for each half and 1024 k) to `sum`: of this thread's channel,
@@ -800,7 +808,10 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (16 * j < cols)
-                            store_tokens<16>(p, t.t0 + (2 * h + half) * cols + 16 * j, channel, sum + 64 * h + 16 * j, sw, bias, ok);
+                            {
+                            const int64_t token = t.t0 + (2 * h + half) * cols + 16 * j;
+                            store_tokens<16>(p, token, channel, sum + 64 * h + 16 * j, [&](int i) { return p.scale_x[token + i]; }, sw, bias, ok);
+                        }
             }
         }
         __syncwarp();
@@ -819,16 +830,15 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
             asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(bad) : "r"(map_to(area + 8, (uint32_t)s)) : "memory");
             ok = ok && bad == 0;
         }
-        if (channel < p.n) {
-            const uint32_t at = operands + (uint32_t)(32 * sub + lane) * 4, turn = (uint32_t)(part * 2 + half);
-            // groups of tokens, shared out over the CTAs of the split and the two warps of each channel
-            if (q.tile_t >= 32 * q.split)
-                for (int c = 16 * (int)turn; c < q.tile_t; c += 32 * q.split)
-                    store_sums<16, CG>(p, at + (uint32_t)c * 512, q.split, part, pair_rank, t.t0 + c, channel, ok);
-            else
-                for (int c = 4 * (int)turn; c < q.tile_t; c += 8 * q.split)
-                    store_sums<4, CG>(p, at + (uint32_t)c * 512, q.split, part, pair_rank, t.t0 + c, channel, ok);
-        }
+        const float sw = channel < p.n ? p.scale_w[channel] : 0.0f, bias = channel < p.n && p.bias ? p.bias[channel] : 0.0f;
+        const uint32_t at = operands + (uint32_t)(32 * sub + lane) * 4, turn = (uint32_t)(part * 2 + half);
+        // groups of tokens, shared out over the CTAs of the split and the two warps of each channel
+        if (q.tile_t >= 32 * q.split)
+            for (int c = 16 * (int)turn; c < q.tile_t; c += 32 * q.split)
+                store_sums<16, CG>(p, at + (uint32_t)c * 512, q.split, part, pair_rank, t.t0 + c, channel, lane, sw, bias, ok);
+        else
+            for (int c = 4 * (int)turn; c < q.tile_t; c += 8 * q.split)
+                store_sums<4, CG>(p, at + (uint32_t)c * 512, q.split, part, pair_rank, t.t0 + c, channel, lane, sw, bias, ok);
         __syncwarp();
     }
     if (q.split > 1)
