@@ -128,11 +128,6 @@ __device__ __forceinline__ float byte_factor(uint32_t amax_bits, float &scale, b
     return __fdiv_rn(127.0f, amax);
 }
 
-__device__ __forceinline__ int8_t to_byte(float v, float inv, bool bad)
-{
-    return bad ? (int8_t)0 : (int8_t)__float2int_rn(__fmul_rn(v, inv));
-}
-
 // Packed f32 pairs: two columns in one instruction, each rounded as on its own.
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 {
@@ -149,6 +144,30 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 }
 
 __device__ __forceinline__ uint64_t both(float v) { return dev::pack2(v, v); }
+
+// rint(v inv) of V values, |v inv| < 2^21: added to 1.5 2^23, the product's nearest whole number is in
+// the low bits.  (The conversion instruction issues at a quarter of that rate: 8192 x 8192 bf16 by
+// it took ROWSA, and without it ROWSB.)
+template <int V> __device__ __forceinline__ Pack<int8_t, V> to_bytes(const float *v, float inv, bool bad)
+{
+    uint32_t b[V];      // (in two roundings: of f32x2 instructions, product and sum may become one)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        b[i] = __float_as_uint(__fadd_rn(__fmul_rn(v[i], inv), 12582912.0f));
+    Pack<int8_t, V> o;
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const uint32_t w = __byte_perm(__byte_perm(b[i], b[i + 1], 0x0040), __byte_perm(b[i + 2], b[i + 3], 0x0040), 0x5410), q = bad ? 0u : w;
+            memcpy(o.e + i, &q, 4);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            o.e[i] = bad ? (int8_t)0 : (int8_t)b[i];
+    }
+    return o;
+}
 
 __device__ __forceinline__ float halves_sum(uint64_t v)
 {
@@ -440,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rows_kernel(c
                 a[r] = 0;
 #pragma unroll
                 for (int i = 0; i < EPT; ++i)
-                    if (column<V>(t, group, i) < p.width)
+                    if (M == RowMode::Quantize || column<V>(t, group, i) < p.width)     // (zeros past the tokens' width)
                         a[r] = max(a[r], magnitude_bits(v[r][i]));
             }
             group_maxima<R, WARP>(a, red[turn][2]);
@@ -462,11 +481,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rows_kernel(c
                     for (int j = 0; j < NV; ++j) {
                         const int c = (t + j * group) * V;
                         if (c < p.width) {
-                            Pack<int8_t, V> o;
-#pragma unroll
-                            for (int i = 0; i < V; ++i)
-                                o.e[i] = to_byte(v[r][j * V + i], inv, bad);
-                            *reinterpret_cast<Pack<int8_t, V> *>(q + c) = o;
+                            *reinterpret_cast<Pack<int8_t, V> *>(q + c) = to_bytes<V>(v[r] + j * V, inv, bad);
                         }
                     }
                 }
@@ -543,11 +558,7 @@ template <typename E, RowMode M, int V> __global__ void __launch_bounds__(1024) 
     }
     for (int64_t c = c0; c < p.width; c += step) {
         output(c);
-        Pack<int8_t, V> o;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            o.e[i] = to_byte(v[i], inv, bad);
-        *reinterpret_cast<Pack<int8_t, V> *>(p.q + row * p.width + c) = o;
+        *reinterpret_cast<Pack<int8_t, V> *>(p.q + row * p.width + c) = to_bytes<V>(v, inv, bad);
     }
 }
 
