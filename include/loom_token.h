@@ -95,10 +95,10 @@ loom_status loom_i8_matmul(const int32_t *d_w_packed, const float *d_scale_w, in
  * the tuning, `path` picks the engine (LOOM_PATH_DIRECT: dp4a; LOOM_PATH_TENSOR:
  * tensor cores, which want both matrices to start on 16 bytes, else LOOM_ERR_ALIGN;
  * LOOM_PATH_STAGED -> LOOM_ERR_ARG; by default tensor cores where that holds and there are
- * more than 8 tokens) and wait_ns limits each device
- * wait of the tensor-core kernel: one that runs out sets LOOM_DEVERR_TIMEOUT, the
- * affected y are NaN (acc INT32_MIN), and the device stays usable.  The engine
- * does not change a result. */
+ * more than 24 tokens, or more than 4 of enough weights to be worth their start) and
+ * wait_ns limits each device wait of the tensor-core kernel: one that runs out sets
+ * LOOM_DEVERR_TIMEOUT, the affected y are NaN (acc INT32_MIN), and the device stays usable.
+ * The engine does not change a result. */
 loom_status loom_i8_matmul_ex(const int32_t *d_w_packed, const float *d_scale_w, int32_t n_rows, int32_t k,
                               const int32_t *d_x_packed, const float *d_scale_x, int32_t tokens, const float *d_bias,
                               void *d_y, int32_t y_dtype, int64_t y_stride, int32_t *d_acc, int32_t *d_error,

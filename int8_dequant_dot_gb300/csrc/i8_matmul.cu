@@ -17,6 +17,12 @@
 //    their order does not matter.
 //  * Rows that are not whole 16-byte pieces (k % 16 != 0, or pointers that are
 //    not 16-byte aligned) take the same path with 4-byte loads.
+//
+//  * Two CTAs share an SM for any number of tokens (128 registers a thread: alone, 8 tokens
+//    took 70 us below).
+//
+// Measured: 8192 x 16384 for 1 token in 20.9 us, the 134 MB of weights at 6.4 TB/s; 4 tokens 25.6 us,
+// 8 tokens 43 us (instruction issue: 32 dp4a for each 16 bytes of weights).
 #include "token_ops.cuh"
 
 namespace loom {
@@ -79,7 +85,7 @@ template <int N> __device__ __forceinline__ void warp_sums(int32_t (&v)[N], int 
 }
 
 template <int T, int KV, int R, bool V16>
-__global__ void __launch_bounds__(32 * DP_WARPS, T <= 4 ? 2 : 1) i8_matmul_dp4a_kernel(const MatmulParams p)
+__global__ void __launch_bounds__(32 * DP_WARPS, 2) i8_matmul_dp4a_kernel(const MatmulParams p)
 {
     extern __shared__ int32_t totals[];   // [rows_per_cta][T]
     constexpr int CHUNK = KV * 512;

@@ -1,5 +1,5 @@
 // i8_matmul_tc.cu -- matrix product of 8-bit tokens and 8-bit weights on the
-// 5th-generation tensor cores (tcgen05, sm_103a), for nine tokens to many.
+// 5th-generation tensor cores (tcgen05, sm_103a), for five tokens to many.
 //
 //   acc[t][r] = sum_k W[r][k] X[t][k],  y[t][r] = (float)acc * (sw[r] * sx[t]) + bias[r]
 //
@@ -18,30 +18,41 @@
 //  * Shared memory moves 128 bytes a cycle, for copies, converters and MMA operands
 //    together, and is what runs out first.  So the f16 weights go to tensor memory
 //    (tcgen05.st; the MMA's A operand) and only the f16 tokens go back to shared memory.
-//    A stage of 128 k of a 256 x 256 pair tile then moves 128 KB in 1024 MMA cycles.
-//  * Roles (20 warps, with one half 28): a loader copies 128 bytes of k of each row into a
-//    ring by TMA, completing on an mbarrier (rows that are not whole 16-byte pieces: see
-//    below); two groups of four converter warps (with one
-//    half: four groups) take stages in turn; one thread issues the MMAs; eight epilogue warps drain finished
-//    accumulators (each thread one channel and half the tokens, 128 running int32 sums in
-//    registers) and store: the lanes of a warp are neighbouring channels of a token.
+//    A stage of 128 k of a 256 x 256 pair tile then moves 128 KB in 1024 MMA cycles
+//    (measured: 1225 cycles a stage).
+//  * Roles (20 warps, with one half 28).  A loader copies 128 bytes of k of each row into a
+//    ring by TMA, completing on an mbarrier.  Two groups of four converter warps (with one
+//    half: four groups) take stages in turn.  One thread issues the MMAs.  Eight epilogue
+//    warps add finished accumulators up, each thread one channel and half the tokens (at
+//    most 128 int32 sums in registers), and store: a warp's lanes are channels of one token.
 //  * Rows whose k is a multiple of 4 alone: TMA needs a row pitch of whole 16s, which four rows
 //    have together.  The matrix is seen as n / 4 rows of 4 k bytes; the rows of one of four
 //    classes (row mod 4) lie at a column of it, and a box of 144 bytes from the 16-byte
 //    boundary before brings their 128 bytes, which the converters shift into place.  The last
 //    n mod 4 rows are copied word by word.  (A bulk copy a row, and four-byte copies for all
 //    rows, took three and two times as long as the boxes.)
-//  * Tensor memory: accumulators of up to 128 tokens, used in turn (two alone, three in a
-//    pair), and a f16 weight buffer for each group of converters.  In a pair a tile of more than 128 tokens is two halves that share each stage: the
-//    accumulator of one half drains while the other's MMAs run, and a third takes the
-//    next 1024 k.
-//  * Registers go where they are needed (setmaxnreg).
+//  * Tensor memory holds the accumulators, of up to 128 tokens each and used in turn (two; for
+//    two halves three), and a buffer of f16 weights for each group of converters.  The two
+//    halves of a tile share each stage: the accumulator of one drains while the other's MMAs
+//    run, and the third takes the next 1024 k.
+//  * Registers go where they are needed (setmaxnreg): the sums.
 //  * With fewer tiles than SMs, k is split over the CTAs (or pairs) of a cluster, and their
 //    int32 sums are added through distributed shared memory: whole numbers, so the bits do
 //    not depend on the split.
 //  * Every wait is bounded; one that runs out sets LOOM_DEVERR_TIMEOUT, every role stops at
 //    its next wait, copies and MMAs in flight finish, tensor memory is freed, affected y are
 //    NaN and acc INT32_MIN.
+//
+// Measured (tokens x n x k, bf16 outputs)
+//   4096 x 16384 x 8192   765 us, 1.44 PFLOP/s (a library's bf16 product of these sizes takes
+//                         520 to 565 us).  Bound by the converters' shared-memory traffic (64
+//                         stages of 1225 cycles a tile), then by a tile's stores (18000 cycles,
+//                         half of them behind the next tile's MMAs), which share those ports.
+//   96 x 65536 x 4096     62 us, 4.4 TB/s: the converters and, every 32 stages, a tile's end.
+//   16 x 8192 x 16384     31 to 33 us, 4.2 TB/s: 64 tiles split over 128 of the SMs, and 5 us
+//                         until the first MMA.
+//   203 x 5001 x 4108     33 us (k = 4112: 27 us): 120 CTAs of 11 stages each; the exchange of
+//                         the sums is a third of it.
 #include "tc_ptx.cuh"
 #include "token_ops.cuh"
 
@@ -349,7 +360,8 @@ __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity)
 // Group `group` of four warps takes every GROUPS-th of the CTA's `stages`.
 template <int CG, int H, bool V16>
 __device__ __forceinline__ void convert_role(const MatmulParams &p, const MatmulTcPlan &q, uint32_t area, uint32_t ring, uint32_t operands,
-                                             uint32_t tmem, int group, int sub, int lane, uint32_t pair_rank, uint32_t leader, uint32_t stages, const Work &work)
+                                             uint32_t tmem, int group, int sub, int lane, uint32_t pair_rank, uint32_t leader, uint32_t stages,
+                                             const Work &work)
 {
     using S = Shape<H>;
     const int b_rows = q.tile_t / CG;
@@ -548,8 +560,8 @@ __device__ __forceinline__ bool mma_role(const MatmulParams &p, const MatmulTcPl
 
 // ---- epilogue ------------------------------------------------------------------------
 // Up to N tokens from `t` on of one channel.  The element type and whether all N are there are
-// decided once, not per element: a branch for each made a tile's stores take 30000 cycles, a
-// quarter of the tile.  The compiler barrier keeps the next tokens' scales behind this call's
+// decided once, not per element: a branch for each made a tile's stores take 30000 cycles, where
+// they now take 18000.  The compiler barrier keeps the next tokens' scales behind this call's
 // stores: the running sums leave few registers.
 template <int N, typename E, typename F>
 __device__ __forceinline__ void put_tokens(const MatmulParams &p, int64_t t, int64_t channel, const int32_t *a, F scale, float sw, float bias, bool ok)
@@ -623,8 +635,8 @@ template <int N> __device__ __forceinline__ void read_sums(uint32_t at, int32_t 
 // `split` CTAs, and their outputs.  The cluster's network carries about 10 bytes a cycle for each CTA,
 // so the own sums are read locally, nothing twice, and each CTA begins with another neighbour.
 template <int N, int CG>
-__device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, int split, int part, uint32_t pair_rank, int64_t t, int64_t channel, int lane, float sw,
-                                           float bias, bool ok)
+__device__ __forceinline__ void store_sums(const MatmulParams &p, uint32_t at, int split, int part, uint32_t pair_rank, int64_t t, int64_t channel,
+                                           int lane, float sw, float bias, bool ok)
 {
     const float sx = lane < N && t + lane < p.tokens ? p.scale_x[t + lane] : 0.0f;      // a lane's token, on its way with the sums
     int32_t a[N], v[N], u[N];
@@ -771,7 +783,8 @@ __global__ void __launch_bounds__(Shape<H>::THREADS, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        convert_role<CG, H, V16>(p, q, area, ring, operands, tmem, (warp - MT_CONV_WARP) >> 2, warp & 3, lane, pair_rank, leader, (uint32_t)(work * (w.step1 - w.step0)), w);
+        convert_role<CG, H, V16>(p, q, area, ring, operands, tmem, (warp - MT_CONV_WARP) >> 2, warp & 3, lane, pair_rank, leader,
+                                 (uint32_t)(work * (w.step1 - w.step0)), w);
         __syncwarp();
     } else {
         if (H == 1)
@@ -862,8 +875,9 @@ bool encode_rows(CUtensorMap *map, const int8_t *base, int64_t pitch, int64_t ou
     }();
     const cuuint64_t dims[2] = {(cuuint64_t)pitch, (cuuint64_t)(outer > 0 ? outer : 1)}, strides[1] = {(cuuint64_t)pitch};
     const cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)rows}, unit[2] = {1, 1};
+    const CUtensorMapSwizzle swizzle = width == MT_KSTEP ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
     return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(base), dims, strides, box, unit,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, width == MT_KSTEP ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -14,6 +14,7 @@ inline int64_t dtype_bytes(int32_t dtype) { return dtype == LOOM_F32 ? 4 : 2; }
 
 // ---- 8-bit matrix product (i8_matmul.cu: dp4a) -----------------------------------
 constexpr int MM_DP4A_PASS = 8;       // tokens per pass of the dp4a kernel
+constexpr int MM_DP4A_MOST = 24;      // tokens that it takes by itself, of aligned matrices
 constexpr int MM_DP4A_CTAS_PER_SM = 2;
 
 struct MatmulParams {

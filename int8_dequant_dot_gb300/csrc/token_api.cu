@@ -61,7 +61,16 @@ loom_status matmul_geometry(int64_t tokens, int64_t n, int64_t k, bool aligned, 
     }
     if (path == LOOM_PATH_TENSOR && !aligned)
         return LOOM_ERR_ALIGN;
-    const bool tensor = path == LOOM_PATH_TENSOR || (path == LOOM_PATH_AUTO && aligned && tokens > MM_DP4A_PASS);
+    // Measured (us, dp4a / tensor cores)    1024 x 1024   4096 x 4096   32768 x 2048   8192 x 16384
+    //   4 tokens                             2.6 / 7.9     4.9 / 10.5   11.7 / 18.0    25.6 / 31.6
+    //   8                                    3.1 / 8.0     7.6 / 10.6   21.9 / 18.0    43.2 / 31.4
+    //   16                                   4.9 / 8.0    13.3 / 10.4   39.9 / 17.9    83.6 / 31.8
+    //   24, 32                 6.8 / 8.0 and 8.5 / 8.0 (256 x 256: 6.0 / 6.5 and 7.5 / 6.3)
+    // A pass of dp4a takes about twice what the weights take the tensor cores, which take 5 us
+    // more to begin and end.
+    const int64_t passes = (tokens + MM_DP4A_PASS - 1) / MM_DP4A_PASS;
+    const bool many = tokens > 4 && (tokens > MM_DP4A_MOST || (2 * passes - 1) * n * k > (36ll << 20));
+    const bool tensor = path == LOOM_PATH_TENSOR || (path == LOOM_PATH_AUTO && aligned && many);
     if (tensor && k > 0 && n > 0 && tokens > 0) {
         matmul_tc_plan(tokens, n, k, k % 16 == 0, sms, plan);
         *out = plain_launch(plan->grid, 1, (uint32_t)matmul_tc_threads(*plan), LOOM_KERNEL_I8_MATMUL_TENSOR, 128u);
@@ -72,7 +81,6 @@ loom_status matmul_geometry(int64_t tokens, int64_t n, int64_t k, bool aligned, 
     const int64_t slots = sms * MM_DP4A_CTAS_PER_SM;
     int64_t per = (n + slots - 1) / slots;
     per = per < 1 ? 1 : per > MM_MAX_ROWS_PER_CTA ? MM_MAX_ROWS_PER_CTA : per;
-    const int64_t passes = (tokens + MM_DP4A_PASS - 1) / MM_DP4A_PASS;
     *out = plain_launch((n + per - 1) / per, passes < 65535 ? passes : 65535, 256, LOOM_KERNEL_I8_MATMUL_DP4A, (uint32_t)per);
     return LOOM_OK;
 }
