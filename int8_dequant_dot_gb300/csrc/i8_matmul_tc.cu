@@ -887,6 +887,8 @@ template <int CG, int H, bool V16> cudaError_t launch_cg(const MatmulParams &p, 
     // setmaxnreg hands out the registers that the launch brought: were there fewer, the
     // epilogue's request would wait for ever
     static std::atomic<uint64_t> done{0};
+    if (q.ahead < Shape<H>::DEPTH)     // (no tile of matmul_tc_plan) the converters would take a stage for copied that is not
+        return cudaErrorInvalidConfiguration;
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), Shape<H>::LAUNCH_REGS, done);
     if (e != cudaSuccess)
         return e;
