@@ -137,3 +137,11 @@ def test_launch_geometry(loom):
         L = cfg(loom.LOOM_OP_I8_MATMUL, [t, n, k, 1, loom.LOOM_PATH_DIRECT, SMS])
         assert L["kernel"] == loom.LOOM_KERNEL_I8_MATMUL_DP4A
         assert L["units_per_cta"] <= 1024 and L["grid"][0] == -(-n // L["units_per_cta"])
+
+
+@pytest.mark.parametrize("t,n,k,tensor", [(1, 65536, 16384, False), (4, 65536, 16384, False), (5, 8192, 16384, True), (8, 4096, 4096, False),
+                                          (8, 32768, 2048, True), (16, 1024, 1024, False), (16, 4096, 4096, True), (24, 1024, 1024, False),
+                                          (24, 2048, 4096, True), (25, 64, 64, True), (4096, 64, 64, True)])
+def test_engine_by_tokens_and_weights(loom, t, n, k, tensor):
+    want = loom.LOOM_KERNEL_I8_MATMUL_TENSOR if tensor else loom.LOOM_KERNEL_I8_MATMUL_DP4A
+    assert loom.loom_token_launch_config(loom.LOOM_OP_I8_MATMUL, [t, n, k, 1, loom.LOOM_PATH_AUTO, SMS])["kernel"] == want
