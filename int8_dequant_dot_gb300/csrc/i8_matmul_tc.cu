@@ -48,9 +48,11 @@
 //                         520 to 565 us).  Bound by the converters' shared-memory traffic (64
 //                         stages of 1225 cycles a tile), then by a tile's stores (18000 cycles,
 //                         half of them behind the next tile's MMAs), which share those ports.
-//   96 x 65536 x 4096     62 us, 4.4 TB/s: the converters and, every 32 stages, a tile's end.
-//   16 x 8192 x 16384     31 to 33 us, 4.2 TB/s: 64 tiles split over 128 of the SMs, and 5 us
-//                         until the first MMA.
+//   96 x 65536 x 4096     62 us, 4.4 TB/s: an MMA takes 84 cycles or more however few its
+//                         tokens, and a stage has eight (770 cycles measured); 256 tiles are
+//                         four waves of pairs, the last a third full.
+//   16 x 8192 x 16384     31 to 33 us, 4.2 TB/s: the same MMAs (780 cycles a stage), 64 tiles
+//                         split over 128 of the SMs.
 //   203 x 5001 x 4108     33 us (k = 4112: 27 us): 120 CTAs of 11 stages each; the exchange of
 //                         the sums is a third of it.
 #include "tc_ptx.cuh"

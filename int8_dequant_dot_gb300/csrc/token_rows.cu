@@ -593,7 +593,7 @@ RingPlan plan_ring(int64_t rows, int64_t grid, int64_t per_sm, int64_t row_bytes
     const int64_t turns = (rows + grid * rows_a_turn - 1) / (grid > 0 ? grid * rows_a_turn : 1);
     stages = stages < 2 ? 2 : stages > RING_MAX_STAGES ? RING_MAX_STAGES : stages;
     stages = stages < turns ? stages : turns;
-    if (stages < 2 || per_sm * (stages * (slot + 8) + 3072) > 226 * 1024)
+    if (stages < 2 || per_sm * (stages * (slot + 8) + 3 * 1024) > 226 * 1024)
         return r;
     r.stages = (int)stages;
     r.place = (uint32_t)place;
@@ -663,7 +663,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, 1) norm_grad_kernel(const No
     const uint64_t policy = dev::l2_evict_first_policy();
     if (!WARP && threadIdx.x == 0)
         for (int i = 0; i < stages && row0 + i * step < p.rows; ++i)
-            ring_fill<E, R>(ring.bars + 8 * i, ring.slots + (uint32_t)i * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride, p.rows, p.width, row0 + i * step, policy);
+            ring_fill<E, R>(ring.bars + 8 * i, ring.slots + (uint32_t)i * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride, p.rows,
+                            p.width, row0 + i * step, policy);
     {
         float g[EPT];
 #pragma unroll
@@ -754,7 +755,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, 1) norm_grad_kernel(const No
             group_sums<2 * R, WARP>(sums, red[turn]);      // behind its barrier the slot is free: every thread has read it
         if (!WARP && stages) {
             if (threadIdx.x == 0 && row0 + stages * step < p.rows && !ring.late)
-                ring_fill<E, R>(ring.bars + 8 * slot, ring.slots + (uint32_t)slot * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride, p.rows, p.width, row0 + stages * step, policy);
+                ring_fill<E, R>(ring.bars + 8 * slot, ring.slots + (uint32_t)slot * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride,
+                                p.rows, p.width, row0 + stages * step, policy);
             if (++slot == stages) {
                 slot = 0;
                 parity ^= 1u;
