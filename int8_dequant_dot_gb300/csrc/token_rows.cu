@@ -297,6 +297,34 @@ __device__ __noinline__ void ring_fill(uint32_t bar, uint32_t to, uint32_t place
         }
 }
 
+// The same for rows of whole 16-byte blocks, all inside: short enough to stand in the loop, where
+// the one thread's way to the next barrier is everyone's.
+template <typename E, int R>
+__device__ __forceinline__ void ring_fill_whole(uint32_t bar, uint32_t to, uint32_t place, const void *a, int64_t a_stride, const void *b, int64_t b_stride,
+                                                int64_t rows, int32_t width, int64_t row, uint64_t policy)
+{
+    const uint32_t bytes = (uint32_t)width * (uint32_t)sizeof(E), here = R == 1 || row + 1 < rows ? R : 1;
+    static_assert(R <= 2, "rows of a turn");
+    dev::mbar_arrive_expect_tx(bar, (b ? 2 : 1) * here * bytes);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (i < (int)here) {
+            dev::bulk_g2s(to + (uint32_t)i * (b ? 2 : 1) * place, static_cast<const E *>(a) + (row + i) * a_stride, bytes, bar, policy);
+            if (b)
+                dev::bulk_g2s(to + (uint32_t)(2 * i + 1) * place, static_cast<const E *>(b) + (row + i) * b_stride, bytes, bar, policy);
+        }
+}
+
+template <typename E, int R, bool WHOLE>
+__device__ __forceinline__ void ring_fill_rows(uint32_t bar, uint32_t to, uint32_t place, const void *a, int64_t a_stride, const void *b, int64_t b_stride,
+                                               int64_t rows, int32_t width, int64_t row, uint64_t policy)
+{
+    if (WHOLE)
+        ring_fill_whole<E, R>(bar, to, place, a, a_stride, b, b_stride, rows, width, row, policy);
+    else
+        ring_fill<E, R>(bar, to, place, a, a_stride, b, b_stride, rows, width, row, policy);
+}
+
 // V elements of a row from column c on, from the ring's slot or from memory.
 template <typename E, int V> __device__ __forceinline__ void read_row(const Ring &r, uint32_t slot_at, const RowSpan<E> &s, const E *row, int64_t c, float *v)
 {
@@ -339,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rows_kernel(c
     const uint64_t policy = dev::l2_evict_first_policy();
     if (!WARP && threadIdx.x == 0)
         for (int i = 0; i < stages && row0 + i * step < p.rows; ++i)
-            ring_fill<E, R>(ring.bars + 8 * i, ring.slots + (uint32_t)i * ring.slot_bytes, place, p.x, p.x_stride, nullptr, 0, p.rows, p.width,
+            ring_fill_rows<E, R, WHOLE>(ring.bars + 8 * i, ring.slots + (uint32_t)i * ring.slot_bytes, place, p.x, p.x_stride, nullptr, 0, p.rows, p.width,
                             row0 + i * step, policy);
     float gain[NP], bias[NP];
     if (KEEP && M != RowMode::Quantize)
@@ -384,7 +412,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rows_kernel(c
         auto refill = [&]() {
             if (!WARP && stages) {
                 if (threadIdx.x == 0 && row0 + stages * step < p.rows && !ring.late)
-                    ring_fill<E, R>(ring.bars + 8 * slot, ring.slots + (uint32_t)slot * ring.slot_bytes, place, p.x, p.x_stride, nullptr, 0, p.rows,
+                    ring_fill_rows<E, R, WHOLE>(ring.bars + 8 * slot, ring.slots + (uint32_t)slot * ring.slot_bytes, place, p.x, p.x_stride, nullptr, 0, p.rows,
                                     p.width, row0 + stages * step, policy);
                 if (++slot == stages) {
                     slot = 0;
@@ -663,7 +691,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, 1) norm_grad_kernel(const No
     const uint64_t policy = dev::l2_evict_first_policy();
     if (!WARP && threadIdx.x == 0)
         for (int i = 0; i < stages && row0 + i * step < p.rows; ++i)
-            ring_fill<E, R>(ring.bars + 8 * i, ring.slots + (uint32_t)i * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride, p.rows,
+            ring_fill_rows<E, R, WHOLE>(ring.bars + 8 * i, ring.slots + (uint32_t)i * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride, p.rows,
                             p.width, row0 + i * step, policy);
     {
         float g[EPT];
@@ -755,7 +783,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, 1) norm_grad_kernel(const No
             group_sums<2 * R, WARP>(sums, red[turn]);      // behind its barrier the slot is free: every thread has read it
         if (!WARP && stages) {
             if (threadIdx.x == 0 && row0 + stages * step < p.rows && !ring.late)
-                ring_fill<E, R>(ring.bars + 8 * slot, ring.slots + (uint32_t)slot * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride,
+                ring_fill_rows<E, R, WHOLE>(ring.bars + 8 * slot, ring.slots + (uint32_t)slot * ring.slot_bytes, place, p.x, p.x_stride, p.dy, p.dy_stride,
                                 p.rows, p.width, row0 + stages * step, policy);
             if (++slot == stages) {
                 slot = 0;
