@@ -720,7 +720,7 @@ def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=Non
             dgain = torch.empty(width, dtype=torch.float32, device=device)
         if dbias is None:
             dbias = torch.empty(width, dtype=torch.float32, device=device)
-    if workspace is None:
+    if workspace is None or (dgain is None and dbias is None):      # dx alone needs none
         wp, wb = None, 0
     elif isinstance(workspace, tuple):
         wp, wb = workspace

@@ -81,7 +81,7 @@ struct NormGradParams {
     void *dx;                   // or NULL
     float *dgain, *dbias;       // or NULL
     float *partial;             // [parts][2][width] partial column sums (workspace), or NULL
-    float *row_sums;            // [rows][2]: rows wider than NG_MAX_WIDTH (workspace)
+    float *row_sums;            // [rows][2]: rows wider than NG_MAX_WIDTH (workspace), or NULL where partial is
 };
 // Geometry of the launch that takes the column sums; *parts (may be NULL) receives the
 // number of partial sums per column.

@@ -355,7 +355,7 @@ extern "C" loom_status loom_layer_norm_backward(const void *d_dy, int64_t dy_str
     const loom_status st = sm_count(&sms);
     if (st != LOOM_OK)
         return st;
-    const bool needs = rows > 0 && (columns || width > NG_MAX_WIDTH);
+    const bool needs = rows > 0 && columns;
     if (needs && (!d_workspace || workspace_bytes < norm_grad_workspace_bytes(rows, width, sms)))
         return LOOM_ERR_ARG;
     loom_launch L;
@@ -376,8 +376,8 @@ extern "C" loom_status loom_layer_norm_backward(const void *d_dy, int64_t dy_str
     p.dgain = d_dgain;
     p.dbias = d_dbias;
     if (needs) {
-        p.partial = columns ? static_cast<float *>(d_workspace) : nullptr;
-        p.row_sums = static_cast<float *>(d_workspace) + parts * 2 * width;
+        p.partial = static_cast<float *>(d_workspace);
+        p.row_sums = p.partial + parts * 2 * width;
     }
     const void *ptrs[] = {d_dy, d_x, d_dx ? d_dx : d_x};
     const int64_t strides[] = {p.dy_stride, p.x_stride, d_dx ? p.dx_stride : p.x_stride};

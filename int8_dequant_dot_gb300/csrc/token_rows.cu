@@ -12,7 +12,7 @@
 //    CTA leaves one partial sum per column in the workspace.  A second launch adds
 //    the partial sums in a fixed order: no atomics, the same bits on every call.
 //    Rows wider than 8192 take two passes: the two sums of each row, then blocks
-//    of columns.
+//    of columns (dx alone: both in one launch, a row a CTA).
 //  * CTAs walk over the rows and copy them ahead into a ring of shared memory (bulk copies),
 //    two rows a turn.
 //  * Loads are as wide as every row's start allows: 16 or 8 bytes, else one element.
@@ -835,7 +835,14 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, 1) norm_grad_kernel(const No
     }
 }
 
-// Rows wider than the registers of a CTA: the two sums of each row ...
+// dx of one element from its row's two means; the same bits in either kernel below.
+__device__ __forceinline__ float dx_of(float d, float xhat, float gain, float rstd, float s1, float s2)
+{
+    return __fmul_rn(rstd, __fmaf_rn(-xhat, s2, __fmaf_rn(d, gain, -s1)));
+}
+
+// Rows wider than the registers of a CTA: the two sums of each row, and, where the columns' sums are
+// not wanted, its dx (the row is read again, from L2: no workspace) ...
 template <typename E, int V> __global__ void __launch_bounds__(1024) long_norm_sums_kernel(const NormGradParams p)
 {
     __shared__ float red[2][32];
@@ -844,9 +851,8 @@ template <typename E, int V> __global__ void __launch_bounds__(1024) long_norm_s
     const E *x = static_cast<const E *>(p.x) + row * p.x_stride;
     const E *dy = static_cast<const E *>(p.dy) + row * p.dy_stride;
     const float mean = p.mean[row], rstd = p.rstd[row];
-    float sums[2] = {0.0f, 0.0f}, xv[V], d[V];
+    float sums[2] = {0.0f, 0.0f}, xv[V], d[V], gain[V];
     for (int64_t c = threadIdx.x * V; c < p.width; c += blockDim.x * V) {
-        float gain[V];
         load_params<V>(p.gain, c, 1.0f, gain);
         load_f32<E, V>(x + c, xv);
         load_f32<E, V>(dy + c, d);
@@ -858,9 +864,24 @@ template <typename E, int V> __global__ void __launch_bounds__(1024) long_norm_s
         }
     }
     group_sums<2, false>(sums, red);
-    if (threadIdx.x == 0) {
-        p.row_sums[2 * row] = __fdiv_rn(sums[0], (float)p.width);
-        p.row_sums[2 * row + 1] = __fdiv_rn(sums[1], (float)p.width);
+    const float s1 = __fdiv_rn(sums[0], (float)p.width), s2 = __fdiv_rn(sums[1], (float)p.width);
+    if (p.row_sums) {
+        if (threadIdx.x == 0) {
+            p.row_sums[2 * row] = s1;
+            p.row_sums[2 * row + 1] = s2;
+        }
+        return;
+    }
+    // (behind the reduction's barrier every thread has read the row: dx may take its place)
+    E *dx = static_cast<E *>(p.dx) + row * p.dx_stride;
+    for (int64_t c = threadIdx.x * V; c < p.width; c += blockDim.x * V) {
+        load_params<V>(p.gain, c, 1.0f, gain);
+        load_f32<E, V>(x + c, xv);
+        load_f32<E, V>(dy + c, d);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            d[i] = dx_of(d[i], (xv[i] - mean) * rstd, gain[i], rstd, s1, s2);
+        store_f32<E, V>(dx + c, d);
     }
 }
 
@@ -889,18 +910,16 @@ __global__ void __launch_bounds__(NG_LONG_THREADS) long_norm_grad_kernel(const N
             const float xh = (xv[i] - mean) * rstd;
             dg[i] = fmaf(d[i], xh, dg[i]);
             db[i] += d[i];
-            d[i] = rstd * (d[i] * gain[i] - s1 - xh * s2);
+            d[i] = dx_of(d[i], xh, gain[i], rstd, s1, s2);
         }
         if (p.dx)
             store_f32<E, V>(static_cast<E *>(p.dx) + row * p.dx_stride + c, d);
     }
-    if (p.partial) {
-        float *out = p.partial + (int64_t)blockIdx.x * 2 * p.width + c;
+    float *out = p.partial + (int64_t)blockIdx.x * 2 * p.width + c;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            out[i] = dg[i];
-            out[p.width + i] = db[i];
-        }
+    for (int i = 0; i < V; ++i) {
+        out[i] = dg[i];
+        out[p.width + i] = db[i];
     }
 }
 
@@ -957,7 +976,7 @@ cudaError_t launch_norm_grad_v(const NormGradParams &p, const loom_launch &L, cu
         S.grid[1] = 1;
         S.block[0] = 1024;
         const cudaError_t e = launch_with(long_norm_sums_kernel<E, V>, S, stream, p);
-        if (e != cudaSuccess)
+        if (e != cudaSuccess || !p.partial)
             return e;
     }
     loom_launch G = L;
