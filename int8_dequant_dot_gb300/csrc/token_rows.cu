@@ -842,8 +842,8 @@ __device__ __forceinline__ float dx_of(float d, float xhat, float gain, float rs
 }
 
 // Rows wider than the registers of a CTA: the two sums of each row, and, where the columns' sums are
-// not wanted, its dx (the row is read again, from L2: no workspace) ...
-template <typename E, int V> __global__ void __launch_bounds__(1024) long_norm_sums_kernel(const NormGradParams p)
+// not wanted (DX), its dx (the row is read again, from L2: no workspace) ...
+template <typename E, int V, bool DX> __global__ void __launch_bounds__(1024) long_norm_sums_kernel(const NormGradParams p)
 {
     __shared__ float red[2][32];
     const int64_t row = blockIdx.x;
@@ -851,8 +851,9 @@ template <typename E, int V> __global__ void __launch_bounds__(1024) long_norm_s
     const E *x = static_cast<const E *>(p.x) + row * p.x_stride;
     const E *dy = static_cast<const E *>(p.dy) + row * p.dy_stride;
     const float mean = p.mean[row], rstd = p.rstd[row];
-    float sums[2] = {0.0f, 0.0f}, xv[V], d[V], gain[V];
+    float sums[2] = {0.0f, 0.0f}, xv[V], d[V];
     for (int64_t c = threadIdx.x * V; c < p.width; c += blockDim.x * V) {
+        float gain[V];
         load_params<V>(p.gain, c, 1.0f, gain);
         load_f32<E, V>(x + c, xv);
         load_f32<E, V>(dy + c, d);
@@ -865,23 +866,24 @@ template <typename E, int V> __global__ void __launch_bounds__(1024) long_norm_s
     }
     group_sums<2, false>(sums, red);
     const float s1 = __fdiv_rn(sums[0], (float)p.width), s2 = __fdiv_rn(sums[1], (float)p.width);
-    if (p.row_sums) {
+    if constexpr (!DX) {
         if (threadIdx.x == 0) {
             p.row_sums[2 * row] = s1;
             p.row_sums[2 * row + 1] = s2;
         }
-        return;
-    }
-    // (behind the reduction's barrier every thread has read the row: dx may take its place)
-    E *dx = static_cast<E *>(p.dx) + row * p.dx_stride;
-    for (int64_t c = threadIdx.x * V; c < p.width; c += blockDim.x * V) {
-        load_params<V>(p.gain, c, 1.0f, gain);
-        load_f32<E, V>(x + c, xv);
-        load_f32<E, V>(dy + c, d);
+    } else {
+        // (behind the reduction's barrier every thread has read the row: dx may take its place)
+        E *dx = static_cast<E *>(p.dx) + row * p.dx_stride;
+        for (int64_t c = threadIdx.x * V; c < p.width; c += blockDim.x * V) {
+            float gain[V];
+            load_params<V>(p.gain, c, 1.0f, gain);
+            load_f32<E, V>(x + c, xv);
+            load_f32<E, V>(dy + c, d);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            d[i] = dx_of(d[i], (xv[i] - mean) * rstd, gain[i], rstd, s1, s2);
-        store_f32<E, V>(dx + c, d);
+            for (int i = 0; i < V; ++i)
+                d[i] = dx_of(d[i], (xv[i] - mean) * rstd, gain[i], rstd, s1, s2);
+            store_f32<E, V>(dx + c, d);
+        }
     }
 }
 
@@ -975,8 +977,10 @@ cudaError_t launch_norm_grad_v(const NormGradParams &p, const loom_launch &L, cu
         S.grid[0] = (uint32_t)p.rows;
         S.grid[1] = 1;
         S.block[0] = 1024;
-        const cudaError_t e = launch_with(long_norm_sums_kernel<E, V>, S, stream, p);
-        if (e != cudaSuccess || !p.partial)
+        if (!p.partial)
+            return launch_with(long_norm_sums_kernel<E, V, true>, S, stream, p);
+        const cudaError_t e = launch_with(long_norm_sums_kernel<E, V, false>, S, stream, p);
+        if (e != cudaSuccess)
             return e;
     }
     loom_launch G = L;
