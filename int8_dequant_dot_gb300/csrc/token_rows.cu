@@ -887,12 +887,13 @@ template <typename E, int V, bool DX> __global__ void __launch_bounds__(1024) lo
     }
 }
 
-// ... then a block of columns (blockIdx.y) of a share of the rows (blockIdx.x).
+// ... then a block of columns (blockIdx.x: there may be more than 65535, where a grid's y ends) of a
+// share of the rows (blockIdx.y).
 constexpr int NG_LONG_THREADS = 256;
 template <typename E, int V>
 __global__ void __launch_bounds__(NG_LONG_THREADS) long_norm_grad_kernel(const NormGradParams p)
 {
-    const int64_t c = ((int64_t)blockIdx.y * NG_LONG_THREADS + threadIdx.x) * V;
+    const int64_t c = ((int64_t)blockIdx.x * NG_LONG_THREADS + threadIdx.x) * V;
     dev::follow_previous_kernel();
     if (c >= p.width)
         return;
@@ -901,7 +902,7 @@ __global__ void __launch_bounds__(NG_LONG_THREADS) long_norm_grad_kernel(const N
 #pragma unroll
     for (int i = 0; i < V; ++i)
         dg[i] = db[i] = 0.0f;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
         const float mean = p.mean[row], rstd = p.rstd[row];
         float xv[V], d[V];
         load_f32<E, V>(static_cast<const E *>(p.x) + row * p.x_stride + c, xv);
@@ -917,7 +918,7 @@ __global__ void __launch_bounds__(NG_LONG_THREADS) long_norm_grad_kernel(const N
         if (p.dx)
             store_f32<E, V>(static_cast<E *>(p.dx) + row * p.dx_stride + c, d);
     }
-    float *out = p.partial + (int64_t)blockIdx.x * 2 * p.width + c;
+    float *out = p.partial + (int64_t)blockIdx.y * 2 * p.width + c;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         out[i] = dg[i];
@@ -984,7 +985,8 @@ cudaError_t launch_norm_grad_v(const NormGradParams &p, const loom_launch &L, cu
             return e;
     }
     loom_launch G = L;
-    G.grid[1] = (uint32_t)((p.width / V + NG_LONG_THREADS - 1) / NG_LONG_THREADS);
+    G.grid[0] = (uint32_t)((p.width / V + NG_LONG_THREADS - 1) / NG_LONG_THREADS);
+    G.grid[1] = L.grid[0];
     return launch_with(long_norm_grad_kernel<E, V>, G, stream, p);
 }
 

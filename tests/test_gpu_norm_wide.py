@@ -43,3 +43,21 @@ def test_dx_alone_needs_no_workspace(env, rows, width, pad, dtype):
     with pytest.raises(loom.LoomError) as e:                  # the columns' sums do need one
         loom.loom_layer_norm_backward(dy, x, mean, rstd, gain, workspace=None)
     assert e.value.status == loom.LOOM_ERR_ARG
+
+
+def test_rows_of_over_sixteen_million_columns(env):
+    # more than 65535 blocks of 256 columns, an odd width: one element an access
+    torch, loom = env
+    rows, width = 2, 65535 * 256 + 1
+    x, dy, gain, mean, rstd = _inputs(torch, rows, width, "float32")
+    dx, dgain, dbias = loom.loom_layer_norm_backward(dy, x, mean, rstd, gain)
+    e = (128 + width / 1024) * U
+    for r in range(rows):
+        xhat, g = (x[r].double() - mean[r].double()) * rstd[r].double(), dy[r].double() * gain.double()
+        want = rstd[r].double() * (g - g.mean() - xhat * (g * xhat).mean())
+        size = rstd[r].double() * (g.abs() + g.abs().mean() + xhat.abs() * (g * xhat).abs().mean())
+        assert bool(((dx[r].double() - want).abs() <= e * size).all())
+    terms = dy.double() * (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    steps = (rows + 24) * U
+    assert bool(((dgain.double() - terms.sum(0)).abs() <= steps * terms.abs().sum(0)).all())
+    assert bool(((dbias.double() - dy.double().sum(0)).abs() <= steps * dy.double().abs().sum(0)).all())
