@@ -15,6 +15,9 @@
  * in stream order, empty work returns LOOM_OK, and the same inputs give the
  * same bits on every call.  Offsets are 64-bit: rows x stride may pass 2^31.
  * `d_error` (may be NULL) is the optional device error word.
+ * Device waits are bounded.  The product's wait_ns (loom_i8_matmul_ex) says what one that runs
+ * out does there; the row operators (2. and the quantisation) wait a second at most for the rows
+ * that they copy ahead, and then read them, and all that follow, directly: same results.
  */
 #ifndef LOOM_TOKEN_H
 #define LOOM_TOKEN_H

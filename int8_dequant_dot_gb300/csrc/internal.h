@@ -11,6 +11,8 @@
 
 namespace loom {
 
+int32_t test_stall();   // test_hooks.h: whether staged kernels issue no copies (0 in libloom.so)
+
 // ---- row sum -------------------------------------------------------------
 constexpr int RS_DEFAULT_WARPS = 1;    // warps per CTA (a CTA's slot frees when its warp ends)
 constexpr int RS_DEFAULT_WARPS_WIDE = 1;  // lanes = 1 (wide rows): a CTA slot frees when its row ends

@@ -19,6 +19,17 @@
 #include "../../include/loom_tuning.h"
 
 namespace loom {
+
+#ifdef LOOM_TEST_HOOKS
+// Test build only (libloom_test.so): while set, the staged kernels issue no
+// copies, so every wait on them runs out after the tuning's wait limit.  The
+// shipping library has no way to turn this on.
+static std::atomic<int32_t> g_test_stall{0};
+int32_t test_stall() { return g_test_stall.load(std::memory_order_relaxed); }
+#else
+int32_t test_stall() { return 0; }
+#endif
+
 namespace {
 
 constexpr uint64_t DEFAULT_WAIT_NS = 1000000000ull;  // 1 s per barrier wait
@@ -53,16 +64,6 @@ struct Tuning {
     uint64_t wait_ns;
     DotTcConfig tc;
 };
-
-#ifdef LOOM_TEST_HOOKS
-// Test build only (libloom_test.so): while set, the staged kernels issue no
-// copies, so every wait on them runs out after the tuning's wait limit.  The
-// shipping library has no way to turn this on.
-std::atomic<int32_t> g_test_stall{0};
-int32_t test_stall() { return g_test_stall.load(std::memory_order_relaxed); }
-#else
-int32_t test_stall() { return 0; }
-#endif
 
 bool valid_warps(int64_t w) { return w == 1 || w == 2 || w == 4 || w == 8; }
 bool valid_chunk(int64_t b) { return b >= 512 && b <= 32768 && b % 512 == 0; }

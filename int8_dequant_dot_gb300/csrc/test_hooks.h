@@ -15,7 +15,9 @@ extern "C" {
 /* While `on` is non-zero, every staged kernel launched by this process issues
  * no copies, so each of its waits runs out after the tuning's wait limit
  * (loom_tuning.wait_ns): the results become NaN, the error word gets
- * LOOM_DEVERR_TIMEOUT, and the device stays usable.  Process-wide. */
+ * LOOM_DEVERR_TIMEOUT, and the device stays usable.  (The token operators'
+ * row kernels wait a second and then read their rows directly: same results,
+ * no error.  The 8-bit product is not concerned.)  Process-wide. */
 void loom_test_inject_stall(int32_t on);
 
 #ifdef __cplusplus

@@ -61,6 +61,7 @@ struct RowsParams {
     int8_t *q;                  // Quantize, NormI8: [rows][width]
     float *scale;
     int32_t *error;
+    int32_t inject_stall;       // test hook: no copies ahead (their waits run out)
 };
 // `vec` is the number of elements per load: the widest of 16 bytes, 8 bytes and one
 // element that every row's start and the width allow (row_vec).
@@ -81,6 +82,7 @@ struct NormGradParams {
     void *dx;                   // or NULL
     float *dgain, *dbias;       // or NULL
     float *partial;             // [parts][2][width] partial column sums (workspace), or NULL
+    int32_t inject_stall;       // test hook: no copies ahead (their waits run out)
     float *row_sums;            // [rows][2]: rows wider than NG_MAX_WIDTH (workspace), or NULL where partial is
 };
 // Geometry of the launch that takes the column sums; *parts (may be NULL) receives the

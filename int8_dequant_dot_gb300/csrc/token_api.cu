@@ -136,6 +136,7 @@ loom_status to_bytes(const void *d_x, int32_t dtype, int64_t rows, int32_t width
     p.q = reinterpret_cast<int8_t *>(q);
     p.scale = scale;
     p.error = error;
+    p.inject_stall = test_stall();
     const void *ptrs[] = {d_x};
     const int64_t strides[] = {p.x_stride};
     // the bytes of a row start 4-byte aligned (width % 4 == 0): packs of at most 4 unless 8 divides the row
@@ -311,6 +312,7 @@ extern "C" loom_status loom_layer_norm(const void *d_x, int32_t dtype, int64_t r
     p.y_stride = used_stride(rows, y_stride);
     p.mean = d_mean;
     p.rstd = d_rstd;
+    p.inject_stall = test_stall();
     const void *ptrs[] = {d_x, d_y};
     const int64_t strides[] = {p.x_stride, p.y_stride};
     return of_cuda(launch_rows(p, RowMode::Norm, dtype, param_vec(row_vec(dtype, width, ptrs, strides, 2), d_gain, d_bias), L,
@@ -375,6 +377,7 @@ extern "C" loom_status loom_layer_norm_backward(const void *d_dy, int64_t dy_str
     p.dx = d_dx;
     p.dgain = d_dgain;
     p.dbias = d_dbias;
+    p.inject_stall = test_stall();
     if (needs) {
         p.partial = static_cast<float *>(d_workspace);
         p.row_sums = p.partial + parts * 2 * width;
