@@ -532,15 +532,17 @@ def loom_stream_floor(src, nbytes: int, schedule: int, depth: int, ctas_per_sm: 
 _torch = None
 _dtypes: dict = {}
 _current_stream = None      # device index -> handle of torch's current stream
+_current_device = None      # -> index of the current device
 
 
 def _lazy():
     """torch, and what the calls below look up in it, on first use."""
-    global _torch, _current_stream
+    global _torch, _current_stream, _current_device
     if _torch is None:
         import torch
         _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _dtypes.update({torch.float32: LOOM_F32, torch.float16: LOOM_F16, torch.bfloat16: LOOM_BF16})
         _torch = torch
     return _torch
@@ -573,21 +575,49 @@ def _floats(where: str, n: int, *tensors):
             raise LoomError(LOOM_ERR_SHAPE, f"{where}: {n} contiguous float32 values are wanted")
 
 
+def _foreign(where: str, t):
+    """A tensor that is not on the call's device: refused, but for pinned host memory, which it reaches."""
+    if t.get_device() >= 0 or not t.is_pinned():
+        raise LoomError(LOOM_ERR_ARG, f"{where}: a tensor on {t.device}, not on the call's device")
+
+
+def _dense(where: str, t, n: int, dtype, device: int):
+    """Address of an operand of n contiguous elements (or more) of type `dtype`; None and raw addresses
+    stay as they are."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise LoomError(LOOM_ERR_SHAPE, f"{where}: {n} contiguous {dtype} values are wanted")
+    if t.get_device() != device:
+        _foreign(where, t)
+    return t.data_ptr()
+
+
+def _packed(where: str, t, nbytes: int, device: int) -> int:
+    """Address of `nbytes` contiguous signed bytes (or more), as such or in int32 words."""
+    dtype = t.dtype
+    size = 1 if dtype is _torch.int8 else 4 if dtype is _torch.int32 else 0
+    if not size or t.numel() * size < nbytes or not t.is_contiguous():
+        raise LoomError(LOOM_ERR_SHAPE, f"{where}: {nbytes} contiguous signed bytes (int8 or int32) are wanted")
+    if t.get_device() != device:
+        _foreign(where, t)
+    return t.data_ptr()
+
+
 def _launch(where: str, like, stream, *args):
     """The library call `where` on the device of `like` and on `stream` (its current one)."""
     fn = getattr(_lib, where)
     device = like.get_device()
     if device < 0:
         raise LoomError(LOOM_ERR_ARG, f"{where}: tensors on a GPU are wanted")
-    cuda = _torch.cuda
     if stream is None:
         stream = _current_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if cuda.current_device() == device:
+    if _current_device() == device:
         status = fn(*args, stream)
     else:
-        with cuda.device(device):
+        with _torch.cuda.device(device):
             status = fn(*args, stream)
     if status != LOOM_OK:
         raise LoomError(status, where)
@@ -607,7 +637,7 @@ def loom_quantize_tokens(x, *, q=None, scale=None, error=None, stream=None):
     tokens, k, stride = _matrix(x, "loom_quantize_tokens")
     dtype = _dtype(x.dtype)
     if q is None:
-        q = torch.empty((tokens, k // 4), dtype=torch.int32, device=x.device)
+        q = torch.empty(tokens, k // 4, dtype=torch.int32, device=x.device)
     if scale is None:
         scale = torch.empty(tokens, dtype=torch.float32, device=x.device)
     _launch("loom_quantize_tokens", x, stream, x.data_ptr(), dtype, tokens, k, stride, _ptr(q), _ptr(scale), _ptr(error))
@@ -626,19 +656,39 @@ def loom_i8_matmul(w_packed, scale_w, n_rows: int, k: int, x_packed, scale_x, to
 def loom_i8_matmul_ex(w_packed, scale_w, n_rows: int, k: int, x_packed, scale_x, tokens: int, *, bias=None, y=None,
                       y_dtype=None, acc=None, want_acc: bool = False, error=None, tuning=None, stream=None):
     tp = ctypes.byref(tuning) if tuning is not None else None
+    if error is not None:
+        _lazy()
+        error = _dense("loom_i8_matmul_ex", error, 1, _torch.int32, w_packed.get_device())
     return _i8_matmul("loom_i8_matmul_ex", w_packed, scale_w, n_rows, k, x_packed, scale_x, tokens, bias, y, y_dtype, acc,
-                      want_acc, stream, _ptr(error), tp)
+                      want_acc, stream, error, tp)
 
 
 def _i8_matmul(where, w_packed, scale_w, n_rows, k, x_packed, scale_x, tokens, bias, y, y_dtype, acc, want_acc, stream, *more):
     torch = _torch or _lazy()
+    device = w_packed.get_device()
     if y is None:
-        y = torch.empty((tokens, n_rows), dtype=torch.float32 if y_dtype is None else y_dtype, device=w_packed.device)
-    if acc is None and want_acc:
-        acc = torch.empty((tokens, n_rows), dtype=torch.int32, device=w_packed.device)
-    stride = _matrix(y, where)[2]
-    _launch(where, w_packed, stream, w_packed.data_ptr(), scale_w.data_ptr(), n_rows, k, x_packed.data_ptr(), scale_x.data_ptr(),
-            tokens, _ptr(bias), y.data_ptr(), _dtype(y.dtype), stride, _ptr(acc), *more)
+        if tokens < 0 or n_rows < 0:
+            raise LoomError(LOOM_ERR_SHAPE, where)
+        y = torch.empty(tokens, n_rows, dtype=torch.float32 if y_dtype is None else y_dtype, device=w_packed.device)
+        stride = n_rows
+    else:
+        rows, width, stride = _matrix(y, where)
+        if rows < tokens or width < n_rows:
+            raise LoomError(LOOM_ERR_SHAPE, f"{where}: y is smaller than {tokens} x {n_rows}")
+        if y.get_device() != device:
+            _foreign(where, y)
+    if acc is not None:
+        acc_at = _dense(where, acc, tokens * n_rows, torch.int32, device)
+    elif want_acc:
+        acc = torch.empty(tokens, n_rows, dtype=torch.int32, device=w_packed.device)
+        acc_at = acc.data_ptr()
+    else:
+        acc_at = None
+    f32, work = torch.float32, tokens > 0 and n_rows > 0       # (without work the operands may be empty)
+    _launch(where, w_packed, stream, _packed(where, w_packed, n_rows * k if work else 0, device),
+            _dense(where, scale_w, n_rows if work else 0, f32, device), n_rows, k,
+            _packed(where, x_packed, tokens * k if work else 0, device), _dense(where, scale_x, tokens if work else 0, f32, device), tokens,
+            _dense(where, bias, n_rows if work else 0, f32, device), y.data_ptr(), _dtype(y.dtype), stride, acc_at, *more)
     return y, acc
 
 
@@ -652,7 +702,7 @@ def loom_layer_norm(x, gain=None, bias=None, eps: float = 1e-5, *, y=None, mean=
     dtype = _dtype(x.dtype)
     _floats("loom_layer_norm", width, gain, bias)
     if y is None:
-        y = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+        y = torch.empty(rows, width, dtype=x.dtype, device=x.device)
         y_stride = width
     else:
         if y.dtype != x.dtype or y.shape != x.shape:
@@ -676,7 +726,7 @@ def loom_layer_norm_i8(x, gain=None, bias=None, eps: float = 1e-5, *, q=None, sc
     dtype = _dtype(x.dtype)
     _floats("loom_layer_norm_i8", width, gain, bias)
     if q is None:
-        q = torch.empty((rows, width // 4), dtype=torch.int32, device=x.device)
+        q = torch.empty(rows, width // 4, dtype=torch.int32, device=x.device)
     if scale is None:
         scale = torch.empty(rows, dtype=torch.float32, device=x.device)
     _launch("loom_layer_norm_i8", x, stream, x.data_ptr(), dtype, rows, width, stride, _ptr(gain), _ptr(bias), eps, _ptr(q),
@@ -714,7 +764,7 @@ def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=Non
             raise LoomError(LOOM_ERR_SHAPE, f"{where}: dx has another type or shape than x")
         dx_stride = _matrix(dx, where)[2]
     elif want_dx:
-        dx = torch.empty((rows, width), dtype=x.dtype, device=device)
+        dx = torch.empty(rows, width, dtype=x.dtype, device=device)
     if want_params:
         if dgain is None:
             dgain = torch.empty(width, dtype=torch.float32, device=device)
