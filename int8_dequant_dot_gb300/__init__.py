@@ -567,18 +567,30 @@ def _matrix(t, where: str):
     raise LoomError(LOOM_ERR_SHAPE, f"{where}: a matrix with contiguous rows is wanted")
 
 
-def _floats(where: str, n: int, *tensors):
-    """The optional tensors are contiguous f32 of n elements each."""
-    f32 = _torch.float32
-    for t in tensors:
-        if t is not None and (t.dtype is not f32 or t.numel() != n or not t.is_contiguous()):
-            raise LoomError(LOOM_ERR_SHAPE, f"{where}: {n} contiguous float32 values are wanted")
-
-
 def _foreign(where: str, t):
     """A tensor that is not on the call's device: refused, but for pinned host memory, which it reaches."""
     if t.get_device() >= 0 or not t.is_pinned():
         raise LoomError(LOOM_ERR_ARG, f"{where}: a tensor on {t.device}, not on the call's device")
+
+
+def _floats(where: str, n: int, device: int, *tensors):
+    """The optional tensors are contiguous f32 of n elements each, on the call's device."""
+    f32 = _torch.float32
+    for t in tensors:
+        if t is not None:
+            if t.dtype is not f32 or t.numel() != n or not t.is_contiguous():
+                raise LoomError(LOOM_ERR_SHAPE, f"{where}: {n} contiguous float32 values are wanted")
+            if t.get_device() != device:
+                _foreign(where, t)
+
+
+def _like(where: str, name: str, t, x, device: int) -> int:
+    """Stride of a matrix `t` of the type and shape of x, on the call's device."""
+    if t.dtype != x.dtype or t.shape != x.shape:
+        raise LoomError(LOOM_ERR_SHAPE, f"{where}: {name} has another type or shape than x")
+    if t.get_device() != device:
+        _foreign(where, t)
+    return _matrix(t, where)[2]
 
 
 def _dense(where: str, t, n: int, dtype, device: int):
@@ -594,7 +606,10 @@ def _dense(where: str, t, n: int, dtype, device: int):
 
 
 def _packed(where: str, t, nbytes: int, device: int) -> int:
-    """Address of `nbytes` contiguous signed bytes (or more), as such or in int32 words."""
+    """Address of `nbytes` contiguous signed bytes (or more), as such or in int32 words; raw addresses stay
+    as they are."""
+    if isinstance(t, int):
+        return t
     dtype = t.dtype
     size = 1 if dtype is _torch.int8 else 4 if dtype is _torch.int32 else 0
     if not size or t.numel() * size < nbytes or not t.is_contiguous():
@@ -634,14 +649,29 @@ def loom_quantize_tokens(x, *, q=None, scale=None, error=None, stream=None):
     """Tokens ``x[tokens][k]`` (float32, float16 or bfloat16) to signed bytes with one scale
     each; returns ``(q_packed int32 [tokens][k/4], scale float32 [tokens])``."""
     torch = _torch or _lazy()
-    tokens, k, stride = _matrix(x, "loom_quantize_tokens")
+    where = "loom_quantize_tokens"
+    tokens, k, stride = _matrix(x, where)
     dtype = _dtype(x.dtype)
+    q, q_at, scale, scale_at, error = _byte_outputs(where, x, tokens, k, q, scale, error)
+    _launch(where, x, stream, x.data_ptr(), dtype, tokens, k, stride, q_at, scale_at, error)
+    return q, scale
+
+
+def _byte_outputs(where, x, tokens, k, q, scale, error):
+    """(q, its address, scale, its address, the error word's address) of a call to bytes."""
+    torch = _torch
+    device = x.get_device()
     if q is None:
         q = torch.empty(tokens, k // 4, dtype=torch.int32, device=x.device)
+        q_at = q.data_ptr()
+    else:
+        q_at = _packed(where, q, tokens * k, device)
     if scale is None:
         scale = torch.empty(tokens, dtype=torch.float32, device=x.device)
-    _launch("loom_quantize_tokens", x, stream, x.data_ptr(), dtype, tokens, k, stride, _ptr(q), _ptr(scale), _ptr(error))
-    return q, scale
+        scale_at = scale.data_ptr()
+    else:
+        scale_at = _dense(where, scale, tokens, torch.float32, device)
+    return q, q_at, scale, scale_at, _dense(where, error, 1, torch.int32, device)
 
 
 def loom_i8_matmul(w_packed, scale_w, n_rows: int, k: int, x_packed, scale_x, tokens: int, *, bias=None, y=None,
@@ -698,23 +728,25 @@ def loom_layer_norm(x, gain=None, bias=None, eps: float = 1e-5, *, y=None, mean=
     float32 or None.  Returns ``(y, mean, rstd)``, the last two float32 per row as the
     backward pass takes them (None without ``want_stats``)."""
     torch = _torch or _lazy()
-    rows, width, stride = _matrix(x, "loom_layer_norm")
-    dtype = _dtype(x.dtype)
-    _floats("loom_layer_norm", width, gain, bias)
+    where = "loom_layer_norm"
+    rows, width, stride = _matrix(x, where)
+    dtype, device = _dtype(x.dtype), x.get_device()
+    _floats(where, width, device, gain, bias)
     if y is None:
         y = torch.empty(rows, width, dtype=x.dtype, device=x.device)
         y_stride = width
     else:
-        if y.dtype != x.dtype or y.shape != x.shape:
-            raise LoomError(LOOM_ERR_SHAPE, "loom_layer_norm: y has another type or shape than x")
-        y_stride = _matrix(y, "loom_layer_norm")[2]
+        y_stride = _like(where, "y", y, x, device)
+    mean_at, rstd_at = _dense(where, mean, rows, torch.float32, device), _dense(where, rstd, rows, torch.float32, device)
     if want_stats:
         if mean is None:
             mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+            mean_at = mean.data_ptr()
         if rstd is None:
             rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _launch("loom_layer_norm", x, stream, x.data_ptr(), dtype, rows, width, stride, _ptr(gain), _ptr(bias), eps, y.data_ptr(),
-            y_stride, _ptr(mean), _ptr(rstd))
+            rstd_at = rstd.data_ptr()
+    _launch(where, x, stream, x.data_ptr(), dtype, rows, width, stride, _ptr(gain), _ptr(bias), eps, y.data_ptr(),
+            y_stride, mean_at, rstd_at)
     return y, mean, rstd
 
 
@@ -722,15 +754,12 @@ def loom_layer_norm_i8(x, gain=None, bias=None, eps: float = 1e-5, *, q=None, sc
     """``loom_quantize_tokens`` of layer norm's rows, which are never written; returns
     ``(q_packed, scale)``."""
     torch = _torch or _lazy()
-    rows, width, stride = _matrix(x, "loom_layer_norm_i8")
+    where = "loom_layer_norm_i8"
+    rows, width, stride = _matrix(x, where)
     dtype = _dtype(x.dtype)
-    _floats("loom_layer_norm_i8", width, gain, bias)
-    if q is None:
-        q = torch.empty(rows, width // 4, dtype=torch.int32, device=x.device)
-    if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _launch("loom_layer_norm_i8", x, stream, x.data_ptr(), dtype, rows, width, stride, _ptr(gain), _ptr(bias), eps, _ptr(q),
-            _ptr(scale), _ptr(error))
+    _floats(where, width, x.get_device(), gain, bias)
+    q, q_at, scale, scale_at, error = _byte_outputs(where, x, rows, width, q, scale, error)
+    _launch(where, x, stream, x.data_ptr(), dtype, rows, width, stride, _ptr(gain), _ptr(bias), eps, q_at, scale_at, error)
     return q, scale
 
 
@@ -752,17 +781,13 @@ def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=Non
     where = "loom_layer_norm_backward"
     rows, width, x_stride = _matrix(x, where)
     dtype = _dtype(x.dtype)
-    dy_stride = _matrix(dy, where)[2]
-    _floats(where, width, gain, dgain, dbias)
-    _floats(where, rows, mean, rstd)
-    device = x.device
-    if dy.dtype != x.dtype or dy.shape != x.shape:
-        raise LoomError(LOOM_ERR_SHAPE, f"{where}: dy has another type or shape than x")
+    device, index = x.device, x.get_device()
+    dy_stride = _like(where, "dy", dy, x, index)
+    _floats(where, width, index, gain, dgain, dbias)
+    _floats(where, rows, index, mean, rstd)
     dx_stride = width
     if dx is not None:
-        if dx.dtype != x.dtype or dx.shape != x.shape:
-            raise LoomError(LOOM_ERR_SHAPE, f"{where}: dx has another type or shape than x")
-        dx_stride = _matrix(dx, where)[2]
+        dx_stride = _like(where, "dx", dx, x, index)
     elif want_dx:
         dx = torch.empty(rows, width, dtype=x.dtype, device=device)
     if want_params:
@@ -776,7 +801,9 @@ def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=Non
         wp, wb = workspace
     else:
         if workspace is AUTO or (isinstance(workspace, str) and workspace == AUTO):
-            if device.index == torch.cuda.current_device():
+            if index < 0:
+                raise LoomError(LOOM_ERR_ARG, f"{where}: tensors on a GPU are wanted")
+            if index == _current_device():
                 nbytes = loom_layer_norm_backward_workspace_bytes(rows, width)
             else:
                 with torch.cuda.device(device):
@@ -785,17 +812,21 @@ def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=Non
             if stream is not None:   # the allocator may hand it out again only after that stream's work
                 handle = stream if isinstance(stream, int) else stream.cuda_stream
                 workspace.record_stream(torch.cuda.ExternalStream(handle, device=device))
+        else:
+            _dense(where, workspace, 0, workspace.dtype, index)
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _launch(where, x, stream, dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, dtype, rows, width, _ptr(gain), mean.data_ptr(),
             rstd.data_ptr(), _ptr(dx), dx_stride, _ptr(dgain), _ptr(dbias), wp, wb)
     return dx, dgain, dbias
 
 
-def _setting(name: str, v, dtype, rows: int):
+def _setting(name: str, v, dtype, rows: int, device: int):
     """(device address or None, host value) of a sampling setting."""
     if isinstance(v, _torch.Tensor):
         if v.dtype != dtype or v.numel() != rows or not v.is_contiguous():
             raise LoomError(LOOM_ERR_SHAPE, f"loom_sample_tokens: {name}: {rows} contiguous {dtype} values are wanted")
+        if v.get_device() != device:
+            _foreign(f"loom_sample_tokens: {name}", v)
         return v.data_ptr(), 0
     return None, v
 
@@ -806,17 +837,24 @@ def loom_sample_tokens(logits, uniform, *, temperature=1.0, top_k=0, top_p=1.0, 
     in [0, 1); each setting is a number for every row or a device tensor with one per row
     (``top_k`` int32, the others float32).  Returns ``(token int32, logprob float32)``."""
     torch = _torch or _lazy()
-    rows, vocab, stride = _matrix(logits, "loom_sample_tokens")
-    dtype = _dtype(logits.dtype)
-    _floats("loom_sample_tokens", rows, uniform)
-    dt, t = _setting("temperature", temperature, torch.float32, rows)
-    dk, k = _setting("top_k", top_k, torch.int32, rows)
-    dp, p = _setting("top_p", top_p, torch.float32, rows)
-    dm, m = _setting("min_p", min_p, torch.float32, rows)
+    where = "loom_sample_tokens"
+    rows, vocab, stride = _matrix(logits, where)
+    dtype, device = _dtype(logits.dtype), logits.get_device()
+    _floats(where, rows, device, uniform)
+    dt, t = _setting("temperature", temperature, torch.float32, rows, device)
+    dk, k = _setting("top_k", top_k, torch.int32, rows, device)
+    dp, p = _setting("top_p", top_p, torch.float32, rows, device)
+    dm, m = _setting("min_p", min_p, torch.float32, rows, device)
     if token is None:
         token = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        token_at = token.data_ptr()
+    else:
+        token_at = _dense(where, token, rows, torch.int32, device)
     if logprob is None and want_logprob:
         logprob = torch.empty(rows, dtype=torch.float32, device=logits.device)
-    _launch("loom_sample_tokens", logits, stream, logits.data_ptr(), dtype, rows, vocab, stride, dt, t, dk, k, dp, p, dm, m,
-            uniform.data_ptr(), _ptr(token), _ptr(logprob), _ptr(error))
+        logprob_at = logprob.data_ptr()
+    else:
+        logprob_at = _dense(where, logprob, rows, torch.float32, device)
+    _launch(where, logits, stream, logits.data_ptr(), dtype, rows, vocab, stride, dt, t, dk, k, dp, p, dm, m,
+            uniform.data_ptr(), token_at, logprob_at, _dense(where, error, 1, torch.int32, device))
     return token, logprob

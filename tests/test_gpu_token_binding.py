@@ -40,3 +40,40 @@ def test_product_operands_on_the_host(env):
     y = torch.full((t + 1, n + 3), float("nan"), dtype=torch.bfloat16, device="cuda")
     assert loom.loom_i8_matmul(*args, bias=bias, y=y)[0] is y
     assert torch.equal(y[:t, :n], want[0].to(torch.bfloat16)) and int(torch.isnan(y).sum()) == (t + 1) * (n + 3) - t * n
+
+
+def test_other_operands_on_the_host(env):
+    torch, loom = env
+    rows, width = 6, 64
+    x, dy = torch.randn(rows, width, device="cuda"), torch.randn(rows, width, device="cuda")
+    gain = torch.rand(width, device="cuda")
+    y, mean, rstd = loom.loom_layer_norm(x, gain)
+    host = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype)   # noqa: E731
+    word = host(1, dtype=torch.int32)
+    cases = [(loom.loom_layer_norm, (x, gain.cpu()), {}), (loom.loom_layer_norm, (x,), {"bias": host(width)}),
+             (loom.loom_layer_norm, (x,), {"y": host(rows, width)}), (loom.loom_layer_norm, (x,), {"mean": host(rows)}),
+             (loom.loom_layer_norm_i8, (x, gain.cpu()), {}), (loom.loom_layer_norm_i8, (x,), {"error": word}),
+             (loom.loom_quantize_tokens, (x,), {"q": host(rows, width // 4, dtype=torch.int32)}), (loom.loom_quantize_tokens, (x,), {"scale": host(rows)}),
+             (loom.loom_quantize_tokens, (x,), {"error": word})]
+    grad = (dy, x, mean, rstd)
+    cases += [(loom.loom_layer_norm_backward, tuple(t.cpu() if j == i else t for j, t in enumerate(grad)), {}) for i in (0, 2, 3)]
+    cases += [(loom.loom_layer_norm_backward, grad, {name: t}) for name, t in (("gain", gain.cpu()), ("dx", host(rows, width)), ("dgain", host(width)),
+                                                                             ("workspace", host(1 << 16)))]
+    u = torch.rand(rows, device="cuda")
+    cases += [(loom.loom_sample_tokens, (x, u.cpu()), {})]
+    cases += [(loom.loom_sample_tokens, (x, u), {name: t}) for name, t in (("temperature", host(rows)), ("top_k", host(rows, dtype=torch.int32)),
+                                                                          ("token", host(rows, dtype=torch.int32)), ("logprob", host(rows)), ("error", word))]
+    for call, args, more in cases:
+        assert _refused(loom, call, *args, **more) == loom.LOOM_ERR_ARG, (call.__name__, list(more))
+    # a device-readable pinned gain, and outputs given as tensors, work
+    again, m2, r2 = torch.empty_like(x), torch.empty(rows + 1, device="cuda"), torch.empty(rows, device="cuda")
+    loom.loom_layer_norm(x, gain.cpu().pin_memory(), y=again, mean=m2, rstd=r2)
+    assert torch.equal(again, y) and torch.equal(m2[:rows], mean) and torch.equal(r2, rstd)
+    q, scale = loom.loom_quantize_tokens(x)
+    q2, s2 = torch.empty(rows, width, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    loom.loom_quantize_tokens(x, q=q2, scale=s2)
+    assert torch.equal(q2, q.view(torch.int8)) and torch.equal(s2, scale)
+    tok, lp = torch.empty(rows, dtype=torch.int32, device="cuda"), torch.empty(rows, device="cuda")
+    want = loom.loom_sample_tokens(x, u)
+    loom.loom_sample_tokens(x, u, token=tok, logprob=lp)
+    assert torch.equal(tok, want[0]) and torch.equal(lp, want[1])

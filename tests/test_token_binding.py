@@ -58,3 +58,51 @@ def test_product_operands_that_do_not_fit(loom, change):
 def test_product_error_word(loom):
     for error in (torch.zeros(1), torch.zeros(0, dtype=torch.int32)):
         assert product(loom, ex=True, error=error) == loom.LOOM_ERR_SHAPE
+
+
+R, W = 6, 32
+Z = torch.zeros
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_outputs_of_the_calls_to_bytes(loom, norm):
+    call = loom.loom_layer_norm_i8 if norm else loom.loom_quantize_tokens
+    x = Z(R, W)
+    for good in ({}, {"q": Z(R, W // 4, dtype=torch.int32)}, {"q": Z(R * W, dtype=torch.int8)}, {"scale": Z(R + 2)},
+                 {"error": Z(1, dtype=torch.int32)}, {"q": 0x10000, "scale": 0x10000, "error": 0x10000}):
+        assert refused(loom, call, x, **good) == loom.LOOM_ERR_ARG
+    for bad in ({"q": Z(R - 1, W // 4, dtype=torch.int32)}, {"q": Z(R, W)}, {"q": Z(R, 2 * W, dtype=torch.int8)[:, :W]}, {"scale": Z(R - 1)},
+                {"scale": Z(R, dtype=torch.float64)}, {"scale": Z(2 * R)[::2]}, {"error": Z(1)}, {"error": Z(0, dtype=torch.int32)}):
+        assert refused(loom, call, x, **bad) == loom.LOOM_ERR_SHAPE
+
+
+def test_outputs_of_layer_norm(loom):
+    x = Z(R, W)
+    for good in ({}, {"mean": Z(R), "rstd": Z(R + 1)}, {"mean": 0x10000}, {"y": Z(R, W + 4)[:, :W]}):
+        assert refused(loom, loom.loom_layer_norm, x, **good) == loom.LOOM_ERR_ARG
+    for bad in ({"mean": Z(R - 1)}, {"rstd": Z(R, dtype=torch.float16)}, {"rstd": Z(2 * R)[::2]}, {"y": Z(R, W - 1)}, {"y": Z(W, R).t()},
+                {"mean": Z(R - 1), "want_stats": False}):
+        assert refused(loom, loom.loom_layer_norm, x, **bad) == loom.LOOM_ERR_SHAPE
+
+
+def test_operands_of_layer_norm_backward(loom):
+    def back(**change):
+        a = {"dy": Z(R, W), "x": Z(R, W), "mean": Z(R), "rstd": Z(R)}
+        a.update({key: change.pop(key) for key in list(change) if key in a})
+        return refused(loom, loom.loom_layer_norm_backward, *a.values(), **change)
+    for good in ({}, {"workspace": Z(9, dtype=torch.uint8)}, {"workspace": (0x10000, 16)}, {"workspace": None}, {"want_params": False}):
+        assert back(**good) == loom.LOOM_ERR_ARG
+    for bad in ({"dy": Z(R - 1, W)}, {"dy": Z(R, W, dtype=torch.float16)}, {"dy": Z(W, R).t()}, {"mean": Z(R + 1)}, {"rstd": Z(2 * R)[::2]},
+                {"gain": Z(W - 1)}, {"dx": Z(R, W - 1)}, {"dgain": Z(W, dtype=torch.float64)}, {"dbias": Z(W + 1)},
+                {"workspace": Z(8, 8)[:, :4]}):
+        assert back(**bad) == loom.LOOM_ERR_SHAPE
+
+
+def test_outputs_of_sampling(loom):
+    l, u = Z(R, W), Z(R)
+    i32 = torch.int32
+    for good in ({}, {"token": Z(R, dtype=i32), "logprob": Z(R)}, {"token": 0x10000}, {"temperature": Z(R)}, {"want_logprob": False}):
+        assert refused(loom, loom.loom_sample_tokens, l, u, **good) == loom.LOOM_ERR_ARG
+    for bad in ({"token": Z(R - 1, dtype=i32)}, {"token": Z(R, dtype=torch.int64)}, {"token": Z(2 * R, dtype=i32)[::2]}, {"logprob": Z(R - 1)},
+                {"logprob": Z(R, dtype=torch.float16)}, {"error": Z(1)}, {"temperature": Z(R - 1)}, {"top_k": Z(R, dtype=torch.int64)}):
+        assert refused(loom, loom.loom_sample_tokens, l, u, **bad) == loom.LOOM_ERR_SHAPE
