@@ -619,6 +619,25 @@ def _packed(where: str, t, nbytes: int, device: int) -> int:
     return t.data_ptr()
 
 
+def _new(stream, like, dtype, *shape):
+    """An uninitialised tensor on the device of `like` for a call on `stream`.  Of another stream than the
+    current one it is taken from that stream's memory, as within torch.cuda.stream(stream): a block of the
+    current stream's may still be in use by what is queued there.  It may then be used on the current stream
+    too (after a wait, as ever) and given up at any time."""
+    empty = _torch.empty
+    if stream is None:
+        return empty(*shape, dtype=dtype, device=like.device)
+    device = like.get_device()
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if device < 0 or handle == _current_stream(device):
+        return empty(*shape, dtype=dtype, device=like.device)
+    cuda = _torch.cuda
+    with cuda.stream(cuda.ExternalStream(handle, device=like.device)):
+        t = empty(*shape, dtype=dtype, device=like.device)
+    t.record_stream(cuda.current_stream(device))
+    return t
+
+
 def _launch(where: str, like, stream, *args):
     """The library call `where` on the device of `like` and on `stream` (its current one)."""
     fn = getattr(_lib, where)
@@ -652,22 +671,22 @@ def loom_quantize_tokens(x, *, q=None, scale=None, error=None, stream=None):
     where = "loom_quantize_tokens"
     tokens, k, stride = _matrix(x, where)
     dtype = _dtype(x.dtype)
-    q, q_at, scale, scale_at, error = _byte_outputs(where, x, tokens, k, q, scale, error)
+    q, q_at, scale, scale_at, error = _byte_outputs(where, stream, x, tokens, k, q, scale, error)
     _launch(where, x, stream, x.data_ptr(), dtype, tokens, k, stride, q_at, scale_at, error)
     return q, scale
 
 
-def _byte_outputs(where, x, tokens, k, q, scale, error):
+def _byte_outputs(where, stream, x, tokens, k, q, scale, error):
     """(q, its address, scale, its address, the error word's address) of a call to bytes."""
     torch = _torch
     device = x.get_device()
     if q is None:
-        q = torch.empty(tokens, k // 4, dtype=torch.int32, device=x.device)
+        q = _new(stream, x, torch.int32, tokens, k // 4)
         q_at = q.data_ptr()
     else:
         q_at = _packed(where, q, tokens * k, device)
     if scale is None:
-        scale = torch.empty(tokens, dtype=torch.float32, device=x.device)
+        scale = _new(stream, x, torch.float32, tokens)
         scale_at = scale.data_ptr()
     else:
         scale_at = _dense(where, scale, tokens, torch.float32, device)
@@ -699,7 +718,7 @@ def _i8_matmul(where, w_packed, scale_w, n_rows, k, x_packed, scale_x, tokens, b
     if y is None:
         if tokens < 0 or n_rows < 0:
             raise LoomError(LOOM_ERR_SHAPE, where)
-        y = torch.empty(tokens, n_rows, dtype=torch.float32 if y_dtype is None else y_dtype, device=w_packed.device)
+        y = _new(stream, w_packed, torch.float32 if y_dtype is None else y_dtype, tokens, n_rows)
         stride = n_rows
     else:
         rows, width, stride = _matrix(y, where)
@@ -710,7 +729,7 @@ def _i8_matmul(where, w_packed, scale_w, n_rows, k, x_packed, scale_x, tokens, b
     if acc is not None:
         acc_at = _dense(where, acc, tokens * n_rows, torch.int32, device)
     elif want_acc:
-        acc = torch.empty(tokens, n_rows, dtype=torch.int32, device=w_packed.device)
+        acc = _new(stream, w_packed, torch.int32, tokens, n_rows)
         acc_at = acc.data_ptr()
     else:
         acc_at = None
@@ -733,17 +752,17 @@ def loom_layer_norm(x, gain=None, bias=None, eps: float = 1e-5, *, y=None, mean=
     dtype, device = _dtype(x.dtype), x.get_device()
     _floats(where, width, device, gain, bias)
     if y is None:
-        y = torch.empty(rows, width, dtype=x.dtype, device=x.device)
+        y = _new(stream, x, x.dtype, rows, width)
         y_stride = width
     else:
         y_stride = _like(where, "y", y, x, device)
     mean_at, rstd_at = _dense(where, mean, rows, torch.float32, device), _dense(where, rstd, rows, torch.float32, device)
     if want_stats:
         if mean is None:
-            mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+            mean = _new(stream, x, torch.float32, rows)
             mean_at = mean.data_ptr()
         if rstd is None:
-            rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+            rstd = _new(stream, x, torch.float32, rows)
             rstd_at = rstd.data_ptr()
     _launch(where, x, stream, x.data_ptr(), dtype, rows, width, stride, _ptr(gain), _ptr(bias), eps, y.data_ptr(),
             y_stride, mean_at, rstd_at)
@@ -758,7 +777,7 @@ def loom_layer_norm_i8(x, gain=None, bias=None, eps: float = 1e-5, *, q=None, sc
     rows, width, stride = _matrix(x, where)
     dtype = _dtype(x.dtype)
     _floats(where, width, x.get_device(), gain, bias)
-    q, q_at, scale, scale_at, error = _byte_outputs(where, x, rows, width, q, scale, error)
+    q, q_at, scale, scale_at, error = _byte_outputs(where, stream, x, rows, width, q, scale, error)
     _launch(where, x, stream, x.data_ptr(), dtype, rows, width, stride, _ptr(gain), _ptr(bias), eps, q_at, scale_at, error)
     return q, scale
 
@@ -789,12 +808,12 @@ def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=Non
     if dx is not None:
         dx_stride = _like(where, "dx", dx, x, index)
     elif want_dx:
-        dx = torch.empty(rows, width, dtype=x.dtype, device=device)
+        dx = _new(stream, x, x.dtype, rows, width)
     if want_params:
         if dgain is None:
-            dgain = torch.empty(width, dtype=torch.float32, device=device)
+            dgain = _new(stream, x, torch.float32, width)
         if dbias is None:
-            dbias = torch.empty(width, dtype=torch.float32, device=device)
+            dbias = _new(stream, x, torch.float32, width)
     if workspace is None or (dgain is None and dbias is None):      # dx alone needs none
         wp, wb = None, 0
     elif isinstance(workspace, tuple):
@@ -808,10 +827,7 @@ def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=Non
             else:
                 with torch.cuda.device(device):
                     nbytes = loom_layer_norm_backward_workspace_bytes(rows, width)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            if stream is not None:   # the allocator may hand it out again only after that stream's work
-                handle = stream if isinstance(stream, int) else stream.cuda_stream
-                workspace.record_stream(torch.cuda.ExternalStream(handle, device=device))
+            workspace = _new(stream, x, torch.uint8, nbytes)
         else:
             _dense(where, workspace, 0, workspace.dtype, index)
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -846,12 +862,12 @@ def loom_sample_tokens(logits, uniform, *, temperature=1.0, top_k=0, top_p=1.0, 
     dp, p = _setting("top_p", top_p, torch.float32, rows, device)
     dm, m = _setting("min_p", min_p, torch.float32, rows, device)
     if token is None:
-        token = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        token = _new(stream, logits, torch.int32, rows)
         token_at = token.data_ptr()
     else:
         token_at = _dense(where, token, rows, torch.int32, device)
     if logprob is None and want_logprob:
-        logprob = torch.empty(rows, dtype=torch.float32, device=logits.device)
+        logprob = _new(stream, logits, torch.float32, rows)
         logprob_at = logprob.data_ptr()
     else:
         logprob_at = _dense(where, logprob, rows, torch.float32, device)

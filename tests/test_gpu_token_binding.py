@@ -77,3 +77,76 @@ def test_other_operands_on_the_host(env):
     want = loom.loom_sample_tokens(x, u)
     loom.loom_sample_tokens(x, u, token=tok, logprob=lp)
     assert torch.equal(tok, want[0]) and torch.equal(lp, want[1])
+
+
+def _busy(torch, nbytes, ms=100):
+    """The current stream will write all of a block of `nbytes` that its allocator holds free, `ms` from now."""
+    torch.cuda._sleep(int(ms * 2e6))
+    block = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    block.fill_(0xff)          # as f32, f16 or bf16: NaN
+    del block
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_outputs_of_a_call_on_another_stream_are_not_what_the_current_one_has_queued(env, as_handle):
+    torch, loom = env
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rows, width, n = 512, 4096, 4096
+    x = torch.randn(rows, width, generator=g, device="cuda")
+    gain, u = torch.rand(width, generator=g, device="cuda"), torch.rand(rows, generator=g, device="cuda")
+    w, sw = torch.randint(-128, 128, (n, width), generator=g, device="cuda", dtype=torch.int8), torch.rand(n, generator=g, device="cuda")
+    q, scale = loom.loom_quantize_tokens(x)
+    _, mean, rstd = loom.loom_layer_norm(x, gain)
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if as_handle else side
+    for call in (lambda **k: loom.loom_layer_norm(x, gain, **k), lambda **k: loom.loom_quantize_tokens(x, **k),
+                 lambda **k: loom.loom_layer_norm_i8(x, gain, **k), lambda **k: loom.loom_i8_matmul(w, sw, n, width, q, scale, rows, want_acc=True, **k),
+                 lambda **k: loom.loom_layer_norm_backward(x, x, mean, rstd, gain, **k), lambda **k: loom.loom_sample_tokens(x, u, **k)):
+        want = call()
+        sizes = sorted({t.numel() * t.element_size() for t in want})
+        torch.cuda.synchronize()
+        for nbytes in sizes:
+            torch.cuda.empty_cache()
+            _busy(torch, nbytes)
+            got = call(stream=s)
+            side.synchronize()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_workspace_of_a_call_on_another_stream(env):
+    # the current stream writes blocks of the workspace's size while the other one takes gradients
+    torch, loom = env
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rows, width = 2000, 4096
+    x, gain = torch.randn(rows, width, generator=g, device="cuda"), torch.rand(width, generator=g, device="cuda")
+    _, mean, rstd = loom.loom_layer_norm(x, gain)
+    want = loom.loom_layer_norm_backward(x, x, mean, rstd, gain, want_dx=False)[1:]
+    nbytes = loom.loom_layer_norm_backward_workspace_bytes(rows, width)
+    side = torch.cuda.Stream()
+    out = []
+    for ms in (0.2, 0.4, 0.6, 0.8, 1.0, 1.3, 1.6, 2.0, 2.5, 3.0) * 2:      # the writes begin about when the call does
+        dgain, dbias = torch.empty(width, device="cuda"), torch.empty(width, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(int(ms * 2e6))
+        for _ in range(200):
+            torch.empty(nbytes, dtype=torch.uint8, device="cuda").fill_(0xff)
+        out.append(loom.loom_layer_norm_backward(x, x, mean, rstd, gain, want_dx=False, dgain=dgain, dbias=dbias, stream=side)[1:])
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for got in out for a, b in zip(want, got))
+
+
+def test_null_and_current_streams(env):
+    torch, loom = env
+    x = torch.randn(9, 128, device="cuda")
+    want = loom.loom_layer_norm(x)
+    torch.cuda.synchronize()
+    for s in (0, torch.cuda.default_stream(), torch.cuda.current_stream(), torch.cuda.current_stream().cuda_stream):
+        assert torch.equal(loom.loom_layer_norm(x, stream=s)[0], want[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for s in (0, side, side.cuda_stream, None):
+            y = loom.loom_layer_norm(x, stream=s)[0]
+            torch.cuda.synchronize()
+            assert torch.equal(y, want[0])
