@@ -43,7 +43,9 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
                                           (LOOM_PATH_*, default auto), sm_count (0 = the current device)} */
 #define LOOM_OP_LAYER_NORM 10          /* workload as LOOM_OP_QUANTIZE_TOKENS, {rows, width, ...} */
 #define LOOM_OP_LAYER_NORM_BACKWARD 11 /* workload {rows, width, dtype, aligned (0/1, default 1),
-                                          sm_count (0 = the current device)}: the first launch */
+                                          sm_count (0 = the current device)}: the first launch of a
+                                          call that wants all gradients (beyond 8192 columns: the rows'
+                                          sums, one row a CTA) */
 #define LOOM_OP_SAMPLE_TOKENS 12       /* workload {rows, vocab, dtype, sm_count (0 = the current device)} */
 
 /* Kernels they select (loom_launch.kernel). */

@@ -155,9 +155,8 @@ __global__ void __launch_bounds__(32 * DP_WARPS, 2) i8_matmul_dp4a_kernel(const 
 }
 
 template <int T, int KV, int R>
-cudaError_t launch_t(const MatmulParams &p, bool vec16, loom_launch L, cudaStream_t stream)
+cudaError_t launch_t(const MatmulParams &p, bool vec16, const loom_launch &L, cudaStream_t stream)
 {
-    L.smem_bytes = (uint32_t)(p.rows_per_cta * T * 4);
     return vec16 ? launch_with(i8_matmul_dp4a_kernel<T, KV, R, true>, L, stream, p)
                  : launch_with(i8_matmul_dp4a_kernel<T, KV, R, false>, L, stream, p);
 }
@@ -166,13 +165,12 @@ cudaError_t launch_t(const MatmulParams &p, bool vec16, loom_launch L, cudaStrea
 
 cudaError_t launch_matmul_dp4a(const MatmulParams &p, bool vec16, const loom_launch &L, cudaStream_t stream)
 {
-    if (p.tokens <= 1)
-        return launch_t<1, 4, 4>(p, vec16, L, stream);
-    if (p.tokens <= 2)
-        return launch_t<2, 4, 4>(p, vec16, L, stream);
-    if (p.tokens <= 4)
-        return launch_t<4, 2, 4>(p, vec16, L, stream);
-    return launch_t<8, 1, 4>(p, vec16, L, stream);
+    switch (matmul_dp4a_tokens(p.tokens)) {
+    case 1: return launch_t<1, 4, 4>(p, vec16, L, stream);
+    case 2: return launch_t<2, 4, 4>(p, vec16, L, stream);
+    case 4: return launch_t<4, 2, 4>(p, vec16, L, stream);
+    default: return launch_t<MM_DP4A_PASS, 1, 4>(p, vec16, L, stream);
+    }
 }
 
 }  // namespace loom

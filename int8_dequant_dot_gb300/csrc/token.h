@@ -16,6 +16,8 @@ inline int64_t dtype_bytes(int32_t dtype) { return dtype == LOOM_F32 ? 4 : 2; }
 constexpr int MM_DP4A_PASS = 8;       // tokens per pass of the dp4a kernel
 constexpr int MM_DP4A_MOST = 24;      // tokens that it takes by itself, of aligned matrices
 constexpr int MM_DP4A_CTAS_PER_SM = 2;
+// tokens that a dp4a kernel is built for, one pass taking up to as many
+inline int matmul_dp4a_tokens(int64_t tokens) { return tokens <= 1 ? 1 : tokens <= 2 ? 2 : tokens <= 4 ? 4 : MM_DP4A_PASS; }
 
 struct MatmulParams {
     const int8_t *w;          // [n][k]
@@ -66,7 +68,7 @@ struct RowsParams {
 // `vec` is the number of elements per load: the widest of 16 bytes, 8 bytes and one
 // element that every row's start and the width allow (row_vec).
 int row_vec(int32_t dtype, int32_t width, const void *const *pointers, const int64_t *strides, int n);
-bool rows_geometry(int64_t rows, int32_t width, int64_t sms, loom_launch *out);
+bool rows_geometry(int64_t rows, int32_t width, int32_t dtype, int64_t sms, loom_launch *out);
 cudaError_t launch_rows(const RowsParams &p, RowMode mode, int32_t dtype, int vec, const loom_launch &L,
                         cudaStream_t stream);
 
@@ -85,9 +87,9 @@ struct NormGradParams {
     int32_t inject_stall;       // test hook: no copies ahead (their waits run out)
     float *row_sums;            // [rows][2]: rows wider than NG_MAX_WIDTH (workspace), or NULL where partial is
 };
-// Geometry of the launch that takes the column sums; *parts (may be NULL) receives the
-// number of partial sums per column.
-bool norm_grad_geometry(int64_t rows, int32_t width, int64_t sms, loom_launch *out, int64_t *parts);
+// Geometry of the first launch of a call that wants all gradients, and the number of partial sums per column.
+void norm_grad_geometry(int64_t rows, int32_t width, int32_t dtype, int64_t sms, loom_launch *out);
+int64_t norm_grad_parts(int64_t rows, int32_t width, int64_t sms);
 int64_t norm_grad_workspace_bytes(int64_t rows, int32_t width, int64_t sms);
 cudaError_t launch_norm_grad(const NormGradParams &p, int32_t dtype, int vec, const loom_launch &L, int64_t parts,
                              cudaStream_t stream);

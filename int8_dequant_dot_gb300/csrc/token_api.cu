@@ -82,6 +82,7 @@ loom_status matmul_geometry(int64_t tokens, int64_t n, int64_t k, bool aligned, 
     int64_t per = (n + slots - 1) / slots;
     per = per < 1 ? 1 : per > MM_MAX_ROWS_PER_CTA ? MM_MAX_ROWS_PER_CTA : per;
     *out = plain_launch((n + per - 1) / per, passes < 65535 ? passes : 65535, 256, LOOM_KERNEL_I8_MATMUL_DP4A, (uint32_t)per);
+    out->smem_bytes = (uint32_t)(per * matmul_dp4a_tokens(tokens) * 4);
     return LOOM_OK;
 }
 
@@ -123,7 +124,7 @@ loom_status to_bytes(const void *d_x, int32_t dtype, int64_t rows, int32_t width
     if (counted != LOOM_OK)
         return counted;
     loom_launch L;
-    if (!rows_geometry(rows, width, sms, &L))
+    if (!rows_geometry(rows, width, dtype, sms, &L))
         return LOOM_ERR_SHAPE;
     RowsParams p = {};
     p.x = d_x;
@@ -171,7 +172,7 @@ extern "C" loom_status loom_token_launch_config(int32_t op, const int64_t *w, in
         const loom_status known_sms = sms ? LOOM_OK : sm_count(&sms);
         if (known_sms != LOOM_OK)
             return known_sms;
-        return rows_geometry(w[0], (int32_t)w[1], sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
+        return rows_geometry(w[0], (int32_t)w[1], (int32_t)w[2], sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
     }
     case LOOM_OP_I8_MATMUL:
         if (n < 3)
@@ -189,7 +190,8 @@ extern "C" loom_status loom_token_launch_config(int32_t op, const int64_t *w, in
             st = sm_count(&sms);
         if (st != LOOM_OK)
             return st;
-        return norm_grad_geometry(w[0], (int32_t)w[1], sms, out, nullptr) ? LOOM_OK : LOOM_ERR_SHAPE;
+        norm_grad_geometry(w[0], (int32_t)w[1], (int32_t)w[2], sms, out);
+        return LOOM_OK;
     }
     case LOOM_OP_SAMPLE_TOKENS: {
         if (n < 3 || !known((int32_t)w[2]) || opt(3, 0) < 0)
@@ -298,7 +300,7 @@ extern "C" loom_status loom_layer_norm(const void *d_x, int32_t dtype, int64_t r
     if (counted != LOOM_OK)
         return counted;
     loom_launch L;
-    if (!rows_geometry(rows, width, sms, &L))
+    if (!rows_geometry(rows, width, dtype, sms, &L))
         return LOOM_ERR_SHAPE;
     RowsParams p = {};
     p.x = d_x;
@@ -361,8 +363,8 @@ extern "C" loom_status loom_layer_norm_backward(const void *d_dy, int64_t dy_str
     if (needs && (!d_workspace || workspace_bytes < norm_grad_workspace_bytes(rows, width, sms)))
         return LOOM_ERR_ARG;
     loom_launch L;
-    int64_t parts = 0;
-    norm_grad_geometry(rows, width, sms, &L, &parts);
+    norm_grad_geometry(rows, width, dtype, sms, &L);
+    const int64_t parts = norm_grad_parts(rows, width, sms);
     NormGradParams p = {};
     p.dy = d_dy;
     p.x = d_x;

@@ -619,6 +619,21 @@ RingPlan plan_ring(int64_t rows, int64_t grid, int64_t per_sm, int64_t row_bytes
     return r;
 }
 
+// The rings of a launch of the geometry below (none where a warp takes a row).
+RingPlan rows_ring(int64_t rows, int32_t width, int64_t row_bytes, const loom_launch &L)
+{
+    if (width <= 32 * ROW_EPT || L.kernel != LOOM_KERNEL_NORM_ROWS)
+        return RingPlan{0, 0, 0};
+    return plan_ring(rows, L.grid[0], rows_per_sm(L.block[0]), row_bytes, 1, (int)L.units_per_cta);
+}
+
+RingPlan norm_grad_ring(int64_t rows, int32_t width, int64_t row_bytes, const loom_launch &L)
+{
+    if (width <= 32 * NG_EPT || width > NG_MAX_WIDTH)
+        return RingPlan{0, 0, 0};
+    return plan_ring(rows, L.grid[0], rows_per_sm(L.block[0]), row_bytes, 2, (int)L.units_per_cta);
+}
+
 template <typename... K, typename P> cudaError_t launch_ring(void (*kernel)(K...), const loom_launch &L, const P &p, const RingPlan &r, std::atomic<uint64_t> &done,
                                                              cudaStream_t stream)
 {
@@ -627,10 +642,9 @@ template <typename... K, typename P> cudaError_t launch_ring(void (*kernel)(K...
 }
 
 template <typename E, RowMode M, int V, int EPT, int R, bool WARP, int THREADS, bool KEEP>
-cudaError_t launch_rows_k(const RowsParams &p, loom_launch L, const RingPlan &r, cudaStream_t stream)
+cudaError_t launch_rows_k(const RowsParams &p, const loom_launch &L, const RingPlan &r, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
-    L.smem_bytes = r.smem_bytes;
     return launch_ring(rows_kernel<E, M, V, EPT, R, WARP, THREADS, KEEP>, L, p, r, done, stream);
 }
 
@@ -639,11 +653,10 @@ cudaError_t launch_rows_v(const RowsParams &p, const loom_launch &L, cudaStream_
 {
     if (L.kernel == LOOM_KERNEL_NORM_LONG)
         return launch_with(long_rows_kernel<E, M, V>, L, stream, p);
+    const RingPlan r = rows_ring(p.rows, p.width, (int64_t)p.width * (int64_t)sizeof(E), L);
     if (p.width <= 32 * ROW_EPT)
-        return launch_rows_k<E, M, V, ROW_EPT, 1, true, 32 * ROW_WARP_ROWS, false>(p, L, RingPlan{0, 0, 0}, stream);
-    const int ept = rows_ept(p.width);
-    const RingPlan r = plan_ring(p.rows, L.grid[0], rows_per_sm(L.block[0]), (int64_t)p.width * (int64_t)sizeof(E), 1, ept == ROW_EPT ? 2 : 1);
-    if (ept == ROW_EPT)
+        return launch_rows_k<E, M, V, ROW_EPT, 1, true, 32 * ROW_WARP_ROWS, false>(p, L, r, stream);
+    if (rows_ept(p.width) == ROW_EPT)
         return launch_rows_k<E, M, V, ROW_EPT, 2, false, 256, true>(p, L, r, stream);
     return p.width <= 512 * ROW_EPT_WIDE ? launch_rows_k<E, M, V, ROW_EPT_WIDE, 1, false, 512, true>(p, L, r, stream)
                                          : launch_rows_k<E, M, V, ROW_EPT_WIDE, 1, false, 1024, false>(p, L, r, stream);
@@ -943,38 +956,32 @@ __global__ void __launch_bounds__(NG_SUM_COLS *NG_SUM_GROUPS)
 }
 
 template <typename E, int V, int EPT, int R, bool WARP>
-cudaError_t launch_norm_grad_k(const NormGradParams &p, loom_launch L, const RingPlan &r, cudaStream_t stream)
+cudaError_t launch_norm_grad_k(const NormGradParams &p, const loom_launch &L, const RingPlan &r, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
-    L.smem_bytes = r.smem_bytes;
     return launch_ring(norm_grad_kernel<E, V, EPT, R, WARP>, L, p, r, done, stream);
 }
 
 template <typename E, int V>
-cudaError_t launch_norm_grad_v(const NormGradParams &p, const loom_launch &L, cudaStream_t stream)
+cudaError_t launch_norm_grad_v(const NormGradParams &p, const loom_launch &L, int64_t parts, cudaStream_t stream)
 {
+    const RingPlan r = norm_grad_ring(p.rows, p.width, (int64_t)p.width * (int64_t)sizeof(E), L);
     if (p.width <= 32 * NG_EPT)
-        return launch_norm_grad_k<E, V, NG_EPT, 1, true>(p, L, RingPlan{0, 0, L.smem_bytes}, stream);
-    if (p.width <= NG_MAX_WIDTH) {
-        const bool two = p.width <= 256 * NG_EPT;
-        const RingPlan r = plan_ring(p.rows, L.grid[0], rows_per_sm(L.block[0]), (int64_t)p.width * (int64_t)sizeof(E), 2, two ? 2 : 1);
-        return two ? launch_norm_grad_k<E, V, NG_EPT, 2, false>(p, L, r, stream)
-                   : launch_norm_grad_k<E, V, 2 * NG_EPT, 1, false>(p, L, r, stream);
-    }
+        return launch_norm_grad_k<E, V, NG_EPT, 1, true>(p, L, r, stream);
+    if (p.width <= NG_MAX_WIDTH)
+        return p.width <= 256 * NG_EPT ? launch_norm_grad_k<E, V, NG_EPT, 2, false>(p, L, r, stream)
+                                       : launch_norm_grad_k<E, V, 2 * NG_EPT, 1, false>(p, L, r, stream);
     if (p.dx) {
-        loom_launch S = L;
-        S.grid[0] = (uint32_t)p.rows;
-        S.grid[1] = 1;
-        S.block[0] = 1024;
         if (!p.partial)
-            return launch_with(long_norm_sums_kernel<E, V, true>, S, stream, p);
-        const cudaError_t e = launch_with(long_norm_sums_kernel<E, V, false>, S, stream, p);
+            return launch_with(long_norm_sums_kernel<E, V, true>, L, stream, p);
+        const cudaError_t e = launch_with(long_norm_sums_kernel<E, V, false>, L, stream, p);
         if (e != cudaSuccess)
             return e;
     }
     loom_launch G = L;
     G.grid[0] = (uint32_t)((p.width / V + NG_LONG_THREADS - 1) / NG_LONG_THREADS);
-    G.grid[1] = L.grid[0];
+    G.grid[1] = (uint32_t)parts;
+    G.block[0] = NG_LONG_THREADS;
     return launch_with(long_norm_grad_kernel<E, V>, G, stream, p);
 }
 
@@ -996,7 +1003,7 @@ int row_vec(int32_t dtype, int32_t width, const void *const *pointers, const int
     return 1;
 }
 
-bool rows_geometry(int64_t rows, int32_t width, int64_t sms, loom_launch *out)
+bool rows_geometry(int64_t rows, int32_t width, int32_t dtype, int64_t sms, loom_launch *out)
 {
     *out = loom_launch{};
     out->grid[1] = out->grid[2] = out->block[1] = out->block[2] = 1;
@@ -1024,6 +1031,7 @@ bool rows_geometry(int64_t rows, int32_t width, int64_t sms, loom_launch *out)
         return false;
     out->grid[0] = (uint32_t)grid;
     out->block[0] = (uint32_t)threads;
+    out->smem_bytes = rows_ring(rows, width, width * dtype_bytes(dtype), *out).smem_bytes;
     return true;
 }
 
@@ -1041,45 +1049,46 @@ cudaError_t launch_rows(const RowsParams &p, RowMode mode, int32_t dtype, int ve
                       : launch_rows_m<__nv_bfloat16, 1>(p, mode, L, stream);
 }
 
-bool norm_grad_geometry(int64_t rows, int32_t width, int64_t sms, loom_launch *out, int64_t *parts)
+// Rows at a time and threads of the launch that takes the column sums, and how many of its CTAs share an SM.
+struct NormGradShape {
+    int64_t rows, threads, per_sm;
+};
+
+static NormGradShape norm_grad_shape(int32_t width)
 {
+    if (width <= 32 * NG_EPT)
+        return {8, 256, 4};
+    if (width > NG_MAX_WIDTH)
+        return {1, NG_LONG_THREADS, 1};
+    const int64_t ept = width <= 256 * NG_EPT ? NG_EPT : 2 * NG_EPT, threads = ((int64_t)width + 32 * ept - 1) / (32 * ept) * 32;
+    return {ept == NG_EPT ? 2 : 1, threads, rows_per_sm(threads)};
+}
+
+int64_t norm_grad_parts(int64_t rows, int32_t width, int64_t sms)
+{
+    const NormGradShape shape = norm_grad_shape(width);
+    const int64_t turns = (rows + shape.rows - 1) / shape.rows, most = shape.per_sm * sms;
+    return turns < most ? turns : most;
+}
+
+void norm_grad_geometry(int64_t rows, int32_t width, int32_t dtype, int64_t sms, loom_launch *out)
+{
+    const NormGradShape shape = norm_grad_shape(width);
+    const bool wide = width > NG_MAX_WIDTH;            // the rows' own sums come first
     *out = loom_launch{};
+    out->grid[0] = (uint32_t)(wide ? rows : norm_grad_parts(rows, width, sms));
+    out->block[0] = (uint32_t)(wide ? 1024 : shape.threads);
     out->grid[1] = out->grid[2] = out->block[1] = out->block[2] = 1;
     out->cluster[0] = out->cluster[1] = out->cluster[2] = 1;
     out->subgroup_size = 32;
     out->kernel = LOOM_KERNEL_NORM_BACKWARD;
-    out->units_per_cta = 1;
-    int64_t threads, per_sm, grid = rows;
-    if (width <= 32 * NG_EPT) {
-        threads = 256;
-        per_sm = 4;
-        out->units_per_cta = 8;
-        out->smem_bytes = (uint32_t)(8 * 2 * width * 4);
-    } else if (width <= NG_MAX_WIDTH) {
-        const int64_t ept = width <= 256 * NG_EPT ? NG_EPT : 2 * NG_EPT;
-        threads = ((int64_t)width + 32 * ept - 1) / (32 * ept) * 32;
-        per_sm = rows_per_sm(threads);
-        out->units_per_cta = ept == NG_EPT ? 2 : 1;          // rows at a time
-    } else {
-        threads = NG_LONG_THREADS;
-        per_sm = 1;
-    }
-    const int64_t most = per_sm * sms;
-    grid = (rows + out->units_per_cta - 1) / out->units_per_cta;
-    grid = grid < most ? grid : most;
-    out->grid[0] = (uint32_t)grid;
-    out->block[0] = (uint32_t)threads;
-    if (parts)
-        *parts = grid;
-    return true;
+    out->units_per_cta = (uint32_t)shape.rows;
+    out->smem_bytes = width <= 32 * NG_EPT ? (uint32_t)(8 * 2 * width * 4) : norm_grad_ring(rows, width, width * dtype_bytes(dtype), *out).smem_bytes;
 }
 
 int64_t norm_grad_workspace_bytes(int64_t rows, int32_t width, int64_t sms)
 {
-    loom_launch L;
-    int64_t parts = 0;
-    norm_grad_geometry(rows, width, sms, &L, &parts);
-    return (parts * 2 * width + (width > NG_MAX_WIDTH ? 2 * rows : 0)) * 4;
+    return (norm_grad_parts(rows, width, sms) * 2 * width + (width > NG_MAX_WIDTH ? 2 * rows : 0)) * 4;
 }
 
 cudaError_t launch_norm_grad(const NormGradParams &p, int32_t dtype, int vec, const loom_launch &L, int64_t parts,
@@ -1088,15 +1097,15 @@ cudaError_t launch_norm_grad(const NormGradParams &p, int32_t dtype, int vec, co
     if (p.rows > 0) {
         cudaError_t e;
         if (dtype == LOOM_F32)
-            e = vec == 4 ? launch_norm_grad_v<float, 4>(p, L, stream) : launch_norm_grad_v<float, 1>(p, L, stream);
+            e = vec == 4 ? launch_norm_grad_v<float, 4>(p, L, parts, stream) : launch_norm_grad_v<float, 1>(p, L, parts, stream);
         else if (dtype == LOOM_F16)
-            e = vec == 8   ? launch_norm_grad_v<__half, 8>(p, L, stream)
-                : vec == 4 ? launch_norm_grad_v<__half, 4>(p, L, stream)
-                           : launch_norm_grad_v<__half, 1>(p, L, stream);
+            e = vec == 8   ? launch_norm_grad_v<__half, 8>(p, L, parts, stream)
+                : vec == 4 ? launch_norm_grad_v<__half, 4>(p, L, parts, stream)
+                           : launch_norm_grad_v<__half, 1>(p, L, parts, stream);
         else
-            e = vec == 8   ? launch_norm_grad_v<__nv_bfloat16, 8>(p, L, stream)
-                : vec == 4 ? launch_norm_grad_v<__nv_bfloat16, 4>(p, L, stream)
-                           : launch_norm_grad_v<__nv_bfloat16, 1>(p, L, stream);
+            e = vec == 8   ? launch_norm_grad_v<__nv_bfloat16, 8>(p, L, parts, stream)
+                : vec == 4 ? launch_norm_grad_v<__nv_bfloat16, 4>(p, L, parts, stream)
+                           : launch_norm_grad_v<__nv_bfloat16, 1>(p, L, parts, stream);
         if (e != cudaSuccess)
             return e;
     }
