@@ -40,7 +40,9 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
 #define LOOM_OP_QUANTIZE_TOKENS 8      /* workload {tokens, k, dtype, aligned (0/1, default 1),
                                           sm_count (0 = the current device)} */
 #define LOOM_OP_I8_MATMUL 9            /* workload {tokens, n, k, aligned (0/1, default 1), path
-                                          (LOOM_PATH_*, default auto), sm_count (0 = the current device)} */
+                                          (LOOM_PATH_*, default auto), sm_count (0 = the current device; the
+                                          tensor cores want two SMs for more than 32 tokens, else
+                                          LOOM_ERR_ARG where they are asked for)} */
 #define LOOM_OP_LAYER_NORM 10          /* workload as LOOM_OP_QUANTIZE_TOKENS, {rows, width, ...} */
 #define LOOM_OP_LAYER_NORM_BACKWARD 11 /* workload {rows, width, dtype, aligned (0/1, default 1),
                                           sm_count (0 = the current device)}: the first launch of a

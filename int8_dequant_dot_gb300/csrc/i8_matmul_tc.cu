@@ -922,7 +922,7 @@ int matmul_tc_threads(const MatmulTcPlan &q) { return q.halves == 1 ? Shape<1>::
 
 // Tile, split of k and grid.  The time of a choice is its waves of tiles times the stages of
 // one tile, plus what a tile (or a split) costs once, in units of a stage.
-void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, bool vec16, int64_t sms, MatmulTcPlan *out)
+bool matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, bool vec16, int64_t sms, MatmulTcPlan *out)
 {
     MatmulTcPlan best = {};
     double best_cost = 0.0;
@@ -948,6 +948,8 @@ void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, bool vec16, int64_t sm
             best.grid = (tiles < slots ? tiles : slots) * size;
         }
     }
+    if (best.split == 0)
+        return false;
     best.cg = cg;
     best.halves = halves;
     best.tile_t = (int32_t)tile_t;
@@ -964,6 +966,7 @@ void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, bool vec16, int64_t sm
     bytes = bytes > 116u * 1024u ? bytes : 116u * 1024u;   // more than half an SM: one CTA, which owns tensor memory
     best.smem_bytes = 2 * MT_AREA + bytes;
     *out = best;
+    return true;
 }
 
 cudaError_t launch_matmul_tc(const MatmulParams &p, const MatmulTcPlan &q, bool vec16, cudaStream_t stream)

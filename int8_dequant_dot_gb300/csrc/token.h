@@ -45,7 +45,8 @@ struct MatmulTcPlan {
     uint32_t stage_bytes, ahead_bytes, smem_bytes;
 };
 int matmul_tc_threads(const MatmulTcPlan &q);
-void matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, bool vec16, int64_t sms, MatmulTcPlan *out);
+// false: more tokens than one CTA takes on fewer than two SMs
+bool matmul_tc_plan(int64_t tokens, int64_t n, int64_t k, bool vec16, int64_t sms, MatmulTcPlan *out);
 cudaError_t launch_matmul_tc(const MatmulParams &p, const MatmulTcPlan &q, bool vec16, cudaStream_t stream);
 cudaError_t launch_matmul_dp4a(const MatmulParams &p, bool vec16, const loom_launch &L, cudaStream_t stream);
 

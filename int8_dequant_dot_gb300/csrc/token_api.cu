@@ -71,13 +71,14 @@ loom_status matmul_geometry(int64_t tokens, int64_t n, int64_t k, bool aligned, 
     const int64_t passes = (tokens + MM_DP4A_PASS - 1) / MM_DP4A_PASS;
     const bool many = tokens > 4 && (tokens > MM_DP4A_MOST || (2 * passes - 1) * n * k > (36ll << 20));
     const bool tensor = path == LOOM_PATH_TENSOR || (path == LOOM_PATH_AUTO && aligned && many);
-    if (tensor && k > 0 && n > 0 && tokens > 0) {
-        matmul_tc_plan(tokens, n, k, k % 16 == 0, sms, plan);
+    if (tensor && k > 0 && n > 0 && tokens > 0 && matmul_tc_plan(tokens, n, k, k % 16 == 0, sms, plan)) {
         *out = plain_launch(plan->grid, 1, (uint32_t)matmul_tc_threads(*plan), LOOM_KERNEL_I8_MATMUL_TENSOR, 128u);
         out->cluster[0] = (uint32_t)(plan->cg * plan->split);
         out->smem_bytes = plan->smem_bytes;
         return LOOM_OK;
     }
+    if (path == LOOM_PATH_TENSOR && k > 0 && n > 0 && tokens > 0)
+        return LOOM_ERR_ARG;
     const int64_t slots = sms * MM_DP4A_CTAS_PER_SM;
     int64_t per = (n + slots - 1) / slots;
     per = per < 1 ? 1 : per > MM_MAX_ROWS_PER_CTA ? MM_MAX_ROWS_PER_CTA : per;

@@ -64,3 +64,20 @@ def test_clusters_of_sampling(loom, vocab, few, many):
     for rows, ranks in ((3, few), (1000, many)):
         L = loom.loom_token_launch_config(loom.LOOM_OP_SAMPLE_TOKENS, [rows, vocab, loom.LOOM_F32, SMS])
         assert L["cluster"] == (ranks, 1, 1) and L["grid"] == (rows * ranks, 1, 1) and L["smem_bytes"] <= SM_BYTES
+
+
+def test_product_on_one_sm(loom):
+    # more than 32 tokens take pairs of CTAs, which one SM cannot hold
+    cfg = lambda t, path, sms: loom.loom_token_launch_config(loom.LOOM_OP_I8_MATMUL, [t, 4096, 1024, 1, path, sms])   # noqa: E731
+    assert cfg(32, loom.LOOM_PATH_TENSOR, 1)["grid"] == (1, 1, 1)
+    assert cfg(33, loom.LOOM_PATH_AUTO, 1)["kernel"] == loom.LOOM_KERNEL_I8_MATMUL_DP4A
+    with pytest.raises(loom.LoomError) as e:
+        cfg(33, loom.LOOM_PATH_TENSOR, 1)
+    assert e.value.status == loom.LOOM_ERR_ARG
+    for t in (33, 300):
+        L = cfg(t, loom.LOOM_PATH_TENSOR, 2)
+        assert L["grid"] == (2, 1, 1) and L["cluster"] == (2, 1, 1)
+    for sms in range(1, 160):
+        for t in (5, 40, 300):
+            L = cfg(t, loom.LOOM_PATH_AUTO, sms)
+            assert L["grid"][0] >= 1 and L["cluster"][0] >= 1 and L["grid"][0] % L["cluster"][0] == 0
