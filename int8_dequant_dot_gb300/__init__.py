@@ -6,9 +6,12 @@ other than LOOM_OK raises LoomError.  Every step of the computation runs in
 libloom's CUDA kernels; there is no fallback, and importing this module
 fails loudly when libloom.so has not been built (see build.py).
 
-Each function accepts either torch tensors or raw integer addresses.  Output
+Each function accepts either torch tensors or raw integer addresses; the token
+operators take their sizes from tensors, check them (type, length, order, device)
+and take addresses for outputs and optional arguments alone.  Output
 tensors may be passed in; when omitted they are allocated with torch (on
-the inputs' device) and returned.
+the inputs' device) and returned.  No call records a gradient: torch's autograd
+sees its outputs as new tensors, and loom_layer_norm_backward is called by hand.
 """
 from __future__ import annotations
 

@@ -48,13 +48,16 @@
 //                         520 to 565 us).  Bound by the converters' shared-memory traffic (64
 //                         stages of 1225 cycles a tile), then by a tile's stores (18000 cycles,
 //                         half of them behind the next tile's MMAs), which share those ports.
-//   96 x 65536 x 4096     62 us, 4.4 TB/s: an MMA takes 84 cycles or more however few its
-//                         tokens, and a stage has eight (770 cycles measured); 256 tiles are
-//                         four waves of pairs, the last a third full.
-//   16 x 8192 x 16384     31 to 33 us, 4.2 TB/s: the same MMAs (780 cycles a stage), 64 tiles
-//                         split over 128 of the SMs.
-//   203 x 5001 x 4108     33 us (k = 4112: 27 us): 120 CTAs of 11 stages each; the exchange of
+//   96 x 65536 x 4096     61 us, 4.4 TB/s: 256 tiles are 3.4 waves of 76 pairs and take four, and
+//                         each begins and ends by itself.  (An MMA takes 84 cycles or more however few
+//                         its tokens, and a stage has eight, 770 cycles measured: full waves of
+//                         those would move 6.4 TB/s.)
+//   16 x 8192 x 16384     31 us, 4.3 TB/s: 64 tiles split over 128 of the SMs, and an exchange of sums.
+//                         (loom_i8_dequant_dot, whole rows on all SMs and no exchange, takes 27 us
+//                         for the same sums as [row][vector] f32.)
+//   203 x 5001 x 4108     31 us (k = 4112: 25 us): 120 CTAs of 11 stages each; the exchange of
 //                         the sums is a third of it.
+// All six forms spill some registers (124 to 164 bytes of stores a thread, 312 to 372 of loads).
 #include "tc_ptx.cuh"
 #include "token_ops.cuh"
 

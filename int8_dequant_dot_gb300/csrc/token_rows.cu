@@ -17,13 +17,19 @@
 //    two rows a turn.
 //  * Loads are as wide as every row's start allows: 16 or 8 bytes, else one element.
 //
-// Measured (bf16 rows x width)
+// Measured (bf16 rows x width where no type is given; graph nodes)
 //   layer norm 16384 x 8192       84 us, 6.4 TB/s (a copy of the same bytes: 79 us)
-//   to bytes 8192 x 8192          34 us, 5.9 TB/s;  layer norm to bytes 62 us, 3.2 TB/s: three
+//              16384 x 2048       27 us, 4.9 TB/s: a turn's barriers for 8 KiB of rows
+//              8000 x 5001        76 us, 2.1 TB/s; 4000 x 5001 f32 40 us, 4.0 TB/s: one element an access
+//              2048 x 40000       133 us, 2.5 TB/s: the row read three times, from L2 where it still is there
+//              8 x 2048 f32       2.5 us: the launch and three trips to memory
+//   to bytes 8192 x 8192          32 us, 6.2 TB/s;  layer norm to bytes 61 us, 3.3 TB/s: three
 //                                 reductions a row, one after the other, and what lies between
-//   backward 16384 x 4096         80 us, 5.0 TB/s; 1001 x 5001 f32 26 us, 2.3 TB/s: seven rows a
-//                                 CTA, then 12 MB of partial sums written and read
-//   layer norm 8 x 2048 f32       3.0 us: the launch and three trips to memory
+//   backward 16384 x 4096         75 us, 5.3 TB/s; 16384 x 2048 46 us; 8192 x 8192 83 us
+//            1001 x 5001 f32      22 us, 2.7 TB/s: seven rows a CTA, then 12 MB of partial sums written
+//                                 and read
+//            4096 x 6144          42 us, 3.6 TB/s: 257 to 511 threads a row leave one CTA an SM
+//            4096 x 12288         151 us, 2.0 TB/s: x and dy are read twice; dx alone 114 us
 #include "token_ops.cuh"
 
 namespace loom {

@@ -31,6 +31,9 @@
 //   1 x 32768     9.0 / 14.1 / 5.8 us
 //   38 x 131072   24 / 45 / 18 us (one wave of clusters)
 //   256 x 131072  99 / 203 / 78 us, 1.7 TB/s for the last; greedy 43 us, 3.1 TB/s
+//   256 x 131072 bf16  95 / 210 / 75 us; greedy 37 us: the passes over f32 copies are the same
+//   256 x 131071  210 us by top-p, 85 us unfiltered (bf16 220 and 85): rows that do not start on 16 bytes
+//                 are loaded one element at a time
 // (An L2 prefetch of the slices that will follow on the same SMs took 2 us from greedy rows and
 // gave 2 us to the others.)
 #include "token_ops.cuh"
