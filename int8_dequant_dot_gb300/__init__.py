@@ -7,8 +7,9 @@ libloom's CUDA kernels; there is no fallback, and importing this module
 fails loudly when libloom.so has not been built (see build.py).
 
 Each function accepts either torch tensors or raw integer addresses; the token
-operators take their sizes from tensors, check them (type, length, order, device)
-and take addresses for outputs and optional arguments alone.  Output
+operators take their sizes from tensors and check them (type, length, order, device);
+addresses they take for packed bytes, scales, statistics, sums and tokens that they
+write, for error words and for the product's bias.  Output
 tensors may be passed in; when omitted they are allocated with torch (on
 the inputs' device) and returned.  No call records a gradient: torch's autograd
 sees its outputs as new tensors, and loom_layer_norm_backward is called by hand.
