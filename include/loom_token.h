@@ -8,7 +8,13 @@
  *  2. layer norm: forward, forward handing out 8-bit tokens, and backward with
  *     the reduction of the gain's and the bias's gradient;
  *  3. the choice of the next token from logits, with temperature, top-k, top-p
- *     and min-p, from given random numbers.
+ *     and min-p, from given random numbers, and in front of it penalties for
+ *     repeated tokens, biases and grammar masks on the logits (loom_adjust_logits);
+ *  4. products of a few 8-bit tokens with 4-bit weights that have a scale for each
+ *     group along k (loom_i4_matvec), also with the matrices of the experts that each
+ *     token goes to (loom_i4_matvec_routed), and the routing that names those experts
+ *     and their weights, as loom_routed_combine takes them (loom_route_tokens, with
+ *     the gradient loom_route_tokens_backward).
  *
  * The conventions of loom.h hold: d_ pointers are device memory of the caller,
  * nothing is allocated or kept, work is enqueued on `stream` (a cudaStream_t)
@@ -49,6 +55,12 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
                                           call that wants all gradients (beyond 8192 columns: the rows'
                                           sums, one row a CTA) */
 #define LOOM_OP_SAMPLE_TOKENS 12       /* workload {rows, vocab, dtype, sm_count (0 = the current device)} */
+#define LOOM_OP_I4_MATVEC 13           /* workload {tokens, n, k, group, experts (0: one matrix, default), routes
+                                          (default 1), sm_count (0 = the current device)}: the first launch */
+#define LOOM_OP_ROUTE_TOKENS 14        /* workload {tokens, experts, sm_count (0 = the current device)} */
+#define LOOM_OP_ROUTE_TOKENS_BACKWARD 15 /* the same */
+#define LOOM_OP_ADJUST_LOGITS 16       /* workload {rows, vocab, marks (0/1: penalties or biases, default 1), sm_count
+                                          (0 = the current device)} */
 
 /* Kernels they select (loom_launch.kernel). */
 #define LOOM_KERNEL_I8_MATMUL_DP4A 18   /* few tokens: dp4a, weights streamed once per pass of up to 8 tokens */
@@ -57,6 +69,10 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
 #define LOOM_KERNEL_NORM_LONG 21        /* rows longer than the registers of a CTA, read again from L2 */
 #define LOOM_KERNEL_NORM_BACKWARD 22    /* CTAs over shares of the rows, column sums in registers */
 #define LOOM_KERNEL_SAMPLE 24           /* logits to token */
+#define LOOM_KERNEL_I4_MATVEC 25        /* units_per_cta = rows of weights (of experts: where all are wanted) */
+#define LOOM_KERNEL_ROUTE 26            /* logits to experts; units_per_cta = tokens */
+#define LOOM_KERNEL_ROUTE_BACKWARD 27   /* units_per_cta = tokens */
+#define LOOM_KERNEL_ADJUST 28           /* a cluster per row; units_per_cta = 1 */
 
 /* As loom_launch_config, for the operators of this header. */
 loom_status loom_token_launch_config(int32_t op, const int64_t *workload, int32_t n_workload, loom_launch *out);
@@ -198,6 +214,126 @@ loom_status loom_sample_tokens(const void *d_logits, int32_t dtype, int64_t rows
                                const float *d_top_p, float top_p, const float *d_min_p, float min_p,
                                const float *d_uniform, int32_t *d_token, float *d_logprob, int32_t *d_error,
                                void *stream);
+
+/*
+ * Logits adjusted before a token is chosen: penalties for tokens that were seen, biases,
+ * a grammar's mask.  For row r, token i and logit l, each step one f32 rounding, in this order:
+ *   seen     (i is among the first lengths[r] tokens of the row's history):
+ *            l = l > 0 ? l / repetition : l * repetition
+ *   counted  c > 0 times at places [prompts[r], lengths[r]) of it:
+ *            l = l - frequency * c (product and difference rounded), then l = l - presence
+ *   biased   l = l + value, of the first of the row's bias entries that names i
+ *   masked   l = -infinity where the row's mask has bit i clear (whatever l was, NaN too)
+ * and one rounding to `dtype`, the type of logits and y.  Logits that no step changes keep their bits.
+ * d_history: int32 [rows][history], rows history_stride elements apart, or NULL (nothing was
+ * seen); tokens outside [0, vocab) are passed over.  d_lengths: int32 [rows], or NULL (all
+ * `history` tokens); a length outside [0, history] is cut and flagged (LOOM_DEVERR_COUNT_RANGE).
+ * d_prompts: int32 [rows], or NULL (0); outside [0, length] it is cut.  Penalties are one device value per row, or,
+ * where that is NULL, the host value for every row; a device repetition that is not above zero counts as 1.
+ * d_bias_ids int32 and d_bias_values f32 [rows][biases], or NULL; ids outside [0, vocab)
+ * (such as the -1 behind a shorter list) are passed over.
+ * d_mask: int32 [masks][ceil(vocab / 32)], token i is bit i % 32 of word i / 32, or NULL.
+ * d_mask_rows: int32 [rows], the mask of each row, negative for none; `masks` or more counts as none and is
+ * flagged.  NULL: row r has mask r, or, where masks is 1, all rows have that one.
+ * d_y may be d_logits (rows, type and stride alike); then only what changes is read and written,
+ * and a mask's words.
+ * Errors: NULL logits or y, one of the bias arrays alone -> LOOM_ERR_NULL; misaligned -> LOOM_ERR_ALIGN;
+ * rows < 0 or > 2^31 - 1, vocab < 1 or > 393216, history < 0 or > 1048575, biases < 0 or > 1024,
+ * masks < 0, masks < rows without d_mask_rows (and not 1), a stride below its row (with more than one
+ * row) -> LOOM_ERR_SHAPE; unknown dtype, a host repetition not above zero or infinite, a host
+ * frequency or presence that is not finite -> LOOM_ERR_ARG.
+ */
+loom_status loom_adjust_logits(const void *d_logits, int32_t dtype, int64_t rows, int32_t vocab, int64_t stride,
+                               const int32_t *d_history, int32_t history, int64_t history_stride,
+                               const int32_t *d_lengths, const int32_t *d_prompts, const float *d_repetition,
+                               float repetition, const float *d_frequency, float frequency, const float *d_presence,
+                               float presence, const int32_t *d_bias_ids, const float *d_bias_values, int32_t biases,
+                               const int32_t *d_mask, int32_t masks, const int32_t *d_mask_rows, void *d_y,
+                               int64_t y_stride, int32_t *d_error, void *stream);
+
+/*
+ * Product of a few 8-bit tokens with 4-bit weights that have a scale for each group of `group`
+ * neighbours along k (the last group of a row may be shorter):
+ *   a[t][r][g] = sum over k in group g of W[r][k] * X[t][k]                       (exact)
+ *   y[t][r]    = d_scale_x[t] * sum over g of scale_w[r][g] * a[t][r][g] + d_bias[r]
+ * the sum over groups in f32, in a fixed order that depends on the sizes alone, and one rounding to `y_dtype`.
+ * d_w_packed: int32 [n_rows][k/8], word j of a row holds elements 8j..8j+7, element 8j+i in
+ * bits [4i, 4i+3] as a signed nibble (-8..7).  d_scale_w: [n_rows][ceil(k / group)] of type
+ * scale_dtype; scales beyond 2^100 in size overflow.  d_x_packed: int32 [tokens][k/4], d_scale_x f32 [tokens], as
+ * loom_quantize_tokens gives them; d_bias f32 [n_rows] or NULL; d_y [tokens][n_rows], rows
+ * `y_stride` elements apart.
+ * For few tokens: the weights are read once for every 32 of them.
+ * Errors: NULL -> LOOM_ERR_NULL; misaligned pointers (4 bytes; scales and d_y: their elements) ->
+ * LOOM_ERR_ALIGN; k % 8 != 0, k > 131064, group not a power of two of at least 32, negative
+ * sizes, y_stride < n_rows (with more than one token) -> LOOM_ERR_SHAPE; unknown dtypes -> LOOM_ERR_ARG.
+ */
+loom_status loom_i4_matvec(const int32_t *d_w_packed, const void *d_scale_w, int32_t scale_dtype, int32_t n_rows,
+                           int32_t k, int32_t group, const int32_t *d_x_packed, const float *d_scale_x, int32_t tokens,
+                           const float *d_bias, void *d_y, int32_t y_dtype, int64_t y_stride, void *stream);
+
+/*
+ * The experts' products: for token t and route j, with e = d_ids[t][j] (int32 [tokens][routes]),
+ *   y[t * routes + j] = loom_i4_matvec of matrix e and the pair's token,
+ * where d_w_packed is [experts][n_rows][k/8], d_scale_w [experts][n_rows][ceil(k / group)] and d_bias
+ * [experts][n_rows] or NULL.  x_rows is `tokens` (a token's routes share its row of X) or
+ * tokens * routes (each pair has a row of X and a scale of its own, as a second layer wants).  A
+ * negative id is a missing route: its row of y is zeros.  An id of `experts` or more is treated so
+ * too and flagged (LOOM_DEVERR_COUNT_RANGE).  A matrix is read once for every 32 pairs that name it,
+ * among 2048 pairs.  y's rows are loom_routed_combine's payload, row t * routes + j of pair (t, j).
+ * Errors: as loom_i4_matvec, and experts < 0 or > 1024, routes < 0 or > 64, tokens * routes > 2^31 - 1,
+ * x_rows neither of the two -> LOOM_ERR_SHAPE.
+ */
+loom_status loom_i4_matvec_routed(const int32_t *d_w_packed, const void *d_scale_w, int32_t scale_dtype, int32_t experts,
+                                  int32_t n_rows, int32_t k, int32_t group, const int32_t *d_x_packed,
+                                  const float *d_scale_x, int64_t x_rows, const int32_t *d_ids, int32_t tokens,
+                                  int32_t routes, const float *d_bias, void *d_y, int32_t y_dtype, int64_t y_stride,
+                                  int32_t *d_error, void *stream);
+
+/* Scores of loom_route_tokens. */
+typedef enum loom_score { LOOM_SCORE_SOFTMAX = 0, LOOM_SCORE_SIGMOID = 1 } loom_score;
+
+/*
+ * Routing: the experts of each token and their weights, from logits [tokens][experts], rows
+ * `stride` elements apart.  An expert whose logit is -infinity or NaN, or whose bias is, is never
+ * chosen (and has no part in a softmax by its logit); +infinity counts as the largest finite f32.
+ *   score[e]  = softmax of the token's logits, or 1 / (1 + exp(-logit))
+ *   choice    by score[e] + d_bias[e] (f32 [experts], NULL: by the score): with more than one group
+ *             (`groups` equal runs of experts), the top_groups groups whose group_best (1 or 2)
+ *             best experts have the largest sum stay (a group with fewer counts those it has);
+ *             then the top_k best experts of those, falling.  The order is that of the real
+ *             numbers; equal ones go to the lower index.
+ *   weight    = factor * score, divided by the sum of the chosen scores where `renormalise`
+ * d_ids int32 and d_weights f32 [tokens][top_k]; where fewer than top_k can be chosen the rest
+ * are -1 and 0, which loom_routed_combine and loom_i4_matvec_routed take as missing routes.
+ * (A row of d_bias values beyond 2^20 in size leaves scores no room in 64 bits.)
+ * d_counts: int32 [experts] or NULL; the number of tokens that go to each expert is added to it (what a
+ * bias for balance is set by).
+ * Errors: NULL logits, ids or weights -> LOOM_ERR_NULL; misaligned -> LOOM_ERR_ALIGN; tokens < 0 or
+ * > 2^31 - 1, experts < 1 or > 1024, top_k < 1, > 32 or > experts, groups < 1 or not a divisor
+ * of experts, top_groups < 1 or > groups, stride < experts (with more than one token) -> LOOM_ERR_SHAPE;
+ * unknown dtype or score, group_best neither 1 nor 2, factor not finite -> LOOM_ERR_ARG.
+ */
+loom_status loom_route_tokens(const void *d_logits, int32_t dtype, int64_t tokens, int32_t experts, int64_t stride,
+                              const float *d_bias, int32_t score, int32_t groups, int32_t top_groups,
+                              int32_t group_best, int32_t top_k, int32_t renormalise, float factor, int32_t *d_ids,
+                              float *d_weights, int32_t *d_counts, void *stream);
+
+/*
+ * Gradient of those weights to the logits, the choice held fixed: d_dlogits [tokens][experts] of
+ * `dtype`, rows dlogits_stride elements apart, from d_dweights f32 [tokens][top_k], the logits and
+ * d_ids.  With g[j] = factor * dweight[j], chosen scores s[j] and S their sum:
+ *   renormalised   h[j] = (g[j] - sum(g s) / S) / S,  else h[j] = g[j]
+ *   softmax        dlogit[e] = score[e] * (sum of h[j] over ids[j] = e  -  sum(h s))
+ *   sigmoid        dlogit[e] = score[e] * (1 - score[e]) * (sum of h[j] over ids[j] = e)
+ * (renormalised softmax scores are taken among the chosen experts, where sum(h s) is zero).
+ * Missing routes (negative ids, or ids of `experts` or more, which are flagged with
+ * LOOM_DEVERR_COUNT_RANGE) take no part; an expert that can't be chosen gets 0.  d_dlogits may be d_logits.
+ * Errors: as loom_route_tokens.
+ */
+loom_status loom_route_tokens_backward(const float *d_dweights, const void *d_logits, int32_t dtype, int64_t tokens,
+                                       int32_t experts, int64_t stride, const int32_t *d_ids, int32_t score,
+                                       int32_t top_k, int32_t renormalise, float factor, void *d_dlogits,
+                                       int64_t dlogits_stride, int32_t *d_error, void *stream);
 
 #ifdef __cplusplus
 }

@@ -52,6 +52,10 @@ LOOM_OP_I8_MATMUL = 9
 LOOM_OP_LAYER_NORM = 10
 LOOM_OP_LAYER_NORM_BACKWARD = 11
 LOOM_OP_SAMPLE_TOKENS = 12
+LOOM_OP_I4_MATVEC = 13
+LOOM_OP_ROUTE_TOKENS = 14
+LOOM_OP_ROUTE_TOKENS_BACKWARD = 15
+LOOM_OP_ADJUST_LOGITS = 16
 
 LOOM_KERNEL_UNPACK = 1
 LOOM_KERNEL_ROWSUM_STAGED = 2
@@ -76,10 +80,17 @@ LOOM_KERNEL_NORM_ROWS = 20
 LOOM_KERNEL_NORM_LONG = 21
 LOOM_KERNEL_NORM_BACKWARD = 22
 LOOM_KERNEL_SAMPLE = 24
+LOOM_KERNEL_I4_MATVEC = 25
+LOOM_KERNEL_ROUTE = 26
+LOOM_KERNEL_ROUTE_BACKWARD = 27
+LOOM_KERNEL_ADJUST = 28
 
 LOOM_F32 = 0
 LOOM_F16 = 1
 LOOM_BF16 = 2
+
+LOOM_SCORE_SOFTMAX = 0
+LOOM_SCORE_SIGMOID = 1
 
 LOOM_MAX_DEPTH = 8
 LOOM_PATH_AUTO = 0
@@ -100,7 +111,8 @@ EXPORTS = (
     "loom_sum_guarded_rows_ex", "loom_routed_combine", "loom_routed_combine_ex", "loom_stage_rows",
     "loom_stream_floor", "loom_token_launch_config", "loom_quantize_tokens", "loom_i8_matmul", "loom_i8_matmul_ex",
     "loom_layer_norm", "loom_layer_norm_i8", "loom_layer_norm_backward", "loom_layer_norm_backward_workspace_bytes",
-    "loom_sample_tokens",
+    "loom_sample_tokens", "loom_adjust_logits", "loom_i4_matvec", "loom_i4_matvec_routed", "loom_route_tokens",
+    "loom_route_tokens_backward",
 )
 
 
@@ -168,6 +180,11 @@ def _bind() -> ctypes.CDLL:
         "loom_layer_norm_backward": [P, i64, P, i64, i32, i64, i32, P, P, P, P, i64, P, P, P, i64, P],
         "loom_layer_norm_backward_workspace_bytes": [i64, i32, ctypes.POINTER(i64)],
         "loom_sample_tokens": [P, i32, i64, i32, i64, P, f32, P, i32, P, f32, P, f32, P, P, P, P, P],
+        "loom_adjust_logits": [P, i32, i64, i32, i64, P, i32, i64, P, P, P, f32, P, f32, P, f32, P, P, i32, P, i32, P, P, i64, P, P],
+        "loom_i4_matvec": [P, P, i32, i32, i32, i32, P, P, i32, P, P, i32, i64, P],
+        "loom_i4_matvec_routed": [P, P, i32, i32, i32, i32, i32, P, P, i64, P, i32, i32, P, P, i32, i64, P, P],
+        "loom_route_tokens": [P, i32, i64, i32, i64, P, i32, i32, i32, i32, i32, i32, f32, P, P, P, P],
+        "loom_route_tokens_backward": [P, P, i32, i64, i32, i64, P, i32, i32, i32, f32, P, i64, P, P],
         "loom_status_string": [i32],
         "loom_abi_version": [],
     }
@@ -840,13 +857,13 @@ def loom_layer_norm_backward(dy, x, mean, rstd, gain=None, *, dx=None, dgain=Non
     return dx, dgain, dbias
 
 
-def _setting(name: str, v, dtype, rows: int, device: int):
-    """(device address or None, host value) of a sampling setting."""
+def _setting(name: str, v, dtype, rows: int, device: int, where: str = "loom_sample_tokens"):
+    """(device address or None, host value) of a setting that rows may have one by one."""
     if isinstance(v, _torch.Tensor):
         if v.dtype != dtype or v.numel() != rows or not v.is_contiguous():
-            raise LoomError(LOOM_ERR_SHAPE, f"loom_sample_tokens: {name}: {rows} contiguous {dtype} values are wanted")
+            raise LoomError(LOOM_ERR_SHAPE, f"{where}: {name}: {rows} contiguous {dtype} values are wanted")
         if v.get_device() != device:
-            _foreign(f"loom_sample_tokens: {name}", v)
+            _foreign(f"{where}: {name}", v)
         return v.data_ptr(), 0
     return None, v
 
@@ -878,3 +895,171 @@ def loom_sample_tokens(logits, uniform, *, temperature=1.0, top_k=0, top_p=1.0, 
     _launch(where, logits, stream, logits.data_ptr(), dtype, rows, vocab, stride, dt, t, dk, k, dp, p, dm, m,
             uniform.data_ptr(), token_at, logprob_at, _dense(where, error, 1, torch.int32, device))
     return token, logprob
+
+
+def loom_adjust_logits(logits, *, history=None, lengths=None, prompts=None, repetition=1.0, frequency=0.0, presence=0.0,
+                       bias_ids=None, bias_values=None, mask=None, mask_rows=None, y=None, error=None, stream=None):
+    """``logits[rows][vocab]`` with penalties for the tokens of ``history`` (int32 ``[rows][n]``, the first
+    ``lengths[row]`` of them, of which the first ``prompts[row]`` count for ``repetition`` alone), biases
+    (``bias_ids`` int32 and ``bias_values`` float32 ``[rows][m]``) and a grammar's ``mask`` (int32
+    ``[masks][ceil(vocab / 32)]`` bits; ``mask_rows`` int32 ``[rows]``, negative for none).  A penalty is a number
+    for every row or a device tensor with one per row.  Returns ``y``, which may be ``logits``."""
+    torch = _torch or _lazy()
+    where = "loom_adjust_logits"
+    rows, vocab, stride = _matrix(logits, where)
+    dtype, device = _dtype(logits.dtype), logits.get_device()
+    i32, f32 = torch.int32, torch.float32
+    n = history_stride = 0
+    if history is not None:
+        if history.dtype is not i32:
+            raise LoomError(LOOM_ERR_SHAPE, f"{where}: history: int32 tokens are wanted")
+        if history.get_device() != device:
+            _foreign(where, history)
+        of, n, history_stride = _matrix(history, where)
+        if of != rows:
+            raise LoomError(LOOM_ERR_SHAPE, f"{where}: history: {rows} rows are wanted")
+    m = 0
+    if bias_ids is not None or bias_values is not None:
+        if bias_ids is None or bias_values is None:
+            raise LoomError(LOOM_ERR_NULL, f"{where}: bias_ids and bias_values come together")
+        m = bias_ids.shape[-1] if bias_ids.dim() == 2 else -1
+        if tuple(bias_ids.shape) != (rows, m) or bias_values.shape != bias_ids.shape:
+            raise LoomError(LOOM_ERR_SHAPE, f"{where}: bias_ids and bias_values: {rows} rows of one length are wanted")
+    masks = 0
+    if mask is not None:
+        masks, words = mask.shape if mask.dim() == 2 else (0, -1)
+        if words != (vocab + 31) // 32:
+            raise LoomError(LOOM_ERR_SHAPE, f"{where}: mask: rows of {(vocab + 31) // 32} words are wanted")
+    dr, r = _setting("repetition", repetition, f32, rows, device, where)
+    df, f = _setting("frequency", frequency, f32, rows, device, where)
+    dp, p = _setting("presence", presence, f32, rows, device, where)
+    if y is None:
+        y = _new(stream, logits, logits.dtype, rows, vocab)
+        y_stride = vocab
+    else:
+        y_stride = _like(where, "y", y, logits, device)
+    _launch(where, logits, stream, logits.data_ptr(), dtype, rows, vocab, stride, _ptr(history), n, history_stride,
+            _dense(where, lengths, rows, i32, device), _dense(where, prompts, rows, i32, device), dr, r, df, f, dp, p,
+            _dense(where, bias_ids, rows * m, i32, device), _dense(where, bias_values, rows * m, f32, device), m,
+            _dense(where, mask, 0, i32, device), masks, _dense(where, mask_rows, rows, i32, device), y.data_ptr(), y_stride,
+            _dense(where, error, 1, i32, device))
+    return y
+
+
+def _i4_operands(where, w_packed, scale_w, matrices, n_rows, k, group, x_packed, scale_x, x_rows, bias, work, device):
+    """Addresses of a 4-bit product's operands: (weights, scales, their type, tokens, their scales, bias)."""
+    groups = -(-k // group) if group > 0 else 0
+    rows = matrices * n_rows if work else 0          # (without work the operands may be empty)
+    f32, i32 = _torch.float32, _torch.int32
+    return (_dense(where, w_packed, rows * (k // 8), i32, device), _dense(where, scale_w, rows * groups, scale_w.dtype, device),
+            _dtype(scale_w.dtype), _packed(where, x_packed, x_rows * k if work else 0, device),
+            _dense(where, scale_x, x_rows if work else 0, f32, device), _dense(where, bias, rows, f32, device))
+
+
+def _product_output(where, stream, y, y_dtype, like, rows, n_rows, device):
+    """(y, its stride) of a product's rows."""
+    if y is None:
+        if rows < 0 or n_rows < 0:
+            raise LoomError(LOOM_ERR_SHAPE, where)
+        return _new(stream, like, _torch.float32 if y_dtype is None else y_dtype, rows, n_rows), n_rows
+    have, width, stride = _matrix(y, where)
+    if have < rows or width < n_rows:
+        raise LoomError(LOOM_ERR_SHAPE, f"{where}: y is smaller than {rows} x {n_rows}")
+    if y.get_device() != device:
+        _foreign(where, y)
+    return y, stride
+
+
+def loom_i4_matvec(w_packed, scale_w, n_rows: int, k: int, group: int, x_packed, scale_x, tokens: int, *, bias=None, y=None,
+                   y_dtype=None, stream=None):
+    """``y[tokens][n_rows]`` of type ``y_dtype`` (float32 by default) from 4-bit weights ``w_packed`` (int32, eight
+    signed nibbles a word, row after row) with a scale of ``scale_w`` (float32, float16 or bfloat16
+    ``[n_rows][ceil(k / group)]``) for each ``group`` of a row, and 8-bit tokens as of ``loom_quantize_tokens``."""
+    _torch or _lazy()
+    where = "loom_i4_matvec"
+    device = w_packed.get_device()
+    y, y_stride = _product_output(where, stream, y, y_dtype, w_packed, tokens, n_rows, device)
+    w, s, s_dtype, x, sx, b = _i4_operands(where, w_packed, scale_w, 1, n_rows, k, group, x_packed, scale_x, tokens, bias,
+                                           tokens > 0 and n_rows > 0, device)
+    _launch(where, w_packed, stream, w, s, s_dtype, n_rows, k, group, x, sx, tokens, b, y.data_ptr(), _dtype(y.dtype), y_stride)
+    return y
+
+
+def loom_i4_matvec_routed(w_packed, scale_w, experts: int, n_rows: int, k: int, group: int, x_packed, scale_x, ids, *,
+                          x_rows: int | None = None, bias=None, y=None, y_dtype=None, error=None, stream=None):
+    """The products of ``loom_i4_matvec`` with the matrix ``ids[t][j]`` of ``experts`` for each pair: ``y[tokens *
+    routes][n_rows]`` (zeros for a negative id), the payload of ``loom_routed_combine``.  ``ids`` int32
+    ``[tokens][routes]``; ``x_rows``: ``tokens`` (the default) where a token's routes share its row of
+    ``x_packed``, or ``tokens * routes``."""
+    torch = _torch or _lazy()
+    where = "loom_i4_matvec_routed"
+    if ids.dim() != 2:
+        raise LoomError(LOOM_ERR_SHAPE, f"{where}: ids: [tokens][routes] are wanted")
+    tokens, routes = ids.shape
+    device = w_packed.get_device()
+    if x_rows is None:
+        x_rows = tokens
+    y, y_stride = _product_output(where, stream, y, y_dtype, w_packed, tokens * routes, n_rows, device)
+    w, s, s_dtype, x, sx, b = _i4_operands(where, w_packed, scale_w, experts, n_rows, k, group, x_packed, scale_x, x_rows, bias,
+                                           tokens > 0 and routes > 0 and n_rows > 0, device)
+    _launch(where, w_packed, stream, w, s, s_dtype, experts, n_rows, k, group, x, sx, x_rows,
+            _dense(where, ids, tokens * routes, torch.int32, device), tokens, routes, b, y.data_ptr(), _dtype(y.dtype), y_stride,
+            _dense(where, error, 1, torch.int32, device))
+    return y
+
+
+_SCORES = {"softmax": LOOM_SCORE_SOFTMAX, "sigmoid": LOOM_SCORE_SIGMOID, LOOM_SCORE_SOFTMAX: LOOM_SCORE_SOFTMAX,
+           LOOM_SCORE_SIGMOID: LOOM_SCORE_SIGMOID}
+
+
+def _score(where: str, score) -> int:
+    code = _SCORES.get(score)
+    if code is None:
+        raise LoomError(LOOM_ERR_ARG, f"{where}: score {score!r}")
+    return code
+
+
+def loom_route_tokens(logits, top_k: int, *, score="softmax", bias=None, groups: int = 1, top_groups: int | None = None,
+                      group_best: int = 1, renormalise: bool = True, factor: float = 1.0, ids=None, weights=None, counts=None,
+                      stream=None):
+    """The ``top_k`` experts of each row of ``logits[tokens][experts]`` and their weights; returns ``(ids int32,
+    weights float32)``, ``[tokens][top_k]``, as ``loom_routed_combine`` takes them.  ``score`` "softmax" or
+    "sigmoid" (or LOOM_SCORE_*); ``bias`` float32 ``[experts]`` counts for the choice alone; of ``groups`` equal runs of experts the best
+    ``top_groups`` (by their ``group_best`` best experts) stay; ``counts`` int32 ``[experts]`` is added to."""
+    torch = _torch or _lazy()
+    where = "loom_route_tokens"
+    tokens, experts, stride = _matrix(logits, where)
+    dtype, device = _dtype(logits.dtype), logits.get_device()
+    if bias is not None:
+        _floats(where, experts, device, bias)
+    if ids is None:
+        ids = _new(stream, logits, torch.int32, tokens, max(top_k, 0))
+    if weights is None:
+        weights = _new(stream, logits, torch.float32, tokens, max(top_k, 0))
+    _launch(where, logits, stream, logits.data_ptr(), dtype, tokens, experts, stride, _ptr(bias), _score(where, score), groups,
+            groups if top_groups is None else top_groups, group_best, top_k, renormalise, factor,
+            _dense(where, ids, tokens * top_k, torch.int32, device), _dense(where, weights, tokens * top_k, torch.float32, device),
+            _dense(where, counts, experts, torch.int32, device))
+    return ids, weights
+
+
+def loom_route_tokens_backward(dweights, logits, ids, *, score="softmax", renormalise: bool = True, factor: float = 1.0,
+                               dlogits=None, error=None, stream=None):
+    """The gradient of ``loom_route_tokens``'s weights to its logits, the choice ``ids`` held fixed, from ``dweights``
+    float32 ``[tokens][top_k]``; returns ``dlogits`` of the logits' type."""
+    torch = _torch or _lazy()
+    where = "loom_route_tokens_backward"
+    tokens, experts, stride = _matrix(logits, where)
+    dtype, device = _dtype(logits.dtype), logits.get_device()
+    if ids.dim() != 2 or ids.shape[0] != tokens:
+        raise LoomError(LOOM_ERR_SHAPE, f"{where}: ids: {tokens} rows are wanted")
+    top_k = ids.shape[1]
+    if dlogits is None:
+        dlogits = _new(stream, logits, logits.dtype, tokens, experts)
+        dstride = experts
+    else:
+        dstride = _like(where, "dlogits", dlogits, logits, device)
+    _launch(where, logits, stream, _dense(where, dweights, tokens * top_k, torch.float32, device), logits.data_ptr(), dtype, tokens,
+            experts, stride, _dense(where, ids, tokens * top_k, torch.int32, device), _score(where, score), top_k, renormalise,
+            factor, dlogits.data_ptr(), dstride, _dense(where, error, 1, torch.int32, device))
+    return dlogits

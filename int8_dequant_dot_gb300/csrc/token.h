@@ -113,4 +113,71 @@ struct SampleParams {
 bool sample_geometry(int64_t rows, int32_t vocab, int64_t sms, loom_launch *out);
 cudaError_t launch_sample(const SampleParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream);
 
+// ---- products with 4-bit weights (i4_matvec.cu) ---------------------------------------
+constexpr int I4_MAX_PAIRS = 2048;       // (token, route) pairs of one launch of the experts' products
+constexpr int I4_MAX_EXPERTS = 1024;
+struct I4Params {
+    const int32_t *w;         // [experts][n][k / 8]
+    const void *scale_w;      // [experts][n][groups]
+    const int8_t *x;          // [x rows][k]
+    const float *scale_x;     // [x rows]
+    const float *bias;        // [experts][n] or NULL
+    const int32_t *ids;       // [pairs], or NULL: one matrix, a pair is a token
+    void *y;                  // [pairs][n], rows y_stride elements apart
+    int32_t *error;
+    int64_t y_stride;
+    int32_t pairs, pairs_per_x;   // rows of y; of them that share a row of x
+    int32_t experts, n, k, group, groups;
+    int32_t scale_dtype, y_dtype;
+    int32_t rows_per_cta;
+};
+void i4_geometry(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t experts, int64_t sms, loom_launch *out);
+cudaError_t launch_i4_matvec(const I4Params &p, const loom_launch &L, cudaStream_t stream);
+
+// ---- routing (token_route.cu) -----------------------------------------------------------
+constexpr int ROUTE_MAX_EXPERTS = 1024, ROUTE_MAX_TOP = 32;
+struct RouteParams {
+    const void *logits;
+    int64_t tokens, stride;
+    int32_t experts, score, groups, top_groups, group_best, top_k, renormalise;
+    float factor;
+    const float *bias;        // [experts] or NULL
+    int32_t *ids;             // [tokens][top_k]
+    float *weights;
+    int32_t *counts;          // [experts] or NULL
+};
+struct RouteGradParams {
+    const float *dweights;    // [tokens][top_k]
+    const void *logits;
+    int64_t tokens, stride, dstride;
+    const int32_t *ids;
+    int32_t experts, score, top_k, renormalise;
+    float factor;
+    void *dlogits;
+    int32_t *error;
+};
+bool route_geometry(int64_t tokens, int32_t experts, bool backward, int64_t sms, loom_launch *out);
+cudaError_t launch_route(const RouteParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream);
+cudaError_t launch_route_grad(const RouteGradParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream);
+
+// ---- adjustment of logits (token_logits.cu) -----------------------------------------------
+constexpr int32_t AL_MAX_VOCAB = 393216, AL_MAX_HISTORY = (1 << 20) - 1, AL_MAX_BIASES = 1024;
+struct AdjustParams {
+    const void *logits;
+    int64_t rows, stride, y_stride, history_stride;
+    int32_t vocab, history, biases, masks;
+    const int32_t *tokens;    // [rows][history] or NULL
+    const int32_t *lengths, *prompts;                              // [rows] or NULL
+    const float *d_repetition, *d_frequency, *d_presence;          // per row, or NULL for the values below
+    float repetition, frequency, presence;
+    const int32_t *bias_ids;  // [rows][biases] or NULL
+    const float *bias_values;
+    const int32_t *mask;      // [masks][ceil(vocab / 32)] or NULL
+    const int32_t *mask_rows; // [rows] or NULL
+    void *y;
+    int32_t *error;
+};
+bool adjust_geometry(int64_t rows, int32_t vocab, bool marks, int64_t sms, loom_launch *out);
+cudaError_t launch_adjust(const AdjustParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream);
+
 }  // namespace loom

@@ -105,6 +105,62 @@ int param_vec(int vec, const void *a, const void *b) { return misaligned(a, 16) 
 // Offsets of a single row do not depend on its stride.
 int64_t used_stride(int64_t rows, int64_t stride) { return rows > 1 ? stride : 0; }
 
+constexpr int64_t I4_MAX_K = 131064, I4_MAX_ROUTES = 64;
+
+loom_status i4_shape(int64_t n, int64_t k, int64_t group)
+{
+    return n < 0 || n > MAX_INT || k < 0 || k > I4_MAX_K || k % 8 || group < 32 || group > MAX_INT || (group & (group - 1))
+               ? LOOM_ERR_SHAPE : LOOM_OK;
+}
+
+// Pairs of one launch of the experts' products: whole tokens, as many as the kernel's lists hold.
+int64_t i4_part(int64_t pairs, int64_t routes)
+{
+    const int64_t most = routes > 0 ? I4_MAX_PAIRS / routes * routes : 0;
+    return pairs < most ? pairs : most;
+}
+
+loom_status i4_call(I4Params p, int64_t x_rows, int64_t y_stride, int32_t routes, cudaStream_t stream)
+{
+    if (i4_shape(p.n, p.k, p.group) != LOOM_OK || p.pairs < 0 || short_stride(p.pairs, y_stride, p.n))
+        return LOOM_ERR_SHAPE;
+    if (!known(p.scale_dtype) || !known(p.y_dtype))
+        return LOOM_ERR_ARG;
+    if (p.pairs == 0 || p.n == 0)
+        return LOOM_OK;
+    const bool data = p.experts > 0 && p.k > 0;         // (without experts every route is missing)
+    if (!p.y || (p.experts > 0 && !p.scale_x) || (data && (!p.w || !p.scale_w || !p.x)) || (routes > 0 && !p.ids))
+        return LOOM_ERR_NULL;
+    if (misaligned(p.w, 4) || misaligned(p.x, 4) || misaligned(p.scale_w, dtype_bytes(p.scale_dtype)) || misaligned(p.scale_x, 4) ||
+        misaligned(p.bias, 4) || misaligned(p.ids, 4) || misaligned(p.error, 4) || misaligned(p.y, dtype_bytes(p.y_dtype)))
+        return LOOM_ERR_ALIGN;
+    int64_t sms = 0;
+    const loom_status counted = sm_count(&sms);
+    if (counted != LOOM_OK)
+        return counted;
+    p.y_stride = used_stride(p.pairs, y_stride);
+    p.groups = (p.k + p.group - 1) / p.group;
+    const int64_t pairs = p.pairs, part = routes > 0 ? i4_part(pairs, routes) : pairs;
+    p.pairs_per_x = x_rows == pairs ? 1 : routes;
+    const I4Params whole = p;
+    for (int64_t at = 0; at < pairs; at += part) {
+        p.pairs = (int32_t)(pairs - at < part ? pairs - at : part);
+        if (routes > 0) {
+            p.ids = whole.ids + at;
+            p.x = whole.x + at / p.pairs_per_x * p.k;
+            p.scale_x = whole.scale_x + at / p.pairs_per_x;
+            p.y = static_cast<char *>(whole.y) + at * p.y_stride * dtype_bytes(p.y_dtype);
+        }
+        loom_launch L;
+        i4_geometry(p.pairs, p.n, p.k, p.group, routes > 0 ? p.experts : 0, sms, &L);
+        p.rows_per_cta = (int32_t)L.units_per_cta;
+        const cudaError_t e = launch_i4_matvec(p, L, stream);
+        if (e != cudaSuccess)
+            return LOOM_ERR_CUDA;
+    }
+    return LOOM_OK;
+}
+
 loom_status to_bytes(const void *d_x, int32_t dtype, int64_t rows, int32_t width, int64_t x_stride, const float *gain,
                      const float *bias, float eps, RowMode mode, int32_t *q, float *scale, int32_t *error, void *stream)
 {
@@ -206,6 +262,43 @@ extern "C" loom_status loom_token_launch_config(int32_t op, const int64_t *w, in
         if (counted != LOOM_OK)
             return counted;
         return sample_geometry(w[0], (int32_t)w[1], sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
+    }
+    case LOOM_OP_I4_MATVEC: {
+        if (n < 4 || opt(6, 0) < 0)
+            return LOOM_ERR_ARG;
+        const int64_t experts = opt(4, 0), routes = opt(5, 1);
+        if (w[0] < 0 || w[0] > MAX_INT || i4_shape(w[1], w[2], w[3]) != LOOM_OK || experts < 0 || experts > I4_MAX_EXPERTS ||
+            routes < 0 || routes > I4_MAX_ROUTES || w[0] * routes > MAX_INT)
+            return LOOM_ERR_SHAPE;
+        int64_t sms = opt(6, 0);
+        const loom_status counted = sms ? LOOM_OK : sm_count(&sms);
+        if (counted != LOOM_OK)
+            return counted;
+        i4_geometry(experts ? i4_part(w[0] * routes, routes) : w[0], w[1], w[2], w[3], experts, sms, out);
+        return LOOM_OK;
+    }
+    case LOOM_OP_ROUTE_TOKENS:
+    case LOOM_OP_ROUTE_TOKENS_BACKWARD: {
+        if (n < 2 || opt(2, 0) < 0)
+            return LOOM_ERR_ARG;
+        if (w[0] < 0 || w[0] > MAX_INT || w[1] < 1 || w[1] > ROUTE_MAX_EXPERTS)
+            return LOOM_ERR_SHAPE;
+        int64_t sms = opt(2, 0);
+        const loom_status counted = sms ? LOOM_OK : sm_count(&sms);
+        if (counted != LOOM_OK)
+            return counted;
+        return route_geometry(w[0], (int32_t)w[1], op == LOOM_OP_ROUTE_TOKENS_BACKWARD, sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
+    }
+    case LOOM_OP_ADJUST_LOGITS: {
+        if (n < 2 || opt(3, 0) < 0)
+            return LOOM_ERR_ARG;
+        if (w[0] < 0 || w[0] > MAX_INT || w[1] < 1 || w[1] > AL_MAX_VOCAB)
+            return LOOM_ERR_SHAPE;
+        int64_t sms = opt(3, 0);
+        const loom_status counted = sms ? LOOM_OK : sm_count(&sms);
+        if (counted != LOOM_OK)
+            return counted;
+        return adjust_geometry(w[0], (int32_t)w[1], opt(2, 1) != 0, sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
     }
     default: return LOOM_ERR_ARG;
     }
@@ -435,4 +528,201 @@ extern "C" loom_status loom_sample_tokens(const void *d_logits, int32_t dtype, i
     p.logprob = d_logprob;
     p.error = d_error;
     return of_cuda(launch_sample(p, dtype, L, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" loom_status loom_i4_matvec(const int32_t *d_w_packed, const void *d_scale_w, int32_t scale_dtype, int32_t n_rows,
+                                      int32_t k, int32_t group, const int32_t *d_x_packed, const float *d_scale_x,
+                                      int32_t tokens, const float *d_bias, void *d_y, int32_t y_dtype, int64_t y_stride,
+                                      void *stream)
+{
+    I4Params p = {};
+    p.w = d_w_packed;
+    p.scale_w = d_scale_w;
+    p.scale_dtype = scale_dtype;
+    p.x = reinterpret_cast<const int8_t *>(d_x_packed);
+    p.scale_x = d_scale_x;
+    p.bias = d_bias;
+    p.y = d_y;
+    p.y_dtype = y_dtype;
+    p.pairs = tokens;
+    p.experts = 1;
+    p.n = n_rows;
+    p.k = k;
+    p.group = group;
+    return i4_call(p, tokens, y_stride, 0, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" loom_status loom_i4_matvec_routed(const int32_t *d_w_packed, const void *d_scale_w, int32_t scale_dtype,
+                                             int32_t experts, int32_t n_rows, int32_t k, int32_t group,
+                                             const int32_t *d_x_packed, const float *d_scale_x, int64_t x_rows,
+                                             const int32_t *d_ids, int32_t tokens, int32_t routes, const float *d_bias,
+                                             void *d_y, int32_t y_dtype, int64_t y_stride, int32_t *d_error, void *stream)
+{
+    if (tokens < 0 || experts < 0 || experts > I4_MAX_EXPERTS || routes < 0 || routes > I4_MAX_ROUTES ||
+        (int64_t)tokens * routes > MAX_INT || (x_rows != tokens && x_rows != (int64_t)tokens * routes))
+        return LOOM_ERR_SHAPE;
+    I4Params p = {};
+    p.w = d_w_packed;
+    p.scale_w = d_scale_w;
+    p.scale_dtype = scale_dtype;
+    p.x = reinterpret_cast<const int8_t *>(d_x_packed);
+    p.scale_x = d_scale_x;
+    p.bias = d_bias;
+    p.ids = d_ids;
+    p.y = d_y;
+    p.y_dtype = y_dtype;
+    p.error = d_error;
+    p.pairs = tokens * routes;
+    p.experts = experts;
+    p.n = n_rows;
+    p.k = k;
+    p.group = group;
+    return i4_call(p, x_rows, y_stride, routes, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" loom_status loom_route_tokens(const void *d_logits, int32_t dtype, int64_t tokens, int32_t experts,
+                                         int64_t stride, const float *d_bias, int32_t score, int32_t groups,
+                                         int32_t top_groups, int32_t group_best, int32_t top_k, int32_t renormalise,
+                                         float factor, int32_t *d_ids, float *d_weights, int32_t *d_counts, void *stream)
+{
+    if (tokens < 0 || tokens > MAX_INT || experts < 1 || experts > ROUTE_MAX_EXPERTS || top_k < 1 || top_k > ROUTE_MAX_TOP ||
+        top_k > experts || groups < 1 || experts % groups || top_groups < 1 || top_groups > groups ||
+        short_stride(tokens, stride, experts))
+        return LOOM_ERR_SHAPE;
+    if (!known(dtype) || (score != LOOM_SCORE_SOFTMAX && score != LOOM_SCORE_SIGMOID) || (group_best != 1 && group_best != 2) ||
+        !std::isfinite(factor))
+        return LOOM_ERR_ARG;
+    if (tokens == 0)
+        return LOOM_OK;
+    if (!d_logits || !d_ids || !d_weights)
+        return LOOM_ERR_NULL;
+    if (misaligned(d_logits, dtype_bytes(dtype)) || misaligned(d_bias, 4) || misaligned(d_ids, 4) || misaligned(d_weights, 4) ||
+        misaligned(d_counts, 4))
+        return LOOM_ERR_ALIGN;
+    int64_t sms = 0;
+    const loom_status counted = sm_count(&sms);
+    if (counted != LOOM_OK)
+        return counted;
+    loom_launch L;
+    if (!route_geometry(tokens, experts, false, sms, &L))
+        return LOOM_ERR_SHAPE;
+    RouteParams p = {};
+    p.logits = d_logits;
+    p.tokens = tokens;
+    p.stride = used_stride(tokens, stride);
+    p.experts = experts;
+    p.score = score;
+    p.groups = top_groups < groups ? groups : 1;        // (all groups: none is left out)
+    p.top_groups = top_groups < groups ? top_groups : 1;
+    p.group_best = group_best;
+    p.top_k = top_k;
+    p.renormalise = renormalise != 0;
+    p.factor = factor;
+    p.bias = d_bias;
+    p.ids = d_ids;
+    p.weights = d_weights;
+    p.counts = d_counts;
+    return of_cuda(launch_route(p, dtype, L, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" loom_status loom_route_tokens_backward(const float *d_dweights, const void *d_logits, int32_t dtype,
+                                                  int64_t tokens, int32_t experts, int64_t stride, const int32_t *d_ids,
+                                                  int32_t score, int32_t top_k, int32_t renormalise, float factor,
+                                                  void *d_dlogits, int64_t dlogits_stride, int32_t *d_error, void *stream)
+{
+    if (tokens < 0 || tokens > MAX_INT || experts < 1 || experts > ROUTE_MAX_EXPERTS || top_k < 1 || top_k > ROUTE_MAX_TOP ||
+        top_k > experts || short_stride(tokens, stride, experts) || short_stride(tokens, dlogits_stride, experts))
+        return LOOM_ERR_SHAPE;
+    if (!known(dtype) || (score != LOOM_SCORE_SOFTMAX && score != LOOM_SCORE_SIGMOID) || !std::isfinite(factor))
+        return LOOM_ERR_ARG;
+    if (tokens == 0)
+        return LOOM_OK;
+    if (!d_dweights || !d_logits || !d_ids || !d_dlogits)
+        return LOOM_ERR_NULL;
+    if (misaligned(d_dweights, 4) || misaligned(d_logits, dtype_bytes(dtype)) || misaligned(d_ids, 4) ||
+        misaligned(d_dlogits, dtype_bytes(dtype)) || misaligned(d_error, 4))
+        return LOOM_ERR_ALIGN;
+    int64_t sms = 0;
+    const loom_status counted = sm_count(&sms);
+    if (counted != LOOM_OK)
+        return counted;
+    loom_launch L;
+    if (!route_geometry(tokens, experts, true, sms, &L))
+        return LOOM_ERR_SHAPE;
+    RouteGradParams p = {};
+    p.dweights = d_dweights;
+    p.logits = d_logits;
+    p.tokens = tokens;
+    p.stride = used_stride(tokens, stride);
+    p.dstride = used_stride(tokens, dlogits_stride);
+    p.ids = d_ids;
+    p.experts = experts;
+    p.score = score;
+    p.top_k = top_k;
+    p.renormalise = renormalise != 0;
+    p.factor = factor;
+    p.dlogits = d_dlogits;
+    p.error = d_error;
+    return of_cuda(launch_route_grad(p, dtype, L, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" loom_status loom_adjust_logits(const void *d_logits, int32_t dtype, int64_t rows, int32_t vocab, int64_t stride,
+                                          const int32_t *d_history, int32_t history, int64_t history_stride,
+                                          const int32_t *d_lengths, const int32_t *d_prompts, const float *d_repetition,
+                                          float repetition, const float *d_frequency, float frequency,
+                                          const float *d_presence, float presence, const int32_t *d_bias_ids,
+                                          const float *d_bias_values, int32_t biases, const int32_t *d_mask, int32_t masks,
+                                          const int32_t *d_mask_rows, void *d_y, int64_t y_stride, int32_t *d_error,
+                                          void *stream)
+{
+    if (rows < 0 || rows > MAX_INT || vocab < 1 || vocab > AL_MAX_VOCAB || short_stride(rows, stride, vocab) ||
+        short_stride(rows, y_stride, vocab) || history < 0 || history > AL_MAX_HISTORY || biases < 0 || biases > AL_MAX_BIASES ||
+        (d_history && short_stride(rows, history_stride, history)) || masks < 0 ||
+        (d_mask && !d_mask_rows && masks < rows && masks != 1))
+        return LOOM_ERR_SHAPE;
+    if (!known(dtype) || (!d_repetition && !(repetition > 0.0f && std::isfinite(repetition))) ||
+        (!d_frequency && !std::isfinite(frequency)) || (!d_presence && !std::isfinite(presence)))
+        return LOOM_ERR_ARG;
+    if (rows == 0)
+        return LOOM_OK;
+    if (!d_logits || !d_y || (biases > 0 && !d_bias_ids != !d_bias_values))
+        return LOOM_ERR_NULL;
+    if (misaligned(d_logits, dtype_bytes(dtype)) || misaligned(d_y, dtype_bytes(dtype)) || misaligned(d_history, 4) ||
+        misaligned(d_lengths, 4) || misaligned(d_prompts, 4) || misaligned(d_repetition, 4) || misaligned(d_frequency, 4) ||
+        misaligned(d_presence, 4) || misaligned(d_bias_ids, 4) || misaligned(d_bias_values, 4) || misaligned(d_mask, 4) ||
+        misaligned(d_mask_rows, 4) || misaligned(d_error, 4))
+        return LOOM_ERR_ALIGN;
+    int64_t sms = 0;
+    const loom_status counted = sm_count(&sms);
+    if (counted != LOOM_OK)
+        return counted;
+    AdjustParams p = {};
+    p.logits = d_logits;
+    p.rows = rows;
+    p.stride = used_stride(rows, stride);
+    p.y_stride = used_stride(rows, y_stride);
+    p.history_stride = used_stride(rows, history_stride);
+    p.vocab = vocab;
+    p.tokens = history > 0 ? d_history : nullptr;
+    p.history = p.tokens ? history : 0;
+    p.lengths = d_lengths;
+    p.prompts = d_prompts;
+    p.d_repetition = d_repetition;
+    p.d_frequency = d_frequency;
+    p.d_presence = d_presence;
+    p.repetition = repetition;
+    p.frequency = frequency;
+    p.presence = presence;
+    p.bias_ids = biases > 0 ? d_bias_ids : nullptr;
+    p.bias_values = d_bias_values;
+    p.biases = p.bias_ids ? biases : 0;
+    p.mask = masks > 0 ? d_mask : nullptr;
+    p.mask_rows = d_mask_rows;
+    p.masks = masks;
+    p.y = d_y;
+    p.error = d_error;
+    loom_launch L;
+    if (!adjust_geometry(rows, vocab, p.tokens || p.bias_ids, sms, &L))
+        return LOOM_ERR_SHAPE;
+    return of_cuda(launch_adjust(p, dtype, L, static_cast<cudaStream_t>(stream)));
 }
