@@ -129,7 +129,6 @@ struct I4Params {
     int32_t pairs, pairs_per_x;   // rows of y; of them that share a row of x
     int32_t experts, n, k, group, groups;
     int32_t scale_dtype, y_dtype;
-    int32_t rows_per_cta;
 };
 void i4_geometry(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t experts, int64_t sms, loom_launch *out);
 cudaError_t launch_i4_matvec(const I4Params &p, const loom_launch &L, cudaStream_t stream);

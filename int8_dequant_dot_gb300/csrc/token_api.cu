@@ -152,8 +152,7 @@ loom_status i4_call(I4Params p, int64_t x_rows, int64_t y_stride, int32_t routes
             p.y = static_cast<char *>(whole.y) + at * p.y_stride * dtype_bytes(p.y_dtype);
         }
         loom_launch L;
-        i4_geometry(p.pairs, p.n, p.k, p.group, routes > 0 ? p.experts : 0, sms, &L);
-        p.rows_per_cta = (int32_t)L.units_per_cta;
+        i4_geometry(p.pairs, p.n, p.k, p.group, routes > 0 ? (p.experts > 0 ? p.experts : 1) : 0, sms, &L);
         const cudaError_t e = launch_i4_matvec(p, L, stream);
         if (e != cudaSuccess)
             return LOOM_ERR_CUDA;
