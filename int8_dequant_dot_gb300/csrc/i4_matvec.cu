@@ -27,12 +27,12 @@
 namespace loom {
 namespace {
 
-constexpr int I4_WARPS = 8, I4_THREADS = 32 * I4_WARPS;
-constexpr int I4_ROWS = 64, I4_CHUNK = 256;                      // of a stage: rows, k
+constexpr int I4_ROWS = 64, I4_CHUNK = 128;                      // of a stage: rows, k
 constexpr int I4_STAGE = I4_ROWS * I4_CHUNK / 2;                 // bytes
-constexpr int I4_HALF = 128;                                     // k between flushes of whole sums
 
 struct I4Shape {          // of a launch
+    int tokens;           // that it is built for: 1 or 2 (dp4a), 8, 16 or 32 (MMA columns)
+    int warps;
     int team;             // warps that share out k
     int depth;            // stages of a warp's ring, 2 or 3
     int vec16;            // rows of W start on 16 bytes
@@ -58,10 +58,11 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4])
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ uint32_t half2_fma(uint32_t a, uint32_t b, uint32_t c)
@@ -86,18 +87,6 @@ __device__ __forceinline__ void token_operands(uint32_t (&b)[4], uint2 x)
 __device__ __forceinline__ uint32_t low_nibbles(uint32_t w) { return (w & 0x000f000fu) ^ 0x00080008u; }
 __device__ __forceinline__ uint32_t high_nibbles(uint32_t w) { return (w & 0x00f000f0u) ^ 0x00800080u; }
 
-// A scale's bits (read ahead), and its value times 2^24.
-__device__ __forceinline__ uint32_t scale_bits(const void *s, int32_t dtype, int64_t at)
-{
-    return dtype == LOOM_F32 ? __ldg(static_cast<const uint32_t *>(s) + at) : (uint32_t)__ldg(static_cast<const unsigned short *>(s) + at);
-}
-__device__ __forceinline__ float scale_value(uint32_t bits, int32_t dtype)
-{
-    const float v = dtype == LOOM_F32 ? __uint_as_float(bits) : dtype == LOOM_F16 ? __half2float(__ushort_as_half((unsigned short)bits))
-                                                                                  : __uint_as_float(bits << 16);
-    return v * 16777216.0f;
-}
-
 // ---- what a CTA works on: runs of rows of one matrix, each with the pairs that want it ------------
 struct Lists {                 // in shared memory, of the experts' products
     uint16_t *expert, *first;  // of each expert that some pair names (first: also behind the last): its first pair
@@ -111,59 +100,110 @@ struct Unit {
     int list, count;           // pairs: places in the list (or numbers)
 };
 
+// A CTA's rows, counted over the matrices that are wanted, as runs of rows of one matrix.
+struct Runs {
+    int64_t left;              // rows from the present run's first on
+    int matrix, row, rows;     // the present run: its matrix (of the wanted ones), first row and rows
+    int first, pairs;          // its pairs
+};
+
+__device__ __forceinline__ void set_run(Runs &w, const I4Params &p, const Lists &l)
+{
+    w.rows = (int)min((int64_t)(p.n - w.row), w.left);
+    if (w.left <= 0)
+        return;
+    w.first = p.ids ? l.first[w.matrix] : 0;
+    w.pairs = p.ids ? l.first[w.matrix + 1] - w.first : p.pairs;
+}
+
+__device__ __forceinline__ Runs first_run(const I4Params &p, const Lists &l)
+{
+    const int64_t rows = (p.ids ? (int64_t)l.experts : 1) * p.n;
+    const int64_t begin = rows * blockIdx.x / gridDim.x;
+    Runs w;
+    w.left = rows * (blockIdx.x + 1) / gridDim.x - begin;
+    w.matrix = (int)(begin / p.n);
+    w.row = (int)(begin - (int64_t)w.matrix * p.n);
+    set_run(w, p, l);
+    return w;
+}
+
+__device__ __forceinline__ void next_run(Runs &w, const I4Params &p, const Lists &l)
+{
+    w.left -= w.rows;
+    ++w.matrix;
+    w.row = 0;
+    set_run(w, p, l);
+}
+
+// The units of a team: up to 64 rows with the pairs of one pass, in turn.
 struct Walk {
-    int64_t begin, end;        // rows of the CTA, counted over the matrices that are wanted
-    int64_t at;                // begin of the present run
-    int q;                     // unit in it
+    Runs run;
+    int q, units;              // unit of the run, of so many: its parts, each `passes` times
+    int passes, part_rows;
     int columns, teams;
 };
+
+__device__ __forceinline__ void set_units(Walk &w)
+{
+    if (w.run.left <= 0)
+        return;
+    w.passes = (w.run.pairs + w.columns - 1) / w.columns;
+    // equal parts of up to 64 rows, as many for each team, unless they would have under 16
+    const int least = (w.run.rows + I4_ROWS - 1) / I4_ROWS;
+    const int parts = min((least + w.teams - 1) / w.teams * w.teams, (w.run.rows + 15) / 16);
+    w.part_rows = (w.run.rows + parts - 1) / parts;
+    w.units = (w.run.rows + w.part_rows - 1) / w.part_rows * w.passes;
+}
 
 // The unit that the walk stands on; false past the last.
 __device__ __forceinline__ bool unit_of(Walk &w, const I4Params &p, const Lists &l, Unit &u)
 {
-    while (w.at < w.end) {
-        const int m = (int)(w.at / p.n), row0 = (int)(w.at % p.n);
-        const int rows = (int)min((int64_t)(p.n - row0), w.end - w.at);
-        const int first = p.ids ? l.first[m] : 0, pairs = p.ids ? l.first[m + 1] - first : p.pairs;
-        const int passes = (pairs + w.columns - 1) / w.columns;
-        const int parts = max((rows + I4_ROWS - 1) / I4_ROWS, min(w.teams, (rows + 15) / 16));
-        if (w.q < parts * passes) {
-            const int part = w.q / passes, pass = w.q % passes;
-            const int r0 = (int)((int64_t)rows * part / parts), r1 = (int)((int64_t)rows * (part + 1) / parts);
-            u.row = row0 + r0;
-            u.rows = r1 - r0;
-            u.matrix_row = (int64_t)(p.ids ? l.expert[m] : 0) * p.n + u.row;
-            u.list = first + pass * w.columns;
-            u.count = min(w.columns, pairs - pass * w.columns);
+    while (w.run.left > 0) {
+        if (w.q < w.units) {
+            const int part = w.passes == 1 ? w.q : w.q / w.passes, pass = w.q - part * w.passes;
+            const int r0 = part * w.part_rows;
+            u.row = w.run.row + r0;
+            u.rows = min(w.part_rows, w.run.rows - r0);
+            u.matrix_row = (int64_t)(p.ids ? l.expert[w.run.matrix] : 0) * p.n + u.row;
+            u.list = w.run.first + pass * w.columns;
+            u.count = min(w.columns, w.run.pairs - pass * w.columns);
             return true;
         }
-        w.q -= parts * passes;
-        w.at += rows;
+        w.q -= w.units;
+        next_run(w.run, p, l);
+        set_units(w);
     }
     return false;
 }
 
-// Sorts the pairs by expert.  counts: [experts] words of scratch.
-__device__ Lists make_lists(const I4Params &p, uint32_t *scratch)
+// The row of X of a pair.
+__device__ __forceinline__ int x_row(const I4Params &p, int pair)
 {
-    __shared__ uint32_t warp_sums[I4_WARPS], missing;
+    return p.pairs_per_x == 1 ? pair : (int)((unsigned)pair / (unsigned)p.pairs_per_x);
+}
+
+// Sorts the pairs by expert.  counts: [experts] words of scratch.
+template <int THREADS> __device__ Lists make_lists(const I4Params &p, uint32_t *scratch)
+{
+    __shared__ uint32_t warp_sums[THREADS / 32], missing;
     Lists l;
     uint32_t *counts = scratch;
     l.expert = reinterpret_cast<uint16_t *>(counts + p.experts);
     l.first = l.expert + p.experts;
     l.pair = l.first + p.experts + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < p.experts; e += I4_THREADS)
+    for (int e = tid; e < p.experts; e += THREADS)
         counts[e] = 0;
     if (tid == 0)
         missing = 0;
     __syncthreads();
-    constexpr int MOST = I4_MAX_PAIRS / I4_THREADS;
+    constexpr int MOST = I4_MAX_PAIRS / THREADS;
     int expert[MOST];
     uint32_t rank[MOST];
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
-        const int at = tid + i * I4_THREADS;
+        const int at = tid + i * THREADS;
         expert[i] = -1;
         rank[i] = 0;
         if (at < p.pairs) {
@@ -178,7 +218,7 @@ __device__ Lists make_lists(const I4Params &p, uint32_t *scratch)
     }
     __syncthreads();
     // pairs in the low half, experts that have some in the high half
-    constexpr int PER = I4_MAX_EXPERTS / I4_THREADS;
+    constexpr int PER = I4_MAX_EXPERTS / THREADS;
     uint32_t own[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -198,7 +238,7 @@ __device__ Lists make_lists(const I4Params &p, uint32_t *scratch)
     __syncthreads();
     uint32_t before = run - sum, all = 0;
 #pragma unroll
-    for (int i = 0; i < I4_WARPS; ++i) {
+    for (int i = 0; i < THREADS / 32; ++i) {
         before += i < warp ? warp_sums[i] : 0u;
         all += warp_sums[i];
     }
@@ -221,7 +261,7 @@ __device__ Lists make_lists(const I4Params &p, uint32_t *scratch)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
-        const int at = tid + i * I4_THREADS;
+        const int at = tid + i * THREADS;
         if (at < p.pairs)
             l.pair[(expert[i] >= 0 ? counts[expert[i]] : (uint32_t)l.pairs) + rank[i]] = (uint16_t)at;
     }
@@ -229,60 +269,62 @@ __device__ Lists make_lists(const I4Params &p, uint32_t *scratch)
     return l;
 }
 
-// The copies of one stage: 128 bytes of up to 64 rows from k = chunk * 256 on.  What lies past the
-// rows or past k is not copied: it meets zeros, or sums that are thrown away.
-__device__ __forceinline__ void copy_stage(const I4Params &p, const I4Shape &s, const Unit &u, int chunk, uint32_t dst, int lane)
+// Missing routes: rows of zeros.
+__device__ __forceinline__ void clear_missing(const I4Params &p, const Lists &l)
 {
-    const int64_t row_bytes = p.k / 2;
-    const char *src = reinterpret_cast<const char *>(p.w) + u.matrix_row * row_bytes + chunk * (I4_CHUNK / 2);
-    const int left = (int)min((int64_t)(I4_CHUNK / 2), row_bytes - (int64_t)chunk * (I4_CHUNK / 2));
-    if (s.vec16) {
-        const int piece = lane & 7, r0 = lane >> 3;
-        if (16 * piece < left) {
-#pragma unroll
-            for (int i = 0; i < I4_ROWS / 4; ++i) {
-                const int r = r0 + 4 * i;
-                if (r < u.rows)
-                    copy_async16(dst + r * 128 + ((piece ^ (r & 7)) << 4), src + r * row_bytes + 16 * piece);
-            }
-        }
-    } else if (4 * lane < left) {
-#pragma unroll 8
-        for (int r = 0; r < u.rows; ++r)
-            copy_async4(dst + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3), src + r * row_bytes + 4 * lane);
+    for (int i = l.pairs; i < p.pairs; ++i) {
+        const int64_t at = l.pair[i] * p.y_stride;
+        for (int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < p.n; r += (int64_t)gridDim.x * blockDim.x)
+            dev::store_as(p.y, p.y_dtype, at + r, 0.0f);
     }
 }
 
-// NT: MMA columns / 8; FL: MMA steps of 32 k between flushes (a group's, 4 at most).
-template <int NT, int FL> __global__ void __launch_bounds__(I4_THREADS, 1) i4_matvec_kernel(const I4Params p, const I4Shape s)
+// The copies of one stage: 64 bytes of up to 64 rows from k = chunk * 128 on.  What lies past the
+// rows or past k is not copied: it meets zeros, or sums that are thrown away.
+__device__ __forceinline__ void copy_stage(const I4Params &p, const I4Shape &s, const Unit &u, int chunk, uint32_t dst, int lane)
+{
+    const int row_bytes = p.k / 2, left = row_bytes - chunk * (I4_CHUNK / 2);
+    const char *src = reinterpret_cast<const char *>(p.w) + u.matrix_row * row_bytes + chunk * (I4_CHUNK / 2);
+    if (s.vec16) {
+        const int piece = lane & 3, r0 = lane >> 2;
+        if (16 * piece < left) {
+            const char *q = src + r0 * (int64_t)row_bytes + 16 * piece;
+            const int64_t step = 8 * (int64_t)row_bytes;
+            const uint32_t to = dst + r0 * 64 + ((piece ^ ((r0 >> 1) & 3)) << 4);
+#pragma unroll
+            for (int i = 0; i < I4_ROWS / 8; ++i)
+                if (u.rows == I4_ROWS || r0 + 8 * i < u.rows)
+                    copy_async16(to + 512 * i, q + i * step);
+        }
+    } else {
+        const int word = lane & 15, r0 = lane >> 4;
+        if (4 * word < left)
+#pragma unroll 8
+            for (int r = r0; r < u.rows; r += 2)
+                copy_async4(dst + r * 64 + (((word >> 2) ^ ((r >> 1) & 3)) << 4) + 4 * (word & 3), src + r * (int64_t)row_bytes + 4 * word);
+    }
+}
+
+// NT: MMA columns / 8; FL: steps of 32 k between flushes (a group's, 4 at most); PAIR: 16-row tiles whose MMAs overlap.
+template <int NT, int FL, int WARPS, int PAIR>
+__global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params p, const I4Shape s)
 {
     extern __shared__ __align__(128) unsigned char i4_shared[];
-    constexpr int STEPS = I4_HALF / 32, FLUSHES = STEPS / FL;        // of half a stage
-    constexpr int SP = 2 * FLUSHES;                                  // scales of a row in a stage
-    constexpr int PAIR = NT == 1 ? 4 : NT == 2 ? 2 : 1;              // 16-row tiles whose MMAs overlap
+    constexpr int STEPS = I4_CHUNK / 32, SP = STEPS / FL;            // SP: flushes, and scales of a row, in a stage
     constexpr int SUM_STRIDE = 8 * NT + 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tig = lane & 3;
     dev::follow_previous_kernel();
 
     Lists l = {};
-    Walk walk;
-    walk.teams = I4_WARPS / s.team;
-    walk.columns = 8 * NT;
     if (p.ids) {
-        l = make_lists(p, reinterpret_cast<uint32_t *>(i4_shared + s.lists));
-        const int64_t rows = (int64_t)l.experts * p.n;
-        walk.begin = rows * blockIdx.x / gridDim.x;
-        walk.end = rows * (blockIdx.x + 1) / gridDim.x;
-        for (int i = l.pairs; i < p.pairs; ++i) {                    // missing routes: rows of zeros
-            const int64_t at = l.pair[i] * p.y_stride;
-            for (int64_t r = (int64_t)blockIdx.x * I4_THREADS + threadIdx.x; r < p.n; r += (int64_t)gridDim.x * I4_THREADS)
-                dev::store_as(p.y, p.y_dtype, at + r, 0.0f);
-        }
-    } else {
-        walk.begin = (int64_t)p.n * blockIdx.x / gridDim.x;
-        walk.end = (int64_t)p.n * (blockIdx.x + 1) / gridDim.x;
+        l = make_lists<32 * WARPS>(p, reinterpret_cast<uint32_t *>(i4_shared + s.lists));
+        clear_missing(p, l);
     }
-    walk.at = walk.begin;
+    Walk walk;
+    walk.run = first_run(p, l);
+    walk.teams = WARPS / s.team;
+    walk.columns = 8 * NT;
+    set_units(walk);
     walk.q = warp / s.team;
     const int part = warp % s.team;
     const int chunks = (p.k + I4_CHUNK - 1) / I4_CHUNK;
@@ -291,23 +333,22 @@ template <int NT, int FL> __global__ void __launch_bounds__(I4_THREADS, 1) i4_ma
     const uint32_t ring = dev::smem_u32(i4_shared) + warp * s.depth * I4_STAGE;
     float *scales = reinterpret_cast<float *>(i4_shared + s.scales) + warp * I4_ROWS * SP;
     float *sums = reinterpret_cast<float *>(i4_shared + s.sums);
+    // ldmatrix: lane's row of a tile, and the piece of 16 bytes that it points at in the first two steps
+    const uint32_t place = (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
 
     // the copies run `depth - 1` stages ahead of the products
     Walk ahead = walk;
     Unit next;
-    bool more = unit_of(ahead, p, l, next);
+    bool more = unit_of(ahead, p, l, next) && c0 < c1;
     int next_chunk = c0, next_slot = 0;
     const auto copy_next = [&]() {
-        while (more && next_chunk >= c1) {          // (no chunk at all: k = 0)
-            ahead.q += ahead.teams;
-            more = unit_of(ahead, p, l, next);
-            next_chunk = c0;
-            if (c0 >= c1)
-                more = false;
-        }
         if (more) {
             copy_stage(p, s, next, next_chunk, ring + next_slot * I4_STAGE, lane);
-            ++next_chunk;
+            if (++next_chunk == c1) {
+                ahead.q += ahead.teams;
+                more = unit_of(ahead, p, l, next);
+                next_chunk = c0;
+            }
         }
         copies_commit();
         next_slot = next_slot + 1 == s.depth ? 0 : next_slot + 1;
@@ -315,7 +356,7 @@ template <int NT, int FL> __global__ void __launch_bounds__(I4_THREADS, 1) i4_ma
     for (int i = 1; i < s.depth; ++i)
         copy_next();
 
-    int slot = 0;
+    int slot = 0, turn = 0;
     Unit u;
     for (; unit_of(walk, p, l, u); walk.q += walk.teams) {
         float acc[4][NT][4];
@@ -326,43 +367,56 @@ template <int NT, int FL> __global__ void __launch_bounds__(I4_THREADS, 1) i4_ma
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     acc[t][j][i] = 0.0f;
-        const int8_t *xp[NT];
+        const int8_t *xp[NT];                // columns that no pair has take the first one's: their sums are not used
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int col = 8 * j + g;
-            xp[j] = nullptr;
-            if (col < u.count) {
-                const int64_t row = p.ids ? l.pair[u.list + col] / p.pairs_per_x : u.list + col;
-                xp[j] = p.x + row * p.k + 8 * tig;
-            }
+            const int col = 8 * j + g < u.count ? 8 * j + g : 0;
+            xp[j] = p.x + (int64_t)x_row(p, p.ids ? l.pair[u.list + col] : u.list + col) * p.k + 8 * tig;
         }
         uint2 raw[STEPS][NT];
-        const auto load_tokens = [&](int k0) {
+        const auto load_tokens = [&](int chunk) {
+            const int k0 = chunk * I4_CHUNK;
+            if (s.x8 && k0 + I4_CHUNK <= p.k) {
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i)
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    raw[i][j] = make_uint2(0, 0);
-                    if (xp[j] && k0 + 32 * i + 8 * tig < p.k) {
+                    for (int i = 0; i < STEPS; ++i)
+                        raw[i][j] = __ldg(reinterpret_cast<const uint2 *>(xp[j] + k0 + 32 * i));
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < STEPS; ++i) {
                         const int8_t *at = xp[j] + k0 + 32 * i;
-                        if (s.x8)
-                            raw[i][j] = __ldg(reinterpret_cast<const uint2 *>(at));
-                        else
+                        raw[i][j] = make_uint2(0, 0);
+                        if (k0 + 32 * i + 8 * tig < p.k)
                             raw[i][j] = make_uint2(__ldg(reinterpret_cast<const uint32_t *>(at)), __ldg(reinterpret_cast<const uint32_t *>(at) + 1));
                     }
-                }
+            }
         };
+        // a stage's scales: lane's are those of elements lane + 32 i of [64 rows][SP]
+        const int64_t scale0 = u.matrix_row * p.groups;
+        int scale_row[2 * SP];
+#pragma unroll
+        for (int i = 0; i < 2 * SP; ++i)
+            scale_row[i] = min((lane + 32 * i) / SP, u.rows - 1) * p.groups;
         uint32_t scale[2 * SP];
         const auto load_scales = [&](int chunk) {
+            const int group = min((chunk * I4_CHUNK + lane % SP * 32 * FL) >> s.log_group, p.groups - 1);
+            if (p.scale_dtype == LOOM_F32) {
+                const uint32_t *at = static_cast<const uint32_t *>(p.scale_w) + scale0 + group;
 #pragma unroll
-            for (int i = 0; i < 2 * SP; ++i) {
-                const int at = lane + 32 * i, row = min(at / SP, u.rows - 1);
-                const int group = min((chunk * I4_CHUNK + at % SP * 32 * FL) >> s.log_group, p.groups - 1);
-                scale[i] = scale_bits(p.scale_w, p.scale_dtype, (u.matrix_row + row) * p.groups + group);
+                for (int i = 0; i < 2 * SP; ++i)
+                    scale[i] = __ldg(at + scale_row[i]);
+            } else {
+                const unsigned short *at = static_cast<const unsigned short *>(p.scale_w) + scale0 + group;
+#pragma unroll
+                for (int i = 0; i < 2 * SP; ++i)
+                    scale[i] = __ldg(at + scale_row[i]);
             }
         };
         if (c0 < c1) {
-            load_tokens(c0 * I4_CHUNK);
+            load_tokens(c0);
             load_scales(c0);
         }
         for (int c = c0; c < c1; ++c) {
@@ -372,151 +426,386 @@ template <int NT, int FL> __global__ void __launch_bounds__(I4_THREADS, 1) i4_ma
                 copies_wait<0>();
             __syncwarp();                    // the stage is there, and the last one read by all lanes
             copy_next();
+            // (the whole sums are in 2^-24)
+            if (p.scale_dtype == LOOM_F16) {
 #pragma unroll
-            for (int i = 0; i < 2 * SP; ++i)
-                scales[lane + 32 * i] = scale_value(scale[i], p.scale_dtype);
-            if (c + 1 < c1)
-                load_scales(c + 1);
-            __syncwarp();
-            const uint32_t stage = ring + slot * I4_STAGE;
-            slot = slot + 1 == s.depth ? 0 : slot + 1;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const int k0 = c * I4_CHUNK + h * I4_HALF;
-                if (k0 >= p.k)
-                    break;
-                uint32_t b[STEPS][NT][4];
-                float start[FLUSHES][NT][2];
+                for (int i = 0; i < 2 * SP; ++i)
+                    scales[lane + 32 * i] = __half2float(__ushort_as_half((unsigned short)scale[i])) * 16777216.0f;
+            } else {
+                const int up = p.scale_dtype == LOOM_BF16 ? 16 : 0;
 #pragma unroll
-                for (int f = 0; f < FLUSHES; ++f)
+                for (int i = 0; i < 2 * SP; ++i)
+                    scales[lane + 32 * i] = __uint_as_float(scale[i] << up) * 16777216.0f;
+            }
+            uint32_t b[STEPS][NT][4];
+            float start[SP][NT][4];
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        int sum = 0;
+            for (int f = 0; f < SP; ++f)
 #pragma unroll
-                        for (int i = f * FL; i < (f + 1) * FL; ++i) {
-                            token_operands(b[i][j], raw[i][j]);
-                            sum = __dp4a((int)raw[i][j].x, 0x01010101, __dp4a((int)raw[i][j].y, 0x01010101, sum));
-                        }
-                        sum += __shfl_xor_sync(dev::FULL_MASK, sum, 1);
-                        sum += __shfl_xor_sync(dev::FULL_MASK, sum, 2);
-                        start[f][j][0] = (float)__shfl_sync(dev::FULL_MASK, sum, 8 * tig) * -4.76837158203125e-07f;      // -8 * 2^-24
-                        start[f][j][1] = (float)__shfl_sync(dev::FULL_MASK, sum, 8 * tig + 4) * -4.76837158203125e-07f;
+                for (int j = 0; j < NT; ++j) {
+                    int sum = 0;
+#pragma unroll
+                    for (int i = f * FL; i < (f + 1) * FL; ++i) {
+                        token_operands(b[i][j], raw[i][j]);
+                        sum = __dp4a((int)raw[i][j].x, 0x01010101, __dp4a((int)raw[i][j].y, 0x01010101, sum));
                     }
-                if (k0 + I4_HALF < min(p.k, c1 * I4_CHUNK))
-                    load_tokens(k0 + I4_HALF);
+                    sum += __shfl_xor_sync(dev::FULL_MASK, sum, 1);
+                    sum += __shfl_xor_sync(dev::FULL_MASK, sum, 2);
+                    const float of = (float)sum * -4.76837158203125e-07f;      // -8 * 2^-24
+                    start[f][j][0] = start[f][j][2] = __shfl_sync(dev::FULL_MASK, of, 8 * tig);
+                    start[f][j][1] = start[f][j][3] = __shfl_sync(dev::FULL_MASK, of, 8 * tig + 4);
+                }
+            if (c + 1 < c1) {
+                load_tokens(c + 1);
+                load_scales(c + 1);
+            }
+            __syncwarp();
+            const uint32_t stage = ring + slot * I4_STAGE + place;
+            slot = slot + 1 == s.depth ? 0 : slot + 1;
 #pragma unroll
-                for (int t0 = 0; t0 < 4; t0 += PAIR) {
-                    if (16 * t0 >= u.rows)
-                        break;
-                    uint32_t w[PAIR][4];
+            for (int t0 = 0; t0 < 4; t0 += PAIR) {
+                if (16 * t0 >= u.rows)
+                    break;
+                uint32_t w[PAIR][4];
 #pragma unroll
-                    for (int f = 0; f < FLUSHES; ++f) {
-                        float sum[PAIR][NT][4];
+                for (int f = 0; f < SP; ++f) {
+                    float sum[PAIR][NT][4];
 #pragma unroll
-                        for (int t = 0; t < PAIR; ++t)
-#pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                sum[t][j][0] = sum[t][j][2] = start[f][j][0];
-                                sum[t][j][1] = sum[t][j][3] = start[f][j][1];
-                            }
-#pragma unroll
-                        for (int i = f * FL; i < (f + 1) * FL; ++i)
-#pragma unroll
-                            for (int t = 0; t < PAIR; ++t) {
-                                if (i % 2 == 0) {       // two steps (16-byte pieces) of 16 rows at a time
-                                    const int row = 16 * (t0 + t) + (lane & 15), piece = 4 * h + i + (lane >> 4);
-                                    load_matrices(w[t], stage + row * 128 + ((piece ^ (row & 7)) << 4));
-                                }
-                                const uint32_t w0 = w[t][2 * (i % 2)], w1 = w[t][2 * (i % 2) + 1];
-                                const uint32_t a0 = low_nibbles(w0), a1 = low_nibbles(w1), a2 = high_nibbles(w0), a3 = high_nibbles(w1);
-                                const uint32_t e0 = low_nibbles(w0 >> 8), e1 = low_nibbles(w1 >> 8), e2 = high_nibbles(w0 >> 8),
-                                               e3 = high_nibbles(w1 >> 8);
-#pragma unroll
-                                for (int j = 0; j < NT; ++j) {
-                                    mma(sum[t][j], a0, a1, a2, a3, b[i][j][0], b[i][j][1]);
-                                    mma(sum[t][j], e0, e1, e2, e3, b[i][j][2], b[i][j][3]);
-                                }
-                            }
+                    for (int i = f * FL; i < (f + 1) * FL; ++i)
 #pragma unroll
                         for (int t = 0; t < PAIR; ++t) {
-                            const int at = (16 * (t0 + t) + g) * SP + h * FLUSHES + f;
-                            const float s0 = scales[at], s1 = scales[at + 8 * SP];
+                            if (i % 2 == 0)         // two steps (16-byte pieces) of 16 rows at a time
+                                load_matrices(w[t], (stage ^ (i << 4)) + (t0 + t) * 1024);
+                            const uint32_t w0 = w[t][2 * (i % 2)], w1 = w[t][2 * (i % 2) + 1];
+                            const uint32_t a0 = low_nibbles(w0), a1 = low_nibbles(w1), a2 = high_nibbles(w0), a3 = high_nibbles(w1);
+                            const uint32_t e0 = low_nibbles(w0 >> 8), e1 = low_nibbles(w1 >> 8), e2 = high_nibbles(w0 >> 8),
+                                           e3 = high_nibbles(w1 >> 8);
 #pragma unroll
                             for (int j = 0; j < NT; ++j) {
-                                acc[t0 + t][j][0] = fmaf(s0, sum[t][j][0], acc[t0 + t][j][0]);
-                                acc[t0 + t][j][1] = fmaf(s0, sum[t][j][1], acc[t0 + t][j][1]);
-                                acc[t0 + t][j][2] = fmaf(s1, sum[t][j][2], acc[t0 + t][j][2]);
-                                acc[t0 + t][j][3] = fmaf(s1, sum[t][j][3], acc[t0 + t][j][3]);
+                                if (i == f * FL)
+                                    mma(sum[t][j], a0, a1, a2, a3, b[i][j][0], b[i][j][1], start[f][j]);
+                                else
+                                    mma(sum[t][j], a0, a1, a2, a3, b[i][j][0], b[i][j][1], sum[t][j]);
+                                mma(sum[t][j], e0, e1, e2, e3, b[i][j][2], b[i][j][3], sum[t][j]);
                             }
+                        }
+#pragma unroll
+                    for (int t = 0; t < PAIR; ++t) {
+                        const float *at = scales + (16 * (t0 + t) + g) * SP + f;
+                        const float s0 = at[0], s1 = at[8 * SP];
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            acc[t0 + t][j][0] = fmaf(s0, sum[t][j][0], acc[t0 + t][j][0]);
+                            acc[t0 + t][j][1] = fmaf(s0, sum[t][j][1], acc[t0 + t][j][1]);
+                            acc[t0 + t][j][2] = fmaf(s1, sum[t][j][2], acc[t0 + t][j][2]);
+                            acc[t0 + t][j][3] = fmaf(s1, sum[t][j][3], acc[t0 + t][j][3]);
                         }
                     }
                 }
             }
         }
-        // the team's sums, 16 rows at a time
+        // the team's sums, 16 rows at a time, in two places used in turn
         const int team_thread = threadIdx.x % (32 * s.team), barrier = 1 + warp / s.team;
-        float *own = sums + warp * 16 * SUM_STRIDE, *first = sums + (warp - part) * 16 * SUM_STRIDE;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             if (16 * t >= u.rows)
                 break;
+            float *own = sums + (turn * WARPS + warp) * 16 * SUM_STRIDE, *first = own - part * 16 * SUM_STRIDE;
+            turn ^= 1;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 float *at = own + g * SUM_STRIDE + 8 * j + 2 * tig;
                 *reinterpret_cast<float2 *>(at) = make_float2(acc[t][j][0], acc[t][j][1]);
                 *reinterpret_cast<float2 *>(at + 8 * SUM_STRIDE) = make_float2(acc[t][j][2], acc[t][j][3]);
             }
-            asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * s.team) : "memory");
-            for (int i = team_thread; i < 128 * NT; i += 32 * s.team) {
+            if (s.team == 1)
+                __syncwarp();
+            else
+                asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * s.team) : "memory");
+            for (int i = team_thread; i < 16 * u.count; i += 32 * s.team) {
                 const int row = i & 15, col = i >> 4;
-                if (16 * t + row < u.rows && col < u.count) {
+                if (16 * t + row < u.rows) {
                     float y = 0.0f;
                     for (int w = 0; w < s.team; ++w)
                         y += first[(16 * w + row) * SUM_STRIDE + col];
-                    const int64_t pair = p.ids ? l.pair[u.list + col] : u.list + col;
-                    y *= __ldg(p.scale_x + pair / p.pairs_per_x);
+                    const int pair = p.ids ? l.pair[u.list + col] : u.list + col;
+                    y *= __ldg(p.scale_x + x_row(p, pair));
                     if (p.bias)
                         y = __fadd_rn(y, __ldg(p.bias + u.matrix_row + 16 * t + row));
                     dev::store_as(p.y, p.y_dtype, pair * p.y_stride + u.row + 16 * t + row, y);
                 }
             }
-            asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * s.team) : "memory");
         }
     }
     copies_wait<0>();
 }
 
-template <int NT, int FL>
-cudaError_t launch_one(const I4Params &p, const I4Shape &s, const loom_launch &L, cudaStream_t stream)
+// ---- one or two tokens: dp4a ------------------------------------------------------------------
+// Lanes across k: 16 bytes of a row (32 weights, one scale) each, so a warp takes 1024 k of R rows at a
+// time with the tokens' bytes for them in registers.  A nibble in a byte's upper half is 16 times a signed
+// weight, so eight weights cost three logic instructions and two dp4a.  Warps share out k where it is long, rows
+// where it is not; a row's sums over lanes meet in shared memory, one place per warp, and are
+// added in a fixed order.
+constexpr int DP_CHUNK = 1024;      // k of a warp's access
+constexpr int DP_RUN = 512;         // rows whose sums a CTA holds
+constexpr int DP_WARPS = 8, DP_THREADS = 32 * DP_WARPS;
+
+// Sums of N values over the warp: afterwards v[0] of lane l is the sum of value l / (32 / N).
+template <int N> __device__ __forceinline__ void sum_lanes(float (&v)[N], int lane)
+{
+    int n = N;
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool up = (lane & m) != 0;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < n) {
+                    const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(dev::FULL_MASK, send, m);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(dev::FULL_MASK, v[0], m);
+        }
+    }
+}
+
+// T tokens, R rows and KV chunks of k together.  V16: rows start on 16 bytes, and a lane holds 16 neighbouring
+// bytes; else the words lane, lane + 32, ... of the chunk.
+template <int T, int R, int KV, bool V16> __global__ void __launch_bounds__(DP_THREADS, 2) i4_dp4a_kernel(const I4Params p, const I4Shape s)
+{
+    extern __shared__ __align__(128) unsigned char i4_shared[];
+    constexpr int Q = V16 ? 1 : 4;                                   // scales of a lane's 32 weights
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    dev::follow_previous_kernel();
+    Lists l = {};
+    if (p.ids) {
+        l = make_lists<DP_THREADS>(p, reinterpret_cast<uint32_t *>(i4_shared + s.lists));
+        clear_missing(p, l);
+    }
+    float *sums = reinterpret_cast<float *>(i4_shared + s.sums);     // [team][rows of the run][T]
+    const int part = warp % s.team, team = warp / s.team, teams = DP_WARPS / s.team;
+    const int chunks = (p.k + DP_CHUNK - 1) / DP_CHUNK;
+    const int c0 = chunks * part / s.team, c1 = chunks * (part + 1) / s.team;
+    const int row_bytes = p.k / 2;
+    for (Runs run = first_run(p, l); run.left > 0;) {
+        const int rows = min(run.rows, DP_RUN);
+        const int64_t matrix_row = (int64_t)(p.ids ? l.expert[run.matrix] : 0) * p.n + run.row;
+        const int r0 = rows * team / teams, r1 = rows * (team + 1) / teams;
+        for (int pass = 0; pass < run.pairs; pass += T) {
+            for (int c = c0; c < c1; c += KV) {
+                // the tokens' bytes: of each word's eight the even ones and the odd ones
+                uint32_t x[T][KV][8];
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                    const int pair = min(pass + t, run.pairs - 1);
+                    const int8_t *xr = p.x + (int64_t)x_row(p, p.ids ? l.pair[run.first + pair] : pair) * p.k;
+#pragma unroll
+                    for (int j = 0; j < KV; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k0 = (c + j) * DP_CHUNK + (V16 ? 32 * lane + 8 * i : 8 * lane + 256 * i);
+                            uint32_t a = 0, b = 0;
+                            if (c + j < c1 && k0 < p.k) {
+                                a = __ldg(reinterpret_cast<const uint32_t *>(xr + k0));
+                                b = __ldg(reinterpret_cast<const uint32_t *>(xr + k0) + 1);
+                            }
+                            x[t][j][2 * i] = __byte_perm(a, b, 0x6420);
+                            x[t][j][2 * i + 1] = __byte_perm(a, b, 0x7531);
+                        }
+                }
+                bool there[KV][Q];
+                int group[KV][Q];
+#pragma unroll
+                for (int j = 0; j < KV; ++j)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const int k0 = (c + j) * DP_CHUNK + (V16 ? 32 * lane : 8 * lane + 256 * q);
+                        there[j][q] = c + j < c1 && k0 < p.k;
+                        group[j][q] = there[j][q] ? k0 >> s.log_group : 0;
+                    }
+                const char *w_row = reinterpret_cast<const char *>(p.w) + (matrix_row + r0) * row_bytes + c * (DP_CHUNK / 2) + (V16 ? 16 : 4) * lane;
+                int64_t scale_row = (matrix_row + r0) * p.groups;
+                for (int r = r0; r < r1; r += R, w_row += R * (int64_t)row_bytes, scale_row += R * p.groups) {
+                    uint4 w[R][KV];
+                    uint32_t scale[R][KV][Q];
+                    const char *at = w_row;
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+#pragma unroll
+                        for (int j = 0; j < KV; ++j) {
+                            uint32_t *o = &w[i][j].x;
+                            w[i][j] = make_uint4(0, 0, 0, 0);
+                            if (V16) {
+                                if (there[j][0])
+                                    w[i][j] = __ldcs(reinterpret_cast<const uint4 *>(at + j * (DP_CHUNK / 2)));
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (there[j][q % Q])
+                                        o[q] = __ldcs(reinterpret_cast<const uint32_t *>(at + j * (DP_CHUNK / 2) + 128 * q));
+                            }
+                        }
+                        if (r + i + 1 < r1)        // (past the last row its own again)
+                            at += row_bytes;
+                    }
+                    if (p.scale_dtype == LOOM_F32) {
+                        const uint32_t *from = static_cast<const uint32_t *>(p.scale_w) + scale_row;
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+#pragma unroll
+                            for (int j = 0; j < KV; ++j)
+#pragma unroll
+                                for (int q = 0; q < Q; ++q)
+                                    scale[i][j][q] = __ldg(from + group[j][q]);
+                            if (r + i + 1 < r1)
+                                from += p.groups;
+                        }
+                    } else {
+                        const unsigned short *from = static_cast<const unsigned short *>(p.scale_w) + scale_row;
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+#pragma unroll
+                            for (int j = 0; j < KV; ++j)
+#pragma unroll
+                                for (int q = 0; q < Q; ++q)
+                                    scale[i][j][q] = __ldg(from + group[j][q]);
+                            if (r + i + 1 < r1)
+                                from += p.groups;
+                        }
+                    }
+                    int a[R][KV][Q][T];
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+#pragma unroll
+                        for (int j = 0; j < KV; ++j) {
+                            const uint32_t *word = &w[i][j].x;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t even = (word[q] << 4) & 0xf0f0f0f0u, odd = word[q] & 0xf0f0f0f0u;
+#pragma unroll
+                                for (int t = 0; t < T; ++t) {
+                                    int &sum = a[i][j][q % Q][t];
+                                    sum = __dp4a((int)even, (int)x[t][j][2 * q], q < Q ? 0 : sum);
+                                    sum = __dp4a((int)odd, (int)x[t][j][2 * q + 1], sum);
+                                }
+                            }
+                        }
+                    float v[R * T];
+                    const bool half = p.scale_dtype == LOOM_F16;
+                    const int up = p.scale_dtype == LOOM_BF16 ? 16 : 0;
+#pragma unroll
+                    for (int i = 0; i < R * T; ++i)
+                        v[i] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+#pragma unroll
+                        for (int j = 0; j < KV; ++j)
+#pragma unroll
+                            for (int q = 0; q < Q; ++q) {
+                                const float f = half ? __half2float(__ushort_as_half((unsigned short)scale[i][j][q])) : __uint_as_float(scale[i][j][q] << up);
+#pragma unroll
+                                for (int t = 0; t < T; ++t)
+                                    v[i * T + t] = fmaf(f, (float)a[i][j][q][t], v[i * T + t]);
+                            }
+                    sum_lanes<R * T>(v, lane);
+                    constexpr int SPAN = 32 / (R * T);
+                    const int i = lane / SPAN / T, t = lane / SPAN % T;
+                    if (lane % SPAN == 0 && r + i < r1) {
+                        float *to = sums + (part * rows + r + i) * T + t;
+                        *to = c == c0 ? v[0] : *to + v[0];
+                    }
+                }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < rows * T; i += DP_THREADS) {
+                const int r = T == 1 ? i : i / T, t = T == 1 ? 0 : i % T;
+                if (pass + t < run.pairs) {
+                    float y = 0.0f;
+                    for (int w = 0; w < s.team && chunks > 0; ++w)
+                        y += sums[w * rows * T + i];
+                    const int pair = p.ids ? l.pair[run.first + pass + t] : pass + t;
+                    y *= __ldg(p.scale_x + x_row(p, pair)) * 0.0625f;
+                    if (p.bias)
+                        y = __fadd_rn(y, __ldg(p.bias + matrix_row + r));
+                    dev::store_as(p.y, p.y_dtype, pair * p.y_stride + run.row + r, y);
+                }
+            }
+            __syncthreads();
+        }
+        if (rows < run.rows) {
+            run.row += rows;
+            run.left -= rows;
+            run.rows -= rows;
+        } else {
+            next_run(run, p, l);
+        }
+    }
+}
+
+template <typename... A> cudaError_t launch_kernel(void (*kernel)(A...), std::atomic<uint64_t> &done, const I4Params &p, const I4Shape &s,
+                                                   const loom_launch &L, cudaStream_t stream)
+{
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), 0, done);
+    return e != cudaSuccess ? e : launch_prepared(kernel, L, stream, p, s);
+}
+
+template <int NT, int FL, int WARPS, int PAIR>
+cudaError_t launch_mma(const I4Params &p, const I4Shape &s, const loom_launch &L, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(i4_matvec_kernel<NT, FL>), 0, done);
-    return e != cudaSuccess ? e : launch_prepared(i4_matvec_kernel<NT, FL>, L, stream, p, s);
+    return launch_kernel(i4_matvec_kernel<NT, FL, WARPS, PAIR>, done, p, s, L, stream);
 }
+
+template <int T, int R, int KV, bool V16>
+cudaError_t launch_dp4a(const I4Params &p, const I4Shape &s, const loom_launch &L, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    return launch_kernel(i4_dp4a_kernel<T, R, KV, V16>, done, p, s, L, stream);
+}
+
+constexpr int i4_warps(int nt) { return nt == 1 ? 16 : 8; }
 
 template <int NT> cudaError_t launch_nt(const I4Params &p, const I4Shape &s, const loom_launch &L, cudaStream_t stream)
 {
-    return p.group == 32 ? launch_one<NT, 1>(p, s, L, stream) : p.group == 64 ? launch_one<NT, 2>(p, s, L, stream) : launch_one<NT, 4>(p, s, L, stream);
+    constexpr int W = i4_warps(NT), PAIR = NT == 4 ? 1 : 2;
+    return p.group == 32 ? launch_mma<NT, 1, W, PAIR>(p, s, L, stream)
+                         : p.group == 64 ? launch_mma<NT, 2, W, PAIR>(p, s, L, stream) : launch_mma<NT, 4, W, PAIR>(p, s, L, stream);
 }
 
-// MMA columns / 8: for the pairs that a matrix has, on average half as many again.
-int i4_columns(int64_t pairs, int64_t experts)
+int log2_floor(int64_t v)
 {
-    const int64_t each = experts ? (3 * pairs + 2 * experts - 1) / (2 * experts) : pairs;
-    return each <= 8 ? 1 : each <= 16 ? 2 : 4;
+    int l = 0;
+    while (v >> (l + 1))
+        ++l;
+    return l;
 }
 
-// Shared memory of a launch (the static arrays of make_lists are counted as 256 bytes).
-uint32_t i4_smem(int64_t pairs, int64_t k, int64_t group, int64_t experts, I4Shape *s)
+// What a launch is built for: tokens of the dp4a kernel (1 or 2), or MMA columns (8, 16, 32), for the
+// pairs that a matrix has -- on average half as many again of the experts' that are wanted.
+// Its warps, ring and shared memory (the static arrays of make_lists are counted as 256 bytes).
+uint32_t i4_shape(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t experts, int64_t sms, I4Shape *s)
 {
-    const int nt = i4_columns(pairs, experts);
-    const int64_t chunks = (k + I4_CHUNK - 1) / I4_CHUNK;
-    s->team = chunks >= 8 ? 8 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
-    const uint32_t scales = I4_WARPS * I4_ROWS * 4 * (group == 32 ? 8 : group == 64 ? 4 : 2), sums = I4_WARPS * 16 * (8 * nt + 2) * 4;
+    const int64_t named = experts ? (pairs < experts ? pairs : experts) : 1;
+    const int64_t each = experts <= 1 ? pairs : pairs <= experts / 4 ? 1 : (3 * pairs + 2 * named - 1) / (2 * named);
+    s->tokens = each <= 2 ? (int)each : each <= 8 ? 8 : each <= 16 ? 16 : 32;
+    const bool few = s->tokens <= 2;
+    s->warps = few ? DP_WARPS : i4_warps(s->tokens / 8);
+    const int64_t chunk = few ? DP_CHUNK : I4_CHUNK, chunks = (k + chunk - 1) / chunk;
+    // A team for each 128 rows of a CTA: teams meet after each 64 rows, the fewer warps the cheaper.
+    // The dp4a kernel's warps take two chunks each, where there are as many.
+    const int64_t units = named * n / sms / (2 * I4_ROWS);
+    int team = few ? s->warps : s->warps >> log2_floor(units < 1 ? 1 : units > s->warps ? s->warps : units);
+    while (team > 1 && team > (few ? chunks / 2 : chunks))
+        team /= 2;
+    s->team = team;
     const uint32_t lists = experts ? (uint32_t)(((8 * experts + 2 + 2 * pairs) + 15) / 16 * 16) : 0;
+    const uint32_t scales = few ? 0 : s->warps * I4_ROWS * 4 * (group == 32 ? 4 : group == 64 ? 2 : 1);
+    const uint32_t sums = few ? (uint32_t)(s->team * DP_RUN * s->tokens * 4) : 2 * s->warps * 16 * (s->tokens + 2) * 4;
     const uint32_t rest = scales + sums + lists;
-    s->depth = 3 * I4_WARPS * I4_STAGE + rest + 256 <= 227 * 1024 ? 3 : 2;
-    s->scales = (uint32_t)(s->depth * I4_WARPS * I4_STAGE);
+    s->depth = few ? 0 : 3 * s->warps * I4_STAGE + rest + 256 <= 227 * 1024 ? 3 : 2;
+    s->scales = (uint32_t)(s->depth * s->warps * I4_STAGE);
     s->sums = s->scales + scales;
     s->lists = s->sums + sums;
     return s->lists + lists;
@@ -528,11 +817,11 @@ void i4_geometry(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t exp
 {
     I4Shape s;
     *out = loom_launch{};
-    out->smem_bytes = i4_smem(pairs, k, group, experts, &s);
-    const int64_t most = (experts ? experts : 1) * n;
-    out->grid[0] = (uint32_t)(most < sms ? (most > 0 ? most : 1) : sms);
+    out->smem_bytes = i4_shape(pairs, n, k, group, experts, sms, &s);
+    const int64_t most = (experts ? (experts < pairs ? experts : pairs) : 1) * n, ctas = s.depth ? sms : 2 * sms;
+    out->grid[0] = (uint32_t)(most < ctas ? (most > 0 ? most : 1) : ctas);
     out->grid[1] = out->grid[2] = out->block[1] = out->block[2] = 1;
-    out->block[0] = I4_THREADS;
+    out->block[0] = 32 * s.warps;
     out->cluster[0] = out->cluster[1] = out->cluster[2] = 1;
     out->subgroup_size = 32;
     const int64_t rows = (most + out->grid[0] - 1) / out->grid[0];
@@ -540,19 +829,18 @@ void i4_geometry(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t exp
     out->kernel = LOOM_KERNEL_I4_MATVEC;
 }
 
-cudaError_t launch_i4_matvec(const I4Params &p, const loom_launch &L, cudaStream_t stream)
+cudaError_t launch_i4_matvec(const I4Params &p, int64_t sms, const loom_launch &L, cudaStream_t stream)
 {
     I4Shape s;
-    const int32_t experts = p.ids ? (p.experts > 0 ? p.experts : 1) : 0;
-    i4_smem(p.pairs, p.k, p.group, experts, &s);
+    i4_shape(p.pairs, p.n, p.k, p.group, p.ids ? (p.experts > 0 ? p.experts : 1) : 0, sms, &s);
     s.vec16 = p.k % 32 == 0 && reinterpret_cast<uintptr_t>(p.w) % 16 == 0;
     s.x8 = reinterpret_cast<uintptr_t>(p.x) % 8 == 0;
-    s.log_group = 5;
-    while (s.log_group < 30 && (1 << s.log_group) < p.group)
-        ++s.log_group;
-    switch (i4_columns(p.pairs, experts)) {
-    case 1: return launch_nt<1>(p, s, L, stream);
-    case 2: return launch_nt<2>(p, s, L, stream);
+    s.log_group = log2_floor(p.group);
+    switch (s.tokens) {
+    case 1: return s.vec16 ? launch_dp4a<1, 8, 2, true>(p, s, L, stream) : launch_dp4a<1, 4, 1, false>(p, s, L, stream);
+    case 2: return s.vec16 ? launch_dp4a<2, 4, 2, true>(p, s, L, stream) : launch_dp4a<2, 4, 1, false>(p, s, L, stream);
+    case 8: return launch_nt<1>(p, s, L, stream);
+    case 16: return launch_nt<2>(p, s, L, stream);
     default: return launch_nt<4>(p, s, L, stream);
     }
 }

@@ -131,7 +131,7 @@ struct I4Params {
     int32_t scale_dtype, y_dtype;
 };
 void i4_geometry(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t experts, int64_t sms, loom_launch *out);
-cudaError_t launch_i4_matvec(const I4Params &p, const loom_launch &L, cudaStream_t stream);
+cudaError_t launch_i4_matvec(const I4Params &p, int64_t sms, const loom_launch &L, cudaStream_t stream);
 
 // ---- routing (token_route.cu) -----------------------------------------------------------
 constexpr int ROUTE_MAX_EXPERTS = 1024, ROUTE_MAX_TOP = 32;

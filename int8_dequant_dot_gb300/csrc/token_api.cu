@@ -153,7 +153,7 @@ loom_status i4_call(I4Params p, int64_t x_rows, int64_t y_stride, int32_t routes
         }
         loom_launch L;
         i4_geometry(p.pairs, p.n, p.k, p.group, routes > 0 ? (p.experts > 0 ? p.experts : 1) : 0, sms, &L);
-        const cudaError_t e = launch_i4_matvec(p, L, stream);
+        const cudaError_t e = launch_i4_matvec(p, sms, L, stream);
         if (e != cudaSuccess)
             return LOOM_ERR_CUDA;
     }
