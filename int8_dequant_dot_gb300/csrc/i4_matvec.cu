@@ -84,8 +84,24 @@ __device__ __forceinline__ void token_operands(uint32_t (&b)[4], uint2 x)
     b[3] = half2_fma(__byte_perm(q, 0x64646464u, 0x4342), sixteenth, m72);
 }
 
-__device__ __forceinline__ uint32_t low_nibbles(uint32_t w) { return (w & 0x000f000fu) ^ 0x00080008u; }
-__device__ __forceinline__ uint32_t high_nibbles(uint32_t w) { return (w & 0x00f000f0u) ^ 0x00800080u; }
+// Nibbles of two halves as (w + 8) 2^-24 and (w + 8) 2^-20.  One instruction, as its two constants are held in
+// registers (where the compiler sees them it takes two).
+struct Nibbles {
+    uint32_t low, low8, high, high8;
+};
+__device__ __forceinline__ Nibbles nibble_masks()
+{
+    Nibbles n;
+    asm volatile("mov.b32 %0, 0x000f000f;\n\tmov.b32 %1, 0x00080008;\n\tmov.b32 %2, 0x00f000f0;\n\tmov.b32 %3, 0x00800080;"
+                 : "=r"(n.low), "=r"(n.low8), "=r"(n.high), "=r"(n.high8));
+    return n;
+}
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t a, uint32_t x)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(w), "r"(a), "r"(x));
+    return d;
+}
 
 // ---- what a CTA works on: runs of rows of one matrix, each with the pairs that want it ------------
 struct Lists {                 // in shared memory, of the experts' products
@@ -333,6 +349,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
     const uint32_t ring = dev::smem_u32(i4_shared) + warp * s.depth * I4_STAGE;
     float *scales = reinterpret_cast<float *>(i4_shared + s.scales) + warp * I4_ROWS * SP;
     float *sums = reinterpret_cast<float *>(i4_shared + s.sums);
+    const Nibbles n = nibble_masks();
     // ldmatrix: lane's row of a tile, and the piece of 16 bytes that it points at in the first two steps
     const uint32_t place = (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
 
@@ -477,9 +494,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
                             if (i % 2 == 0)         // two steps (16-byte pieces) of 16 rows at a time
                                 load_matrices(w[t], (stage ^ (i << 4)) + (t0 + t) * 1024);
                             const uint32_t w0 = w[t][2 * (i % 2)], w1 = w[t][2 * (i % 2) + 1];
-                            const uint32_t a0 = low_nibbles(w0), a1 = low_nibbles(w1), a2 = high_nibbles(w0), a3 = high_nibbles(w1);
-                            const uint32_t e0 = low_nibbles(w0 >> 8), e1 = low_nibbles(w1 >> 8), e2 = high_nibbles(w0 >> 8),
-                                           e3 = high_nibbles(w1 >> 8);
+                            const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
+                            const uint32_t a0 = and_xor(w0, n.low, n.low8), a1 = and_xor(w1, n.low, n.low8);
+                            const uint32_t a2 = and_xor(w0, n.high, n.high8), a3 = and_xor(w1, n.high, n.high8);
+                            const uint32_t e0 = and_xor(v0, n.low, n.low8), e1 = and_xor(v1, n.low, n.low8);
+                            const uint32_t e2 = and_xor(v0, n.high, n.high8), e3 = and_xor(v1, n.high, n.high8);
 #pragma unroll
                             for (int j = 0; j < NT; ++j) {
                                 if (i == f * FL)
