@@ -295,29 +295,46 @@ __device__ __forceinline__ void clear_missing(const I4Params &p, const Lists &l)
     }
 }
 
-// The copies of one stage: 64 bytes of up to 64 rows from k = chunk * 128 on.  What lies past the
+// A warp's copies, which run ahead of its products: 64 bytes of up to 64 rows a stage.  What lies past the
 // rows or past k is not copied: it meets zeros, or sums that are thrown away.
-__device__ __forceinline__ void copy_stage(const I4Params &p, const I4Shape &s, const Unit &u, int chunk, uint32_t dst, int lane)
+struct Copies {
+    Walk walk;
+    const char *src;           // of this lane's first row in the stage
+    int limit, chunk;          // rows of the unit from that one on
+    uint32_t at;               // where the next stage goes, of this lane's first piece
+    bool more;
+};
+
+__device__ __forceinline__ void start_unit(Copies &c, const I4Params &p, const I4Shape &s, const Lists &l, int chunk, int lane)
 {
-    const int row_bytes = p.k / 2, left = row_bytes - chunk * (I4_CHUNK / 2);
-    const char *src = reinterpret_cast<const char *>(p.w) + u.matrix_row * row_bytes + chunk * (I4_CHUNK / 2);
+    Unit u;
+    c.more = unit_of(c.walk, p, l, u);
+    c.chunk = chunk;
+    if (!c.more)
+        return;
+    const int r0 = s.vec16 ? lane >> 2 : lane >> 4, row_bytes = p.k / 2;
+    c.limit = u.rows - r0;
+    c.src = reinterpret_cast<const char *>(p.w) + (u.matrix_row + r0) * row_bytes + chunk * (I4_CHUNK / 2) + (s.vec16 ? 16 * (lane & 3) : 4 * (lane & 15));
+}
+
+__device__ __forceinline__ void copy_stage(const Copies &c, const I4Params &p, const I4Shape &s, int lane)
+{
+    const int row_bytes = p.k / 2, left = row_bytes - c.chunk * (I4_CHUNK / 2);
     if (s.vec16) {
-        const int piece = lane & 3, r0 = lane >> 2;
-        if (16 * piece < left) {
-            const char *q = src + r0 * (int64_t)row_bytes + 16 * piece;
-            const int64_t step = 8 * (int64_t)row_bytes;
-            const uint32_t to = dst + r0 * 64 + ((piece ^ ((r0 >> 1) & 3)) << 4);
+        const int rows = 16 * (lane & 3) < left ? c.limit : 0;
+        const uint32_t step = 8u * (uint32_t)row_bytes;
 #pragma unroll
-            for (int i = 0; i < I4_ROWS / 8; ++i)
-                if (u.rows == I4_ROWS || r0 + 8 * i < u.rows)
-                    copy_async16(to + 512 * i, q + i * step);
-        }
-    } else {
+        for (int i = 0; i < I4_ROWS / 8; ++i)
+            if (8 * i < rows)
+                copy_async16(c.at + 512 * i, c.src + (uint64_t)step * i);
+    } else if (4 * (lane & 15) < left) {
         const int word = lane & 15, r0 = lane >> 4;
-        if (4 * word < left)
+        const uint32_t stage = c.at - (r0 * 64 + (((word >> 2) ^ (r0 >> 1)) << 4) + 4 * (word & 3));
 #pragma unroll 8
-            for (int r = r0; r < u.rows; r += 2)
-                copy_async4(dst + r * 64 + (((word >> 2) ^ ((r >> 1) & 3)) << 4) + 4 * (word & 3), src + r * (int64_t)row_bytes + 4 * word);
+        for (int r = 0; r < c.limit; r += 2) {
+            const int row = r0 + r;
+            copy_async4(stage + row * 64 + (((word >> 2) ^ ((row >> 1) & 3)) << 4) + 4 * (word & 3), c.src + r * (int64_t)row_bytes);
+        }
     }
 }
 
@@ -354,26 +371,34 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
     const uint32_t place = (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
 
     // the copies run `depth - 1` stages ahead of the products
-    Walk ahead = walk;
-    Unit next;
-    bool more = unit_of(ahead, p, l, next) && c0 < c1;
-    int next_chunk = c0, next_slot = 0;
+    Copies ahead;
+    ahead.walk = walk;
+    const int word = lane & 15;
+    const uint32_t first_place = s.vec16 ? (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4)
+                                         : (lane >> 4) * 64 + ((word >> 2) << 4) + 4 * (word & 3);
+    const uint32_t ring_end = ring + s.depth * I4_STAGE;
+    ahead.at = ring + first_place;
+    start_unit(ahead, p, s, l, c0, lane);
+    ahead.more = ahead.more && c0 < c1;
     const auto copy_next = [&]() {
-        if (more) {
-            copy_stage(p, s, next, next_chunk, ring + next_slot * I4_STAGE, lane);
-            if (++next_chunk == c1) {
-                ahead.q += ahead.teams;
-                more = unit_of(ahead, p, l, next);
-                next_chunk = c0;
+        if (ahead.more) {
+            copy_stage(ahead, p, s, lane);
+            ahead.src += I4_CHUNK / 2;
+            if (++ahead.chunk == c1) {
+                ahead.walk.q += ahead.walk.teams;
+                start_unit(ahead, p, s, l, c0, lane);
             }
         }
         copies_commit();
-        next_slot = next_slot + 1 == s.depth ? 0 : next_slot + 1;
+        ahead.at += I4_STAGE;
+        if (ahead.at >= ring_end)
+            ahead.at -= s.depth * I4_STAGE;
     };
     for (int i = 1; i < s.depth; ++i)
         copy_next();
 
-    int slot = 0, turn = 0;
+    int turn = 0;
+    uint32_t stage = ring + place;
     Unit u;
     for (; unit_of(walk, p, l, u); walk.q += walk.teams) {
         float acc[4][NT][4];
@@ -477,8 +502,6 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
                 load_scales(c + 1);
             }
             __syncwarp();
-            const uint32_t stage = ring + slot * I4_STAGE + place;
-            slot = slot + 1 == s.depth ? 0 : slot + 1;
 #pragma unroll
             for (int t0 = 0; t0 < 4; t0 += PAIR) {
                 if (16 * t0 >= u.rows)
@@ -522,6 +545,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
                     }
                 }
             }
+            stage += I4_STAGE;
+            if (stage >= ring_end)
+                stage -= s.depth * I4_STAGE;
         }
         // the team's sums, 16 rows at a time, in two places used in turn
         const int team_thread = threadIdx.x % (32 * s.team), barrier = 1 + warp / s.team;
@@ -812,9 +838,9 @@ uint32_t i4_shape(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t ex
     const bool few = s->tokens <= 2;
     s->warps = few ? DP_WARPS : i4_warps(s->tokens / 8);
     const int64_t chunk = few ? DP_CHUNK : I4_CHUNK, chunks = (k + chunk - 1) / chunk;
-    // A team for each 128 rows of a CTA: teams meet after each 64 rows, the fewer warps the cheaper.
+    // A team for each 48 rows of a CTA or more: its warps meet after each 64 rows, the fewer the cheaper.
     // The dp4a kernel's warps take two chunks each, where there are as many.
-    const int64_t units = named * n / sms / (2 * I4_ROWS);
+    const int64_t units = named * n / sms / (3 * I4_ROWS / 4);
     int team = few ? s->warps : s->warps >> log2_floor(units < 1 ? 1 : units > s->warps ? s->warps : units);
     while (team > 1 && team > (few ? chunks / 2 : chunks))
         team /= 2;
