@@ -38,7 +38,7 @@ struct I4Shape {          // of a launch
     int vec16;            // rows of W start on 16 bytes
     int x8;               // rows of X start on 8 bytes
     int log_group;
-    uint32_t scales, sums, lists;   // offsets in shared memory behind the rings
+    uint32_t scales, sums, ways, lists;   // offsets in shared memory behind the rings
 };
 
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void *src)
@@ -105,7 +105,8 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t a, uint32_t x)
 
 // ---- what a CTA works on: runs of rows of one matrix, each with the pairs that want it ------------
 struct Lists {                 // in shared memory, of the experts' products
-    uint16_t *expert, *first;  // of each expert that some pair names (first: also behind the last): its first pair
+    // of each expert that some pair names (the latter two also behind the last): it, its first pair, passes before it
+    uint16_t *expert, *first, *passes;
     uint16_t *pair;            // sorted by expert, the missing ones last
     int experts, pairs;        // that are named; that are not missing
 };
@@ -116,40 +117,57 @@ struct Unit {
     int list, count;           // pairs: places in the list (or numbers)
 };
 
-// A CTA's rows, counted over the matrices that are wanted, as runs of rows of one matrix.
+// A CTA's share of the rows of the matrices that are wanted, a row counted once for each pass over it, as runs of
+// rows of one matrix.
 struct Runs {
-    int64_t left;              // rows from the present run's first on
-    int matrix, row, rows;     // the present run: its matrix (of the wanted ones), first row and rows
+    int64_t begin, end;        // the share
+    int matrix, matrices;      // of the wanted ones: the present run's, all
+    int row, rows;             // the run's first row and rows
     int first, pairs;          // its pairs
 };
 
-__device__ __forceinline__ void set_run(Runs &w, const I4Params &p, const Lists &l)
+// The run of matrix w.matrix or the next one that has rows; false past the last.
+__device__ __forceinline__ bool find_run(Runs &w, const I4Params &p, const Lists &l)
 {
-    w.rows = (int)min((int64_t)(p.n - w.row), w.left);
-    if (w.left <= 0)
-        return;
-    w.first = p.ids ? l.first[w.matrix] : 0;
-    w.pairs = p.ids ? l.first[w.matrix + 1] - w.first : p.pairs;
+    for (; w.matrix < w.matrices; ++w.matrix) {
+        const int before = p.ids ? l.passes[w.matrix] : 0, passes = p.ids ? l.passes[w.matrix + 1] - before : 1;
+        const int64_t base = (int64_t)before * p.n, b = max(w.begin - base, (int64_t)0), e = min(w.end - base, (int64_t)passes * p.n);
+        if (e <= 0)
+            break;
+        w.row = (int)(passes == 1 ? b : b / passes);
+        w.rows = (int)(passes == 1 ? e : e / passes) - w.row;
+        if (w.rows > 0) {
+            w.first = p.ids ? l.first[w.matrix] : 0;
+            w.pairs = p.ids ? l.first[w.matrix + 1] - w.first : p.pairs;
+            return true;
+        }
+    }
+    w.matrix = w.matrices;
+    return false;
 }
 
-__device__ __forceinline__ Runs first_run(const I4Params &p, const Lists &l)
+__device__ __forceinline__ bool first_run(Runs &w, const I4Params &p, const Lists &l)
 {
-    const int64_t rows = (p.ids ? (int64_t)l.experts : 1) * p.n;
-    const int64_t begin = rows * blockIdx.x / gridDim.x;
-    Runs w;
-    w.left = rows * (blockIdx.x + 1) / gridDim.x - begin;
-    w.matrix = (int)(begin / p.n);
-    w.row = (int)(begin - (int64_t)w.matrix * p.n);
-    set_run(w, p, l);
-    return w;
+    w.matrices = p.ids ? l.experts : 1;
+    const int64_t all = (int64_t)(p.ids ? l.passes[l.experts] : 1) * p.n;
+    w.begin = all * blockIdx.x / gridDim.x;
+    w.end = all * (blockIdx.x + 1) / gridDim.x;
+    w.matrix = 0;
+    if (p.ids) {                               // the last matrix that begins at or before the share
+        int step = 1;
+        while (2 * step < w.matrices)
+            step *= 2;
+        for (; step > 0; step /= 2)
+            if (w.matrix + step < w.matrices && (int64_t)l.passes[w.matrix + step] * p.n <= w.begin)
+                w.matrix += step;
+    }
+    return find_run(w, p, l);
 }
 
-__device__ __forceinline__ void next_run(Runs &w, const I4Params &p, const Lists &l)
+__device__ __forceinline__ bool next_run(Runs &w, const I4Params &p, const Lists &l)
 {
-    w.left -= w.rows;
     ++w.matrix;
-    w.row = 0;
-    set_run(w, p, l);
+    return find_run(w, p, l);
 }
 
 // The units of a team: up to 64 rows with the pairs of one pass, in turn.
@@ -158,11 +176,12 @@ struct Walk {
     int q, units;              // unit of the run, of so many: its parts, each `passes` times
     int passes, part_rows;
     int columns, teams;
+    bool more;
 };
 
 __device__ __forceinline__ void set_units(Walk &w)
 {
-    if (w.run.left <= 0)
+    if (!w.more)
         return;
     w.passes = (w.run.pairs + w.columns - 1) / w.columns;
     // equal parts of up to 64 rows, as many for each team, unless they would have under 16
@@ -175,7 +194,7 @@ __device__ __forceinline__ void set_units(Walk &w)
 // The unit that the walk stands on; false past the last.
 __device__ __forceinline__ bool unit_of(Walk &w, const I4Params &p, const Lists &l, Unit &u)
 {
-    while (w.run.left > 0) {
+    while (w.more) {
         if (w.q < w.units) {
             const int part = w.passes == 1 ? w.q : w.q / w.passes, pass = w.q - part * w.passes;
             const int r0 = part * w.part_rows;
@@ -187,7 +206,7 @@ __device__ __forceinline__ bool unit_of(Walk &w, const I4Params &p, const Lists 
             return true;
         }
         w.q -= w.units;
-        next_run(w.run, p, l);
+        w.more = next_run(w.run, p, l);
         set_units(w);
     }
     return false;
@@ -200,14 +219,16 @@ __device__ __forceinline__ int x_row(const I4Params &p, int pair)
 }
 
 // Sorts the pairs by expert.  counts: [experts] words of scratch.
-template <int THREADS> __device__ Lists make_lists(const I4Params &p, uint32_t *scratch)
+template <int THREADS> __device__ Lists make_lists(const I4Params &p, uint32_t *scratch, int columns)
 {
-    __shared__ uint32_t warp_sums[THREADS / 32], missing;
+    __shared__ uint64_t warp_sums[THREADS / 32];
+    __shared__ uint32_t missing;
     Lists l;
     uint32_t *counts = scratch;
     l.expert = reinterpret_cast<uint16_t *>(counts + p.experts);
     l.first = l.expert + p.experts;
-    l.pair = l.first + p.experts + 1;
+    l.passes = l.first + p.experts + 1;
+    l.pair = l.passes + p.experts + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < p.experts; e += THREADS)
         counts[e] = 0;
@@ -233,47 +254,51 @@ template <int THREADS> __device__ Lists make_lists(const I4Params &p, uint32_t *
         }
     }
     __syncthreads();
-    // pairs in the low half, experts that have some in the high half
-    constexpr int PER = I4_MAX_EXPERTS / THREADS;
-    uint32_t own[PER], sum = 0;
+    // three running sums in one word: pairs, from bit 20 on passes, from bit 40 on experts that have pairs
+    constexpr int PER = (I4_MAX_EXPERTS + THREADS - 1) / THREADS;
+    uint64_t own[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = tid * PER + i;
-        own[i] = e < p.experts ? counts[e] : 0u;
-        own[i] |= own[i] ? 0x10000u : 0u;
+        const uint32_t n = e < p.experts ? counts[e] : 0u;
+        own[i] = n ? n | ((uint64_t)((n + columns - 1) / columns) << 20) | (1ull << 40) : 0ull;
         sum += own[i];
     }
-    uint32_t run = sum;
+    uint64_t run = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t up = __shfl_up_sync(dev::FULL_MASK, run, d);
-        run += lane >= d ? up : 0u;
+        const uint64_t up = __shfl_up_sync(dev::FULL_MASK, run, d);
+        run += lane >= d ? up : 0ull;
     }
     if (lane == 31)
         warp_sums[warp] = run;
     __syncthreads();
-    uint32_t before = run - sum, all = 0;
+    uint64_t before = run - sum, all = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
-        before += i < warp ? warp_sums[i] : 0u;
+        before += i < warp ? warp_sums[i] : 0ull;
         all += warp_sums[i];
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = tid * PER + i;
         if (e < p.experts) {
-            counts[e] = before & 0xffffu;
+            counts[e] = (uint32_t)before & 0xfffffu;
             if (own[i]) {
-                l.expert[before >> 16] = (uint16_t)e;
-                l.first[before >> 16] = (uint16_t)before;
+                const int at = (int)(before >> 40);
+                l.expert[at] = (uint16_t)e;
+                l.first[at] = (uint16_t)(before & 0xfffffu);
+                l.passes[at] = (uint16_t)((before >> 20) & 0xfffffu);
             }
         }
         before += own[i];
     }
-    l.pairs = (int)(all & 0xffffu);
-    l.experts = (int)(all >> 16);
-    if (tid == 0)
+    l.pairs = (int)(all & 0xfffffu);
+    l.experts = (int)(all >> 40);
+    if (tid == 0) {
         l.first[l.experts] = (uint16_t)l.pairs;
+        l.passes[l.experts] = (uint16_t)((all >> 20) & 0xfffffu);
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
@@ -298,18 +323,36 @@ __device__ __forceinline__ void clear_missing(const I4Params &p, const Lists &l)
 // A warp's copies, which run ahead of its products: 64 bytes of up to 64 rows a stage.  What lies past the
 // rows or past k is not copied: it meets zeros, or sums that are thrown away.
 struct Copies {
-    Walk walk;
     const char *src;           // of this lane's first row in the stage
     int limit, chunk;          // rows of the unit from that one on
     uint32_t at;               // where the next stage goes, of this lane's first piece
     bool more;
 };
 
-__device__ __forceinline__ void start_unit(Copies &c, const I4Params &p, const I4Shape &s, const Lists &l, int chunk, int lane)
+// A warp's way through its units, in shared memory (registers hold the sums): where its copies stand, and the units
+// that they have begun, for the products (at most two of them ahead).
+struct Way {
+    Walk walk;
+    Unit queue[4];
+    int made;
+};
+
+__device__ __forceinline__ void start_unit(Copies &c, Way *way, const I4Params &p, const I4Shape &s, const Lists &l, int chunk, int lane)
 {
+    Walk w = way->walk;
     Unit u;
-    c.more = unit_of(c.walk, p, l, u);
+    c.more = unit_of(w, p, l, u);
     c.chunk = chunk;
+    u.count = c.more ? u.count : 0;
+    const int at = way->made;
+    __syncwarp();
+    if (lane == 0) {
+        w.q += w.teams;
+        way->walk = w;
+        way->queue[at & 3] = u;
+        way->made = at + 1;
+    }
+    __syncwarp();
     if (!c.more)
         return;
     const int r0 = s.vec16 ? lane >> 2 : lane >> 4, row_bytes = p.k / 2;
@@ -345,20 +388,29 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
     extern __shared__ __align__(128) unsigned char i4_shared[];
     constexpr int STEPS = I4_CHUNK / 32, SP = STEPS / FL;            // SP: flushes, and scales of a row, in a stage
     constexpr int SUM_STRIDE = 8 * NT + 2;
+    constexpr bool EARLY = false;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tig = lane & 3;
     dev::follow_previous_kernel();
 
     Lists l = {};
     if (p.ids) {
-        l = make_lists<32 * WARPS>(p, reinterpret_cast<uint32_t *>(i4_shared + s.lists));
+        l = make_lists<32 * WARPS>(p, reinterpret_cast<uint32_t *>(i4_shared + s.lists), 8 * NT);
         clear_missing(p, l);
     }
-    Walk walk;
-    walk.run = first_run(p, l);
-    walk.teams = WARPS / s.team;
-    walk.columns = 8 * NT;
-    set_units(walk);
-    walk.q = warp / s.team;
+    Way *way = reinterpret_cast<Way *>(i4_shared + s.ways) + warp;
+    {
+        Walk walk;
+        walk.more = first_run(walk.run, p, l);
+        walk.teams = WARPS / s.team;
+        walk.columns = 8 * NT;
+        walk.q = warp / s.team;
+        set_units(walk);
+        if (lane == 0) {
+            way->walk = walk;
+            way->made = 0;
+        }
+        __syncwarp();
+    }
     const int part = warp % s.team;
     const int chunks = (p.k + I4_CHUNK - 1) / I4_CHUNK;
     const int c0 = chunks * part / s.team, c1 = chunks * (part + 1) / s.team;
@@ -372,22 +424,18 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
 
     // the copies run `depth - 1` stages ahead of the products
     Copies ahead;
-    ahead.walk = walk;
     const int word = lane & 15;
     const uint32_t first_place = s.vec16 ? (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4)
                                          : (lane >> 4) * 64 + ((word >> 2) << 4) + 4 * (word & 3);
     const uint32_t ring_end = ring + s.depth * I4_STAGE;
     ahead.at = ring + first_place;
-    start_unit(ahead, p, s, l, c0, lane);
-    ahead.more = ahead.more && c0 < c1;
+    start_unit(ahead, way, p, s, l, c0, lane);
     const auto copy_next = [&]() {
-        if (ahead.more) {
+        if (ahead.more && c0 < c1) {
             copy_stage(ahead, p, s, lane);
             ahead.src += I4_CHUNK / 2;
-            if (++ahead.chunk == c1) {
-                ahead.walk.q += ahead.walk.teams;
-                start_unit(ahead, p, s, l, c0, lane);
-            }
+            if (++ahead.chunk == c1)
+                start_unit(ahead, way, p, s, l, c0, lane);
         }
         copies_commit();
         ahead.at += I4_STAGE;
@@ -399,8 +447,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
 
     int turn = 0;
     uint32_t stage = ring + place;
-    Unit u;
-    for (; unit_of(walk, p, l, u); walk.q += walk.teams) {
+    for (int done = 0;; ++done) {
+        if (c0 >= c1 && done > 0)                 // (no k: no copies begin a unit)
+            start_unit(ahead, way, p, s, l, c0, lane);
+        const Unit u = way->queue[done & 3];
+        if (u.count == 0)
+            break;
         float acc[4][NT][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -479,6 +531,14 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
                 for (int i = 0; i < 2 * SP; ++i)
                     scales[lane + 32 * i] = __uint_as_float(scale[i] << up) * 16777216.0f;
             }
+            uint32_t early[EARLY ? 4 : 1][2][4];          // where registers allow it: the stage's weights, whose way takes as long
+            if (EARLY) {                                  // as the tokens' conversion
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        load_matrices(early[t % (EARLY ? 4 : 1)][i], (stage ^ (i << 5)) + t * 1024);
+            }
             uint32_t b[STEPS][NT][4];
             float start[SP][NT][4];
 #pragma unroll
@@ -514,9 +574,10 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
                     for (int i = f * FL; i < (f + 1) * FL; ++i)
 #pragma unroll
                         for (int t = 0; t < PAIR; ++t) {
-                            if (i % 2 == 0)         // two steps (16-byte pieces) of 16 rows at a time
+                            if (!EARLY && i % 2 == 0)         // two steps (16-byte pieces) of 16 rows at a time
                                 load_matrices(w[t], (stage ^ (i << 4)) + (t0 + t) * 1024);
-                            const uint32_t w0 = w[t][2 * (i % 2)], w1 = w[t][2 * (i % 2) + 1];
+                            const uint32_t *of = EARLY ? early[(t0 + t) % (EARLY ? 4 : 1)][i / 2] : w[t];
+                            const uint32_t w0 = of[2 * (i % 2)], w1 = of[2 * (i % 2) + 1];
                             const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
                             const uint32_t a0 = and_xor(w0, n.low, n.low8), a1 = and_xor(w1, n.low, n.low8);
                             const uint32_t a2 = and_xor(w0, n.high, n.high8), a3 = and_xor(w1, n.high, n.high8);
@@ -626,7 +687,7 @@ template <int T, int R, int KV, bool V16> __global__ void __launch_bounds__(DP_T
     dev::follow_previous_kernel();
     Lists l = {};
     if (p.ids) {
-        l = make_lists<DP_THREADS>(p, reinterpret_cast<uint32_t *>(i4_shared + s.lists));
+        l = make_lists<DP_THREADS>(p, reinterpret_cast<uint32_t *>(i4_shared + s.lists), T);
         clear_missing(p, l);
     }
     float *sums = reinterpret_cast<float *>(i4_shared + s.sums);     // [team][rows of the run][T]
@@ -634,7 +695,8 @@ template <int T, int R, int KV, bool V16> __global__ void __launch_bounds__(DP_T
     const int chunks = (p.k + DP_CHUNK - 1) / DP_CHUNK;
     const int c0 = chunks * part / s.team, c1 = chunks * (part + 1) / s.team;
     const int row_bytes = p.k / 2;
-    for (Runs run = first_run(p, l); run.left > 0;) {
+    Runs run;
+    for (bool more = first_run(run, p, l); more;) {
         const int rows = min(run.rows, DP_RUN);
         const int64_t matrix_row = (int64_t)(p.ids ? l.expert[run.matrix] : 0) * p.n + run.row;
         const int r0 = rows * team / teams, r1 = rows * (team + 1) / teams;
@@ -781,10 +843,9 @@ template <int T, int R, int KV, bool V16> __global__ void __launch_bounds__(DP_T
         }
         if (rows < run.rows) {
             run.row += rows;
-            run.left -= rows;
             run.rows -= rows;
         } else {
-            next_run(run, p, l);
+            more = next_run(run, p, l);
         }
     }
 }
@@ -845,14 +906,15 @@ uint32_t i4_shape(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t ex
     while (team > 1 && team > (few ? chunks / 2 : chunks))
         team /= 2;
     s->team = team;
-    const uint32_t lists = experts ? (uint32_t)(((8 * experts + 2 + 2 * pairs) + 15) / 16 * 16) : 0;
+    const uint32_t lists = experts ? (uint32_t)(((10 * experts + 4 + 2 * pairs) + 15) / 16 * 16) : 0;
     const uint32_t scales = few ? 0 : s->warps * I4_ROWS * 4 * (group == 32 ? 4 : group == 64 ? 2 : 1);
     const uint32_t sums = few ? (uint32_t)(s->team * DP_RUN * s->tokens * 4) : 2 * s->warps * 16 * (s->tokens + 2) * 4;
-    const uint32_t rest = scales + sums + lists;
+    const uint32_t ways = few ? 0 : s->warps * sizeof(Way), rest = scales + sums + ways + lists;
     s->depth = few ? 0 : 3 * s->warps * I4_STAGE + rest + 256 <= 227 * 1024 ? 3 : 2;
     s->scales = (uint32_t)(s->depth * s->warps * I4_STAGE);
     s->sums = s->scales + scales;
-    s->lists = s->sums + sums;
+    s->ways = s->sums + sums;
+    s->lists = s->ways + ways;
     return s->lists + lists;
 }
 
