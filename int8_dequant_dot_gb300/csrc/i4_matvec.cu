@@ -175,7 +175,7 @@ struct Walk {
     Runs run;
     int q, units;              // unit of the run, of so many: its parts, each `passes` times
     int passes, part_rows;
-    int columns, teams;
+    int columns, teams, most;  // most: rows of a unit
     bool more;
 };
 
@@ -184,9 +184,7 @@ __device__ __forceinline__ void set_units(Walk &w)
     if (!w.more)
         return;
     w.passes = (w.run.pairs + w.columns - 1) / w.columns;
-    // equal parts of up to 64 rows, as many for each team, unless they would have under 16
-    const int least = (w.run.rows + I4_ROWS - 1) / I4_ROWS;
-    const int parts = min((least + w.teams - 1) / w.teams * w.teams, (w.run.rows + 15) / 16);
+    const int parts = (w.run.rows + w.most - 1) / w.most;
     w.part_rows = (w.run.rows + parts - 1) / parts;
     w.units = (w.run.rows + w.part_rows - 1) / w.part_rows * w.passes;
 }
@@ -335,6 +333,7 @@ struct Way {
     Walk walk;
     Unit queue[4];
     int made;
+    uint32_t sums;             // where the warp's last sums lie
 };
 
 __device__ __forceinline__ void start_unit(Copies &c, Way *way, const I4Params &p, const I4Shape &s, const Lists &l, int chunk, int lane)
@@ -387,7 +386,6 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
 {
     extern __shared__ __align__(128) unsigned char i4_shared[];
     constexpr int STEPS = I4_CHUNK / 32, SP = STEPS / FL;            // SP: flushes, and scales of a row, in a stage
-    constexpr int SUM_STRIDE = 8 * NT + 2;
     constexpr bool EARLY = false;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tig = lane & 3;
     dev::follow_previous_kernel();
@@ -404,6 +402,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
         walk.teams = WARPS / s.team;
         walk.columns = 8 * NT;
         walk.q = warp / s.team;
+        // a team's share of the CTA's rows in units of whole 16, 64 at most
+        const int64_t share = (walk.run.end - walk.run.begin + walk.teams - 1) / walk.teams;
+        walk.most = share >= I4_ROWS ? I4_ROWS : ((int)share + 15) / 16 * 16;
         set_units(walk);
         if (lane == 0) {
             way->walk = walk;
@@ -417,7 +418,6 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
 
     const uint32_t ring = dev::smem_u32(i4_shared) + warp * s.depth * I4_STAGE;
     float *scales = reinterpret_cast<float *>(i4_shared + s.scales) + warp * I4_ROWS * SP;
-    float *sums = reinterpret_cast<float *>(i4_shared + s.sums);
     const Nibbles n = nibble_masks();
     // ldmatrix: lane's row of a tile, and the piece of 16 bytes that it points at in the first two steps
     const uint32_t place = (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
@@ -445,7 +445,6 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
     for (int i = 1; i < s.depth; ++i)
         copy_next();
 
-    int turn = 0;
     uint32_t stage = ring + place;
     for (int done = 0;; ++done) {
         if (c0 >= c1 && done > 0)                 // (no k: no copies begin a unit)
@@ -610,37 +609,70 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
             if (stage >= ring_end)
                 stage -= s.depth * I4_STAGE;
         }
-        // the team's sums, 16 rows at a time, in two places used in turn
-        const int team_thread = threadIdx.x % (32 * s.team), barrier = 1 + warp / s.team;
+        const auto finish = [&](float y, int row, int col) {
+            const int pair = p.ids ? l.pair[u.list + col] : u.list + col;
+            y *= __ldg(p.scale_x + x_row(p, pair));
+            if (p.bias)
+                y = __fadd_rn(y, __ldg(p.bias + u.matrix_row + row));
+            dev::store_as(p.y, p.y_dtype, pair * p.y_stride + u.row + row, y);
+        };
+        if (s.team == 1) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if (16 * t >= u.rows)
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int col = 8 * j + 2 * tig + i;
+                    if (col < u.count) {
+                        const int pair = p.ids ? l.pair[u.list + col] : u.list + col;
+                        const float sx = __ldg(p.scale_x + x_row(p, pair));
+                        const int64_t at = pair * p.y_stride + u.row;
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int row = 16 * t + 8 * h + g;
+                                if (row < u.rows) {
+                                    const float y = acc[t][j][2 * h + i] * sx;
+                                    dev::store_as(p.y, p.y_dtype, at + row, p.bias ? __fadd_rn(y, __ldg(p.bias + u.matrix_row + row)) : y);
+                                }
+                            }
+                    }
+                }
+            continue;
+        }
+        // The team's sums meet in the stages that were read last, which no copy is under way to, as
+        // [rows][columns]; where they do not hold all 64 rows, in two rounds.
+        constexpr int ROUNDS = 32 * NT * I4_ROWS > I4_STAGE ? 2 : 1, ROWS = I4_ROWS / ROUNDS, TILES = 4 / ROUNDS;
+        const int team_thread = threadIdx.x - 32 * (warp - part), barrier = 1 + warp / s.team;
+        const uint32_t offset = (stage == ring + place ? ring_end : stage - place) - I4_STAGE - dev::smem_u32(i4_shared);
+        float *own = reinterpret_cast<float *>(i4_shared + offset);
+        __syncwarp();                                       // (all lanes have read the stage)
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            if (r * ROWS >= u.rows)
                 break;
-            float *own = sums + (turn * WARPS + warp) * 16 * SUM_STRIDE, *first = own - part * 16 * SUM_STRIDE;
-            turn ^= 1;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float *at = own + g * SUM_STRIDE + 8 * j + 2 * tig;
-                *reinterpret_cast<float2 *>(at) = make_float2(acc[t][j][0], acc[t][j][1]);
-                *reinterpret_cast<float2 *>(at + 8 * SUM_STRIDE) = make_float2(acc[t][j][2], acc[t][j][3]);
-            }
-            if (s.team == 1)
-                __syncwarp();
-            else
-                asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * s.team) : "memory");
-            for (int i = team_thread; i < 16 * u.count; i += 32 * s.team) {
-                const int row = i & 15, col = i >> 4;
-                if (16 * t + row < u.rows) {
+            for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    float *at = own + (16 * t + g) * 8 * NT + 8 * j + 2 * tig;
+                    *reinterpret_cast<float2 *>(at) = make_float2(acc[r * TILES + t][j][0], acc[r * TILES + t][j][1]);
+                    *reinterpret_cast<float2 *>(at + 64 * NT) = make_float2(acc[r * TILES + t][j][2], acc[r * TILES + t][j][3]);
+                }
+            if (lane == 0)
+                way->sums = offset;
+            asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * s.team) : "memory");
+            for (int i = team_thread; i < ROWS * 8 * NT; i += 32 * s.team) {
+                const int row = r * ROWS + i / (8 * NT), col = i % (8 * NT);
+                if (row < u.rows && col < u.count) {
                     float y = 0.0f;
+#pragma unroll 4
                     for (int w = 0; w < s.team; ++w)
-                        y += first[(16 * w + row) * SUM_STRIDE + col];
-                    const int pair = p.ids ? l.pair[u.list + col] : u.list + col;
-                    y *= __ldg(p.scale_x + x_row(p, pair));
-                    if (p.bias)
-                        y = __fadd_rn(y, __ldg(p.bias + u.matrix_row + 16 * t + row));
-                    dev::store_as(p.y, p.y_dtype, pair * p.y_stride + u.row + 16 * t + row, y);
+                        y += reinterpret_cast<const float *>(i4_shared + (way - part + w)->sums)[i];
+                    finish(y, row, col);
                 }
             }
+            asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * s.team) : "memory");
         }
     }
     copies_wait<0>();
@@ -908,7 +940,7 @@ uint32_t i4_shape(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t ex
     s->team = team;
     const uint32_t lists = experts ? (uint32_t)(((10 * experts + 4 + 2 * pairs) + 15) / 16 * 16) : 0;
     const uint32_t scales = few ? 0 : s->warps * I4_ROWS * 4 * (group == 32 ? 4 : group == 64 ? 2 : 1);
-    const uint32_t sums = few ? (uint32_t)(s->team * DP_RUN * s->tokens * 4) : 2 * s->warps * 16 * (s->tokens + 2) * 4;
+    const uint32_t sums = few ? (uint32_t)(s->team * DP_RUN * s->tokens * 4) : 0;
     const uint32_t ways = few ? 0 : s->warps * sizeof(Way), rest = scales + sums + ways + lists;
     s->depth = few ? 0 : 3 * s->warps * I4_STAGE + rest + 256 <= 227 * 1024 ? 3 : 2;
     s->scales = (uint32_t)(s->depth * s->warps * I4_STAGE);
