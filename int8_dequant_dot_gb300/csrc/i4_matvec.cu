@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
 {
     extern __shared__ __align__(128) unsigned char i4_shared[];
     constexpr int STEPS = I4_CHUNK / 32, SP = STEPS / FL;            // SP: flushes, and scales of a row, in a stage
-    constexpr bool EARLY = false;
+    constexpr bool EARLY = NT <= 2 && WARPS == 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, tig = lane & 3;
     dev::follow_previous_kernel();
 
@@ -903,13 +903,11 @@ cudaError_t launch_dp4a(const I4Params &p, const I4Shape &s, const loom_launch &
     return launch_kernel(i4_dp4a_kernel<T, R, KV, V16>, done, p, s, L, stream);
 }
 
-constexpr int i4_warps(int nt) { return nt == 1 ? 16 : 8; }
-
-template <int NT> cudaError_t launch_nt(const I4Params &p, const I4Shape &s, const loom_launch &L, cudaStream_t stream)
+template <int NT, int WARPS> cudaError_t launch_nt(const I4Params &p, const I4Shape &s, const loom_launch &L, cudaStream_t stream)
 {
-    constexpr int W = i4_warps(NT), PAIR = NT == 4 ? 1 : 2;
-    return p.group == 32 ? launch_mma<NT, 1, W, PAIR>(p, s, L, stream)
-                         : p.group == 64 ? launch_mma<NT, 2, W, PAIR>(p, s, L, stream) : launch_mma<NT, 4, W, PAIR>(p, s, L, stream);
+    constexpr int PAIR = NT == 4 ? 1 : NT == 1 && WARPS == 8 ? 4 : 2;
+    return p.group == 32 ? launch_mma<NT, 1, WARPS, PAIR>(p, s, L, stream)
+                         : p.group == 64 ? launch_mma<NT, 2, WARPS, PAIR>(p, s, L, stream) : launch_mma<NT, 4, WARPS, PAIR>(p, s, L, stream);
 }
 
 int log2_floor(int64_t v)
@@ -929,11 +927,15 @@ uint32_t i4_shape(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t ex
     const int64_t each = experts <= 1 ? pairs : pairs <= experts / 4 ? 1 : (3 * pairs + 2 * named - 1) / (2 * named);
     s->tokens = each <= 2 ? (int)each : each <= 8 ? 8 : each <= 16 ? 16 : 32;
     const bool few = s->tokens <= 2;
-    s->warps = few ? DP_WARPS : i4_warps(s->tokens / 8);
+    // Eight warps with 255 registers each load a stage's weights before they convert its tokens; sixteen hide more where
+    // each has rows of its own (measured, 8 tokens: 8192 x 16384 21.3 us by 8 warps, 22.3 by 16, 65536 x 2048 21.1 and
+    // 23.3; 32 tokens to 8 of 64 experts of 2048 x 4096 70 and 64).
+    const int64_t rows = named * n / sms;
+    s->warps = few ? DP_WARPS : s->tokens == 8 && rows >= 12 * I4_ROWS ? 16 : 8;
     const int64_t chunk = few ? DP_CHUNK : I4_CHUNK, chunks = (k + chunk - 1) / chunk;
     // A team for each 48 rows of a CTA or more: its warps meet after each 64 rows, the fewer the cheaper.
     // The dp4a kernel's warps take two chunks each, where there are as many.
-    const int64_t units = named * n / sms / (3 * I4_ROWS / 4);
+    const int64_t units = rows / (3 * I4_ROWS / 4);
     int team = few ? s->warps : s->warps >> log2_floor(units < 1 ? 1 : units > s->warps ? s->warps : units);
     while (team > 1 && team > (few ? chunks / 2 : chunks))
         team /= 2;
@@ -978,9 +980,9 @@ cudaError_t launch_i4_matvec(const I4Params &p, int64_t sms, const loom_launch &
     switch (s.tokens) {
     case 1: return s.vec16 ? launch_dp4a<1, 8, 2, true>(p, s, L, stream) : launch_dp4a<1, 4, 1, false>(p, s, L, stream);
     case 2: return s.vec16 ? launch_dp4a<2, 4, 2, true>(p, s, L, stream) : launch_dp4a<2, 4, 1, false>(p, s, L, stream);
-    case 8: return launch_nt<1>(p, s, L, stream);
-    case 16: return launch_nt<2>(p, s, L, stream);
-    default: return launch_nt<4>(p, s, L, stream);
+    case 8: return s.warps == 16 ? launch_nt<1, 16>(p, s, L, stream) : launch_nt<1, 8>(p, s, L, stream);
+    case 16: return launch_nt<2, 8>(p, s, L, stream);
+    default: return launch_nt<4, 8>(p, s, L, stream);
     }
 }
 
