@@ -206,3 +206,63 @@ def test_history_rows_apart(env):
     buffer = torch.randint(0, 300, (4, 64), device="cuda", dtype=torch.int32)
     view = buffer[:, 5:25]
     assert torch.equal(loom.loom_adjust_logits(logits, history=view, repetition=1.5), loom.loom_adjust_logits(logits, history=view.contiguous(), repetition=1.5))
+
+
+# many rows: a kernel that copies, then one for the marked tokens alone, by a table or (long histories) a word a token
+@pytest.mark.parametrize("rows,vocab,n,biases,masks", [(320, 2000, 300, 9, 0), (330, 9000, 9000, 1024, 3), (400, 3001, 12000, 5, 2), (310, 70001, 11000, 20, 2), (305, 40, 10240, 0, 1),
+                                                       (306, 64, 0, 1024, 0), (700, 1, 5, 3, 1)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_many_rows(env, rows, vocab, n, biases, masks, dtype):
+    torch, loom = env
+    g = torch.Generator(device="cuda").manual_seed(vocab + rows)
+    logits = (torch.randn(rows, vocab, generator=g, device="cuda") * 3).to(getattr(torch, dtype))
+    kw = everything(torch, rows, vocab, n, biases, masks, rows + vocab)
+    some = torch.randperm(rows, generator=g, device="cuda")[:12].sort()[0]
+    at = lambda r: {k: v[r] if isinstance(v, torch.Tensor) and k != "mask" else v for k, v in kw.items()}   # noqa: E731
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = loom.loom_adjust_logits(logits, error=err, **kw)
+    assert same(torch, y[some], definition(torch, logits[some], **at(some))) and int(err) == 0
+    # each row by itself is the same row
+    for lo in range(0, rows, 64):
+        part = torch.arange(lo, min(lo + 64, rows), device="cuda")
+        assert same(torch, loom.loom_adjust_logits(logits[part], **at(part)), y[part])
+    copy = logits.clone()
+    assert loom.loom_adjust_logits(copy, y=copy, **kw) is copy and same(torch, copy, y)
+    wide = torch.full((rows, vocab + 7), 7.5, dtype=logits.dtype, device="cuda")
+    wide[:, 3:3 + vocab] = logits
+    out = torch.full((rows, vocab + 4), 9.5, dtype=logits.dtype, device="cuda")
+    loom.loom_adjust_logits(wide[:, 3:3 + vocab], y=out[:, 1:1 + vocab], **kw)
+    assert same(torch, out[:, 1:1 + vocab], y) and bool((out[:, 0] == 9.5).all()) and bool((out[:, 1 + vocab:] == 9.5).all())
+    loom.loom_adjust_logits(wide[:, 3:3 + vocab], y=wide[:, 3:3 + vocab], **kw)
+    assert same(torch, wide[:, 3:3 + vocab], y) and bool((wide[:, :3] == 7.5).all()) and bool((wide[:, 3 + vocab:] == 7.5).all())
+    kw["lengths"][rows - 1] = n + 1
+    if n:
+        loom.loom_adjust_logits(logits, error=err, **kw)
+        assert int(err) == loom.LOOM_DEVERR_COUNT_RANGE
+
+
+def test_kernels_in_a_row(env):
+    # inputs written by the kernel before, at once: many rows' second kernel begins before its first has ended
+    torch, loom = env
+    rows, vocab, n = 400, 20000, 600
+    logits = torch.randn(rows, vocab, device="cuda")
+    history = torch.zeros(rows, n, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    for turn in range(20):
+        g = torch.Generator(device="cuda").manual_seed(turn)
+        new = torch.randint(0, vocab, (rows, n), generator=g, device="cuda", dtype=torch.int32)
+        torch.cuda.synchronize()
+        history.copy_(new)
+        lengths.fill_(n - turn)
+        logits.copy_(logits.flip(0))
+        y = loom.loom_adjust_logits(logits, history=history, lengths=lengths, repetition=1.5, presence=0.25)
+        z = loom.loom_adjust_logits(y, history=history, frequency=0.5)
+        token, _ = loom.loom_sample_tokens(z, torch.zeros(rows, device="cuda"), temperature=0.0)
+        seen = torch.zeros(rows, vocab + 1, dtype=torch.bool, device="cuda").scatter_(1, history[:, :n - turn].long(), True)[:, :vocab]
+        count = torch.zeros(rows, vocab, device="cuda").scatter_add_(1, history.long(), torch.ones(rows, n, device="cuda"))
+        # (a quotient by way of 64 bits: torch divides f32 by a number as a product with its reciprocal)
+        want = torch.where(seen, torch.where(logits > 0, (logits.double() / 1.5).float(), logits * 1.5), logits)
+        first = torch.zeros(rows, vocab, device="cuda").scatter_add_(1, history[:, :n - turn].long(), torch.ones(rows, n - turn, device="cuda"))
+        want = torch.where(first > 0, want - 0.25, want)
+        want = torch.where(count > 0, want - 0.5 * count, want)
+        assert torch.equal(z, want) and torch.equal(token.long(), want.argmax(1))
