@@ -177,6 +177,6 @@ struct AdjustParams {
     int32_t *error;
 };
 bool adjust_geometry(int64_t rows, int32_t vocab, bool marks, int64_t sms, loom_launch *out);
-cudaError_t launch_adjust(const AdjustParams &p, int32_t dtype, int64_t sms, const loom_launch &L, cudaStream_t stream);
+cudaError_t launch_adjust(const AdjustParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream);
 
 }  // namespace loom

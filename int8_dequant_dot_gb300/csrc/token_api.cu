@@ -723,5 +723,5 @@ extern "C" loom_status loom_adjust_logits(const void *d_logits, int32_t dtype, i
     loom_launch L;
     if (!adjust_geometry(rows, vocab, p.tokens || p.bias_ids, sms, &L))
         return LOOM_ERR_SHAPE;
-    return of_cuda(launch_adjust(p, dtype, sms, L, static_cast<cudaStream_t>(stream)));
+    return of_cuda(launch_adjust(p, dtype, L, static_cast<cudaStream_t>(stream)));
 }
