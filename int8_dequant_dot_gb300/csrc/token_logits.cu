@@ -9,9 +9,9 @@
 //    is the slice's on a list of its own, and marks the list's tokens, one word a token in shared memory:
 //    bits 0..19 occurrences behind the prompt, bit 20 seen in the prompt, bits 21..31 the bias entry (AL_ENTRY - its
 //    place, so that the largest is the first of several).  Sums and maxima of whole numbers: their order does not
-//    matter.  When the slice is copied the lists' tokens are adjusted, out of L2; of several threads that come upon a
-//    token, the one that exchanges its mark for zero does it.  The lists keep warps full: 1 token of 19 is a given
-//    slice's, and 32 of them cost as much as one.
+//    matter.  Those that mark a token first stay on the list, and when the slice is copied the lists' tokens are
+//    adjusted, out of L2.  (Histories of more than 4096 tokens take the lists a batch at a time, and all of the
+//    slice's marks are looked through.)  The lists keep warps full: 1 token of 19 is a given slice's, and 32 of them cost as much as one.
 //
 // Measured (f32)
 //   1 x 32768, history 2000, biases, a mask   AL_T1 us
@@ -132,8 +132,7 @@ __global__ void __launch_bounds__(AL_THREADS, 2) adjust_kernel(const AdjustParam
     __syncthreads();
 
     // The history's tokens of this warp that are the slice's, a batch at a time, on the warp's list as places in the
-    // slice, with bit 15 for those of the prompt.  Where there is one batch alone the list is made once.
-    // (A row's last slice may begin past the row.)
+    // slice, with bit 15 for those of the prompt.  (A row's last slice may begin past the row.)
     const uint32_t begin = (uint32_t)min(max(first, 0), p.vocab), count = (uint32_t)min(first + SLICE, p.vocab) - begin;
     const int lane = threadIdx.x & 31;
     uint16_t *list = reinterpret_cast<uint16_t *>(marks + SLICE) + (threadIdx.x >> 5) * LIST;
@@ -154,43 +153,63 @@ __global__ void __launch_bounds__(AL_THREADS, 2) adjust_kernel(const AdjustParam
         }
         __syncwarp();
     };
-    const auto each_token = [&](bool again, auto f) {
-        for (int i0 = threadIdx.x; i0 - lane < s.length; i0 += AL_BATCH * AL_THREADS) {
-            if (s.length > AL_BATCH * AL_THREADS && (again || i0 >= AL_BATCH * AL_THREADS))
+    const auto load_batch = [&](int i0) {
 #pragma unroll
-                for (int j = 0; j < AL_BATCH; ++j)
-                    early[j] = i0 + j * AL_THREADS < s.length ? (uint32_t)__ldg(tokens + i0 + j * AL_THREADS) : AL_NONE;
-            if (!again || s.length > AL_BATCH * AL_THREADS)
-                make_list(i0);
-            for (int i = lane; i < listed; i += 32)
-                f((uint32_t)list[i]);
+        for (int j = 0; j < AL_BATCH; ++j)
+            early[j] = i0 + j * AL_THREADS < s.length ? (uint32_t)__ldg(tokens + i0 + j * AL_THREADS) : AL_NONE;
+    };
+    bool fresh_bias[AL_MAX_BIASES / AL_THREADS];
+    if (MARKS) {
+        for (int i0 = threadIdx.x; i0 - lane < s.length; i0 += AL_BATCH * AL_THREADS) {
+            if (i0 >= AL_BATCH * AL_THREADS)
+                load_batch(i0);
+            make_list(i0);
+            if (s.length > AL_BATCH * AL_THREADS) {
+                for (int l = lane; l < listed; l += 32) {
+                    const uint32_t t = list[l];
+                    if (t & 0x8000u)
+                        atomicOr(marks + (t & 0x7fffu), AL_SEEN);
+                    else
+                        atomicAdd(marks + t, 1u);
+                }
+                __syncwarp();
+                continue;
+            }
+            // those that mark a token first stay on the list
+            int kept = 0;
+            for (int l = 0; l < listed; l += 32) {
+                uint32_t t = 0, old = 1;
+                if (l + lane < listed) {
+                    t = list[l + lane];
+                    old = t & 0x8000u ? atomicOr(marks + (t & 0x7fffu), AL_SEEN) : atomicAdd(marks + t, 1u);
+                }
+                const unsigned those = __ballot_sync(dev::FULL_MASK, old == 0);
+                if (old == 0)
+                    list[kept + __popc(those & ((1u << lane) - 1u))] = (uint16_t)(t & 0x7fffu);
+                kept += __popc(those);
+            }
+            listed = kept;
             __syncwarp();
         }
-    };
-    const auto each_bias = [&](auto f) {
-        for (int i = threadIdx.x; i < p.biases; i += AL_THREADS) {
-            const uint32_t token = (uint32_t)(i < AL_THREADS ? id : __ldg(ids + i));
-            if (token - begin < count)
-                f(token - (uint32_t)first, i);
-        }
-    };
-    if (MARKS) {
-        each_token(false, [&](uint32_t t) {
-            if (t & 0x8000u)
-                atomicOr(marks + (t & 0x7fffu), AL_SEEN);
-            else
-                atomicAdd(marks + t, 1u);
-        });
         // the first of several entries stays: theirs are the upper bits, whatever the lower ones count meanwhile
-        each_bias([&](uint32_t t, int i) {
-            const uint32_t entry = AL_ENTRY - (uint32_t)i;
-            for (uint32_t old = marks[t]; (old >> 21) < entry;) {
-                const uint32_t now = atomicCAS(marks + t, old, (old & (AL_SEEN | AL_COUNT)) | (entry << 21));
-                if (now == old)
-                    break;
-                old = now;
+#pragma unroll
+        for (int j = 0; j < AL_MAX_BIASES / AL_THREADS; ++j) {
+            const int i = threadIdx.x + j * AL_THREADS;
+            fresh_bias[j] = false;
+            if (i < p.biases) {
+                const uint32_t token = (uint32_t)(j == 0 ? id : __ldg(ids + i)), entry = AL_ENTRY - (uint32_t)i;
+                uint32_t *mark = marks + (token - (uint32_t)first);
+                if (token - begin < count)
+                    for (uint32_t old = *mark; (old >> 21) < entry;) {
+                        const uint32_t now = atomicCAS(mark, old, (old & (AL_SEEN | AL_COUNT)) | (entry << 21));
+                        if (now == old) {
+                            fresh_bias[j] = old == 0;
+                            break;
+                        }
+                        old = now;
+                    }
             }
-        });
+        }
     }
     if (!in_place || s.mask) {
 #pragma unroll
@@ -225,14 +244,25 @@ __global__ void __launch_bounds__(AL_THREADS, 2) adjust_kernel(const AdjustParam
     }
     if (MARKS) {
         __syncthreads();
-        const auto adjust = [&](uint32_t place) {
-            const uint32_t mark = marks[place] ? atomicExch(marks + place, 0u) : 0u;
+        const auto adjust = [&](uint32_t place, uint32_t mark) {
             const int t = first + (int)place;
             if (mark && (!s.mask || ((mask[(t >> 5) - word0] >> (t & 31)) & 1)))
                 y[t] = dev::from_f32<E>(adjusted(dev::to_f32(x[t]), mark, s, bias));
         };
-        each_token(true, [&](uint32_t t) { adjust(t & 0x7fffu); });
-        each_bias([&](uint32_t t, int) { adjust(t); });
+        if (s.length <= AL_BATCH * AL_THREADS) {
+            for (int l = lane; l < listed; l += 32)
+                adjust(list[l], marks[list[l]]);
+#pragma unroll
+            for (int j = 0; j < AL_MAX_BIASES / AL_THREADS; ++j)
+                if (fresh_bias[j]) {
+                    const uint32_t place = (uint32_t)(j == 0 ? id : __ldg(ids + threadIdx.x + j * AL_THREADS)) - (uint32_t)first;
+                    adjust(place, marks[place]);
+                }
+        } else {                                // a long history's tokens were not kept: all marks are looked through
+            for (int i = threadIdx.x; i < SLICE; i += AL_THREADS)
+                if (marks[i])
+                    adjust(i, marks[i]);
+        }
     }
 }
 
