@@ -300,12 +300,12 @@ typedef enum loom_score { LOOM_SCORE_SOFTMAX = 0, LOOM_SCORE_SIGMOID = 1 } loom_
  *   choice    by score[e] + d_bias[e] (f32 [experts], NULL: by the score): with more than one group
  *             (`groups` equal runs of experts), the top_groups groups whose group_best (1 or 2)
  *             best experts have the largest sum stay (a group with fewer counts those it has);
- *             then the top_k best experts of those, falling.  The order is that of the real
- *             numbers; equal ones go to the lower index.
+ *             then the top_k best experts of those, falling.  With no bias, or the same for all, experts
+ *             (and groups by their best one) have the order of their logits; else sums are compared as
+ *             64-bit floating point has them.  Equal ones go to the lower index.
  *   weight    = factor * score, divided by the sum of the chosen scores where `renormalise`
  * d_ids int32 and d_weights f32 [tokens][top_k]; where fewer than top_k can be chosen the rest
  * are -1 and 0, which loom_routed_combine and loom_i4_matvec_routed take as missing routes.
- * (A row of d_bias values beyond 2^20 in size leaves scores no room in 64 bits.)
  * d_counts: int32 [experts] or NULL; the number of tokens that go to each expert is added to it (what a
  * bias for balance is set by).
  * Errors: NULL logits, ids or weights -> LOOM_ERR_NULL; misaligned -> LOOM_ERR_ALIGN; tokens < 0 or

@@ -1,5 +1,16 @@
 // token_route.cu -- routing: the experts of each token and their weights from logits, and the
-// gradient of those weights (sm_103a).  One warp takes a token, its scores in shared memory.
+// gradient of those weights (sm_103a).
+//
+// Design
+//  * A warp takes a token, a lane a run of neighbouring experts in registers (1 to 32 of them): groups of
+//    experts are runs of lanes, and a tie's lowest expert is the lowest lane's.
+//  * The choice is that of real numbers, made in f32 where f32 tells: with no bias (or the same for all) the order of scores
+//    is that of the logits; else the scores plus bias are ranked with a bound of their error, and a token whose
+//    order it leaves open (two neighbours among the chosen and the next one, or groups at the cut, nearer than that)
+//    is ranked again in 64 bits.  On the 64-bit units of this GPU (2 lanes an SM and clock) all tokens would
+//    take 640 us of 16384 x 256; of normal logits one in a thousand does.
+//  * The largest of what is left is found by a maximum over the lane's keys (floats as ordered whole numbers) and one over
+//    the warp, top_k times.  What bounds many tokens is the instructions of that, not the logits' bytes.
 #include <cfloat>
 
 #include "token_ops.cuh"
@@ -52,82 +63,293 @@ __device__ __forceinline__ double score_of(int kind, double l, double m, double 
     return kind == LOOM_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / sum;
 }
 
-template <typename E> __global__ void __launch_bounds__(32 * RT_WARPS) route_kernel(const RouteParams p)
+// The experts of a token in 64 bits: the chosen one of each lane below top_k, or -1.  choose: [2][experts], the warp's.
+// ranked: experts by scores and bias, else by logits; by_sums: groups by scores and bias, else by logits.
+template <typename E>
+__device__ __noinline__ int route_exactly(const RouteParams &p, const E *l, double *choose, int lane, bool ranked, bool by_sums)
 {
-    extern __shared__ double route_smem[];
+    double *group = choose + p.experts;
+    double m = -INFINITY, sum = 0;
+    for (int e = lane; e < p.experts; e += 32)
+        m = fmax(m, (double)logit_of(dev::to_f32(l[e])));
+    m = warp_max(m);
+    if (p.score == LOOM_SCORE_SOFTMAX && m > -INFINITY) {
+        for (int e = lane; e < p.experts; e += 32)
+            sum += exp((double)logit_of(dev::to_f32(l[e])) - m);
+        sum = warp_sum(sum);
+    }
+    for (int e = lane; e < p.experts; e += 32) {
+        const float v = logit_of(dev::to_f32(l[e]));
+        const float b = p.bias ? logit_of(p.bias[e]) : 0.0f;
+        choose[e] = v == -INFINITY || b == -INFINITY ? -INFINITY : ranked || by_sums ? score_of(p.score, v, m, sum) + (double)b : (double)v;
+    }
+    __syncwarp();
+    if (p.groups > 1) {
+        const int size = p.experts / p.groups;
+        for (int g = lane; g < p.groups; g += 32) {
+            double a = -INFINITY, b = -INFINITY;
+            for (int i = 0; i < size; ++i) {
+                const double v = choose[g * size + i];
+                b = fmax(b, fmin(a, v));
+                a = fmax(a, v);
+            }
+            group[g] = p.group_best == 2 && b > -INFINITY ? a + b : a;
+        }
+        __syncwarp();
+        for (int i = 0; i < p.top_groups; ++i) {
+            const int g = warp_argmax(group, p.groups, lane);
+            __syncwarp();
+            if (g >= 0 && lane == 0)
+                group[g] = NAN;        // kept: never the largest again
+            __syncwarp();
+        }
+        for (int e = lane; e < p.experts; e += 32)
+            if (!isnan(group[e / size]))
+                choose[e] = -INFINITY;
+            else if (!ranked && choose[e] > -INFINITY)
+                choose[e] = (double)logit_of(dev::to_f32(l[e]));
+        __syncwarp();
+    }
+    int mine = -1;
+    for (int i = 0; i < p.top_k; ++i) {
+        const int e = warp_argmax(choose, p.experts, lane);
+        if (lane == i)
+            mine = e;
+        __syncwarp();
+        if (e >= 0 && lane == 0)
+            choose[e] = -INFINITY;
+        __syncwarp();
+    }
+    return mine;
+}
+
+__device__ __forceinline__ float warp_max_f(float v)
+{
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(dev::FULL_MASK, v, m));
+    return v;
+}
+__device__ __forceinline__ float warp_sum_f(float v)
+{
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1)
+        v += __shfl_xor_sync(dev::FULL_MASK, v, m);
+    return v;
+}
+
+// A float as a whole number of the same order; INT_MIN is what cannot be chosen.
+__device__ __forceinline__ int key_of(float v)
+{
+    const int b = __float_as_int(v);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float float_of(int key) { return __int_as_float(key ^ ((key >> 31) & 0x7fffffff)); }
+constexpr int RT_NONE = -0x7fffffff - 1;
+
+// A lane's PER neighbouring values of a row of n, -infinity past it.  `packs`: accesses of several elements are aligned
+// and lie in the row or past it as a whole.
+template <typename E, int PER> __device__ __forceinline__ void load_run(const E *row, int n, bool packs, int lane, float (&v)[PER])
+{
+    constexpr int C = PER < 16 / (int)sizeof(E) ? PER : 16 / (int)sizeof(E);
+    struct alignas(sizeof(E) * C) Pack {
+        E e[C];
+    };
+    if (packs) {
+#pragma unroll
+        for (int i = 0; i < PER / C; ++i) {
+            const int at = lane * PER + i * C;
+            Pack q;
+            if (at < n)
+                q = *reinterpret_cast<const Pack *>(row + at);
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                v[i * C + j] = at < n ? dev::to_f32(q.e[j]) : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            v[j] = lane * PER + j < n ? dev::to_f32(row[lane * PER + j]) : -INFINITY;
+    }
+}
+
+template <typename E, int PER> __host__ __device__ bool packs_of(const void *row, int64_t stride, int n)
+{
+    constexpr int C = PER < 16 / (int)sizeof(E) ? PER : 16 / (int)sizeof(E);
+    return reinterpret_cast<uintptr_t>(row) % (sizeof(E) * C) == 0 && stride % C == 0 && n % C == 0;
+}
+
+template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) route_kernel(const RouteParams p, int close, int packs)
+{
+    extern __shared__ double route_smem[];           // [warps][2][experts] where f32 may not tell, then the counts
     dev::follow_previous_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    double *choose = route_smem + (size_t)warp * 2 * p.experts, *group = choose + p.experts;
+    double *exact = route_smem + (size_t)warp * 2 * p.experts;
+    int *counts = reinterpret_cast<int *>(route_smem + (close ? (size_t)RT_WARPS * 2 * p.experts : 0));
+    if (p.counts) {
+        for (int e = threadIdx.x; e < p.experts; e += 32 * RT_WARPS)
+            counts[e] = 0;
+        __syncthreads();
+    }
+    const bool soft = p.score == LOOM_SCORE_SOFTMAX;
+    // the bias of the lane's experts, its size, and whether it is the same for all
+    float bias[PER], size = 0.0f;
+    bool ranked = false;                             // by scores and bias; else by logits
+    if (p.bias) {
+        float low = INFINITY, high = -INFINITY;
+        load_run<float, PER>(p.bias, p.experts, packs_of<float, PER>(p.bias, 0, p.experts), lane, bias);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            bias[j] = logit_of(bias[j]);
+            if (bias[j] > -INFINITY) {
+                low = fminf(low, bias[j]);
+                high = fmaxf(high, bias[j]);
+            }
+        }
+        low = -warp_max_f(-low);
+        high = warp_max_f(high);
+        ranked = low < high;
+        size = fmaxf(fabsf(low), fabsf(high));
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            bias[j] = 0.0f;
+    }
+    const bool by_sums = p.groups > 1 && (p.group_best == 2 || ranked);
+    const bool scored = ranked || by_sums;
     for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < p.tokens; t += (int64_t)gridDim.x * RT_WARPS) {
         const E *l = static_cast<const E *>(p.logits) + t * p.stride;
-        double m = -INFINITY, sum = 0;
-        for (int e = lane; e < p.experts; e += 32)
-            m = fmax(m, (double)logit_of(dev::to_f32(l[e])));
-        m = warp_max(m);
-        if (p.score == LOOM_SCORE_SOFTMAX && m > -INFINITY) {
-            for (int e = lane; e < p.experts; e += 32)
-                sum += exp((double)logit_of(dev::to_f32(l[e])) - m);
-            sum = warp_sum(sum);
+        float v[PER], score[PER];
+        load_run<E, PER>(l, p.experts, packs, lane, v);
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            v[j] = logit_of(v[j]);
+            m = fmaxf(m, v[j]);
         }
-        for (int e = lane; e < p.experts; e += 32) {
-            const float v = logit_of(dev::to_f32(l[e]));
-            const float b = p.bias ? logit_of(p.bias[e]) : 0.0f;
-            choose[e] = v == -INFINITY || b == -INFINITY ? -INFINITY : score_of(p.score, v, m, sum) + (double)b;
+        m = warp_max_f(m);
+        float sum = 0.0f, largest = 1.0f;
+        if (soft && (scored || !p.renormalise)) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                score[j] = v[j] > -INFINITY ? expf(v[j] - m) : 0.0f;
+                sum += score[j];
+            }
+            sum = warp_sum_f(sum);
         }
-        __syncwarp();
+        if (scored) {
+            if (soft) {
+                largest = 1.0f / sum;
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    score[j] = __fdiv_rn(score[j], sum);
+            } else {
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    score[j] = __frcp_rn(1.0f + expf(-v[j]));
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                score[j] += bias[j];
+        }
+        // Bound of a score's error.  Sigmoid: the exponential's 2 units in the last place, two roundings: below
+        // 2^-21.  Softmax: exponential and difference, s |l - m| 2^-24 <= 0.37 2^-24 and 4 2^-24 s; the sum's terms the same
+        // on average (their |l - m| is an entropy, below 7) and 37 + 5 roundings; below 2^-18 (s + 2^-7).  And the
+        // rounding of the sum with the bias.
+        const float error = (soft ? 3.8146973e-6f * (largest + 0.0078125f) : 4.7683716e-7f) + 5.9604645e-8f * (size + largest);
+        int key[PER];
+        bool open = false;                           // f32 does not tell
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            key[j] = v[j] == -INFINITY || bias[j] == -INFINITY ? RT_NONE : key_of(ranked ? score[j] : v[j]);
         if (p.groups > 1) {
-            const int size = p.experts / p.groups;
-            for (int g = lane; g < p.groups; g += 32) {
-                double a = -INFINITY, b = -INFINITY;
-                for (int i = 0; i < size; ++i) {
-                    const double v = choose[g * size + i];
-                    b = fmax(b, fmin(a, v));
-                    a = fmax(a, v);
+            const int members = p.experts / p.groups, lanes = members / PER;
+            if (lanes * PER == members && (lanes & (lanes - 1)) == 0 && lanes > 0 && p.groups <= 32) {
+                float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const float q = key[j] == RT_NONE ? -INFINITY : by_sums ? score[j] : v[j];
+                    b = fmaxf(b, fminf(a, q));
+                    a = fmaxf(a, q);
                 }
-                group[g] = p.group_best == 2 && b > -INFINITY ? a + b : a;
+                for (int d = 1; d < lanes; d <<= 1) {
+                    const float oa = __shfl_xor_sync(dev::FULL_MASK, a, d), ob = __shfl_xor_sync(dev::FULL_MASK, b, d);
+                    b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+                    a = fmaxf(a, oa);
+                }
+                const float of = p.group_best == 2 && b > -INFINITY ? a + b : a;
+                const float mine = __shfl_sync(dev::FULL_MASK, of, lane < p.groups ? lane * lanes : 0);
+                int above = 0;                       // groups that come before this lane's
+                for (int g = 0; g < p.groups; ++g) {
+                    const float other = __shfl_sync(dev::FULL_MASK, of, g * lanes);
+                    above += other > mine || (other == mine && g < lane);
+                }
+                const bool stays = lane < p.groups && above < p.top_groups && mine > -INFINITY;
+                const float lowest = -warp_max_f(stays ? -mine : -INFINITY);
+                const float highest = warp_max_f(lane < p.groups && !stays ? mine : -INFINITY);
+                open = by_sums && lowest - highest <= 2.5f * (float)p.group_best * error;      // (two sums, and their own rounding)
+                const unsigned kept = __ballot_sync(dev::FULL_MASK, stays);
+                if (!((kept >> (lane / lanes)) & 1u))
+#pragma unroll
+                    for (int j = 0; j < PER; ++j)
+                        key[j] = RT_NONE;
+            } else {
+                open = true;                         // groups that are no runs of lanes
             }
-            __syncwarp();
-            for (int i = 0; i < p.top_groups; ++i) {
-                const int g = warp_argmax(group, p.groups, lane);
-                __syncwarp();
-                if (g >= 0 && lane == 0)
-                    group[g] = NAN;        // kept: never the largest again
-                __syncwarp();
+        }
+        int mine = -1, before = 0;
+        if (!open)
+            for (int i = 0; i < p.top_k + (ranked ? 1 : 0); ++i) {
+                int best = key[0];
+#pragma unroll
+                for (int j = 1; j < PER; ++j)
+                    best = max(best, key[j]);
+                const int top = __reduce_max_sync(dev::FULL_MASK, best);
+                if (top == RT_NONE)
+                    break;
+                if (ranked && i > 0 && float_of(before) - float_of(top) <= 2.0f * error) {
+                    open = true;
+                    break;
+                }
+                before = top;
+                const int from = __ffs(__ballot_sync(dev::FULL_MASK, best == top)) - 1;
+                int at = 0;
+#pragma unroll
+                for (int j = PER - 1; j >= 0; --j)
+                    at = key[j] == top ? j : at;
+                if (lane == from)
+#pragma unroll
+                    for (int j = 0; j < PER; ++j)
+                        key[j] = j == at ? RT_NONE : key[j];
+                at = __shfl_sync(dev::FULL_MASK, from * PER + at, from);
+                if (lane == i && i < p.top_k)
+                    mine = at;
             }
-            for (int e = lane; e < p.experts; e += 32)
-                if (!isnan(group[e / size]))
-                    choose[e] = -INFINITY;
-            __syncwarp();
-        }
-        int mine = -1;
-        for (int i = 0; i < p.top_k; ++i) {
-            const int e = warp_argmax(choose, p.experts, lane);
-            if (lane == i)
-                mine = e;
-            __syncwarp();
-            if (e >= 0 && lane == 0)
-                choose[e] = -INFINITY;
-            __syncwarp();
-        }
-        double w = 0;
-        const double v = mine >= 0 ? (double)logit_of(dev::to_f32(l[mine])) : -INFINITY;
-        if (p.renormalise && p.score == LOOM_SCORE_SOFTMAX)
-            m = warp_max(v);
-        const double low = warp_max(v);
-        if (mine >= 0) {
-            // sigmoids far below zero are exponentials, which may be taken relative to the largest
-            const bool far = p.renormalise && p.score == LOOM_SCORE_SIGMOID && low < -600;
-            w = far ? exp(v - low) : score_of(p.score, v, m, p.renormalise ? 1.0 : sum);
-        }
+        if (open)
+            mine = route_exactly<E>(p, l, exact, lane, ranked, by_sums);
+        // the weights of the chosen; renormalised, softmax scores are taken relative to the largest of them, and sigmoids
+        // far below zero (where they are exponentials) as well
+        const float lm = mine >= 0 ? logit_of(dev::to_f32(l[mine])) : -INFINITY;
+        float w = 0.0f;
+        const float top = p.renormalise ? warp_max_f(lm) : m;
+        if (mine >= 0)
+            w = soft || (p.renormalise && top < -60.0f) ? expf(lm - top) : __frcp_rn(1.0f + expf(-lm));
         if (p.renormalise)
-            w /= warp_sum(w);
+            w = __fdiv_rn(w, warp_sum_f(w));
+        else if (soft)
+            w = __fdiv_rn(w, sum);
         if (lane < p.top_k) {
             p.ids[t * p.top_k + lane] = mine;
-            p.weights[t * p.top_k + lane] = mine >= 0 ? (float)(w * p.factor) : 0.0f;
-            if (mine >= 0 && p.counts)
-                atomicAdd(p.counts + mine, 1);
+            p.weights[t * p.top_k + lane] = mine >= 0 ? w * p.factor : 0.0f;
+            if (p.counts && mine >= 0)
+                atomicAdd(counts + mine, 1);
         }
-        __syncwarp();
+    }
+    if (p.counts) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.experts; e += 32 * RT_WARPS)
+            if (counts[e])
+                atomicAdd(p.counts + e, counts[e]);
     }
 }
 
@@ -195,7 +417,7 @@ template <typename E> __global__ void __launch_bounds__(32 * RT_WARPS) route_gra
 bool route_geometry(int64_t tokens, int32_t experts, bool backward, int64_t sms, loom_launch *out)
 {
     *out = loom_launch{};
-    const int64_t ctas = (tokens + RT_WARPS - 1) / RT_WARPS, most = 4 * sms;
+    const int64_t ctas = (tokens + RT_WARPS - 1) / RT_WARPS, most = 8 * sms;
     out->grid[0] = (uint32_t)(ctas < most ? ctas : most);
     out->grid[1] = out->grid[2] = out->block[1] = out->block[2] = 1;
     out->block[0] = 32 * RT_WARPS;
@@ -207,11 +429,40 @@ bool route_geometry(int64_t tokens, int32_t experts, bool backward, int64_t sms,
     return true;
 }
 
+namespace {
+
+template <typename E, int PER> cudaError_t launch_per(const RouteParams &p, loom_launch L, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(route_kernel<E, PER>), 0, done);
+    if (e != cudaSuccess)
+        return e;
+    const bool close = p.bias || p.groups > 1;      // where f32 may not tell
+    L.smem_bytes = (uint32_t)((close ? RT_WARPS * 2 * p.experts * sizeof(double) : 0) + (p.counts ? p.experts * sizeof(int) : 0));
+    return launch_prepared(route_kernel<E, PER>, L, stream, p, (int)close, (int)packs_of<E, PER>(p.logits, p.stride, p.experts));
+}
+
+template <typename E> cudaError_t launch_e(const RouteParams &p, const loom_launch &L, cudaStream_t stream)
+{
+    const int per = (p.experts + 31) / 32;
+    if (per <= 1)
+        return launch_per<E, 1>(p, L, stream);
+    if (per <= 2)
+        return launch_per<E, 2>(p, L, stream);
+    if (per <= 4)
+        return launch_per<E, 4>(p, L, stream);
+    if (per <= 8)
+        return launch_per<E, 8>(p, L, stream);
+    return per <= 16 ? launch_per<E, 16>(p, L, stream) : launch_per<E, 32>(p, L, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_route(const RouteParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream)
 {
     if (dtype == LOOM_F32)
-        return launch_with(route_kernel<float>, L, stream, p);
-    return dtype == LOOM_F16 ? launch_with(route_kernel<__half>, L, stream, p) : launch_with(route_kernel<__nv_bfloat16>, L, stream, p);
+        return launch_e<float>(p, L, stream);
+    return dtype == LOOM_F16 ? launch_e<__half>(p, L, stream) : launch_e<__nv_bfloat16>(p, L, stream);
 }
 
 cudaError_t launch_route_grad(const RouteGradParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream)

@@ -46,19 +46,25 @@ def definition(torch, logits, top_k, score="softmax", bias=None, groups=1, top_g
     l = clean(torch, logits)
     t, e = l.shape
     choose = scores(torch, l, score)
+    ranked_by = choose
     if bias is not None:
-        choose = choose + clean(torch, bias)
-    choose = torch.where(l == -INF, torch.full_like(choose, -INF), choose)
+        b = clean(torch, bias)
+        choose = choose + b
+        ranked_by = choose if float(b[b > -INF].max()) > float(b[b > -INF].min()) else torch.where(b > -INF, l, torch.full_like(l, -INF))
+    else:
+        ranked_by = l           # (the order of the scores, and of those that 64 bits do not tell from zero)
+    choose, ranked_by = (torch.where(l == -INF, torch.full_like(choose, -INF), q) for q in (choose, ranked_by))
     top_groups = groups if top_groups is None else top_groups
     if top_groups < groups:
-        of = choose.view(t, groups, e // groups)
+        of = (choose if group_best == 2 else ranked_by).view(t, groups, e // groups)
         best = torch.sort(of, dim=2, descending=True)[0][:, :, :group_best]
         total = torch.where(best == -INF, torch.zeros_like(best), best).sum(2)
         total = torch.where(best[:, :, 0] == -INF, torch.full_like(total, -INF), total)
         kept = torch.sort(total, dim=1, descending=True, stable=True)[1][:, :top_groups]
         keep = torch.zeros_like(total, dtype=torch.bool).scatter_(1, kept, True)
-        choose = torch.where(keep[:, :, None], of, torch.full_like(of, -INF)).reshape(t, e)
-    ranked, ids = torch.sort(choose, dim=1, descending=True, stable=True)
+        of = ranked_by.view(t, groups, e // groups)
+        ranked_by = torch.where(keep[:, :, None], of, torch.full_like(of, -INF)).reshape(t, e)
+    ranked, ids = torch.sort(ranked_by, dim=1, descending=True, stable=True)
     ids, there = ids[:, :top_k], ranked[:, :top_k] > -INF
     chosen = torch.where(there, l.gather(1, ids), torch.full_like(ranked[:, :top_k], -INF))
     if renormalise:
