@@ -9,8 +9,12 @@
 //    order it leaves open (two neighbours among the chosen and the next one, or groups at the cut, nearer than that)
 //    is ranked again in 64 bits.  On the 64-bit units of this GPU (2 lanes an SM and clock) all tokens would
 //    take 640 us of 16384 x 256; of normal logits one in a thousand does.
-//  * The largest of what is left is found by a maximum over the lane's keys (floats as ordered whole numbers) and one over
-//    the warp, top_k times.  What bounds many tokens is the instructions of that, not the logits' bytes.
+//  * The chosen ones are found top_k + 1 times as the warp's maximum of the lanes' largest keys.  A key is a float as
+//    an ordered whole number whose last 5 to 10 bits are the expert's, so that the maximum names it; a lane has its keys
+//    sorted (16 and more are searched) and drops the first.  Where two neighbours differ in those bits alone (1 token
+//    in 200 of normal logits) the choice is made again with whole keys, and where f32 leaves sigmoids' order
+//    open, in 64 bits for those near the last one chosen.
+//    What bounds many tokens is the instructions of that, not the logits' bytes.
 #include <cfloat>
 
 #include "token_ops.cuh"
@@ -123,13 +127,6 @@ __device__ __noinline__ int route_exactly(const RouteParams &p, const E *l, doub
     return mine;
 }
 
-__device__ __forceinline__ float warp_max_f(float v)
-{
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(dev::FULL_MASK, v, m));
-    return v;
-}
 __device__ __forceinline__ float warp_sum_f(float v)
 {
 #pragma unroll
@@ -146,6 +143,26 @@ __device__ __forceinline__ int key_of(float v)
 }
 __device__ __forceinline__ float float_of(int key) { return __int_as_float(key ^ ((key >> 31) & 0x7fffffff)); }
 constexpr int RT_NONE = -0x7fffffff - 1;
+
+__device__ __forceinline__ float warp_max_f(float v) { return float_of(__reduce_max_sync(dev::FULL_MASK, key_of(v))); }      // (of no NaN)
+
+// Falling order of N keys, by the merging network of Batcher (1968).
+template <int N> __device__ __forceinline__ void sort_keys(int (&k)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (j + i + q < N && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
+                        const int a = k[j + i], b = k[j + i + q];
+                        k[j + i] = max(a, b);
+                        k[j + i + q] = min(a, b);
+                    }
+}
 
 // A lane's PER neighbouring values of a row of n, -infinity past it.  `packs`: accesses of several elements are aligned
 // and lie in the row or past it as a whole.
@@ -221,15 +238,15 @@ template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) 
         const E *l = static_cast<const E *>(p.logits) + t * p.stride;
         float v[PER], score[PER];
         load_run<E, PER>(l, p.experts, packs, lane, v);
-        float m = -INFINITY;
+        float m = -INFINITY, sum = 0.0f, largest = 1.0f;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
+        for (int j = 0; j < PER; ++j)
             v[j] = logit_of(v[j]);
-            m = fmaxf(m, v[j]);
-        }
-        m = warp_max_f(m);
-        float sum = 0.0f, largest = 1.0f;
         if (soft && (scored || !p.renormalise)) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                m = fmaxf(m, v[j]);
+            m = warp_max_f(m);
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 score[j] = v[j] > -INFINITY ? expf(v[j] - m) : 0.0f;
@@ -246,14 +263,14 @@ template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) 
             } else {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-                    score[j] = __frcp_rn(1.0f + expf(-v[j]));
+                    score[j] = __fdividef(1.0f, 1.0f + __expf(-v[j]));
             }
 #pragma unroll
             for (int j = 0; j < PER; ++j)
                 score[j] += bias[j];
         }
-        // Bound of a score's error.  Sigmoid: the exponential's 2 units in the last place, two roundings: below
-        // 2^-21.  Softmax: exponential and difference, s |l - m| 2^-24 <= 0.37 2^-24 and 4 2^-24 s; the sum's terms the same
+        // Bound of a score's error.  Sigmoid s: the exponential's 2 + 1.173 |l| units in the last place (2^-23), of
+        // which s (1 - s), 0.63 units at most, passes on; a rounding; the quotient's 2 units: below 2^-21.  Softmax: exponential and difference, s |l - m| 2^-24 <= 0.37 2^-24 and 4 2^-24 s; the sum's terms the same
         // on average (their |l - m| is an entropy, below 7) and 37 + 5 roundings; below 2^-18 (s + 2^-7).  And the
         // rounding of the sum with the bias.
         const float error = (soft ? 3.8146973e-6f * (largest + 0.0078125f) : 4.7683716e-7f) + 5.9604645e-8f * (size + largest);
@@ -297,13 +314,59 @@ template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) 
                 open = true;                         // groups that are no runs of lanes
             }
         }
-        int mine = -1, before = 0;
-        if (!open)
+        int mine = -1;
+        bool again = false;                          // the first bits of two keys are alike
+        float least = -INFINITY;                     // of the chosen ones, not above it
+        if (!open) {
+            constexpr int LOW = PER * 32 - 1;
+            int u[PER], own = RT_NONE, top = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                u[j] = key[j] == RT_NONE ? RT_NONE : (key[j] & ~LOW) | (LOW - (lane * PER + j));
+            if (PER <= 8)
+                sort_keys(u);
+            for (int i = 0; i <= p.top_k; ++i) {
+                int best = u[0];
+                if (PER > 8)
+#pragma unroll
+                    for (int j = 1; j < PER; ++j)
+                        best = max(best, u[j]);
+                top = __reduce_max_sync(dev::FULL_MASK, best);
+                if (top == RT_NONE || i == p.top_k)
+                    break;
+                own = lane == i ? top : own;
+                if (best == top) {
+                    if (PER <= 8) {
+#pragma unroll
+                        for (int j = 0; j + 1 < PER; ++j)
+                            u[j] = u[j + 1];
+                        u[PER - 1] = RT_NONE;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < PER; ++j)
+                            u[j] = u[j] == top ? RT_NONE : u[j];
+                    }
+                }
+            }
+            int next = __shfl_down_sync(dev::FULL_MASK, own, 1);
+            if (lane == p.top_k - 1)
+                next = top;
+            const bool pair = own != RT_NONE && next != RT_NONE;
+            again = __any_sync(dev::FULL_MASK, pair && (ranked ? float_of(own & ~LOW) - float_of(next | LOW) <= 2.0f * error : (own ^ next) <= LOW && (own ^ next) >= 0));
+            least = __shfl_sync(dev::FULL_MASK, own == RT_NONE ? -INFINITY : float_of(own & ~LOW), p.top_k - 1);
+            mine = own == RT_NONE ? -1 : LOW - (own & LOW);
+        }
+        if (again) {                                 // whole keys
+            int rest[PER], before = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                rest[j] = key[j];
+            mine = -1;
             for (int i = 0; i < p.top_k + (ranked ? 1 : 0); ++i) {
-                int best = key[0];
+                int best = rest[0];
 #pragma unroll
                 for (int j = 1; j < PER; ++j)
-                    best = max(best, key[j]);
+                    best = max(best, rest[j]);
                 const int top = __reduce_max_sync(dev::FULL_MASK, best);
                 if (top == RT_NONE)
                     break;
@@ -316,17 +379,56 @@ template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) 
                 int at = 0;
 #pragma unroll
                 for (int j = PER - 1; j >= 0; --j)
-                    at = key[j] == top ? j : at;
+                    at = rest[j] == top ? j : at;
                 if (lane == from)
 #pragma unroll
                     for (int j = 0; j < PER; ++j)
-                        key[j] = j == at ? RT_NONE : key[j];
+                        rest[j] = j == at ? RT_NONE : rest[j];
                 at = __shfl_sync(dev::FULL_MASK, from * PER + at, from);
                 if (lane == i && i < p.top_k)
                     mine = at;
             }
-        if (open)
-            mine = route_exactly<E>(p, l, exact, lane, ranked, by_sums);
+        }
+        if (open) {
+            // sigmoids: of those near enough to the least chosen one or above it, the lane's is taken in 64 bits
+            int near = 0;
+            if (again && !soft && least > -INFINITY) {
+                unsigned own = 0;
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    own |= (key[j] != RT_NONE && score[j] >= least - 4.0f * error) << j;
+                int run = __popc(own);
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int up = __shfl_up_sync(dev::FULL_MASK, run, d);
+                    run += lane >= d ? up : 0;
+                }
+                near = __shfl_sync(dev::FULL_MASK, run, 31);
+                if (near <= 32) {
+                    int *list = reinterpret_cast<int *>(exact);
+                    run -= __popc(own);
+                    for (unsigned left = own; left; left &= left - 1u)
+                        list[run++] = lane * PER + __ffs(left) - 1;
+                    __syncwarp();
+                    const int e = lane < near ? list[lane] : 0;
+                    const double b = p.bias ? (double)logit_of(p.bias[e]) : 0.0;
+                    const double of = lane < near ? score_of(LOOM_SCORE_SIGMOID, (double)logit_of(dev::to_f32(l[e])), 0, 1) + b : -INFINITY;
+                    int above = 0;
+                    for (int i = 0; i < near; ++i) {
+                        const double other = __shfl_sync(dev::FULL_MASK, of, i);
+                        above += other > of || (other == of && i < lane);       // (the list is in the experts' order)
+                    }
+                    __syncwarp();
+                    if (lane < near && above < p.top_k)
+                        list[above] = e;
+                    __syncwarp();
+                    mine = lane < p.top_k ? list[lane] : -1;
+                    __syncwarp();
+                }
+            }
+            if (near == 0 || near > 32)
+                mine = route_exactly<E>(p, l, exact, lane, ranked, by_sums);
+        }
         // the weights of the chosen; renormalised, softmax scores are taken relative to the largest of them, and sigmoids
         // far below zero (where they are exponentials) as well
         const float lm = mine >= 0 ? logit_of(dev::to_f32(l[mine])) : -INFINITY;
