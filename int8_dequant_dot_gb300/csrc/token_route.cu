@@ -7,8 +7,9 @@
 //  * The choice is that of real numbers, made in f32 where f32 tells: with no bias (or the same for all) the order of scores
 //    is that of the logits; else the scores plus bias are ranked with a bound of their error, and a token whose
 //    order it leaves open (two neighbours among the chosen and the next one, or groups at the cut, nearer than that)
-//    is ranked again in 64 bits.  On the 64-bit units of this GPU (2 lanes an SM and clock) all tokens would
-//    take 640 us of 16384 x 256; of normal logits one in a thousand does.
+//    is ranked in 64 bits, of those experts alone that may make a difference, one a lane (all of a token's where they are
+//    more than 32).  64-bit units are few on this GPU (2 lanes an SM and clock): all tokens of 16384 x 256 would
+//    take 640 us, and a single one in full held up the kernel for 25 us; of normal logits one in a thousand is open.
 //  * The chosen ones are found top_k + 1 times as the warp's maximum of the lanes' largest keys.  A key is a float as
 //    an ordered whole number whose last 5 to 10 bits are the expert's, so that the maximum names it; a lane has its keys
 //    sorted (16 and more are searched) and drops the first.  Where two neighbours differ in those bits alone (1 token
@@ -22,7 +23,7 @@
 namespace loom {
 namespace {
 
-constexpr int RT_WARPS = 4;
+constexpr int RT_WARPS = 4, RT_CTAS = 8;
 
 // +infinity counts as the largest finite f32; NaN (and -infinity) as -infinity.
 __device__ __forceinline__ float logit_of(float l) { return isnan(l) ? -INFINITY : fminf(l, FLT_MAX); }
@@ -196,7 +197,50 @@ template <typename E, int PER> __host__ __device__ bool packs_of(const void *row
     return reinterpret_cast<uintptr_t>(row) % (sizeof(E) * C) == 0 && stride % C == 0 && n % C == 0;
 }
 
-template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) route_kernel(const RouteParams p, int close, int packs)
+// The experts of a warp whose bits are set (lane's run, PER each), up to 32 of them, on a list in the experts' order;
+// returns their number, which may be more.
+template <int PER> __device__ __forceinline__ int list_of(unsigned own, int *list, int lane)
+{
+    int run = __popc(own);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(dev::FULL_MASK, run, d);
+        run += lane >= d ? up : 0;
+    }
+    const int all = __shfl_sync(dev::FULL_MASK, run, 31);
+    if (all <= 32) {
+        run -= __popc(own);
+        for (unsigned left = own; left; left &= left - 1u)
+            list[run++] = lane * PER + __ffs(left) - 1;
+    }
+    __syncwarp();
+    return all;
+}
+
+// In 64 bits the score and bias of the lane's expert (of no expert: -infinity).  Without a bias softmax scores may
+// have any common factor.
+template <typename E> __device__ __noinline__ double precise_score(const RouteParams &p, const E *l, int e, int lane)
+{
+    double m = 0, sum = 1;
+    if (p.score == LOOM_SCORE_SOFTMAX) {
+        m = -INFINITY;
+        for (int i = lane; i < p.experts; i += 32)
+            m = fmax(m, (double)logit_of(dev::to_f32(l[i])));
+        m = warp_max(m);
+        if (p.bias) {
+            sum = 0;
+            for (int i = lane; i < p.experts; i += 32)
+                sum += exp((double)logit_of(dev::to_f32(l[i])) - m);
+            sum = warp_sum(sum);
+        }
+    }
+    if (e < 0)
+        return -INFINITY;
+    return score_of(p.score, (double)logit_of(dev::to_f32(l[e])), m, sum) + (p.bias ? (double)logit_of(p.bias[e]) : 0.0);
+}
+
+template <typename E, int PER, bool GROUPS>
+__global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_kernel(const RouteParams p, int close, int packs)
 {
     extern __shared__ double route_smem[];           // [warps][2][experts] where f32 may not tell, then the counts
     dev::follow_previous_kernel();
@@ -232,7 +276,10 @@ template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) 
         for (int j = 0; j < PER; ++j)
             bias[j] = 0.0f;
     }
-    const bool by_sums = p.groups > 1 && (p.group_best == 2 || ranked);
+    const bool by_sums = GROUPS && (p.group_best == 2 || ranked);
+    const int members = GROUPS ? p.experts / p.groups : PER;
+    // groups that are runs of a power of two of whole lanes: of so many, else 0
+    const int runs = members % PER == 0 && (members / PER & (members / PER - 1)) == 0 ? members / PER : 0;
     const bool scored = ranked || by_sums;
     for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < p.tokens; t += (int64_t)gridDim.x * RT_WARPS) {
         const E *l = static_cast<const E *>(p.logits) + t * p.stride;
@@ -279,39 +326,113 @@ template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) 
 #pragma unroll
         for (int j = 0; j < PER; ++j)
             key[j] = v[j] == -INFINITY || bias[j] == -INFINITY ? RT_NONE : key_of(ranked ? score[j] : v[j]);
-        if (p.groups > 1) {
-            const int members = p.experts / p.groups, lanes = members / PER;
-            if (lanes * PER == members && (lanes & (lanes - 1)) == 0 && lanes > 0 && p.groups <= 32) {
-                float a = -INFINITY, b = -INFINITY;
+        if (GROUPS && p.groups > 32) {
+            open = true;
+        } else if (GROUPS) {
+            // lane g has group g's value: its best, or its two best
+            const float limit = 2.5f * (float)p.group_best * error;     // of the difference of two (and the sums' own rounding)
+            float best1 = -INFINITY, best2 = -INFINITY;
+            if (runs > 0) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
                     const float q = key[j] == RT_NONE ? -INFINITY : by_sums ? score[j] : v[j];
-                    b = fmaxf(b, fminf(a, q));
-                    a = fmaxf(a, q);
+                    best2 = fmaxf(best2, fminf(best1, q));
+                    best1 = fmaxf(best1, q);
                 }
-                for (int d = 1; d < lanes; d <<= 1) {
-                    const float oa = __shfl_xor_sync(dev::FULL_MASK, a, d), ob = __shfl_xor_sync(dev::FULL_MASK, b, d);
-                    b = fmaxf(fmaxf(b, ob), fminf(a, oa));
-                    a = fmaxf(a, oa);
+                for (int d = 1; d < runs; d <<= 1) {
+                    const float o1 = __shfl_xor_sync(dev::FULL_MASK, best1, d), o2 = __shfl_xor_sync(dev::FULL_MASK, best2, d);
+                    best2 = fmaxf(fmaxf(best2, o2), fminf(best1, o1));
+                    best1 = fmaxf(best1, o1);
                 }
-                const float of = p.group_best == 2 && b > -INFINITY ? a + b : a;
-                const float mine = __shfl_sync(dev::FULL_MASK, of, lane < p.groups ? lane * lanes : 0);
-                int above = 0;                       // groups that come before this lane's
-                for (int g = 0; g < p.groups; ++g) {
-                    const float other = __shfl_sync(dev::FULL_MASK, of, g * lanes);
-                    above += other > mine || (other == mine && g < lane);
-                }
-                const bool stays = lane < p.groups && above < p.top_groups && mine > -INFINITY;
-                const float lowest = -warp_max_f(stays ? -mine : -INFINITY);
-                const float highest = warp_max_f(lane < p.groups && !stays ? mine : -INFINITY);
-                open = by_sums && lowest - highest <= 2.5f * (float)p.group_best * error;      // (two sums, and their own rounding)
-                const unsigned kept = __ballot_sync(dev::FULL_MASK, stays);
-                if (!((kept >> (lane / lanes)) & 1u))
+                const int at = lane < p.groups ? lane * runs : 0;
+                best1 = __shfl_sync(dev::FULL_MASK, best1, at);
+                best2 = __shfl_sync(dev::FULL_MASK, best2, at);
+            } else {                                 // groups that are no runs of lanes, by way of shared memory
+                float *all = reinterpret_cast<float *>(exact);
 #pragma unroll
-                    for (int j = 0; j < PER; ++j)
-                        key[j] = RT_NONE;
-            } else {
-                open = true;                         // groups that are no runs of lanes
+                for (int j = 0; j < PER; ++j)
+                    if (lane * PER + j < p.experts)
+                        all[lane * PER + j] = key[j] == RT_NONE ? -INFINITY : by_sums ? score[j] : v[j];
+                __syncwarp();
+                for (int g = 0; g < p.groups; ++g) {
+                    float a = -INFINITY, b = -INFINITY;
+                    for (int i = lane; i < members; i += 32) {
+                        const float q = all[g * members + i];
+                        b = fmaxf(b, fminf(a, q));
+                        a = fmaxf(a, q);
+                    }
+                    const float first = warp_max_f(a);
+                    const int from = __ffs(__ballot_sync(dev::FULL_MASK, a == first)) - 1;
+                    const float second = warp_max_f(lane == from ? b : a);
+                    if (lane == g) {
+                        best1 = first;
+                        best2 = second;
+                    }
+                }
+                __syncwarp();
+            }
+            const float own = lane >= p.groups ? -INFINITY : p.group_best == 2 && best2 > -INFINITY ? best1 + best2 : best1;
+            int above = 0;                           // groups that come before this lane's
+            for (int g = 0; g < p.groups; ++g) {
+                const float other = __shfl_sync(dev::FULL_MASK, own, g);
+                above += other > own || (other == own && g < lane);
+            }
+            bool stays = above < p.top_groups && own > -INFINITY;
+            const float lowest = -warp_max_f(stays ? -own : -INFINITY), highest = warp_max_f(stays ? -INFINITY : own);
+            if (by_sums && highest > -INFINITY && lowest - highest <= limit) {
+                // the groups that may be on either side of the cut, in 64 bits: of each those members that may count
+                const bool near = own >= lowest - limit && own <= highest + limit && own > -INFINITY;
+                const int sure = __popc(__ballot_sync(dev::FULL_MASK, own > highest + limit));
+                float *least = reinterpret_cast<float *>(exact);
+                int *list = reinterpret_cast<int *>(exact) + 32;
+                if (lane < p.groups)
+                    least[lane] = !near ? INFINITY : (p.group_best == 2 && best2 > -INFINITY ? best2 : best1) - 4.0f * error;
+                __syncwarp();
+                unsigned wanted = 0;
+                int group = lane * PER / members, left = members - (lane * PER - group * members);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    if (lane * PER + j < p.experts)
+                        wanted |= (unsigned)(key[j] != RT_NONE && score[j] >= least[group]) << j;
+                    if (--left == 0) {
+                        ++group;
+                        left = members;
+                    }
+                }
+                __syncwarp();
+                const int n = list_of<PER>(wanted, list, lane);
+                if (n > 32) {
+                    open = true;
+                } else {
+                    const int e = lane < n ? list[lane] : -1;
+                    const double score64 = precise_score<E>(p, l, e, lane);
+                    double first = -INFINITY, second = -INFINITY;
+                    for (int i = 0; i < n; ++i) {
+                        const double q = __shfl_sync(dev::FULL_MASK, score64, i);
+                        if (__shfl_sync(dev::FULL_MASK, e, i) / members == lane) {
+                            second = fmax(second, fmin(first, q));
+                            first = fmax(first, q);
+                        }
+                    }
+                    const double own64 = !near ? -INFINITY : p.group_best == 2 && second > -INFINITY ? first + second : first;
+                    int above64 = sure;
+                    for (int g = 0; g < p.groups; ++g) {
+                        const double other = __shfl_sync(dev::FULL_MASK, own64, g);
+                        above64 += other > own64 || (other == own64 && other > -INFINITY && g < lane);
+                    }
+                    stays = own > highest + limit || (near && above64 < p.top_groups);
+                }
+            }
+            const unsigned kept = __ballot_sync(dev::FULL_MASK, stays);
+            int group = lane * PER / members, left = members - (lane * PER - group * members);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (!((kept >> (group & 31)) & 1u))
+                    key[j] = RT_NONE;
+                if (--left == 0) {
+                    ++group;
+                    left = members;
+                }
             }
         }
         int mine = -1;
@@ -390,29 +511,18 @@ template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) 
             }
         }
         if (open) {
-            // sigmoids: of those near enough to the least chosen one or above it, the lane's is taken in 64 bits
+            // of those near enough to the least chosen one or above it, the lane's is taken in 64 bits
             int near = 0;
-            if (again && !soft && least > -INFINITY) {
-                unsigned own = 0;
+            if (again && least > -INFINITY) {
+                unsigned wanted = 0;
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-                    own |= (key[j] != RT_NONE && score[j] >= least - 4.0f * error) << j;
-                int run = __popc(own);
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int up = __shfl_up_sync(dev::FULL_MASK, run, d);
-                    run += lane >= d ? up : 0;
-                }
-                near = __shfl_sync(dev::FULL_MASK, run, 31);
+                    wanted |= (unsigned)(key[j] != RT_NONE && score[j] >= least - 4.0f * error) << j;
+                int *list = reinterpret_cast<int *>(exact);
+                near = list_of<PER>(wanted, list, lane);
                 if (near <= 32) {
-                    int *list = reinterpret_cast<int *>(exact);
-                    run -= __popc(own);
-                    for (unsigned left = own; left; left &= left - 1u)
-                        list[run++] = lane * PER + __ffs(left) - 1;
-                    __syncwarp();
-                    const int e = lane < near ? list[lane] : 0;
-                    const double b = p.bias ? (double)logit_of(p.bias[e]) : 0.0;
-                    const double of = lane < near ? score_of(LOOM_SCORE_SIGMOID, (double)logit_of(dev::to_f32(l[e])), 0, 1) + b : -INFINITY;
+                    const int e = lane < near ? list[lane] : -1;
+                    const double of = precise_score<E>(p, l, e, lane);
                     int above = 0;
                     for (int i = 0; i < near; ++i) {
                         const double other = __shfl_sync(dev::FULL_MASK, of, i);
@@ -455,62 +565,106 @@ template <typename E, int PER> __global__ void __launch_bounds__(32 * RT_WARPS) 
     }
 }
 
-template <typename E> __global__ void __launch_bounds__(32 * RT_WARPS) route_grad_kernel(const RouteGradParams p)
+template <typename E, int PER> __device__ __forceinline__ void store_run(E *row, int n, bool packs, int lane, const float (&v)[PER])
 {
-    extern __shared__ double route_smem[];
+    constexpr int C = PER < 16 / (int)sizeof(E) ? PER : 16 / (int)sizeof(E);
+    struct alignas(sizeof(E) * C) Pack {
+        E e[C];
+    };
+    if (packs) {
+#pragma unroll
+        for (int i = 0; i < PER / C; ++i) {
+            const int at = lane * PER + i * C;
+            Pack q;
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                q.e[j] = dev::from_f32<E>(v[i * C + j]);
+            if (at < n)
+                *reinterpret_cast<Pack *>(row + at) = q;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (lane * PER + j < n)
+                row[lane * PER + j] = dev::from_f32<E>(v[j]);
+    }
+}
+
+// A warp a token: the row without the choice (zeros, or the softmax's common part) in packs, then the chosen experts'
+// gradients over it, each by its lane.  FULL: a softmax that is not renormalised, which needs all logits; the others
+// read the chosen ones alone, and what bounds them is the rows written.
+template <typename E, int PER, bool FULL>
+__global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_grad_kernel(const RouteGradParams p, int packs)
+{
     dev::follow_previous_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    double *full = route_smem + (size_t)warp * 2 * p.experts;
+    const bool soft = p.score == LOOM_SCORE_SOFTMAX;
     for (int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp; t < p.tokens; t += (int64_t)gridDim.x * RT_WARPS) {
         const E *l = static_cast<const E *>(p.logits) + t * p.stride;
         E *d = static_cast<E *>(p.dlogits) + t * p.dstride;
-        const bool soft = p.score == LOOM_SCORE_SOFTMAX;
-        int e = lane < p.top_k ? p.ids[t * p.top_k + lane] : -1;
+        int e = lane < p.top_k ? __ldg(p.ids + t * p.top_k + lane) : -1;
+        float g = lane < p.top_k ? p.factor * __ldg(p.dweights + t * p.top_k + lane) : 0.0f;
+        float v[PER], m = -INFINITY, sum = 0.0f;
+        if (FULL) {
+            load_run<E, PER>(l, p.experts, packs, lane, v);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                v[j] = logit_of(v[j]);
+                m = fmaxf(m, v[j]);
+            }
+            m = warp_max_f(m);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                v[j] = v[j] > -INFINITY ? expf(v[j] - m) : 0.0f;
+                sum += v[j];
+            }
+            sum = warp_sum_f(sum);
+        }
         if (e >= p.experts) {
             dev::flag_error(p.error, LOOM_DEVERR_COUNT_RANGE);
             e = -1;
         }
-        float v = e >= 0 ? logit_of(dev::to_f32(l[e])) : -INFINITY;
-        if (v == -INFINITY)
+        const float le = e >= 0 ? logit_of(dev::to_f32(l[e])) : -INFINITY;
+        if (le == -INFINITY) {
             e = -1;
-        const double g = e >= 0 ? (double)p.factor * p.dweights[t * p.top_k + lane] : 0.0;
-        double m = -INFINITY, sum = 0;
-        if (p.renormalise) {
-            m = warp_max((double)v);
-        } else if (soft) {
-            for (int i = lane; i < p.experts; i += 32)
-                m = fmax(m, (double)logit_of(dev::to_f32(l[i])));
-            m = warp_max(m);
-            for (int i = lane; i < p.experts; i += 32)
-                sum += m > -INFINITY ? exp((double)logit_of(dev::to_f32(l[i])) - m) : 0.0;
-            sum = warp_sum(sum);
+            g = 0.0f;
         }
-        // chosen scores; renormalised ones relative to their sum
-        const bool far = p.renormalise && !soft && m < -600;
-        double s = e < 0 ? 0.0 : far ? exp(v - m) : score_of(p.score, v, m, p.renormalise ? 1.0 : sum), h = g;
-        if (p.renormalise) {
-            s /= warp_sum(s);                           // now w / factor
-            h = g - warp_sum(g * s);                    // h S of the header
+        // chosen scores; renormalised, relative to their sum, and sigmoids far below zero as the exponentials that they are
+        float s = 0.0f, h = g, common = 0.0f;
+        if (!FULL && p.renormalise) {
+            const float top = warp_max_f(le);
+            if (e >= 0)
+                s = soft || top < -60.0f ? expf(le - top) : __frcp_rn(1.0f + expf(-le));
+            const float all = warp_sum_f(s);
+            s = e >= 0 ? __fdiv_rn(s, all) : 0.0f;
+            h = g - warp_sum_f(g * s);                      // (h S of the header)
+        } else if (e >= 0) {
+            s = soft ? __fdiv_rn(expf(le - m), sum) : __frcp_rn(1.0f + expf(-le));
         }
-        const double common = soft && !p.renormalise ? warp_sum(h * s) : 0.0;
-        for (int i = lane; i < p.experts; i += 32)
-            full[i] = 0;
-        __syncwarp();
-        for (int j = 0; j < p.top_k; ++j) {             // an id may come twice
-            if (lane == j && e >= 0)
-                full[e] += soft ? s * h : s * h * score_of(LOOM_SCORE_SIGMOID, -v, 0, 1);
-            __syncwarp();
-        }
-        for (int i = lane; i < p.experts; i += 32) {
-            double out = full[i];
-            if (soft && !p.renormalise) {
-                const float li = logit_of(dev::to_f32(l[i]));
-                if (li > -INFINITY)
-                    out -= exp(li - m) / sum * common;
+        if (FULL)
+            common = warp_sum_f(h * s);
+        float part = e >= 0 ? s * h : 0.0f;
+        if (!soft)
+            part *= __frcp_rn(1.0f + expf(le));             // 1 - score
+        // an expert that comes more than once: the sum, by its first lane, in the order of the lanes
+        const unsigned same = __match_any_sync(dev::FULL_MASK, e);
+        bool first = e >= 0 && (same & ((1u << lane) - 1u)) == 0;
+        if (__any_sync(dev::FULL_MASK, e >= 0 && !first)) {
+            float total = 0.0f;
+            for (int i = 0; i < p.top_k; ++i) {
+                const float other = __shfl_sync(dev::FULL_MASK, part, i);
+                total += (same >> i) & 1u ? other : 0.0f;
             }
-            d[i] = dev::from_f32<E>((float)out);
+            part = total;
         }
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            v[j] = FULL && sum > 0.0f ? -__fdiv_rn(v[j], sum) * common : 0.0f;
+        __syncwarp();                                       // (the row may be the logits': they have been read)
+        store_run<E, PER>(d, p.experts, packs, lane, v);
         __syncwarp();
+        if (first)
+            d[e] = dev::from_f32<E>(FULL ? part - s * common : part);
     }
 }
 
@@ -519,13 +673,13 @@ template <typename E> __global__ void __launch_bounds__(32 * RT_WARPS) route_gra
 bool route_geometry(int64_t tokens, int32_t experts, bool backward, int64_t sms, loom_launch *out)
 {
     *out = loom_launch{};
-    const int64_t ctas = (tokens + RT_WARPS - 1) / RT_WARPS, most = 8 * sms;
+    const int64_t ctas = (tokens + RT_WARPS - 1) / RT_WARPS, most = 16 * sms;
     out->grid[0] = (uint32_t)(ctas < most ? ctas : most);
     out->grid[1] = out->grid[2] = out->block[1] = out->block[2] = 1;
     out->block[0] = 32 * RT_WARPS;
     out->cluster[0] = out->cluster[1] = out->cluster[2] = 1;
     out->subgroup_size = 32;
-    out->smem_bytes = (uint32_t)(RT_WARPS * 2 * experts * sizeof(double));
+    out->smem_bytes = backward ? 0 : (uint32_t)(RT_WARPS * 2 * experts * sizeof(double) + experts * sizeof(int));     // (with a bias and counts)
     out->units_per_cta = RT_WARPS;
     out->kernel = backward ? LOOM_KERNEL_ROUTE_BACKWARD : LOOM_KERNEL_ROUTE;
     return true;
@@ -533,15 +687,20 @@ bool route_geometry(int64_t tokens, int32_t experts, bool backward, int64_t sms,
 
 namespace {
 
-template <typename E, int PER> cudaError_t launch_per(const RouteParams &p, loom_launch L, cudaStream_t stream)
+template <typename E, int PER, bool GROUPS> cudaError_t launch_one(const RouteParams &p, loom_launch L, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(route_kernel<E, PER>), 0, done);
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(route_kernel<E, PER, GROUPS>), 0, done);
     if (e != cudaSuccess)
         return e;
-    const bool close = p.bias || p.groups > 1;      // where f32 may not tell
+    const bool close = p.bias || GROUPS;            // where f32 may not tell
     L.smem_bytes = (uint32_t)((close ? RT_WARPS * 2 * p.experts * sizeof(double) : 0) + (p.counts ? p.experts * sizeof(int) : 0));
-    return launch_prepared(route_kernel<E, PER>, L, stream, p, (int)close, (int)packs_of<E, PER>(p.logits, p.stride, p.experts));
+    return launch_prepared(route_kernel<E, PER, GROUPS>, L, stream, p, (int)close, (int)packs_of<E, PER>(p.logits, p.stride, p.experts));
+}
+
+template <typename E, int PER> cudaError_t launch_per(const RouteParams &p, const loom_launch &L, cudaStream_t stream)
+{
+    return p.groups > 1 ? launch_one<E, PER, true>(p, L, stream) : launch_one<E, PER, false>(p, L, stream);
 }
 
 template <typename E> cudaError_t launch_e(const RouteParams &p, const loom_launch &L, cudaStream_t stream)
@@ -558,6 +717,27 @@ template <typename E> cudaError_t launch_e(const RouteParams &p, const loom_laun
     return per <= 16 ? launch_per<E, 16>(p, L, stream) : launch_per<E, 32>(p, L, stream);
 }
 
+template <typename E, int PER> cudaError_t launch_grad(const RouteGradParams &p, const loom_launch &L, cudaStream_t stream)
+{
+    const int packs = packs_of<E, PER>(p.logits, p.stride, p.experts) && packs_of<E, PER>(p.dlogits, p.dstride, p.experts);
+    return p.score == LOOM_SCORE_SOFTMAX && !p.renormalise ? launch_with(route_grad_kernel<E, PER, true>, L, stream, p, packs)
+                                                           : launch_with(route_grad_kernel<E, PER, false>, L, stream, p, packs);
+}
+
+template <typename E> cudaError_t launch_grad_e(const RouteGradParams &p, const loom_launch &L, cudaStream_t stream)
+{
+    const int per = (p.experts + 31) / 32;
+    if (per <= 1)
+        return launch_grad<E, 1>(p, L, stream);
+    if (per <= 2)
+        return launch_grad<E, 2>(p, L, stream);
+    if (per <= 4)
+        return launch_grad<E, 4>(p, L, stream);
+    if (per <= 8)
+        return launch_grad<E, 8>(p, L, stream);
+    return per <= 16 ? launch_grad<E, 16>(p, L, stream) : launch_grad<E, 32>(p, L, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_route(const RouteParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream)
@@ -570,9 +750,8 @@ cudaError_t launch_route(const RouteParams &p, int32_t dtype, const loom_launch 
 cudaError_t launch_route_grad(const RouteGradParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream)
 {
     if (dtype == LOOM_F32)
-        return launch_with(route_grad_kernel<float>, L, stream, p);
-    return dtype == LOOM_F16 ? launch_with(route_grad_kernel<__half>, L, stream, p)
-                             : launch_with(route_grad_kernel<__nv_bfloat16>, L, stream, p);
+        return launch_grad_e<float>(p, L, stream);
+    return dtype == LOOM_F16 ? launch_grad_e<__half>(p, L, stream) : launch_grad_e<__nv_bfloat16>(p, L, stream);
 }
 
 }  // namespace loom
