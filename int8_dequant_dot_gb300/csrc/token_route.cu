@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
             }
             bool stays = above < p.top_groups && own > -INFINITY;
             const float lowest = -warp_max_f(stays ? -own : -INFINITY), highest = warp_max_f(stays ? -INFINITY : own);
-            if (by_sums && highest > -INFINITY && lowest - highest <= limit) {
+            if (by_sums && highest > -INFINITY && !(lowest - highest > limit)) {       // (two infinite sums: no number)
                 // the groups that may be on either side of the cut, in 64 bits: of each those members that may count
                 const bool near = own >= lowest - limit && own <= highest + limit && own > -INFINITY;
                 const int sure = __popc(__ballot_sync(dev::FULL_MASK, own > highest + limit));
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
             if (lane == p.top_k - 1)
                 next = top;
             const bool pair = own != RT_NONE && next != RT_NONE;
-            again = __any_sync(dev::FULL_MASK, pair && (ranked ? float_of(own & ~LOW) - float_of(next | LOW) <= 2.0f * error : (own ^ next) <= LOW && (own ^ next) >= 0));
+            again = __any_sync(dev::FULL_MASK, pair && (ranked ? !(float_of(own & ~LOW) - float_of(next | LOW) > 2.0f * error) : (own ^ next) <= LOW && (own ^ next) >= 0));
             least = __shfl_sync(dev::FULL_MASK, own == RT_NONE ? -INFINITY : float_of(own & ~LOW), p.top_k - 1);
             mine = own == RT_NONE ? -1 : LOW - (own & LOW);
         }
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
                 const int top = __reduce_max_sync(dev::FULL_MASK, best);
                 if (top == RT_NONE)
                     break;
-                if (ranked && i > 0 && float_of(before) - float_of(top) <= 2.0f * error) {
+                if (ranked && i > 0 && !(float_of(before) - float_of(top) > 2.0f * error)) {
                     open = true;
                     break;
                 }

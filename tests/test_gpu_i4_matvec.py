@@ -133,8 +133,11 @@ def test_outputs_in_place_of_the_callers(env):
     # no k: the bias alone; no tokens, no rows: nothing
     none = torch.empty(0, dtype=torch.int32, device="cuda")
     bias = torch.randn(n, device="cuda")
-    y = loom.loom_i4_matvec(none, torch.empty(0, device="cuda"), n, 0, 32, none, sx, t, bias=bias)
-    assert torch.equal(y, bias.expand(t, n))
+    for some in (1, 2, t):
+        y = loom.loom_i4_matvec(none, torch.empty(0, device="cuda"), n, 0, 32, none, sx, some, bias=bias)
+        assert torch.equal(y, bias.expand(some, n))
+    routed = loom.loom_i4_matvec_routed(none, torch.empty(0, device="cuda"), 3, n, 0, 32, none, sx, torch.tensor([[0, -1, 2]], dtype=torch.int32, device="cuda"), bias=bias.repeat(3))
+    assert torch.equal(routed[0], bias) and not bool(routed[1].any()) and torch.equal(routed[2], bias)
     assert loom.loom_i4_matvec(pack(torch, v), s, n, k, 64, x, sx, 0).shape == (0, n)
 
 

@@ -205,6 +205,22 @@ def test_counts_strides_and_outputs(env):
     assert torch.equal(loom.loom_route_tokens_backward(d, far, ids[:2].clone()), loom.loom_route_tokens_backward(d, logits[:2].contiguous(), ids[:2].clone()))
 
 
+def test_biases_that_settle_the_choice(env):
+    # +infinity counts as the largest f32, whose sums f32 does not hold
+    torch, _ = env
+    g = torch.Generator(device="cuda").manual_seed(5)
+    logits = torch.randn(40, 64, generator=g, device="cuda")
+    bias = 0.1 * torch.randn(64, generator=g, device="cuda")
+    bias[[3, 9, 10, 33]] = INF
+    bias[[20, 21]] = 3.0e38
+    bias[[50, 51]] = -3.0e38
+    for score in ("softmax", "sigmoid"):
+        check(env, logits, 6, score=score, bias=bias)
+        for groups, top in ((8, 3), (8, 1), (4, 2)):
+            for best in (1, 2):
+                check(env, logits, 6, score=score, bias=bias, groups=groups, top_groups=top, group_best=best)
+
+
 # ---- gradient ---------------------------------------------------------------------------------
 def gradient(torch, dw, logits, ids, score, renormalise, factor):
     """(dlogits, the size that bounds its error) in 64 bits."""
