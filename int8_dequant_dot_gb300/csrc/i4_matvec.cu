@@ -150,8 +150,13 @@ __device__ __forceinline__ bool first_run(Runs &w, const I4Params &p, const List
 {
     w.matrices = p.ids ? l.experts : 1;
     const int64_t all = (int64_t)(p.ids ? l.passes[l.experts] : 1) * p.n;
-    w.begin = all * blockIdx.x / gridDim.x;
-    w.end = all * (blockIdx.x + 1) / gridDim.x;
+    if (all * gridDim.x <= 0xffffffffll) {         // (a quotient of 32 bits takes a fifth of one of 64)
+        w.begin = (uint32_t)all * blockIdx.x / gridDim.x;
+        w.end = (uint32_t)all * (blockIdx.x + 1) / gridDim.x;
+    } else {
+        w.begin = all * blockIdx.x / gridDim.x;
+        w.end = all * (blockIdx.x + 1) / gridDim.x;
+    }
     w.matrix = 0;
     if (p.ids) {                               // the last matrix that begins at or before the share
         int step = 1;
@@ -228,6 +233,46 @@ template <int THREADS> __device__ Lists make_lists(const I4Params &p, uint32_t *
     l.passes = l.first + p.experts + 1;
     l.pair = l.passes + p.experts + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.pairs <= 32) {            // by one warp, a pair a lane
+        __shared__ int totals[2];
+        if (warp == 0) {
+            int e = lane < p.pairs ? p.ids[lane] : -1;
+            if (e >= p.experts) {
+                if (blockIdx.x == 0)
+                    dev::flag_error(p.error, LOOM_DEVERR_COUNT_RANGE);
+                e = -1;
+            }
+            const unsigned same = __match_any_sync(dev::FULL_MASK, e), valid = __ballot_sync(dev::FULL_MASK, e >= 0);
+            const bool first = e >= 0 && (same & ((1u << lane) - 1u)) == 0;
+            const int own = first ? (__popc(same) + columns - 1) / columns : 0;
+            int place = 0, smaller = 0, passes = 0;          // pairs, experts and their passes that come before
+            for (int i = 0; i < p.pairs; ++i) {
+                const int other = __shfl_sync(dev::FULL_MASK, e, i), p_i = __shfl_sync(dev::FULL_MASK, own, i);
+                const bool less = other >= 0 && other < e;
+                place += less || (other >= 0 && other == e && i < lane);
+                smaller += less && p_i > 0;
+                passes += less ? p_i : 0;
+            }
+            const int pairs = __popc(valid), experts = __popc(__ballot_sync(dev::FULL_MASK, first)), all = __reduce_add_sync(dev::FULL_MASK, own);
+            if (first) {
+                l.expert[smaller] = (uint16_t)e;
+                l.first[smaller] = (uint16_t)place;
+                l.passes[smaller] = (uint16_t)passes;
+            }
+            if (lane < p.pairs)
+                l.pair[e >= 0 ? place : pairs + __popc(~valid & ((1u << lane) - 1u))] = (uint16_t)lane;
+            if (lane == 0) {
+                l.first[experts] = (uint16_t)pairs;
+                l.passes[experts] = (uint16_t)all;
+                totals[0] = pairs;
+                totals[1] = experts;
+            }
+        }
+        __syncthreads();
+        l.pairs = totals[0];
+        l.experts = totals[1];
+        return l;
+    }
     for (int e = tid; e < p.experts; e += THREADS)
         counts[e] = 0;
     if (tid == 0)
