@@ -4,24 +4,34 @@
 //   y[t][r] = sx[t] * sum_g s[r][g] a[t][r][g] + bias[r],  a = sum_{k in g} W[r][k] X[t][k]
 //
 // Design
-//  * Bound: the n k / 2 bytes of W.  One CTA an SM takes an equal share of the rows (of all rows of
-//    the experts that some pair names), so no partial sums leave a CTA and every row is read once.
+//  * Bound: the n k / 2 bytes of W.  One CTA an SM (two for one or two tokens) takes an equal share of the rows (of
+//    all rows of the experts that some pair names, counted once for each pass over them), so no partial sums leave
+//    a CTA and every row is read once for up to 32 tokens.
 //  * The tensor cores make the sums exact.  A weight's nibble is turned into w + 8 (one XOR) and its bits
 //    are taken as a subnormal f16, (w + 8) 2^-24, or four places higher, (w + 8) 2^-20; those of the second kind
 //    meet a token's byte / 16.  So eight weights cost five logic instructions and no conversion, and
-//    every product is a whole multiple of 2^-24 whose sums over 128 k stay below 2^24 of them:
+//    every product is a whole multiple of 2^-24 whose sums over 128 k stay below 2^18 of them:
 //    f16 MMAs (m16n8k16) with f32 sums lose nothing.  The 8 too many per weight is taken off by starting the sums
-//    at -8 times the sum of the token's bytes.  (Rates measured, per SM and clock: f16 1000 products, s8
-//    260, dp4a 256.)
-//  * A warp takes 64 rows x 256 k at a time: 128 bytes of each row, copied ahead into its own ring of
+//    at -8 times the sum of the token's bytes.  (Rates measured, products per SM and clock: f16 1000, e4m3 3750, s8
+//    260, dp4a 256.  e4m3, whose codes 0 to 15 are whole numbers too, with bytes as two halves: exact, but 28 us
+//    for the 20.6 of 8 tokens below.)
+//  * A warp takes 64 rows x 128 k at a time: 64 bytes of each row, copied ahead into its own ring of
 //    shared memory (cp.async, 16 bytes; 4 where rows do not start on 16 bytes), 16-byte pieces swizzled by
 //    row, so that ldmatrix hands each lane whole words of eight neighbouring weights without conflicts.  The
 //    order of k inside an MMA follows from that and is the same for the tokens' bytes.
-//  * The warps of a team (8 of them, fewer for short rows) share out k; each keeps f32 sums of its rows
-//    for up to 32 tokens in registers over its part of k, adding a group's whole number times the
-//    scale, and the team adds them up in a fixed order in shared memory.
-//  * The experts' pairs are sorted by expert in each CTA (counts, a scan, lists in shared memory).  Which
-//    column of an MMA a pair takes does not change its sums.
+//  * The warps of a team share out k (all of a CTA's where it has one unit of rows, down to one warp where there are as
+//    many units as warps); each keeps f32 sums of its rows for up to 32 tokens in registers over its part of k,
+//    adding a group's whole number times the scale, and the team adds them up in a fixed order in shared
+//    memory, in the stage that each warp read last.
+//  * The experts' pairs are sorted by expert in each CTA (counts, a scan, lists in shared memory; up to 32 of them by
+//    one warp).  Which column of an MMA a pair takes does not change its sums.
+//  * What bounds it: one token the bytes and 4 us to start and end; more of them instructions (500 a stage, of which
+//    unpacking and MMAs 243, the tokens' conversion 60 for each eight), 1.3 to 1.8 a clock.  Copies alone take 14 us of
+//    the 20.6.
+//
+// Measured (8192 x 16384, groups of 128, f16 scales): 1 token 14.8 us (4.7 TB/s), 2 16.6, 3 20.4, 8 20.6, 16 26.4, 32 43.6;
+// 16 tokens with groups of 64 30, of 32 36.  Experts of 2048 x 4096, 8 of 64: 1 token 10.6 us, 4 27, 16 59, 32 63 (269 MB,
+// 4.3 TB/s).  5 x 5001 x 4104, groups of 32, f32 scales 11.6 us.
 #include "token_ops.cuh"
 
 namespace loom {
@@ -734,8 +744,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
 // ---- one or two tokens: dp4a ------------------------------------------------------------------
 // Lanes across k: 16 bytes of a row (32 weights, one scale) each, so a warp takes 1024 k of R rows at a
 // time with the tokens' bytes for them in registers.  A nibble in a byte's upper half is 16 times a signed
-// weight, so eight weights cost three logic instructions and two dp4a.  Warps share out k where it is long, rows
-// where it is not; a row's sums over lanes meet in shared memory, one place per warp, and are
+// weight, so eight weights cost three logic instructions and two dp4a (8192 x 16384: 14.8 us for one token where the
+// tensor cores take 20).  Warps share out k where it is long, rows where it is not; a row's sums over lanes meet in shared memory, one place per warp, and are
 // added in a fixed order.
 constexpr int DP_CHUNK = 1024;      // k of a warp's access
 constexpr int DP_RUN = 512;         // rows whose sums a CTA holds

@@ -11,14 +11,17 @@
 //    place, so that the largest is the first of several).  Sums and maxima of whole numbers: their order does not
 //    matter.  Those that mark a token first stay on the list, and when the slice is copied the lists' tokens are
 //    adjusted, out of L2.  (Histories of more than 4096 tokens take the lists a batch at a time, and all of the
-//    slice's marks are looked through.)  The lists keep warps full: 1 token of 19 is a given slice's, and 32 of them cost as much as one.
+//    slice's marks are looked through.)  The lists keep warps full: where 1 token of 19 is a given slice's, 32 of them
+//    cost as much as one.
 //
 // Measured (f32)
-//   1 x 32768, history 2000, biases, a mask   AL_T1 us
-//   256 x 131072, history 4096 (2048 on average), 64 biases, masks for half of the rows   AL_T us (copy and mask alone 41)
-// (Tried: marks looked up for every logit, 56 us; a bit a token, numbers by running counts and marks by numbers, 55 us; a cluster sharing out the history and marking each other's slices,
-// 96 us, as most tokens of a text are in one slice; a second kernel for the marked tokens, 57 us, which
-// finds them in DRAM again.)
+//   1 x 32768, history 2000, biases, a mask   3.0 us
+//   256 x 131072, history 4096 (2048 on average), 64 biases, masks for half of the rows   53 us (copy and mask alone 41;
+//   bf16 45 us; history 131072 280 us)
+// (Tried: marks looked up for every logit, 56 us; a bit a token, numbers by running counts and marks by numbers, 55 us; a
+// cluster sharing out the history and marking each other's slices, 96 us, as most tokens of a text are in one slice;
+// a second kernel for the marked tokens, 57 us, which finds them in DRAM again; CTAs that load the next slice while they
+// adjust one, 76 us.)
 #include "token_ops.cuh"
 
 namespace loom {
