@@ -745,8 +745,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
 // Lanes across k: 16 bytes of a row (32 weights, one scale) each, so a warp takes 1024 k of R rows at a
 // time with the tokens' bytes for them in registers.  A nibble in a byte's upper half is 16 times a signed
 // weight, so eight weights cost three logic instructions and two dp4a (8192 x 16384: 14.8 us for one token where the
-// tensor cores take 20).  Warps share out k where it is long, rows where it is not; a row's sums over lanes meet in shared memory, one place per warp, and are
-// added in a fixed order.
+// tensor cores take 20).  Warps share out k where it is long, rows where it is not; a row's sums over lanes meet in
+// shared memory, one place per warp, and are added in a fixed order.
 constexpr int DP_CHUNK = 1024;      // k of a warp's access
 constexpr int DP_RUN = 512;         // rows whose sums a CTA holds
 constexpr int DP_WARPS = 8, DP_THREADS = 32 * DP_WARPS;

@@ -321,9 +321,10 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
                 score[j] += bias[j];
         }
         // Bound of a score's error.  Sigmoid s: the exponential's 2 + 1.173 |l| units in the last place (2^-23), of
-        // which s (1 - s), 0.63 units at most, passes on; a rounding; the quotient's 2 units: below 2^-21.  Softmax: exponential and difference, s |l - m| 2^-24 <= 0.37 2^-24 and 4 2^-24 s; the sum's terms the same
-        // on average (their |l - m| is an entropy, below 7) and 37 + 5 roundings; below 2^-18 (s + 2^-7).  And the
-        // rounding of the sum with the bias.
+        // which s (1 - s), 0.63 units at most, passes on; a rounding; the quotient's 2 units: below 2^-21.  Softmax:
+        // exponential and difference, s |l - m| 2^-24 <= 0.37 2^-24 and 4 2^-24 s; the sum's terms the same on average
+        // (their |l - m| is an entropy, below 7) and 37 + 5 roundings; below 2^-18 (s + 2^-7).  And the rounding of the
+        // sum with the bias.
         const float error = (soft ? 3.8146973e-6f * (largest + 0.0078125f) : 4.7683716e-7f) + 5.9604645e-8f * (size + largest);
         int key[PER];
         bool open = false;                           // f32 does not tell
@@ -477,7 +478,9 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
             if (lane == p.top_k - 1)
                 next = top;
             const bool pair = own != RT_NONE && next != RT_NONE;
-            again = __any_sync(dev::FULL_MASK, pair && (ranked ? !(float_of(own & ~LOW) - float_of(next | LOW) > 2.0f * error) : (own ^ next) <= LOW && (own ^ next) >= 0));
+            const bool near = ranked ? !(float_of(own & ~LOW) - float_of(next | LOW) > 2.0f * error)
+                                     : (own ^ next) <= LOW && (own ^ next) >= 0;
+            again = __any_sync(dev::FULL_MASK, pair && near);
             least = __shfl_sync(dev::FULL_MASK, own == RT_NONE ? -INFINITY : float_of(own & ~LOW), p.top_k - 1);
             mine = own == RT_NONE ? -1 : LOW - (own & LOW);
         }
