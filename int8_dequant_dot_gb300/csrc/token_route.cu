@@ -29,6 +29,9 @@ namespace {
 
 constexpr int RT_WARPS = 4, RT_CTAS = 8;
 
+// Places of 64 bits of a warp where f32 may not tell: two for each expert, or 32 groups' bounds and a list of 32 experts.
+__host__ __device__ constexpr int exact_places(int experts) { return experts < 16 ? 32 : 2 * experts; }
+
 // +infinity counts as the largest finite f32; NaN (and -infinity) as -infinity.
 __device__ __forceinline__ float logit_of(float l) { return isnan(l) ? -INFINITY : fminf(l, FLT_MAX); }
 
@@ -246,11 +249,11 @@ template <typename E> __device__ __noinline__ double precise_score(const RoutePa
 template <typename E, int PER, bool GROUPS>
 __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_kernel(const RouteParams p, int close, int packs)
 {
-    extern __shared__ double route_smem[];           // [warps][2][experts] where f32 may not tell, then the counts
+    extern __shared__ double route_smem[];           // [warps][exact_places] where f32 may not tell, then the counts
     dev::follow_previous_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    double *exact = route_smem + (size_t)warp * 2 * p.experts;
-    int *counts = reinterpret_cast<int *>(route_smem + (close ? (size_t)RT_WARPS * 2 * p.experts : 0));
+    double *exact = route_smem + (size_t)warp * exact_places(p.experts);
+    int *counts = reinterpret_cast<int *>(route_smem + (close ? (size_t)RT_WARPS * exact_places(p.experts) : 0));
     if (p.counts) {
         for (int e = threadIdx.x; e < p.experts; e += 32 * RT_WARPS)
             counts[e] = 0;
@@ -686,7 +689,7 @@ bool route_geometry(int64_t tokens, int32_t experts, bool backward, int64_t sms,
     out->block[0] = 32 * RT_WARPS;
     out->cluster[0] = out->cluster[1] = out->cluster[2] = 1;
     out->subgroup_size = 32;
-    out->smem_bytes = backward ? 0 : (uint32_t)(RT_WARPS * 2 * experts * sizeof(double) + experts * sizeof(int));     // (with a bias and counts)
+    out->smem_bytes = backward ? 0 : (uint32_t)(RT_WARPS * exact_places(experts) * sizeof(double) + experts * sizeof(int));     // (with a bias and counts)
     out->units_per_cta = RT_WARPS;
     out->kernel = backward ? LOOM_KERNEL_ROUTE_BACKWARD : LOOM_KERNEL_ROUTE;
     return true;
@@ -701,7 +704,7 @@ template <typename E, int PER, bool GROUPS> cudaError_t launch_one(const RoutePa
     if (e != cudaSuccess)
         return e;
     const bool close = p.bias || GROUPS;            // where f32 may not tell
-    L.smem_bytes = (uint32_t)((close ? RT_WARPS * 2 * p.experts * sizeof(double) : 0) + (p.counts ? p.experts * sizeof(int) : 0));
+    L.smem_bytes = (uint32_t)((close ? RT_WARPS * exact_places(p.experts) * sizeof(double) : 0) + (p.counts ? p.experts * sizeof(int) : 0));
     return launch_prepared(route_kernel<E, PER, GROUPS>, L, stream, p, (int)close, (int)packs_of<E, PER>(p.logits, p.stride, p.experts));
 }
 

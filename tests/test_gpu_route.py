@@ -143,6 +143,23 @@ def test_ties_go_to_the_lower_index(env):
     check(env, coarse, 10, score="sigmoid", groups=8, top_groups=3, group_best=2)
 
 
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("e,groups,top", [(2, 2, 1), (4, 2, 1), (6, 3, 2), (8, 8, 3), (8, 4, 2), (8, 2, 1), (9, 3, 1), (10, 5, 2), (10, 2, 1), (12, 6, 2), (15, 5, 3), (16, 16, 5)])
+def test_ties_among_a_few_experts_in_groups(env, e, groups, top, best):
+    """Few experts, most groups alike at the cut: every warp lists those that 64 bits are to tell apart, at once."""
+    torch, loom = env
+    g = torch.Generator(device="cuda").manual_seed(e + groups)
+    logits = torch.randint(0, 3, (2000, e), generator=g, device="cuda").float()
+    k = min(e, max(1, e // groups * top - 1))
+    for bias in (None, torch.randint(0, 2, (e,), generator=g, device="cuda") * 0.25):
+        counts = torch.zeros(e, dtype=torch.int32, device="cuda")
+        kw = dict(score="sigmoid", bias=bias, groups=groups, top_groups=top, group_best=best)
+        ids, _ = check(env, logits, k, **kw)
+        again, _ = loom.loom_route_tokens(logits, k, counts=counts, **kw)
+        assert torch.equal(ids, again)
+        assert torch.equal(counts.long(), torch.bincount(ids[ids >= 0].long(), minlength=e))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("e,k", [(40, 6), (256, 8), (1024, 16)])
 def test_choices_that_32_bits_do_not_tell_apart(env, score, e, k):
