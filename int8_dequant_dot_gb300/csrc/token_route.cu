@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
         int key[PER];
         bool open = false;                           // f32 does not tell
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            key[j] = v[j] == -INFINITY || bias[j] == -INFINITY ? RT_NONE : key_of(ranked ? score[j] : v[j]);
+        for (int j = 0; j < PER; ++j)                // (+ 0: the two zeros are equal)
+            key[j] = v[j] == -INFINITY || bias[j] == -INFINITY ? RT_NONE : key_of((ranked ? score[j] : v[j]) + 0.0f);
         if (GROUPS && p.groups > 32) {
             open = true;
         } else if (GROUPS) {

@@ -143,6 +143,16 @@ def test_ties_go_to_the_lower_index(env):
     check(env, coarse, 10, score="sigmoid", groups=8, top_groups=3, group_best=2)
 
 
+@pytest.mark.parametrize("e", [20, 256, 1000])
+def test_both_zeros_are_one_logit(env, e):
+    torch, _ = env
+    g = torch.Generator(device="cuda").manual_seed(e)
+    for dtype in (torch.float32, torch.float16, torch.bfloat16):
+        zeros = torch.where(torch.rand(64, e, generator=g, device="cuda") < 0.5, -0.0, 0.0).to(dtype)
+        for kw in ({}, {"score": "sigmoid"}, {"bias": torch.full((e,), 0.5, device="cuda")}, {"groups": 5 if e % 5 == 0 else 4, "top_groups": 2}):
+            check(env, zeros, 9, **kw)
+
+
 @pytest.mark.parametrize("best", [1, 2])
 @pytest.mark.parametrize("e,groups,top", [(2, 2, 1), (4, 2, 1), (6, 3, 2), (8, 8, 3), (8, 4, 2), (8, 2, 1), (9, 3, 1), (10, 5, 2), (10, 2, 1), (12, 6, 2), (15, 5, 3), (16, 16, 5)])
 def test_ties_among_a_few_experts_in_groups(env, e, groups, top, best):
