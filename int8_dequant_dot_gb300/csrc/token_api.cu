@@ -113,10 +113,11 @@ loom_status i4_shape(int64_t n, int64_t k, int64_t group)
                ? LOOM_ERR_SHAPE : LOOM_OK;
 }
 
-// Pairs of one launch of the experts' products: whole tokens, as many as the kernel's lists hold.
+// Pairs of one launch: of the experts' products (routes > 0) whole tokens, as many as the kernel's lists hold; else tokens,
+// as many as leave its sums of 32 bits room.
 int64_t i4_part(int64_t pairs, int64_t routes)
 {
-    const int64_t most = routes > 0 ? I4_MAX_PAIRS / routes * routes : 0;
+    const int64_t most = routes > 0 ? I4_MAX_PAIRS / routes * routes : (int64_t)1 << 24;
     return pairs < most ? pairs : most;
 }
 
@@ -140,17 +141,15 @@ loom_status i4_call(I4Params p, int64_t x_rows, int64_t y_stride, int32_t routes
         return counted;
     p.y_stride = used_stride(p.pairs, y_stride);
     p.groups = (p.k + p.group - 1) / p.group;
-    const int64_t pairs = p.pairs, part = routes > 0 ? i4_part(pairs, routes) : pairs;
+    const int64_t pairs = p.pairs, part = i4_part(pairs, routes);
     p.pairs_per_x = x_rows == pairs ? 1 : routes;
     const I4Params whole = p;
     for (int64_t at = 0; at < pairs; at += part) {
         p.pairs = (int32_t)(pairs - at < part ? pairs - at : part);
-        if (routes > 0) {
-            p.ids = whole.ids + at;
-            p.x = whole.x + at / p.pairs_per_x * p.k;
-            p.scale_x = whole.scale_x + at / p.pairs_per_x;
-            p.y = static_cast<char *>(whole.y) + at * p.y_stride * dtype_bytes(p.y_dtype);
-        }
+        p.ids = routes > 0 ? whole.ids + at : nullptr;
+        p.x = whole.x + at / p.pairs_per_x * p.k;
+        p.scale_x = whole.scale_x + at / p.pairs_per_x;
+        p.y = static_cast<char *>(whole.y) + at * p.y_stride * dtype_bytes(p.y_dtype);
         loom_launch L;
         i4_geometry(p.pairs, p.n, p.k, p.group, routes > 0 ? (p.experts > 0 ? p.experts : 1) : 0, sms, &L);
         const cudaError_t e = launch_i4_matvec(p, sms, L, stream);
@@ -273,7 +272,7 @@ extern "C" loom_status loom_token_launch_config(int32_t op, const int64_t *w, in
         const loom_status counted = sms ? LOOM_OK : sm_count(&sms);
         if (counted != LOOM_OK)
             return counted;
-        i4_geometry(experts ? i4_part(w[0] * routes, routes) : w[0], w[1], w[2], w[3], experts, sms, out);
+        i4_geometry(experts ? i4_part(w[0] * routes, routes) : i4_part(w[0], 0), w[1], w[2], w[3], experts, sms, out);
         return LOOM_OK;
     }
     case LOOM_OP_ROUTE_TOKENS:

@@ -228,3 +228,17 @@ def test_weights_past_31_bits(env):
     y = loom.loom_i4_matvec_routed(w, scale, experts, n, k, 128, x, sx, ids)
     assert torch.equal(y, loom.loom_i4_matvec_routed(w[-1:].clone(), s.clone(), 1, n, k, 128, x, sx, torch.zeros_like(ids)))
     check(torch, y[:, -50:], *definition(torch, v[-50:], s[-50:], x, sx, 128), k, 128)
+
+
+@pytest.mark.parametrize("t,n,k", [((1 << 24) + 37, 1, 8), ((1 << 25) + 1, 2, 8)])
+def test_tokens_of_several_launches(env, t, n, k):
+    # whole sums: exact, whatever the order
+    torch, loom = env
+    g = torch.Generator(device="cuda").manual_seed(n)
+    v = torch.randint(-8, 8, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    x = torch.randint(-128, 128, (t, k), generator=g, device="cuda", dtype=torch.int8)
+    sx = torch.where(torch.arange(t, device="cuda") % 3 == 0, 2.0, 0.5)
+    y = torch.full((t + 3, n), 7.0, device="cuda")
+    loom.loom_i4_matvec(pack(torch, v), torch.ones(n, 1, device="cuda"), n, k, 32, x, sx, t, y=y)
+    want = (x.float() @ v.float().t()) * sx[:, None]       # (below 2^14: exact in f32 as well)
+    assert torch.equal(y[:t], want) and bool((y[t:] == 7.0).all())

@@ -168,3 +168,9 @@ def test_binding_adjust(loom):
                 {"mask": z(2, 3, dtype=i32)}, {"mask": z(2, 4)}, {"mask": z(8, dtype=i32)}, {"mask_rows": z(3, dtype=i32)}, {"y": z(4, 99)}, {"error": z(1)}):
         assert f(**{**ok, **bad}) == loom.LOOM_ERR_SHAPE
     assert f(bias_ids=z(4, 2, dtype=i32)) == loom.LOOM_ERR_NULL and f(bias_values=z(4, 2)) == loom.LOOM_ERR_NULL
+
+
+def test_launch_config_of_the_most_tokens(loom):
+    for work in ([(1 << 31) - 1, 1, 8, 32, 0, 1, SMS], [(1 << 31) - 1, 8, 64, 32, 4, 1, SMS], [(1 << 24) + 1, 8192, 16384, 128, 0, 1, SMS]):
+        L = loom.loom_token_launch_config(loom.LOOM_OP_I4_MATVEC, work)
+        assert 1 <= L["grid"][0] <= 2 * SMS and L["smem_bytes"] <= 227 * 1024
