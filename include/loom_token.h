@@ -72,7 +72,7 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
 #define LOOM_KERNEL_I4_MATVEC 25        /* units_per_cta = rows of weights (of experts: where all are wanted) */
 #define LOOM_KERNEL_ROUTE 26            /* logits to experts; units_per_cta = tokens */
 #define LOOM_KERNEL_ROUTE_BACKWARD 27   /* units_per_cta = tokens */
-#define LOOM_KERNEL_ADJUST 28           /* a cluster per row; units_per_cta = 1 */
+#define LOOM_KERNEL_ADJUST 28           /* slices of rows; units_per_cta = tokens of a slice */
 
 /* As loom_launch_config, for the operators of this header. */
 loom_status loom_token_launch_config(int32_t op, const int64_t *workload, int32_t n_workload, loom_launch *out);
@@ -239,8 +239,8 @@ loom_status loom_sample_tokens(const void *d_logits, int32_t dtype, int64_t rows
  * and a mask's words.
  * Errors: NULL logits or y, one of the bias arrays alone -> LOOM_ERR_NULL; misaligned -> LOOM_ERR_ALIGN;
  * rows < 0 or > 2^31 - 1, vocab < 1 or > 393216, history < 0 or > 1048575, biases < 0 or > 1024,
- * masks < 0, masks < rows without d_mask_rows (and not 1), a stride below its row (with more than one
- * row) -> LOOM_ERR_SHAPE; unknown dtype, a host repetition not above zero or infinite, a host
+ * masks < 0, masks < rows without d_mask_rows (and not 1), a stride below its row, or d_y that is d_logits with
+ * another stride (with more than one row) -> LOOM_ERR_SHAPE; unknown dtype, a host repetition not above zero or infinite, a host
  * frequency or presence that is not finite -> LOOM_ERR_ARG.
  */
 loom_status loom_adjust_logits(const void *d_logits, int32_t dtype, int64_t rows, int32_t vocab, int64_t stride,
@@ -327,8 +327,9 @@ loom_status loom_route_tokens(const void *d_logits, int32_t dtype, int64_t token
  *   sigmoid        dlogit[e] = score[e] * (1 - score[e]) * (sum of h[j] over ids[j] = e)
  * (renormalised softmax scores are taken among the chosen experts, where sum(h s) is zero).
  * Missing routes (negative ids, or ids of `experts` or more, which are flagged with
- * LOOM_DEVERR_COUNT_RANGE) take no part; an expert that can't be chosen gets 0.  d_dlogits may be d_logits.
- * Errors: as loom_route_tokens.
+ * LOOM_DEVERR_COUNT_RANGE) take no part; an expert that can't be chosen gets 0.  d_dlogits may be d_logits (with its stride).
+ * Errors: as loom_route_tokens, and d_dlogits that is d_logits with another stride (with more than one token) ->
+ * LOOM_ERR_SHAPE.
  */
 loom_status loom_route_tokens_backward(const float *d_dweights, const void *d_logits, int32_t dtype, int64_t tokens,
                                        int32_t experts, int64_t stride, const int32_t *d_ids, int32_t score,

@@ -629,7 +629,8 @@ extern "C" loom_status loom_route_tokens_backward(const float *d_dweights, const
                                                   void *d_dlogits, int64_t dlogits_stride, int32_t *d_error, void *stream)
 {
     if (tokens < 0 || tokens > MAX_INT || experts < 1 || experts > ROUTE_MAX_EXPERTS || top_k < 1 || top_k > ROUTE_MAX_TOP ||
-        top_k > experts || short_stride(tokens, stride, experts) || short_stride(tokens, dlogits_stride, experts))
+        top_k > experts || short_stride(tokens, stride, experts) || short_stride(tokens, dlogits_stride, experts) ||
+        (d_logits && d_logits == d_dlogits && tokens > 1 && stride != dlogits_stride))
         return LOOM_ERR_SHAPE;
     if (!known(dtype) || (score != LOOM_SCORE_SOFTMAX && score != LOOM_SCORE_SIGMOID) || !std::isfinite(factor))
         return LOOM_ERR_ARG;
@@ -676,7 +677,8 @@ extern "C" loom_status loom_adjust_logits(const void *d_logits, int32_t dtype, i
     if (rows < 0 || rows > MAX_INT || vocab < 1 || vocab > AL_MAX_VOCAB || short_stride(rows, stride, vocab) ||
         short_stride(rows, y_stride, vocab) || history < 0 || history > AL_MAX_HISTORY || biases < 0 || biases > AL_MAX_BIASES ||
         (d_history && short_stride(rows, history_stride, history)) || masks < 0 ||
-        (d_mask && !d_mask_rows && masks < rows && masks != 1))
+        (d_mask && !d_mask_rows && masks < rows && masks != 1) ||
+        (d_logits && d_logits == d_y && rows > 1 && stride != y_stride))
         return LOOM_ERR_SHAPE;
     if (!known(dtype) || (!d_repetition && !(repetition > 0.0f && std::isfinite(repetition))) ||
         (!d_frequency && !std::isfinite(frequency)) || (!d_presence && !std::isfinite(presence)))

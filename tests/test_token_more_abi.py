@@ -174,3 +174,15 @@ def test_launch_config_of_the_most_tokens(loom):
     for work in ([(1 << 31) - 1, 1, 8, 32, 0, 1, SMS], [(1 << 31) - 1, 8, 64, 32, 4, 1, SMS], [(1 << 24) + 1, 8192, 16384, 128, 0, 1, SMS]):
         L = loom.loom_token_launch_config(loom.LOOM_OP_I4_MATVEC, work)
         assert 1 <= L["grid"][0] <= 2 * SMS and L["smem_bytes"] <= 227 * 1024
+
+
+def test_in_place_with_two_strides_is_refused(loom):
+    lib = loom.library()
+    def adjust(rows, stride, y_stride):
+        return lib.loom_adjust_logits(A, 3, rows, 100, stride, None, 0, 0, None, None, None, 1.0, None, 0.0, None, 0.0, None, None, 0, None, 0, None, A,
+                                      y_stride, None, None)
+    def gradient(tokens, stride, dstride):
+        return lib.loom_route_tokens_backward(A + 64, A, 3, tokens, 64, stride, A + 128, 0, 8, 1, 1.0, A, dstride, None, None)
+    for call in (adjust, gradient):             # (an unknown type is what is refused otherwise)
+        assert call(2, 200, 100) == call(2, 100, 200) == loom.LOOM_ERR_SHAPE
+        assert call(2, 200, 200) == call(1, 200, 100) == loom.LOOM_ERR_ARG
