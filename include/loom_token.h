@@ -232,7 +232,7 @@ loom_status loom_sample_tokens(const void *d_logits, int32_t dtype, int64_t rows
  * where that is NULL, the host value for every row; a device repetition that is not above zero counts as 1.
  * d_bias_ids int32 and d_bias_values f32 [rows][biases], or NULL; ids outside [0, vocab)
  * (such as the -1 behind a shorter list) are passed over.
- * d_mask: int32 [masks][ceil(vocab / 32)], token i is bit i % 32 of word i / 32, or NULL.
+ * d_mask: int32 [masks][ceil(vocab / 32)], token i is bit i % 32 of word i / 32, or NULL (as with masks 0: none).
  * d_mask_rows: int32 [rows], the mask of each row, negative for none; `masks` or more counts as none and is
  * flagged.  NULL: row r has mask r, or, where masks is 1, all rows have that one.
  * d_y may be d_logits (rows, type and stride alike); then only what changes is read and written,
