@@ -337,8 +337,8 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
         if (GROUPS && p.groups > 32) {
             open = true;
         } else if (GROUPS) {
-            // lane g has group g's value: its best, or its two best
-            const float limit = 2.5f * (float)p.group_best * error;     // of the difference of two (and the sums' own rounding)
+            // lane g has group g's value: its best, or half of its two best ones' sum, which f32 holds whatever they are
+            const float limit = 2.5f * error;        // of the difference of two (and the sums' own rounding)
             float best1 = -INFINITY, best2 = -INFINITY;
             if (runs > 0) {
 #pragma unroll
@@ -379,17 +379,18 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
                 }
                 __syncwarp();
             }
-            const float own = lane >= p.groups ? -INFINITY : p.group_best == 2 && best2 > -INFINITY ? best1 + best2 : best1;
+            const bool has = lane < p.groups && best1 > -INFINITY;      // (two lowest finite scores make no empty group)
+            const float own = !has ? -INFINITY : p.group_best == 1 ? best1 : 0.5f * best1 + (best2 > -INFINITY ? 0.5f * best2 : 0.0f);
             int above = 0;                           // groups that come before this lane's
             for (int g = 0; g < p.groups; ++g) {
                 const float other = __shfl_sync(dev::FULL_MASK, own, g);
                 above += other > own || (other == own && g < lane);
             }
-            bool stays = above < p.top_groups && own > -INFINITY;
+            bool stays = above < p.top_groups && has;
             const float lowest = -warp_max_f(stays ? -own : -INFINITY), highest = warp_max_f(stays ? -INFINITY : own);
-            if (by_sums && highest > -INFINITY && !(lowest - highest > limit)) {       // (two infinite sums: no number)
+            if (by_sums && highest > -INFINITY && !(lowest - highest > limit)) {
                 // the groups that may be on either side of the cut, in 64 bits: of each those members that may count
-                const bool near = own >= lowest - limit && own <= highest + limit && own > -INFINITY;
+                const bool near = own >= lowest - limit && own <= highest + limit && has;
                 const int sure = __popc(__ballot_sync(dev::FULL_MASK, own > highest + limit));
                 float *least = reinterpret_cast<float *>(exact);
                 int *list = reinterpret_cast<int *>(exact) + 32;
