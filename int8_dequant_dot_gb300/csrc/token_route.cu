@@ -151,6 +151,7 @@ __device__ __forceinline__ int key_of(float v)
 }
 __device__ __forceinline__ float float_of(int key) { return __int_as_float(key ^ ((key >> 31) & 0x7fffffff)); }
 constexpr int RT_NONE = -0x7fffffff - 1;
+constexpr float RT_UNIT = 6.1e-8f;               // a rounding of f32, 2^-24 of its result, with room for those of a bound
 
 __device__ __forceinline__ float warp_max_f(float v) { return float_of(__reduce_max_sync(dev::FULL_MASK, key_of(v))); }      // (of no NaN)
 
@@ -328,7 +329,8 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
         // exponential and difference, s |l - m| 2^-24 <= 0.37 2^-24 and 4 2^-24 s; the sum's terms the same on average
         // (their |l - m| is an entropy, below 7) and 37 + 5 roundings; below 2^-18 (s + 2^-7).  And the rounding of the
         // sum with the bias.
-        const float error = (soft ? 3.8146973e-6f * (largest + 0.0078125f) : 4.7683716e-7f) + 5.9604645e-8f * (size + largest);
+        const float of_score = soft ? 3.8146973e-6f * (largest + 0.0078125f) : 4.7683716e-7f;
+        const float error = of_score + 5.9604645e-8f * (size + largest);
         int key[PER];
         bool open = false;                           // f32 does not tell
 #pragma unroll
@@ -338,7 +340,6 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
             open = true;
         } else if (GROUPS) {
             // lane g has group g's value: its best, or half of its two best ones' sum, which f32 holds whatever they are
-            const float limit = 2.5f * error;        // of the difference of two (and the sums' own rounding)
             float best1 = -INFINITY, best2 = -INFINITY;
             if (runs > 0) {
 #pragma unroll
@@ -387,15 +388,20 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
                 above += other > own || (other == own && g < lane);
             }
             bool stays = above < p.top_groups && has;
-            const float lowest = -warp_max_f(stays ? -own : -INFINITY), highest = warp_max_f(stays ? -INFINITY : own);
-            if (by_sums && highest > -INFINITY && !(lowest - highest > limit)) {
+            // Bound of own's error: of_score and a rounding with the bias (2^-24 of the sum, 6.1e-8 with room) of each one, as
+            // much again of the halves' sum, none above the larger's, and of own - off and own + off.
+            const float size1 = fabsf(best1), size2 = best2 > -INFINITY ? fabsf(best2) : 0.0f;
+            const float off = of_score + 3.0f * RT_UNIT * fmaxf(size1, size2);
+            const float lowest = -warp_max_f(stays ? off - own : -INFINITY), highest = warp_max_f(has && !stays ? own + off : -INFINITY);
+            if (by_sums && highest > -INFINITY && !(lowest > highest)) {
                 // the groups that may be on either side of the cut, in 64 bits: of each those members that may count
-                const bool near = own >= lowest - limit && own <= highest + limit && has;
-                const int sure = __popc(__ballot_sync(dev::FULL_MASK, own > highest + limit));
+                const bool surely = stays && own - off > highest, near = has && !surely && own + off >= lowest;
+                const int sure = __popc(__ballot_sync(dev::FULL_MASK, surely));
                 float *least = reinterpret_cast<float *>(exact);
                 int *list = reinterpret_cast<int *>(exact) + 32;
+                const float last = p.group_best == 2 && best2 > -INFINITY ? best2 : best1;
                 if (lane < p.groups)
-                    least[lane] = !near ? INFINITY : (p.group_best == 2 && best2 > -INFINITY ? best2 : best1) - 4.0f * error;
+                    least[lane] = !near ? INFINITY : last - 4.0f * (of_score + RT_UNIT * fabsf(last));
                 __syncwarp();
                 unsigned wanted = 0;
                 int group = lane * PER / members, left = members - (lane * PER - group * members);
@@ -429,7 +435,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
                         const double other = __shfl_sync(dev::FULL_MASK, own64, g);
                         above64 += other > own64 || (other == own64 && other > -INFINITY && g < lane);
                     }
-                    stays = own > highest + limit || (near && above64 < p.top_groups);
+                    stays = surely || (near && above64 < p.top_groups);
                 }
             }
             const unsigned kept = __ballot_sync(dev::FULL_MASK, stays);

@@ -31,3 +31,28 @@ def test_the_last_group_of_lowest_biases(env):  # noqa: F811
     bias[:2] = 0.0
     ids, _ = check(env, torch.zeros(3, 8, device="cuda"), 4, score="sigmoid", bias=bias, groups=4, top_groups=2, group_best=2)
     assert ids.tolist() == [[0, 1, 2, 3]] * 3
+
+
+def test_sums_of_two_at_the_worst_roundings(env):  # noqa: F811
+    """Scores + 63.5 lie in [64, 65), 2^-17 apart in f32, and the sums of two are 2^-16 apart.  Group 0's scores are just above the
+    middle of two places and group 1's just below it, so that scores some 1e-7 off are rounded apart by four halves of
+    2^-17; the places are chosen for the sums, ties of 2^-16, to be rounded apart as well: 2^-15 in favour of group 1 where group 0
+    has the larger sum."""
+    torch, _ = env
+    t, step = 1 << 16, 2.0 ** -17
+    g = torch.Generator(device="cuda").manual_seed(3)
+    draw = lambda n: torch.randint(0, n, (t,), generator=g, device="cuda")   # noqa: E731
+    a0, a1 = 8000 + 2 * draw(4000), 8001 + 4 * draw(2000)                 # even, odd
+    a0 += (1 - a0 - a1) % 4                                               # (a sum of 4 i + 1)
+    b0 = 8001 + 2 * draw(2000)
+    b0 = torch.minimum(b0, a0 + a1)
+    b1 = a0 + a1 - b0
+    sides = torch.tensor([1.0, 1.0, -1.0, -1.0], device="cuda", dtype=torch.float64)
+    middle = 0.5 + (torch.stack([a0, a1, b0, b1], 1).double() + 0.5) * step
+    off = 1e-9 + 3e-8 * torch.rand(t, 4, generator=g, device="cuda", dtype=torch.float64)
+    s = middle + sides * off
+    logits = torch.log(s / (1 - s)).float()
+    exact = 1 / (1 + torch.exp(-logits.double()))
+    sums = exact[:, :2].sum(1) - exact[:, 2:].sum(1)
+    assert bool((sums.abs() < 4e-7).all()) and bool(((a0 + a1) % 4 == 1).all()) and bool((b1 % 2 == 0).all())
+    check(env, logits, 2, score="sigmoid", bias=torch.full((4,), 63.5, device="cuda"), groups=2, top_groups=1, group_best=2)
