@@ -261,8 +261,8 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
         __syncthreads();
     }
     const bool soft = p.score == LOOM_SCORE_SOFTMAX;
-    // the bias of the lane's experts, its size, and whether it is the same for all
-    float bias[PER], size = 0.0f;
+    // the bias of the lane's experts, and whether it is the same for all
+    float bias[PER];
     bool ranked = false;                             // by scores and bias; else by logits
     if (p.bias) {
         float low = INFINITY, high = -INFINITY;
@@ -278,7 +278,6 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
         low = -warp_max_f(-low);
         high = warp_max_f(high);
         ranked = low < high;
-        size = fmaxf(fabsf(low), fabsf(high));
     } else {
 #pragma unroll
         for (int j = 0; j < PER; ++j)
@@ -327,10 +326,11 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
         // Bound of a score's error.  Sigmoid s: the exponential's 2 + 1.173 |l| units in the last place (2^-23), of
         // which s (1 - s), 0.63 units at most, passes on; a rounding; the quotient's 2 units: below 2^-21.  Softmax:
         // exponential and difference, s |l - m| 2^-24 <= 0.37 2^-24 and 4 2^-24 s; the sum's terms the same on average
-        // (their |l - m| is an entropy, below 7) and 37 + 5 roundings; below 2^-18 (s + 2^-7).  And the rounding of the
-        // sum with the bias.
+        // (their |l - m| is an entropy, below 7) and 37 + 5 roundings; below 2^-18 (s + 2^-7).  And the rounding of its
+        // own sum with the bias: a low bias, such as a mask's, makes that of no other one less sure.
         const float of_score = soft ? 3.8146973e-6f * (largest + 0.0078125f) : 4.7683716e-7f;
-        const float error = of_score + 5.9604645e-8f * (size + largest);
+        const auto told = [&](float a, float b) { return a - b > 2.0f * (of_score + RT_UNIT * fmaxf(fabsf(a), fabsf(b))); };     // a is above b
+        const auto reach = [&](float a) { return a - 4.0f * (of_score + RT_UNIT * fabsf(a)); };      // what is below it is below a's
         int key[PER];
         bool open = false;                           // f32 does not tell
 #pragma unroll
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
                 int *list = reinterpret_cast<int *>(exact) + 32;
                 const float last = p.group_best == 2 && best2 > -INFINITY ? best2 : best1;
                 if (lane < p.groups)
-                    least[lane] = !near ? INFINITY : last - 4.0f * (of_score + RT_UNIT * fabsf(last));
+                    least[lane] = !near ? INFINITY : reach(last);
                 __syncwarp();
                 unsigned wanted = 0;
                 int group = lane * PER / members, left = members - (lane * PER - group * members);
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
             if (lane == p.top_k - 1)
                 next = top;
             const bool pair = own != RT_NONE && next != RT_NONE;
-            const bool near = ranked ? !(float_of(own & ~LOW) - float_of(next | LOW) > 2.0f * error)
+            const bool near = ranked ? !told(float_of(own & ~LOW), float_of(next | LOW))
                                      : (own ^ next) <= LOW && (own ^ next) >= 0;
             again = __any_sync(dev::FULL_MASK, pair && near);
             least = __shfl_sync(dev::FULL_MASK, own == RT_NONE ? -INFINITY : float_of(own & ~LOW), p.top_k - 1);
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
                 const int top = __reduce_max_sync(dev::FULL_MASK, best);
                 if (top == RT_NONE)
                     break;
-                if (ranked && i > 0 && !(float_of(before) - float_of(top) > 2.0f * error)) {
+                if (ranked && i > 0 && !told(float_of(before), float_of(top))) {
                     open = true;
                     break;
                 }
@@ -532,9 +532,10 @@ __global__ void __launch_bounds__(32 * RT_WARPS, PER <= 8 ? RT_CTAS : 3) route_k
             int near = 0;
             if (again && least > -INFINITY) {
                 unsigned wanted = 0;
+                const float from = reach(least);
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-                    wanted |= (unsigned)(key[j] != RT_NONE && score[j] >= least - 4.0f * error) << j;
+                    wanted |= (unsigned)(key[j] != RT_NONE && score[j] >= from) << j;
                 int *list = reinterpret_cast<int *>(exact);
                 near = list_of<PER>(wanted, list, lane);
                 if (near <= 32) {

@@ -56,3 +56,37 @@ def test_sums_of_two_at_the_worst_roundings(env):  # noqa: F811
     sums = exact[:, :2].sum(1) - exact[:, 2:].sum(1)
     assert bool((sums.abs() < 4e-7).all()) and bool(((a0 + a1) % 4 == 1).all()) and bool((b1 % 2 == 0).all())
     check(env, logits, 2, score="sigmoid", bias=torch.full((4,), 63.5, device="cuda"), groups=2, top_groups=1, group_best=2)
+
+
+def times(torch, call):
+    for _ in range(3):
+        call()
+    best = float("inf")
+    for _ in range(20):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(4):
+            call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("masked", ["one", "half", "groups"])
+@pytest.mark.parametrize("low", [-1.0e4, -1.0e9, LOWEST])
+def test_a_finite_mask_costs_no_time(env, score, masked, low):  # noqa: F811
+    # (ranking all tokens in 64 bits takes 20 times as long; calls this long do not wait for the host)
+    torch, loom = env
+    g = torch.Generator(device="cuda").manual_seed(4)
+    t, e = 16384, 256
+    logits, bias = torch.randn(t, e, generator=g, device="cuda") * 2, 0.05 * torch.randn(e, generator=g, device="cuda")
+    with_mask = bias.clone()
+    with_mask[{"one": slice(7, 8), "half": slice(0, e, 2), "groups": slice(32, 160)}[masked]] = low
+    for kw in ({}, {"groups": 8, "top_groups": 4, "group_best": 2}):
+        check(env, logits[:512], 8, score=score, bias=with_mask, **kw)
+        ids, weights = loom.loom_route_tokens(logits, 8)
+        call = lambda b: loom.loom_route_tokens(logits, 8, score=score, bias=b, ids=ids, weights=weights, **kw)   # noqa: E731, B023
+        plain, other = times(torch, lambda: call(bias)), times(torch, lambda: call(with_mask))
+        assert other <= 2 * plain, (kw, other, plain)
