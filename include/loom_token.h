@@ -60,7 +60,8 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
 #define LOOM_OP_ROUTE_TOKENS 14        /* workload {tokens, experts, sm_count (0 = the current device)} */
 #define LOOM_OP_ROUTE_TOKENS_BACKWARD 15 /* the same */
 #define LOOM_OP_ADJUST_LOGITS 16       /* workload {rows, vocab, marks (0/1: penalties or biases, default 1), sm_count
-                                          (0 = the current device)} */
+                                          (0 = the current device), dtype (default f32), access (2, default: the rows of
+                                          logits and y start on 16 bytes; 1: they start alike, elsewhere; 0: not alike)} */
 
 /* Kernels they select (loom_launch.kernel). */
 #define LOOM_KERNEL_I8_MATMUL_DP4A 18   /* few tokens: dp4a, weights streamed once per pass of up to 8 tokens */

@@ -176,7 +176,10 @@ struct AdjustParams {
     void *y;
     int32_t *error;
 };
-bool adjust_geometry(int64_t rows, int32_t vocab, bool marks, int64_t sms, loom_launch *out);
+// Where the rows of logits and y start in their 16 bytes: at different places, at the same, on them.
+enum { AL_APART = 0, AL_ALIKE = 1, AL_ALIGNED = 2 };
+int adjust_access(const AdjustParams &p, int bytes);          // bytes: of an element
+bool adjust_geometry(int64_t rows, int32_t vocab, bool marks, int bytes, int access, int64_t sms, loom_launch *out);
 cudaError_t launch_adjust(const AdjustParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream);
 
 }  // namespace loom

@@ -288,7 +288,8 @@ extern "C" loom_status loom_token_launch_config(int32_t op, const int64_t *w, in
         return route_geometry(w[0], (int32_t)w[1], op == LOOM_OP_ROUTE_TOKENS_BACKWARD, sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
     }
     case LOOM_OP_ADJUST_LOGITS: {
-        if (n < 2 || opt(3, 0) < 0)
+        const int64_t dtype = opt(4, LOOM_F32), access = opt(5, AL_ALIGNED);
+        if (n < 2 || opt(3, 0) < 0 || dtype < 0 || dtype > LOOM_BF16 || access < AL_APART || access > AL_ALIGNED)
             return LOOM_ERR_ARG;
         if (w[0] < 0 || w[0] > MAX_INT || w[1] < 1 || w[1] > AL_MAX_VOCAB)
             return LOOM_ERR_SHAPE;
@@ -296,7 +297,7 @@ extern "C" loom_status loom_token_launch_config(int32_t op, const int64_t *w, in
         const loom_status counted = sms ? LOOM_OK : sm_count(&sms);
         if (counted != LOOM_OK)
             return counted;
-        return adjust_geometry(w[0], (int32_t)w[1], opt(2, 1) != 0, sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
+        return adjust_geometry(w[0], (int32_t)w[1], opt(2, 1) != 0, dtype_bytes((int32_t)dtype), (int)access, sms, out) ? LOOM_OK : LOOM_ERR_SHAPE;
     }
     default: return LOOM_ERR_ARG;
     }
@@ -722,7 +723,8 @@ extern "C" loom_status loom_adjust_logits(const void *d_logits, int32_t dtype, i
     p.y = d_y;
     p.error = d_error;
     loom_launch L;
-    if (!adjust_geometry(rows, vocab, p.tokens || p.bias_ids, sms, &L))
+    const int bytes = dtype_bytes(dtype);
+    if (!adjust_geometry(rows, vocab, p.tokens || p.bias_ids, bytes, adjust_access(p, bytes), sms, &L))
         return LOOM_ERR_SHAPE;
     return of_cuda(launch_adjust(p, dtype, L, static_cast<cudaStream_t>(stream)));
 }

@@ -297,65 +297,57 @@ __global__ void __launch_bounds__(AL_THREADS, 2) adjust_kernel(const AdjustParam
 // Shared memory of a slice: its mask's words, a word for each token and the warps' lists.
 int64_t smem_of(bool marks, int64_t slice) { return (slice / 32 + 4) / 4 * 16 + (marks ? 4 * slice + AL_THREADS * AL_BATCH * 2 : 0); }
 
-template <typename E, int N, int U, bool MARKS> cudaError_t launch_one(const AdjustParams &p, loom_launch L, int slices, cudaStream_t stream)
+template <typename E, int N, int U, bool MARKS> cudaError_t launch_one(const AdjustParams &p, const loom_launch &L, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
+    static_assert(AL_THREADS * N * U <= 32768, "places have 15 bits");
     const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(adjust_kernel<E, N, U, MARKS>), 0, done);
-    if (e != cudaSuccess)
-        return e;
-    if (p.rows * slices > 0x7fffffff)
-        return cudaErrorInvalidConfiguration;
-    L.grid[0] = (uint32_t)(p.rows * slices);
-    L.smem_bytes = (uint32_t)smem_of(MARKS, AL_THREADS * N * U);
-    return launch_prepared(adjust_kernel<E, N, U, MARKS>, L, stream, p, slices);
+    return e != cudaSuccess ? e : launch_prepared(adjust_kernel<E, N, U, MARKS>, L, stream, p, (int)(L.grid[0] / p.rows));
 }
 
 template <typename E, int N, int U> cudaError_t launch_u(const AdjustParams &p, const loom_launch &L, cudaStream_t stream)
 {
-    constexpr int SLICE = AL_THREADS * N * U;
-    static_assert(SLICE <= 32768, "places have 15 bits");
-    // rows that do not all start on an access's boundary reach up to N - 1 places further
-    const bool even = reinterpret_cast<uintptr_t>(p.logits) % (N * sizeof(E)) == 0 && p.stride % N == 0;
-    const int slices = (p.vocab + (even ? 0 : N - 1) + SLICE - 1) / SLICE;
-    return p.tokens || p.bias_ids ? launch_one<E, N, U, true>(p, L, slices, stream) : launch_one<E, N, U, false>(p, L, slices, stream);
+    return p.tokens || p.bias_ids ? launch_one<E, N, U, true>(p, L, stream) : launch_one<E, N, U, false>(p, L, stream);
 }
 
-// Tokens of a slice: shorter ones while there are SMs without one.
-int slice_of(int64_t rows, int32_t vocab, int64_t sms)
-{
-    int slice = AL_SLICE;
-    while (slice > AL_LEAST && rows * ((vocab + slice - 1) / slice) < 2 * sms)
-        slice /= 2;
-    return slice;
-}
-
-template <typename E> cudaError_t launch_e(const AdjustParams &p, int slice, const loom_launch &L, cudaStream_t stream)
+template <typename E> cudaError_t launch_e(const AdjustParams &p, const loom_launch &L, cudaStream_t stream)
 {
     constexpr int N = 16 / (int)sizeof(E);
-    if (p.logits == p.y && !p.tokens && !p.bias_ids && !p.mask)
-        return cudaSuccess;
-    const auto phase = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 16; };
-    if (phase(p.logits) != phase(p.y) || (p.stride - p.y_stride) % N)
-        return slice > AL_LEAST ? launch_u<E, 1, 16>(p, L, stream) : launch_u<E, 1, 4>(p, L, stream);
-    if (slice >= 8 * AL_THREADS * N)
-        return launch_u<E, N, 8 * (int)sizeof(E) / 4>(p, L, stream);       // (16-bit types: at most 4)
-    if (slice >= 4 * AL_THREADS * N)
-        return launch_u<E, N, 4>(p, L, stream);
-    if (slice >= 2 * AL_THREADS * N)
-        return launch_u<E, N, 2>(p, L, stream);
-    return launch_u<E, N, 1>(p, L, stream);
+    if (adjust_access(p, (int)sizeof(E)) == AL_APART)
+        return L.units_per_cta == 16 * AL_THREADS ? launch_u<E, 1, 16>(p, L, stream) : launch_u<E, 1, 4>(p, L, stream);
+    switch (L.units_per_cta / (AL_THREADS * N)) {
+    case 8: return launch_u<E, N, 8 * (int)sizeof(E) / 4>(p, L, stream);       // (16-bit types: at most 4)
+    case 4: return launch_u<E, N, 4>(p, L, stream);
+    case 2: return launch_u<E, N, 2>(p, L, stream);
+    default: return launch_u<E, N, 1>(p, L, stream);
+    }
 }
 
 }  // namespace
 
-bool adjust_geometry(int64_t rows, int32_t vocab, bool marks, int64_t sms, loom_launch *out)
+int adjust_access(const AdjustParams &p, int bytes)
 {
-    const int slice = slice_of(rows, vocab, sms);
-    const int64_t ctas = rows * ((vocab + slice - 1) / slice);
-    if (ctas > 0x7fffffff)
+    const auto phase = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 16; };
+    const int n = 16 / bytes;
+    if (phase(p.logits) != phase(p.y) || (p.stride - p.y_stride) % n)
+        return AL_APART;
+    return phase(p.logits) == 0 && p.stride % n == 0 ? AL_ALIGNED : AL_ALIKE;
+}
+
+bool adjust_geometry(int64_t rows, int32_t vocab, bool marks, int bytes, int access, int64_t sms, loom_launch *out)
+{
+    int slice = AL_SLICE;                    // shorter ones while there are SMs without one
+    while (slice > AL_LEAST && rows * ((vocab + slice - 1) / slice) < 2 * sms)
+        slice /= 2;
+    // accesses of 16 bytes: one of a thread at least; of one element: 16 or 4
+    const int n = 16 / bytes;
+    slice = access != AL_APART ? (slice > AL_THREADS * n ? slice : AL_THREADS * n) : slice > AL_LEAST ? 16 * AL_THREADS : 4 * AL_THREADS;
+    // rows that do not all start on an access's boundary reach up to n - 1 places further
+    const int64_t slices = (vocab + (access == AL_ALIKE ? n - 1 : 0) + slice - 1) / slice;
+    if (rows * slices > 0x7fffffff)
         return false;
     *out = loom_launch{};
-    out->grid[0] = (uint32_t)ctas;
+    out->grid[0] = (uint32_t)(rows * slices);
     out->block[0] = AL_THREADS;
     out->grid[1] = out->grid[2] = out->block[1] = out->block[2] = 1;
     out->cluster[0] = out->cluster[1] = out->cluster[2] = 1;
@@ -368,10 +360,11 @@ bool adjust_geometry(int64_t rows, int32_t vocab, bool marks, int64_t sms, loom_
 
 cudaError_t launch_adjust(const AdjustParams &p, int32_t dtype, const loom_launch &L, cudaStream_t stream)
 {
-    const int slice = (int)L.units_per_cta;
+    if (p.logits == p.y && !p.tokens && !p.bias_ids && !p.mask)
+        return cudaSuccess;
     if (dtype == LOOM_F32)
-        return launch_e<float>(p, slice, L, stream);
-    return dtype == LOOM_F16 ? launch_e<__half>(p, slice, L, stream) : launch_e<__nv_bfloat16>(p, slice, L, stream);
+        return launch_e<float>(p, L, stream);
+    return dtype == LOOM_F16 ? launch_e<__half>(p, L, stream) : launch_e<__nv_bfloat16>(p, L, stream);
 }
 
 }  // namespace loom
