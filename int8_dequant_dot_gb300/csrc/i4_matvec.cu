@@ -39,12 +39,12 @@ namespace {
 
 constexpr int I4_ROWS = 64, I4_CHUNK = 128;                      // of a stage: rows, k
 constexpr int I4_STAGE = I4_ROWS * I4_CHUNK / 2;                 // bytes
+constexpr int I4_DEPTH = 3;                                      // stages of a warp's ring
 
 struct I4Shape {          // of a launch
     int tokens;           // that it is built for: 1 or 2 (dp4a), 8, 16 or 32 (MMA columns)
     int warps;
     int team;             // warps that share out k
-    int depth;            // stages of a warp's ring, 2 or 3
     int vec16;            // rows of W start on 16 bytes
     int x8;               // rows of X start on 8 bytes
     int log_group;
@@ -373,7 +373,7 @@ __device__ __forceinline__ void clear_missing(const I4Params &p, const Lists &l)
     }
 }
 
-// A warp's copies, which run ahead of its products: 64 bytes of up to 64 rows a stage.  What lies past the
+// A warp's copies, which run two stages ahead of its products: 64 bytes of up to 64 rows a stage.  What lies past the
 // rows or past k is not copied: it meets zeros, or sums that are thrown away.
 struct Copies {
     const char *src;           // of this lane's first row in the stage
@@ -479,18 +479,17 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
     const int chunks = (p.k + I4_CHUNK - 1) / I4_CHUNK;
     const int c0 = chunks * part / s.team, c1 = chunks * (part + 1) / s.team;
 
-    const uint32_t ring = dev::smem_u32(i4_shared) + warp * s.depth * I4_STAGE;
+    const uint32_t ring = dev::smem_u32(i4_shared) + warp * I4_DEPTH * I4_STAGE;
     float *scales = reinterpret_cast<float *>(i4_shared + s.scales) + warp * I4_ROWS * SP;
     const Nibbles n = nibble_masks();
     // ldmatrix: lane's row of a tile, and the piece of 16 bytes that it points at in the first two steps
     const uint32_t place = (lane & 15) * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
 
-    // the copies run `depth - 1` stages ahead of the products
     Copies ahead;
     const int word = lane & 15;
     const uint32_t first_place = s.vec16 ? (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4)
                                          : (lane >> 4) * 64 + ((word >> 2) << 4) + 4 * (word & 3);
-    const uint32_t ring_end = ring + s.depth * I4_STAGE;
+    const uint32_t ring_end = ring + I4_DEPTH * I4_STAGE;
     ahead.at = ring + first_place;
     start_unit(ahead, way, p, s, l, c0, lane);
     const auto copy_next = [&]() {
@@ -503,9 +502,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
         copies_commit();
         ahead.at += I4_STAGE;
         if (ahead.at >= ring_end)
-            ahead.at -= s.depth * I4_STAGE;
+            ahead.at -= I4_DEPTH * I4_STAGE;
     };
-    for (int i = 1; i < s.depth; ++i)
+    for (int i = 1; i < I4_DEPTH; ++i)
         copy_next();
 
     uint32_t stage = ring + place;
@@ -576,10 +575,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
             load_scales(c0);
         }
         for (int c = c0; c < c1; ++c) {
-            if (s.depth == 3)
-                copies_wait<1>();
-            else
-                copies_wait<0>();
+            copies_wait<I4_DEPTH - 2>();
             __syncwarp();                    // the stage is there, and the last one read by all lanes
             copy_next();
             // (the whole sums are in 2^-24)
@@ -670,7 +666,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
             }
             stage += I4_STAGE;
             if (stage >= ring_end)
-                stage -= s.depth * I4_STAGE;
+                stage -= I4_DEPTH * I4_STAGE;
         }
         const auto finish = [&](float y, int row, int col) {
             const int pair = p.ids ? l.pair[u.list + col] : u.list + col;
@@ -981,9 +977,12 @@ int log2_floor(int64_t v)
     return l;
 }
 
+// Bytes of the experts' lists (make_lists).
+constexpr int64_t list_bytes(int64_t experts, int64_t pairs) { return (10 * experts + 4 + 2 * pairs + 15) / 16 * 16; }
+
 // What a launch is built for: tokens of the dp4a kernel (1 or 2), or MMA columns (8, 16, 32), for the
 // pairs that a matrix has -- on average half as many again of the experts' that are wanted.
-// Its warps, ring and shared memory (the static arrays of make_lists are counted as 256 bytes).
+// Its warps and shared memory (the static arrays of make_lists are counted as 256 bytes).
 uint32_t i4_shape(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t experts, int64_t sms, I4Shape *s)
 {
     const int64_t named = experts ? (pairs < experts ? pairs : experts) : 1;
@@ -1003,17 +1002,13 @@ uint32_t i4_shape(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t ex
     while (team > 1 && team > (few ? chunks / 2 : chunks))
         team /= 2;
     s->team = team;
-    const uint32_t lists = experts ? (uint32_t)(((10 * experts + 4 + 2 * pairs) + 15) / 16 * 16) : 0;
-    const uint32_t scales = few ? 0 : s->warps * I4_ROWS * 4 * (group == 32 ? 4 : group == 64 ? 2 : 1);
-    const uint32_t sums = few ? (uint32_t)(s->team * DP_RUN * s->tokens * 4) : 0;
-    const uint32_t ways = few ? 0 : s->warps * sizeof(Way), rest = scales + sums + ways + lists;
-    s->depth = few ? 0 : 3 * s->warps * I4_STAGE + rest + 256 <= 227 * 1024 ? 3 : 2;
-    s->scales = (uint32_t)(s->depth * s->warps * I4_STAGE);
-    s->sums = s->scales + scales;
-    s->ways = s->sums + sums;
-    s->lists = s->ways + ways;
-    return s->lists + lists;
+    s->scales = few ? 0 : (uint32_t)(s->warps * I4_DEPTH * I4_STAGE);
+    s->sums = s->scales + (few ? 0 : s->warps * I4_ROWS * 4 * (group == 32 ? 4 : group == 64 ? 2 : 1));
+    s->ways = s->sums + (few ? (uint32_t)(s->team * DP_RUN * s->tokens * 4) : 0);
+    s->lists = s->ways + (few ? 0 : s->warps * (uint32_t)sizeof(Way));
+    return s->lists + (experts ? (uint32_t)list_bytes(experts, pairs) : 0);
 }
+static_assert(16 * (I4_DEPTH * I4_STAGE + I4_ROWS * 16 + (int)sizeof(Way)) + list_bytes(I4_MAX_EXPERTS, I4_MAX_PAIRS) + 256 <= 227 * 1024, "the most there is");
 
 }  // namespace
 
@@ -1022,7 +1017,7 @@ void i4_geometry(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t exp
     I4Shape s;
     *out = loom_launch{};
     out->smem_bytes = i4_shape(pairs, n, k, group, experts, sms, &s);
-    const int64_t most = (experts ? (experts < pairs ? experts : pairs) : 1) * n, ctas = s.depth ? sms : 2 * sms;
+    const int64_t most = (experts ? (experts < pairs ? experts : pairs) : 1) * n, ctas = s.tokens > 2 ? sms : 2 * sms;
     out->grid[0] = (uint32_t)(most < ctas ? (most > 0 ? most : 1) : ctas);
     out->grid[1] = out->grid[2] = out->block[1] = out->block[2] = 1;
     out->block[0] = 32 * s.warps;
