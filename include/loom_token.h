@@ -57,7 +57,8 @@ typedef enum loom_dtype { LOOM_F32 = 0, LOOM_F16 = 1, LOOM_BF16 = 2 } loom_dtype
 #define LOOM_OP_SAMPLE_TOKENS 12       /* workload {rows, vocab, dtype, sm_count (0 = the current device)} */
 #define LOOM_OP_I4_MATVEC 13           /* workload {tokens, n, k, group, experts (0: one matrix, default), routes
                                           (default 1), sm_count (0 = the current device)}: the first launch */
-#define LOOM_OP_ROUTE_TOKENS 14        /* workload {tokens, experts, sm_count (0 = the current device)} */
+#define LOOM_OP_ROUTE_TOKENS 14        /* workload {tokens, experts, sm_count (0 = the current device)}; the shared memory is
+                                          that of a call with a bias or groups, and counts (others take less) */
 #define LOOM_OP_ROUTE_TOKENS_BACKWARD 15 /* the same */
 #define LOOM_OP_ADJUST_LOGITS 16       /* workload {rows, vocab, marks (0/1: penalties or biases, default 1), sm_count
                                           (0 = the current device), dtype (default f32), access (2, default: the rows of
@@ -228,7 +229,8 @@ loom_status loom_sample_tokens(const void *d_logits, int32_t dtype, int64_t rows
  * and one rounding to `dtype`, the type of logits and y.  Logits that no step changes keep their bits.
  * d_history: int32 [rows][history], rows history_stride elements apart, or NULL (nothing was
  * seen); tokens outside [0, vocab) are passed over.  d_lengths: int32 [rows], or NULL (all
- * `history` tokens); a length outside [0, history] is cut and flagged (LOOM_DEVERR_COUNT_RANGE).
+ * `history` tokens); a length outside [0, history] is cut and flagged (LOOM_DEVERR_COUNT_RANGE; where there is no history, NULL
+ * or of 0 tokens, lengths and prompts are not looked at).
  * d_prompts: int32 [rows], or NULL (0); outside [0, length] it is cut.  Penalties are one device value per row, or,
  * where that is NULL, the host value for every row; a device repetition that is not above zero counts as 1.
  * d_bias_ids int32 and d_bias_values f32 [rows][biases], or NULL; ids outside [0, vocab)
@@ -257,7 +259,8 @@ loom_status loom_adjust_logits(const void *d_logits, int32_t dtype, int64_t rows
  * neighbours along k (the last group of a row may be shorter):
  *   a[t][r][g] = sum over k in group g of W[r][k] * X[t][k]                       (exact)
  *   y[t][r]    = d_scale_x[t] * sum over g of scale_w[r][g] * a[t][r][g] + d_bias[r]
- * the sum over groups in f32, in a fixed order that depends on the sizes alone, and one rounding to `y_dtype`.
+ * the sum over groups in f32, and one rounding to `y_dtype`.  Its order is fixed by the sizes, by the GPU's number of SMs and,
+ * for one or two tokens, by whether all rows of W start on 16 bytes: the same weights elsewhere may give other last bits.
  * d_w_packed: int32 [n_rows][k/8], word j of a row holds elements 8j..8j+7, element 8j+i in
  * bits [4i, 4i+3] as a signed nibble (-8..7).  d_scale_w: [n_rows][ceil(k / group)] of type
  * scale_dtype; scales beyond 2^100 in size overflow.  d_x_packed: int32 [tokens][k/4], d_scale_x f32 [tokens], as
@@ -279,8 +282,12 @@ loom_status loom_i4_matvec(const int32_t *d_w_packed, const void *d_scale_w, int
  * [experts][n_rows] or NULL.  x_rows is `tokens` (a token's routes share its row of X) or
  * tokens * routes (each pair has a row of X and a scale of its own, as a second layer wants).  A
  * negative id is a missing route: its row of y is zeros.  An id of `experts` or more is treated so
- * too and flagged (LOOM_DEVERR_COUNT_RANGE).  A matrix is read once for every 32 pairs that name it,
- * among 2048 pairs.  y's rows are loom_routed_combine's payload, row t * routes + j of pair (t, j).
+ * too and flagged (LOOM_DEVERR_COUNT_RANGE).  A launch takes up to 2048 pairs and goes through a matrix once for every 1, 2,
+ * 8, 16 or 32 of them that name it.  The width is the same for all: the smallest that is not below one and a half times the
+ * average pairs / min(pairs, experts), or 32 (with up to a fourth as many pairs as experts 1; with one expert its
+ * pairs are the average).  Experts that far more pairs name than others therefore cost more passes: 64 tokens to 8
+ * of 64 experts of 2048 x 4096 take 89 us, with half of the pairs on two experts 150 to 180.
+ * y's rows are loom_routed_combine's payload, row t * routes + j of pair (t, j).
  * Errors: as loom_i4_matvec, and experts < 0 or > 1024, routes < 0 or > 64, tokens * routes > 2^31 - 1,
  * x_rows neither of the two -> LOOM_ERR_SHAPE.
  */
