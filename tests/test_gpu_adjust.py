@@ -208,7 +208,7 @@ def test_history_rows_apart(env):
     assert torch.equal(loom.loom_adjust_logits(logits, history=view, repetition=1.5), loom.loom_adjust_logits(logits, history=view.contiguous(), repetition=1.5))
 
 
-# many rows: a kernel that copies, then one for the marked tokens alone, by a table or (long histories) a word a token
+# many rows: slices of the largest size, with histories on both sides of 4096 tokens (lists of marked tokens, or all marks looked through)
 @pytest.mark.parametrize("rows,vocab,n,biases,masks", [(320, 2000, 300, 9, 0), (330, 9000, 9000, 1024, 3), (400, 3001, 12000, 5, 2), (310, 70001, 11000, 20, 2), (305, 40, 10240, 0, 1),
                                                        (306, 64, 0, 1024, 0), (700, 1, 5, 3, 1)])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
@@ -242,7 +242,7 @@ def test_many_rows(env, rows, vocab, n, biases, masks, dtype):
 
 
 def test_kernels_in_a_row(env):
-    # inputs written by the kernel before, at once: many rows' second kernel begins before its first has ended
+    # inputs written by the kernel before, at once: a kernel is scheduled before the one in front of it has ended
     torch, loom = env
     rows, vocab, n = 400, 20000, 600
     logits = torch.randn(rows, vocab, device="cuda")
