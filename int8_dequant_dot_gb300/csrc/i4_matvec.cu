@@ -6,7 +6,8 @@
 // Design
 //  * Bound: the n k / 2 bytes of W.  One CTA an SM (two for one or two tokens) takes an equal share of the rows (of
 //    all rows of the experts that some pair names, counted once for each pass over them), so no partial sums leave
-//    a CTA and every row is read once for up to 32 tokens.
+//    a CTA.  A row is gone through once for as many pairs as the launch has columns for (1, 2, 8, 16 or 32): one matrix's
+//    as its tokens want, up to 32; the experts' as their average number of pairs wants (i4_shape).
 //  * The tensor cores make the sums exact.  A weight's nibble is turned into w + 8 (one XOR) and its bits
 //    are taken as a subnormal f16, (w + 8) 2^-24, or four places higher, (w + 8) 2^-20; those of the second kind
 //    meet a token's byte / 16.  So eight weights cost five logic instructions and no conversion, and
@@ -14,7 +15,7 @@
 //    f16 MMAs (m16n8k16) with f32 sums lose nothing.  The 8 too many per weight is taken off by starting the sums
 //    at -8 times the sum of the token's bytes.  (Rates measured, products per SM and clock: f16 1000, e4m3 3750, s8
 //    260, dp4a 256.  e4m3, whose codes 0 to 15 are whole numbers too, with bytes as two halves: exact, but 28 us
-//    for the 20.6 of 8 tokens below.)
+//    for the 20.9 of 8 tokens below.)
 //  * A warp takes 64 rows x 128 k at a time: 64 bytes of each row, copied ahead into its own ring of
 //    shared memory (cp.async, 16 bytes; 4 where rows do not start on 16 bytes), 16-byte pieces swizzled by
 //    row, so that ldmatrix hands each lane whole words of eight neighbouring weights without conflicts.  The
@@ -27,11 +28,12 @@
 //    one warp).  Which column of an MMA a pair takes does not change its sums.
 //  * What bounds it: one token the bytes and 4 us to start and end; more of them instructions (500 a stage, of which
 //    unpacking and MMAs 243, the tokens' conversion 60 for each eight), 1.3 to 1.8 a clock.  Copies alone take 14 us of
-//    the 20.6.
+//    the 20.9.  The kernels of 32 columns spill (12 bytes with groups of 128, 80 of 64, 396 of 32).
 //
-// Measured (8192 x 16384, groups of 128, f16 scales): 1 token 14.8 us (4.7 TB/s), 2 16.6, 3 20.4, 8 20.6, 16 26.4, 32 43.6;
-// 16 tokens with groups of 64 30, of 32 36.  Experts of 2048 x 4096, 8 of 64: 1 token 10.6 us, 4 27, 16 59, 32 63 (269 MB,
-// 4.3 TB/s).  5 x 5001 x 4104, groups of 32, f32 scales 11.6 us.
+// Measured as nodes of a CUDA graph (8192 x 16384, groups of 128, f16 scales): 1 token 14.7 us (4.7 TB/s), 2 16.5, 3 20.6, 8 20.9,
+// 16 25.9, 32 42.8; 16 tokens with groups of 64 29.9, of 32 35.6.  Experts of 2048 x 4096, 8 of 64: 1 token 10.6 us, 4 27, 16 58,
+// 32 62.6 (269 MB, 4.3 TB/s).  5 x 5001 x 4104, groups of 32, f32 scales 11.6 us.  (A small call through the binding takes 11 to
+// 13 us, the host's part.)
 #include "token_ops.cuh"
 
 namespace loom {
@@ -740,7 +742,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) i4_matvec_kernel(const I4Params
 // ---- one or two tokens: dp4a ------------------------------------------------------------------
 // Lanes across k: 16 bytes of a row (32 weights, one scale) each, so a warp takes 1024 k of R rows at a
 // time with the tokens' bytes for them in registers.  A nibble in a byte's upper half is 16 times a signed
-// weight, so eight weights cost three logic instructions and two dp4a (8192 x 16384: 14.8 us for one token where the
+// weight, so eight weights cost three logic instructions and two dp4a (8192 x 16384: 14.7 us for one token where the
 // tensor cores take 20).  Warps share out k where it is long, rows where it is not; a row's sums over lanes meet in
 // shared memory, one place per warp, and are added in a fixed order.
 constexpr int DP_CHUNK = 1024;      // k of a warp's access
@@ -981,7 +983,9 @@ int log2_floor(int64_t v)
 constexpr int64_t list_bytes(int64_t experts, int64_t pairs) { return (10 * experts + 4 + 2 * pairs + 15) / 16 * 16; }
 
 // What a launch is built for: tokens of the dp4a kernel (1 or 2), or MMA columns (8, 16, 32), for the
-// pairs that a matrix has -- on average half as many again of the experts' that are wanted.
+// pairs that a matrix has -- on average half as many again of the experts' that are wanted.  The host does not know the ids:
+// uneven ones take more passes (64 tokens to 8 of 64 experts 89 us, all tokens to the same 8 46, half of
+// the pairs to two experts 150 to 180).
 // Its warps and shared memory (the static arrays of make_lists are counted as 256 bytes).
 uint32_t i4_shape(int64_t pairs, int64_t n, int64_t k, int64_t group, int64_t experts, int64_t sms, I4Shape *s)
 {

@@ -14,10 +14,12 @@
 //    slice's marks are looked through.)  The lists keep warps full: where 1 token of 19 is a given slice's, 32 of them
 //    cost as much as one.
 //
-// Measured (f32)
-//   1 x 32768, history 2000, biases, a mask   3.0 us
-//   256 x 131072, history 4096 (2048 on average), 64 biases, masks for half of the rows   52.3 us (copy and mask alone 41;
-//   bf16 43.5 us; history 131072 273 us)
+// Measured as nodes of a CUDA graph (f32)
+//   1 x 32768, history 2000, biases, a mask   3.1 us (a call through the binding 17, the host's part)
+//   256 x 131072, history 4096 (2048 on average), 64 biases, masks for half of the rows   52.2 us (copy and mask alone 41;
+//   bf16 43.4 us; histories of 5000 64, 8192 74, 16384 97, 131072 273 us)
+//   the same in place, history 4096 and a mask of half of the tokens for every row: 78 us, bf16 41 (to another y 55 and 45):
+//   what a mask changes is read when that is known, not ahead
 // (Tried: marks looked up for every logit, 56 us; a bit a token, numbers by running counts and marks by numbers, 55 us; a
 // cluster sharing out the history and marking each other's slices, 96 us, as most tokens of a text are in one slice;
 // a second kernel for the marked tokens, 57 us, which finds them in DRAM again; CTAs that load the next slice while they

@@ -8,7 +8,9 @@
 //    is that of the logits; else the scores plus bias are ranked with a bound of their error, and a token whose
 //    order it leaves open (two neighbours among the chosen and the next one, or groups at the cut, nearer than that)
 //    is ranked in 64 bits, of those experts alone that may make a difference, one a lane (all of a token's where they are
-//    more than 32).  64-bit units are few on this GPU (2 lanes an SM and clock): all tokens of 16384 x 256 would
+//    more than 32, or where there are more than 32 groups).  A sum's bound goes by its own size, so that a finite mask in the
+//    bias (-1e9, the lowest f32) opens no other expert's order: 16384 x 256 take 19.8 us with one or with half of them masked, 19.7 without.
+//    64-bit units are few on this GPU (2 lanes an SM and clock): all tokens of 16384 x 256 would
 //    take 640 us, and a single one in full held up the kernel for 25 us; of normal logits one in a thousand is open.
 //  * The chosen ones are found top_k + 1 times as the warp's maximum of the lanes' largest keys.  A key is a float as
 //    an ordered whole number whose last 5 to 10 bits are the expert's, so that the maximum names it; a lane has its keys
@@ -17,9 +19,9 @@
 //    open, in 64 bits for those near the last one chosen.
 //    What bounds many tokens is the instructions of that, not the logits' bytes.
 //
-// Measured: 1 x 64 1.9 us; 16384 x 256 f32, sigmoid, top 8: 14.4 us, with a bias 19.9, with 4 of 8 groups as well 25.8
-// (1190 instructions a token, 2.7 a clock); softmax 37.7.  Gradient of 16384 x 256: 7.6 us renormalised, 10.3 of a
-// softmax over all.
+// Measured as nodes of a CUDA graph: 1 x 64 2.0 us (a call through the binding 13, the host's part); 16384 x 256 f32, sigmoid, top 8:
+// 14.4 us, with a bias 19.7, with 4 of 8 groups as well 25.6 (1190 instructions a token, 2.7 a clock); softmax 37.2; with 16 of 64
+// groups, all in 64 bits, 600.  Gradient of 16384 x 256: 7.6 us renormalised, 10.2 of a softmax over all.
 #include <cfloat>
 
 #include "token_ops.cuh"
