@@ -20,7 +20,7 @@
 //    What bounds many tokens is the instructions of that, not the logits' bytes.
 //
 // Measured as nodes of a CUDA graph: 1 x 64 2.0 us (a call through the binding 13, the host's part); 16384 x 256 f32, sigmoid, top 8:
-// 14.4 us, with a bias 19.7, with 4 of 8 groups as well 25.6 (1190 instructions a token, 2.7 a clock); softmax 37.2; with 16 of 64
+// 14.4 us, with a bias 19.7, with 4 of 8 groups as well 25.6 (1195 instructions a token, 2.7 a clock); softmax 37.2; with 16 of 64
 // groups, all in 64 bits, 600.  Gradient of 16384 x 256: 7.6 us renormalised, 10.2 of a softmax over all.
 #include <cfloat>
 
